@@ -43,27 +43,27 @@ def listed():
         # one step of a chunked prompt deep in a 32K context, the Llama layer shape
         _chunk("chunk 2048 in 32K", 1, 32, 8, (4, 8, 4, 8), 256, (30720, 30720), (2048, 2048)),
         # a batch that mixes prompt chunks and single tokens, ragged, small permuted pages
-        _chunk("mixed chunks, paged 64", 16, 32, 8, (2, 8, 4, 8), 64, (4096, 8192), (1, 509)),
+        _chunk("mixed chunks paged 64", 16, 32, 8, (2, 8, 4, 8), 64, (4096, 8192), (1, 509)),
         # checking a few drafted tokens of each sequence, the 40-head layer with 9-bit V codes
-        _chunk("5 drafted tokens, batch 16", 16, 40, 8, (2, 8, 4, 9), 256, (8000, 16384), (5, 5)),
+        _chunk("5 drafted tokens batch 16", 16, 40, 8, (2, 8, 4, 9), 256, (8000, 16384), (5, 5)),
         # a whole prompt from an empty cache, 1.5-bit codes
-        _chunk("prompt of 2049, 1.5 bit", 1, 32, 8, (8, 12, 8, 12), 256, (0, 0), (2049, 2049)),
+        _chunk("prompt of 2049 at 1.5 bit", 1, 32, 8, (8, 12, 8, 12), 256, (0, 0), (2049, 2049)),
         # single tokens of many long sequences, window of 4096 and four sinks
-        _chunk("window 4096, batch 64", 64, 40, 8, (2, 8, 4, 9), 256, (9001, 16384), (1, 1), 4096, 4),
+        _chunk("window 4096 batch 64", 64, 40, 8, (2, 8, 4, 9), 256, (9001, 16384), (1, 1), 4096, 4),
         # prompt chunks with a short window and sinks that end inside a page
-        _chunk("window 1024, chunks of 1000", 4, 32, 8, (4, 8, 4, 8), 256, (5000, 20011), (777, 1000), 1024, 68),
+        _chunk("window 1024 chunks of 1000", 4, 32, 8, (4, 8, 4, 8), 256, (5000, 20011), (777, 1000), 1024, 68),
         # the smallest call: one token of one short conversation
-        _chunk("one token, window 256", 1, 8, 2, (2, 8, 4, 8), 64, (333, 333), (1, 1), 256, 4),
+        _chunk("one token window 256", 1, 8, 2, (2, 8, 4, 8), 64, (333, 333), (1, 1), 256, 4),
         # one new token for each sequence of a large decode batch
-        _slots("slots, 256 decode tokens", 256, 64, (1, 8192), (1, 1)),
+        _slots("slots 256 decode tokens", 256, 64, (1, 8192), (1, 1)),
         # a step that admits long prompts beside decode tokens
-        _slots("slots, 120K prompt tokens", 48, 256, (0, 5000), (1, 5001)),
+        _slots("slots 120K prompt tokens", 48, 256, (0, 5000), (1, 5001)),
         # one decode step's q, k, v
-        _rotary("rotary, 64 tokens", 64, 32, 8, "fp16", 128, False, "none", 1.0, 131072),
+        _rotary("rotary 64 tokens", 64, 32, 8, "fp16", 128, False, "none", 1.0, 131072),
         # a prompt chunk out of a bf16 projection, half of the head rotated, interleaved pairs
-        _rotary("rotary, 4099 bf16", 4099, 40, 8, "bf16", 64, True, "linear", 4.0, 32768),
+        _rotary("rotary 4099 bf16", 4099, 40, 8, "bf16", 64, True, "linear", 4.0, 32768),
         # a long prompt, frequencies scaled by parts for far positions
-        _rotary("rotary, 32768 far", 32768, 32, 8, "fp16", 128, False, "parts", 16.0, 1000000),
+        _rotary("rotary 32768 far", 32768, 32, 8, "fp16", 128, False, "parts", 16.0, 1000000),
     ]
 
 
