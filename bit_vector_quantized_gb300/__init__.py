@@ -5,8 +5,8 @@ in the library's CUDA kernels):
 
 * ``vq_*`` functions mirror the C ABI of include/vqattn.h one to one: they take
   device pointers as Python ints and raise :class:`VQError` on a non-OK status.
-* ``encode_kv`` / ``decode_attention`` / ``alloc_pools`` / ``alloc_workspace``
-  accept torch tensors (PyTorch supplies device memory and streams), check
+* ``encode_kv`` / ``decode_attention`` / ``append_slots`` / ``rotary`` /
+  ``alloc_pools`` / ``alloc_workspace`` and their like accept torch tensors (PyTorch supplies device memory and streams), check
   dtypes, shapes and devices, and pass their pointers to the ``vq_*`` calls.
 
 There is no fallback: if libvqattn.so has not been built the first call raises.
@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libvqattn.so")
@@ -29,6 +29,9 @@ VQ_ERR_CUDA = -4
 STATUS_NAMES = {0: "VQ_OK", -1: "VQ_ERR_INVALID_ARG", -2: "VQ_ERR_UNSUPPORTED",
                 -3: "VQ_ERR_WORKSPACE", -4: "VQ_ERR_CUDA"}
 VQ_DEV_OK, VQ_DEV_BAD_PAGE, VQ_DEV_BAD_SLOT, VQ_DEV_TIMEOUT, VQ_DEV_BAD_CONFIG = 0, 1, 2, 3, 4
+VQ_DEV_BAD_LENGTH, VQ_DEV_NO_PAGES = 5, 6
+VQ_FP16, VQ_BF16 = 0, 1
+VQ_ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3, "wavelength": 4}
 
 # every symbol include/vqattn.h declares
 EXPORTED = ("vq_code_row_bytes", "vq_check_layout", "vq_encode_kv", "vq_decode_workspace_bytes",
@@ -36,8 +39,8 @@ EXPORTED = ("vq_code_row_bytes", "vq_check_layout", "vq_encode_kv", "vq_decode_w
             "vq_decode_partial",
             "vq_decode_partial_method", "vq_decode_combine", "vq_decode_step", "vq_dequantize_kv",
             "vq_decode_residual_workspace_bytes", "vq_decode_attention_residual",
-            "vq_decode_attention_static", "vq_static_scratch_bytes", "vq_last_error",
-            "vq_version")
+            "vq_decode_attention_static", "vq_static_scratch_bytes", "vq_append_slots",
+            "vq_rotary", "vq_last_error", "vq_version")
 
 
 class VQError(RuntimeError):
@@ -59,6 +62,26 @@ class vq_layout(ctypes.Structure):
 def make_layout(head_dim=128, num_q_heads=32, num_kv_heads=8, k_sub=4, k_bits=8, v_sub=4,
                 v_bits=8, page_size=256) -> vq_layout:
     return vq_layout(head_dim, num_q_heads, num_kv_heads, k_sub, k_bits, v_sub, v_bits, page_size)
+
+
+class vq_rotary_config(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low_turns", ctypes.c_double),
+                ("high_turns", ctypes.c_double), ("attention_factor", ctypes.c_double)]
+
+
+def make_rotary(head_dim=128, rotary_dim=128, interleaved=False, base=10000.0, scaling="none",
+                factor=1.0, original_len=8192, low_turns=1.0, high_turns=32.0,
+                attention_factor=1.0) -> vq_rotary_config:
+    """Rotary positions (see vq_rotary_config in the header); scaling is "none", "linear",
+    "base", "parts" or "wavelength"."""
+    if scaling not in VQ_ROTARY_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} is not one of {sorted(VQ_ROTARY_SCALINGS)}")
+    return vq_rotary_config(head_dim, rotary_dim, int(bool(interleaved)),
+                            VQ_ROTARY_SCALINGS[scaling], base, factor, original_len, low_turns,
+                            high_turns, attention_factor)
 
 
 _lib = None
@@ -98,6 +121,10 @@ def lib() -> ctypes.CDLL:
             "vq_decode_attention_static": (I32, [LP, I32, P, P, P, P, P, P, I64, P, I32, P, I32,
                                                  ctypes.c_float, I32, P, P, P]),
             "vq_static_scratch_bytes": (SZ, []),
+            "vq_append_slots": (I32, [I32, P, P, P, I32, P, I32, P, I32, I64, I32, P, P, P, P, P,
+                                      P, P]),
+            "vq_rotary": (I32, [ctypes.POINTER(vq_rotary_config), I32, P, I32, P, I64, I32, P, P,
+                                I64, P, I64, I32, P, P, P]),
             "vq_last_error": (ctypes.c_char_p, []),
             "vq_version": (ctypes.c_char_p, []),
         }
@@ -247,6 +274,24 @@ def vq_decode_attention_static(layout, batch, q, lambda_, codebook_k, codebook_v
 
 def vq_static_scratch_bytes() -> int:
     return int(lib().vq_static_scratch_bytes())
+
+
+def vq_append_slots(batch, seq_lens, new_lens, page_table, max_pages_per_seq, free_pages,
+                    free_capacity, num_free, page_size, num_pages, max_tokens, seq_lens_out,
+                    num_free_out, cu_new_lens, slot_mapping, positions, status=None,
+                    stream=None) -> None:
+    _check(lib().vq_append_slots(batch, _ptr(seq_lens), _ptr(new_lens), _ptr(page_table),
+                                 max_pages_per_seq, _ptr(free_pages), free_capacity,
+                                 _ptr(num_free), page_size, num_pages, max_tokens,
+                                 _ptr(seq_lens_out), _ptr(num_free_out), _ptr(cu_new_lens),
+                                 _ptr(slot_mapping), _ptr(positions), _ptr(status), _ptr(stream)))
+
+
+def vq_rotary(config, num_tokens, positions, dtype, q, q_stride, num_q_heads, q_out, k, k_stride,
+              v, v_stride, num_kv_heads, k_out, v_out, stream=None) -> None:
+    _check(lib().vq_rotary(ctypes.byref(config), num_tokens, _ptr(positions), dtype, _ptr(q),
+                           q_stride, num_q_heads, _ptr(q_out), _ptr(k), k_stride, _ptr(v),
+                           v_stride, num_kv_heads, _ptr(k_out), _ptr(v_out), _ptr(stream)))
 
 
 def vq_last_error() -> str:
@@ -491,3 +536,129 @@ def decode_step(layout: vq_layout, q, k_new, v_new, lambda_, codebook_k, codeboo
                    _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
                    _dev_ptr(status, torch.int32, "status", (1,)), _stream(stream))
     return out
+
+
+# ------------------------------------------------- torch layer: serving step ---
+# These calls run on the device of their tensors whatever the current one is, and
+# make the outputs and workspaces that they are not given on the stream they run on.
+
+class _Launch:
+    """Device and stream of one call: enters the tensors' device and, where `stream` is given,
+    that stream, so that what the call allocates belongs to it."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.ctx = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return _torch().cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _arg(t, dtype, name, device, shape=None):
+    """data_ptr of a tensor argument (contiguous, of this type and shape, on this device)."""
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return _dev_ptr(t, dtype, name, shape)
+
+
+class AppendedSlots(NamedTuple):
+    seq_lens: object      # int32 [B]
+    num_free: object      # int32 [1]
+    cu_new_lens: object   # int32 [B + 1]
+    slot_mapping: object  # int64 [max_tokens]
+    positions: object     # int32 [max_tokens]
+
+
+def append_slots(seq_lens, new_lens, page_table, free_pages, num_free, page_size: int,
+                 num_pages: int, max_tokens: int, seq_lens_out=None, num_free_out=None,
+                 cu_new_lens=None, slot_mapping=None, positions=None, status=None,
+                 stream=None) -> AppendedSlots:
+    """Page tables, slots, positions and row offsets of one step (see vq_append_slots):
+    page_table [B][max_pages] is extended in place with pages off the free stack."""
+    torch = _torch()
+    if not isinstance(seq_lens, torch.Tensor) or not seq_lens.is_cuda:
+        raise TypeError("seq_lens must be a CUDA tensor")
+    B, dev, i32 = seq_lens.shape[0], seq_lens.device, torch.int32
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B][max_pages]")
+    with _Launch(dev, stream) as st:
+        new = lambda t, n, dt: torch.empty(n, dtype=dt, device=dev) if t is None else t  # noqa: E731
+        r = AppendedSlots(new(seq_lens_out, B, i32), new(num_free_out, 1, i32),
+                          new(cu_new_lens, B + 1, i32), new(slot_mapping, max_tokens, torch.int64),
+                          new(positions, max_tokens, i32))
+        vq_append_slots(B, _arg(seq_lens, i32, "seq_lens", dev, (B,)),
+                        _arg(new_lens, i32, "new_lens", dev, (B,)),
+                        _arg(page_table, i32, "page_table", dev, (B, page_table.shape[1])),
+                        page_table.shape[1],
+                        _arg(free_pages, i32, "free_pages", dev, (free_pages.numel(),)),
+                        free_pages.numel(), _arg(num_free, i32, "num_free", dev, (1,)), page_size,
+                        num_pages, max_tokens, _arg(r.seq_lens, i32, "seq_lens_out", dev, (B,)),
+                        _arg(r.num_free, i32, "num_free_out", dev, (1,)),
+                        _arg(r.cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)),
+                        _arg(r.slot_mapping, torch.int64, "slot_mapping", dev, (max_tokens,)),
+                        _arg(r.positions, i32, "positions", dev, (max_tokens,)),
+                        _arg(status, i32, "status", dev, (1,)), st)
+    return r
+
+
+def _rows_arg(t, dtype, name, device, tokens, head_dim):
+    """(data_ptr, token stride) of [T][heads][D] rows whose heads are contiguous."""
+    if t is None:
+        return None, 0
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({tokens}, heads, {head_dim})")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else max(t.shape[1] * head_dim, 8)
+
+
+def rotary(config: vq_rotary_config, positions, q=None, k=None, v=None, q_out=None, k_out=None,
+           v_out=None, stream=None):
+    """(q, k, v) fp16 [T][heads][D]: q and k turned by positions (int32 [T]), v carried along.
+    Inputs are fp16 or bf16, all of one type, and may be slices of one fused projection; one
+    not given comes back as None.  An output may be its own (fp16, contiguous) input."""
+    torch = _torch()
+    some = q if q is not None else k if k is not None else v
+    if some is None:
+        raise ValueError("q, k and v are all None")
+    if some.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"q, k and v must be float16 or bfloat16, got {some.dtype}")
+    T, D, dev = positions.shape[0], config.head_dim, some.device
+    if k is not None and v is not None and k.shape[1] != v.shape[1]:
+        raise ValueError("k and v have different numbers of heads")
+    with _Launch(dev, stream) as st:
+        a, out = [], []
+        for x, o, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
+            a.append(_rows_arg(x, some.dtype, name, dev, T, D))
+            if x is not None and o is None:
+                o = torch.empty((T, x.shape[1], D), dtype=torch.float16, device=dev)
+            elif x is None and o is not None:
+                raise ValueError(f"{name}_out is given without {name}")
+            out.append(o)
+        kv = k if k is not None else v
+        ptr = [None if o is None else _arg(o, torch.float16, n, dev, (T, x.shape[1], D))
+               for o, x, n in zip(out, (q, k, v), ("q_out", "k_out", "v_out"))]
+        vq_rotary(config, T, _arg(positions, torch.int32, "positions", dev, (T,)),
+                  VQ_BF16 if some.dtype == torch.bfloat16 else VQ_FP16, a[0][0], a[0][1],
+                  0 if q is None else q.shape[1], ptr[0], a[1][0], a[1][1], a[2][0], a[2][1],
+                  0 if kv is None else kv.shape[1], ptr[1], ptr[2], st)
+    return tuple(out)

@@ -907,3 +907,183 @@ vq_status vq_decode_attention_residual(const vq_layout* layout, int32_t batch, c
 }
 
 }  // extern "C"
+
+// ---- page tables, slot maps and rotary positions -------------------------------
+namespace {
+
+// The frequencies of a rotary configuration as 64-bit fractions of a turn
+// per position; false when they are not finite.
+bool rotary_frequencies(const vq_rotary_config& c, unsigned long long (&freq)[64]) {
+  const double kTwoPi = 6.283185307179586;
+  const double r = c.rotary_dim;
+  double base = c.base;
+  if (c.scaling == VQ_ROTARY_BASE && c.rotary_dim > 2) base *= std::pow(c.factor, r / (r - 2.0));
+  double lo = 0, hi = 0;
+  if (c.scaling == VQ_ROTARY_PARTS) {
+    auto at = [&](double turns) { return r * std::log(c.original_len / (turns * kTwoPi)) / (2.0 * std::log(base)); };
+    lo = std::max(std::floor(at(c.high_turns)), 0.0);
+    hi = std::min(std::ceil(at(c.low_turns)), r - 1.0);
+  }
+  for (int i = 0; i < 64; ++i) freq[i] = 0;
+  for (int i = 0; i < c.rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / r);
+    if (c.scaling == VQ_ROTARY_LINEAR) {
+      f /= c.factor;
+    } else if (c.scaling == VQ_ROTARY_PARTS) {
+      const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+      f = f * (1.0 - ramp) + f / c.factor * ramp;
+    } else if (c.scaling == VQ_ROTARY_WAVELENGTH) {
+      const double w = std::min(std::max((c.original_len * f / kTwoPi - c.low_turns) / (c.high_turns - c.low_turns), 0.0), 1.0);
+      f = w * f + (1.0 - w) * f / c.factor;
+    }
+    double turns = f / kTwoPi;
+    if (!std::isfinite(turns)) return false;
+    turns -= std::floor(turns);
+    const double scaled = turns * 18446744073709551616.0;  // 2^64
+    freq[i] = scaled >= 18446744073709551615.0 ? 0ULL : static_cast<unsigned long long>(scaled);
+  }
+  return true;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+vq_status vq_append_slots(int32_t batch, const int32_t* seq_lens, const int32_t* new_lens,
+                          int32_t* page_table, int32_t max_pages_per_seq,
+                          const int32_t* free_pages, int32_t free_capacity,
+                          const int32_t* num_free, int32_t page_size, int64_t num_pages,
+                          int32_t max_tokens, int32_t* seq_lens_out, int32_t* num_free_out,
+                          int32_t* cu_new_lens, int64_t* slot_mapping, int32_t* positions,
+                          int32_t* status, void* stream) {
+  if (batch < 0) return fail(VQ_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (batch > vqk::kSlotsMaxBatch)
+    return fail(VQ_ERR_UNSUPPORTED, "batch %d > %d", batch, vqk::kSlotsMaxBatch);
+  if (page_size < 16 || page_size % 16)
+    return fail(VQ_ERR_INVALID_ARG, "page_size %d must be a positive multiple of 16", page_size);
+  if (num_pages < 1) return fail(VQ_ERR_INVALID_ARG, "num_pages %lld < 1", (long long)num_pages);
+  if (max_pages_per_seq < 1) return fail(VQ_ERR_INVALID_ARG, "max_pages_per_seq %d < 1", max_pages_per_seq);
+  if (free_capacity < 0) return fail(VQ_ERR_INVALID_ARG, "free_capacity %d < 0", free_capacity);
+  if (max_tokens < 0 || max_tokens > (1 << 30))
+    return fail(VQ_ERR_INVALID_ARG, "max_tokens %d not in 0..2^30", max_tokens);
+  // an empty batch, free list or row list may come with NULL pointers
+  const void* ptrs[] = {seq_lens, new_lens, page_table, seq_lens_out, free_pages, num_free,
+                        num_free_out, cu_new_lens, slot_mapping, positions};
+  const char* names[] = {"seq_lens", "new_lens", "page_table", "seq_lens_out", "free_pages", "num_free",
+                         "num_free_out", "cu_new_lens", "slot_mapping", "positions"};
+  for (int i = 0; i < 10; ++i) {
+    const bool may_be_null = i < 4 ? batch == 0 : i == 4 ? free_capacity == 0 : i >= 8 && max_tokens == 0;
+    if (!ptrs[i] && !may_be_null) return fail(VQ_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if (!aligned16(ptrs[i])) return fail(VQ_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  vqk::SlotsParams p{};
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.num_free = num_free;
+  p.page_table = page_table;
+  p.seq_lens_out = seq_lens_out;
+  p.num_free_out = num_free_out;
+  p.cu_new_lens = cu_new_lens;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.max_pages = max_pages_per_seq;
+  p.free_capacity = free_capacity;
+  p.page_size = page_size;
+  p.max_tokens = max_tokens;
+  cudaError_t e = vqk::launch_slots(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vq_append_slots launch");
+  return VQ_OK;
+}
+
+vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const int32_t* positions,
+                    int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
+                    void* q_out, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                    int32_t num_kv_heads, void* k_out, void* v_out, void* stream) {
+  if (!config) return fail(VQ_ERR_INVALID_ARG, "config is NULL");
+  const vq_rotary_config& c = *config;
+  if (c.head_dim != 128)
+    return fail(VQ_ERR_UNSUPPORTED, "head_dim %d: this build implements head_dim 128", c.head_dim);
+  if (c.rotary_dim < 2 || c.rotary_dim > c.head_dim || c.rotary_dim % 2)
+    return fail(VQ_ERR_INVALID_ARG, "rotary_dim %d must be even and in 2..%d", c.rotary_dim, c.head_dim);
+  if (c.scaling < VQ_ROTARY_NONE || c.scaling > VQ_ROTARY_WAVELENGTH)
+    return fail(VQ_ERR_INVALID_ARG, "scaling %d is not a vq_rotary_scaling", c.scaling);
+  if (!(c.base >= 1.0) || !std::isfinite(c.base)) return fail(VQ_ERR_INVALID_ARG, "base must be finite and >= 1");
+  if (!(c.attention_factor > 0.0) || !std::isfinite(c.attention_factor))
+    return fail(VQ_ERR_INVALID_ARG, "attention_factor must be finite and > 0");
+  if (c.scaling != VQ_ROTARY_NONE && (!(c.factor > 0.0) || !std::isfinite(c.factor)))
+    return fail(VQ_ERR_INVALID_ARG, "factor must be finite and > 0");
+  if (c.scaling == VQ_ROTARY_PARTS || c.scaling == VQ_ROTARY_WAVELENGTH) {
+    if (!(c.original_len > 0.0) || !std::isfinite(c.original_len) || !(c.low_turns > 0.0) ||
+        !(c.high_turns > c.low_turns) || !std::isfinite(c.high_turns))
+      return fail(VQ_ERR_INVALID_ARG, "original_len > 0 and 0 < low_turns < high_turns are needed");
+    if (c.scaling == VQ_ROTARY_PARTS && !(c.base > 1.0))
+      return fail(VQ_ERR_INVALID_ARG, "scaling by parts needs a base > 1");
+  }
+  if (dtype != VQ_FP16 && dtype != VQ_BF16) return fail(VQ_ERR_INVALID_ARG, "dtype %d is not a vq_dtype", dtype);
+  if (num_tokens < 0) return fail(VQ_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_tokens == 0) return VQ_OK;  // empty tensors may come with NULL pointers
+  if (!positions || !aligned16(positions))
+    return fail(VQ_ERR_INVALID_ARG, "positions is NULL or not 16-byte aligned");
+  const void* src[] = {q, k, v};
+  void* dst[] = {q_out, k_out, v_out};
+  const int64_t stride[] = {q_stride, k_stride, v_stride};
+  const int32_t heads[] = {num_q_heads, num_kv_heads, num_kv_heads};
+  const char* names[] = {"q", "k", "v"};
+  vqk::RotaryParams p{};
+  size_t in_bytes[3] = {}, out_bytes[3] = {};
+  bool any = false;
+  for (int i = 0; i < 3; ++i) {
+    if (!src[i] != !dst[i]) return fail(VQ_ERR_INVALID_ARG, "%s and %s_out go together", names[i], names[i]);
+    if (!src[i]) continue;
+    any = true;
+    if (!aligned16(src[i]) || !aligned16(dst[i]))
+      return fail(VQ_ERR_INVALID_ARG, "%s or %s_out is not 16-byte aligned", names[i], names[i]);
+    if (heads[i] < 1 || heads[i] > 4096) return fail(VQ_ERR_INVALID_ARG, "%d heads of %s: 1..4096", heads[i], names[i]);
+    const int64_t row = static_cast<int64_t>(heads[i]) * c.head_dim;
+    if (stride[i] < row || stride[i] % 8 || stride[i] > (1LL << 31))
+      return fail(VQ_ERR_INVALID_ARG, "%s_stride %lld must be a multiple of 8, at least %lld and at most 2^31", names[i],
+                  (long long)stride[i], (long long)row);
+    p.src[i] = src[i];
+    p.dst[i] = dst[i];
+    p.stride[i] = stride[i];
+    p.heads[i] = heads[i];
+    in_bytes[i] = 2 * (static_cast<size_t>(num_tokens - 1) * stride[i] + row);
+    out_bytes[i] = 2 * static_cast<size_t>(num_tokens) * row;
+  }
+  if (!any) return fail(VQ_ERR_INVALID_ARG, "q, k and v are all NULL");
+  for (int o = 0; o < 3; ++o) {
+    if (!dst[o]) continue;
+    for (int i = 0; i < 3; ++i) {
+      if (!src[i]) continue;
+      const bool in_place = i == o && dst[o] == src[i] && dtype == VQ_FP16 && in_bytes[i] == out_bytes[o];
+      if (!in_place && overlap(dst[o], out_bytes[o], src[i], in_bytes[i]))
+        return fail(VQ_ERR_INVALID_ARG, "%s_out overlaps %s", names[o], names[i]);
+      if (i > o && dst[i] && overlap(dst[o], out_bytes[o], dst[i], out_bytes[i]))
+        return fail(VQ_ERR_INVALID_ARG, "%s_out overlaps %s_out", names[o], names[i]);
+    }
+    if (overlap(dst[o], out_bytes[o], positions, 4 * static_cast<size_t>(num_tokens)))
+      return fail(VQ_ERR_INVALID_ARG, "%s_out overlaps positions", names[o]);
+  }
+  if (!rotary_frequencies(c, p.freq)) return fail(VQ_ERR_INVALID_ARG, "the frequencies are not finite");
+  p.positions = positions;
+  p.factor = static_cast<float>(c.attention_factor);
+  p.rotary_dim = c.rotary_dim;
+  p.interleaved = c.interleaved != 0;
+  p.num_tokens = num_tokens;
+  const int sms = device_sms();
+  if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
+  cudaError_t e = vqk::launch_rotary(p, dtype == VQ_BF16, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vq_rotary launch");
+  return VQ_OK;
+}
+
+}  // extern "C"

@@ -14,7 +14,8 @@ constexpr int kHeadDim = 128;
 constexpr int kChunk = 16;  // tokens per mma row block
 
 enum DeviceStatus : int32_t {
-  kDevOk = 0, kDevBadPage = 1, kDevBadSlot = 2, kDevTimeout = 3, kDevBadConfig = 4
+  kDevOk = 0, kDevBadPage = 1, kDevBadSlot = 2, kDevTimeout = 3, kDevBadConfig = 4,
+  kDevBadLength = 5, kDevNoPages = 6
 };
 
 __device__ __forceinline__ void report(int32_t* status, int32_t code) {

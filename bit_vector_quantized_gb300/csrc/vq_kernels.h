@@ -126,6 +126,35 @@ struct CombineParams {
   int group;                  // Hq / Hkv (row / group = pair)
 };
 
+// Rotary positions: tensor 0 queries, 1 keys, 2 values (carried along).
+struct RotaryParams {
+  const int32_t* positions;    // [T]; negative: the token is skipped
+  const void* src[3];          // [T] rows of `stride` elements, heads x 128 from the row's start
+  void* dst[3];                // fp16 [T][heads][128]
+  long long stride[3];
+  int heads[3];                // 0: absent
+  unsigned long long freq[64]; // turns per position of pair i, as a 64-bit fraction
+  float factor;                // multiplies sine and cosine
+  int rotary_dim, interleaved;
+  int num_tokens;
+  int heads_per_y;             // heads one blockIdx.y serves (set by the launcher)
+};
+
+struct SlotsParams {
+  const int32_t* seq_lens;     // [B] cached tokens (may be seq_lens_out)
+  const int32_t* new_lens;     // [B]
+  const int32_t* free_pages;   // [free_capacity], the stack's top at num_free - 1
+  const int32_t* num_free;     // [1] (may be num_free_out)
+  int32_t* page_table;         // [B][max_pages]
+  int32_t* seq_lens_out;       // [B]
+  int32_t* num_free_out;       // [1]
+  int32_t* cu_new_lens;        // [B + 1]
+  int64_t* slot_mapping;       // [max_tokens]
+  int32_t* positions;          // [max_tokens]
+  int32_t* status;
+  long long num_pages;
+  int batch, max_pages, free_capacity, page_size, max_tokens;
+};
 
 constexpr int kProducerWarps = 4;  // TMA-issuing warps (one in four stages each)
 constexpr int kMaxUnitsPerCta = 256;
@@ -284,5 +313,8 @@ cudaError_t launch_decode_balanced(const DecodeParams& p, int k_sub, int k_bits,
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool overlap);
 cudaError_t launch_dequant(const DequantParams& p, int grid_x, cudaStream_t stream);
 int dequant_tokens_per_cta();
+cudaError_t launch_rotary(RotaryParams p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream);
+constexpr int kSlotsMaxBatch = 16384;
 
 }  // namespace vqk

@@ -73,8 +73,10 @@ typedef enum vq_device_status {
   VQ_DEV_BAD_PAGE = 1,       /* page_table entry outside [0, num_pages): page skipped */
   VQ_DEV_BAD_SLOT = 2,       /* slot_mapping entry >= num_pages * page_size: token skipped */
   VQ_DEV_TIMEOUT = 3,        /* an asynchronous-copy wait exceeded its time limit */
-  VQ_DEV_BAD_CONFIG = 4      /* launch parameters the kernel cannot honour: it did nothing
+  VQ_DEV_BAD_CONFIG = 4,     /* launch parameters the kernel cannot honour: it did nothing
                                 (not reachable through this ABI's validated calls) */
+  VQ_DEV_BAD_LENGTH = 5,     /* a length, count or row offset outside its range (see the call) */
+  VQ_DEV_NO_PAGES = 6        /* vq_append_slots: the step needs more pages than are free */
 } vq_device_status;
 
 /*
@@ -403,6 +405,105 @@ vq_status vq_decode_attention_residual(const vq_layout* layout, int32_t batch, c
                                        float softmax_scale, int32_t num_splits, void* out,
                                        void* workspace, size_t workspace_bytes, int32_t* status,
                                        void* stream);
+
+/*
+ * Page tables, slot map, positions and row offsets of one serving step, from
+ * request lengths that live on the device: what vq_encode_kv (slot_mapping),
+ * vq_rotary (positions), vq_chunk_attention (cu_new_lens, seq_lens,
+ * page_table) and the decode calls read, made in one kernel without a copy to
+ * the host, so a whole step can be captured in a graph.
+ *   Sequence b has seq_lens[b] cached tokens and brings new_lens[b] more.
+ *   Pages it lacks, ceil((seq_lens + new_lens) / P) - ceil(seq_lens / P), come
+ *   off the top of the free stack, sequences in order, pages of a sequence in
+ *   order: the first page taken is free_pages[*num_free - 1].
+ *   seq_lens, new_lens  int32 [batch].
+ *   page_table    int32 [batch][max_pages_per_seq]; entries of the pages that
+ *                 are taken are written, all others are left as they are.
+ *   free_pages    int32 [free_capacity], only read; num_free int32 [1].  To
+ *                 give a finished sequence's pages back, write them at
+ *                 free_pages[*num_free ..] and raise *num_free.
+ *   seq_lens_out  int32 [batch] = seq_lens + new_lens; may be seq_lens.
+ *   num_free_out  int32 [1] = pages still free; may be num_free.
+ *   cu_new_lens   int32 [batch + 1]: exclusive sums of new_lens; the step's
+ *                 rows of sequence b are cu_new_lens[b] .. cu_new_lens[b+1]-1.
+ *   slot_mapping  int64 [max_tokens], positions int32 [max_tokens]: the slot
+ *                 and the position of every row; rows from
+ *                 cu_new_lens[batch] on get -1 (skipped by vq_encode_kv and
+ *                 vq_rotary).
+ * All or nothing: a negative length, a sequence past max_pages_per_seq pages,
+ * more than max_tokens new tokens or num_free outside [0, free_capacity]
+ * (VQ_DEV_BAD_LENGTH), too few free pages (VQ_DEV_NO_PAGES) or a page outside
+ * [0, num_pages) among those the step uses (VQ_DEV_BAD_PAGE) report that
+ * status, take no page, copy seq_lens and num_free through and leave every
+ * row at -1 and every offset at 0.
+ *   batch 0 .. 16384, max_tokens 0 .. 2^30, page_size as in vq_layout.
+ * Outputs other than the two pairs named above must not overlap inputs.
+ */
+vq_status vq_append_slots(int32_t batch, const int32_t* seq_lens, const int32_t* new_lens,
+                          int32_t* page_table, int32_t max_pages_per_seq,
+                          const int32_t* free_pages, int32_t free_capacity,
+                          const int32_t* num_free, int32_t page_size, int64_t num_pages,
+                          int32_t max_tokens, int32_t* seq_lens_out, int32_t* num_free_out,
+                          int32_t* cu_new_lens, int64_t* slot_mapping, int32_t* positions,
+                          int32_t* status, void* stream);
+
+/* How vq_rotary scales its frequencies for contexts longer than the ones they
+ * were made for (factor s, original length L, base c, r = rotary_dim,
+ * f_i = c^(-2i / r) for pair i of r / 2). */
+typedef enum vq_rotary_scaling {
+  VQ_ROTARY_NONE = 0,
+  VQ_ROTARY_LINEAR = 1,      /* f_i / s: positions interpolated */
+  VQ_ROTARY_BASE = 2,        /* base c s^(r / (r - 2)) (r > 2) */
+  VQ_ROTARY_PARTS = 3,       /* pairs with more than high_turns turns in L keep f_i, with less than
+                                low_turns get f_i / s, linear in i between the (rounded-out) bounds
+                                i(t) = r ln(L / (2 pi t)) / (2 ln c) */
+  VQ_ROTARY_WAVELENGTH = 4   /* weight w = clamp((L f_i / 2 pi - low_turns) / (high_turns - low_turns), 0, 1):
+                                w f_i + (1 - w) f_i / s */
+} vq_rotary_scaling;
+
+/* Element type of vq_rotary's inputs. */
+typedef enum vq_dtype { VQ_FP16 = 0, VQ_BF16 = 1 } vq_dtype;
+
+/* Rotary positions (host struct, read during the call only). */
+typedef struct vq_rotary_config {
+  int32_t head_dim;          /* D (this build: 128) */
+  int32_t rotary_dim;        /* r: even, 2 .. D; elements r .. D-1 of a head pass through */
+  int32_t interleaved;       /* 1: pairs (2i, 2i+1); 0: pairs (i, i + r/2) */
+  int32_t scaling;           /* vq_rotary_scaling */
+  double base;               /* c >= 1 */
+  double factor;             /* s > 0 (unused for VQ_ROTARY_NONE) */
+  double original_len;       /* L > 0 (PARTS, WAVELENGTH) */
+  double low_turns;          /* 0 < low_turns < high_turns (PARTS, WAVELENGTH) */
+  double high_turns;
+  double attention_factor;   /* m > 0: multiplies the turned elements of q and of k */
+} vq_rotary_config;
+
+/*
+ * Turn queries and keys by their positions, ahead of vq_encode_kv and the
+ * attention calls (which take q and k as they attend: the smoothing and
+ * Hadamard transform of VecInfer act on the turned keys).  For token t and
+ * pair i of every q and k head, x = positions[t] f_i:
+ *     (a, b) -> m (a cos x - b sin x,  b cos x + a sin x)
+ * in fp32, rounded once to fp16.  Angles are reduced exactly: any position in
+ * [0, 2^31) keeps fp32 accuracy.
+ *   positions     int32 [num_tokens]; a negative position skips the token (its
+ *                 output rows are left as they were).
+ *   dtype         element type of q, k and v (vq_dtype).
+ *   q, k, v       token t's heads x D elements start at element
+ *                 t * q_stride (k_stride, v_stride): strides in elements,
+ *                 multiples of 8 and at least heads x D, so the three can be
+ *                 slices of one fused projection.  Any of them may be NULL
+ *                 (with its output), not all.  v is copied (and converted).
+ *   q_out         fp16 [num_tokens][num_q_heads][D]; k_out and v_out fp16
+ *                 [num_tokens][num_kv_heads][D].  An output may be its own
+ *                 input (dtype VQ_FP16, stride heads x D); otherwise outputs
+ *                 must not overlap inputs (VQ_ERR_INVALID_ARG).
+ * num_tokens == 0 is a no-op returning VQ_OK.
+ */
+vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const int32_t* positions,
+                    int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
+                    void* q_out, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                    int32_t num_kv_heads, void* k_out, void* v_out, void* stream);
 
 /*
  * Decode attention for callers that cannot allocate device memory.
