@@ -39,8 +39,8 @@ EXPORTED = ("vq_code_row_bytes", "vq_check_layout", "vq_encode_kv", "vq_decode_w
             "vq_decode_partial",
             "vq_decode_partial_method", "vq_decode_combine", "vq_decode_step", "vq_dequantize_kv",
             "vq_decode_residual_workspace_bytes", "vq_decode_attention_residual",
-            "vq_decode_attention_static", "vq_static_scratch_bytes", "vq_append_slots",
-            "vq_rotary", "vq_last_error", "vq_version")
+            "vq_decode_attention_static", "vq_static_scratch_bytes", "vq_chunk_attention",
+            "vq_chunk_workspace_bytes", "vq_append_slots", "vq_rotary", "vq_last_error", "vq_version")
 
 
 class VQError(RuntimeError):
@@ -121,6 +121,9 @@ def lib() -> ctypes.CDLL:
             "vq_decode_attention_static": (I32, [LP, I32, P, P, P, P, P, P, I64, P, I32, P, I32,
                                                  ctypes.c_float, I32, P, P, P]),
             "vq_static_scratch_bytes": (SZ, []),
+            "vq_chunk_attention": (I32, [LP, I32, I32, P, P, P, P, P, P, I64, P, I32, P, I32, P, I32,
+                                         I32, I32, ctypes.c_float, P, P, SZ, P, P]),
+            "vq_chunk_workspace_bytes": (SZ, [LP, I32, I32, I32, I32, I32]),
             "vq_append_slots": (I32, [I32, P, P, P, I32, P, I32, P, I32, I64, I32, P, P, P, P, P,
                                       P, P]),
             "vq_rotary": (I32, [ctypes.POINTER(vq_rotary_config), I32, P, I32, P, I64, I32, P, P,
@@ -274,6 +277,24 @@ def vq_decode_attention_static(layout, batch, q, lambda_, codebook_k, codebook_v
 
 def vq_static_scratch_bytes() -> int:
     return int(lib().vq_static_scratch_bytes())
+
+
+def vq_chunk_attention(layout, batch, num_tokens, q, lambda_, codebook_k, codebook_v, k_pool,
+                       v_pool, num_pages, page_table, max_pages_per_seq, seq_lens, max_seq_len,
+                       cu_new_lens, max_new_len, window, num_sinks, softmax_scale, out, workspace,
+                       workspace_bytes, status=None, stream=None) -> None:
+    _check(lib().vq_chunk_attention(
+        ctypes.byref(layout), batch, num_tokens, _ptr(q), _ptr(lambda_), _ptr(codebook_k),
+        _ptr(codebook_v), _ptr(k_pool), _ptr(v_pool), num_pages, _ptr(page_table),
+        max_pages_per_seq, _ptr(seq_lens), max_seq_len, _ptr(cu_new_lens), max_new_len, window,
+        num_sinks, float(softmax_scale), _ptr(out), _ptr(workspace), workspace_bytes,
+        _ptr(status), _ptr(stream)))
+
+
+def vq_chunk_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len,
+                             num_sms=0) -> int:
+    return int(lib().vq_chunk_workspace_bytes(ctypes.byref(layout), batch, num_tokens,
+                                              max_seq_len, max_new_len, num_sms))
 
 
 def vq_append_slots(batch, seq_lens, new_lens, page_table, max_pages_per_seq, free_pages,
@@ -571,6 +592,58 @@ def _arg(t, dtype, name, device, shape=None):
     if t is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     return _dev_ptr(t, dtype, name, shape)
+
+
+def alloc_chunk_workspace(layout: vq_layout, batch: int, num_tokens: int, max_seq_len: int,
+                          max_new_len: int, device="cuda"):
+    torch = _torch()
+    device = torch.device(device)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            n = vq_chunk_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len)
+    else:
+        n = vq_chunk_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len)
+    if n == 0:
+        raise VQError(VQ_ERR_INVALID_ARG, "cannot size the workspace")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def chunk_attention(layout: vq_layout, q, lambda_, codebook_k, codebook_v, k_pool, v_pool,
+                    page_table, seq_lens, max_seq_len: int, cu_new_lens=None,
+                    max_new_len: int = 1, window: int = 0, num_sinks: int = 0, out=None,
+                    workspace=None, softmax_scale: float = 0.0, status=None, stream=None):
+    """fp16 [T][Hq][D] attention of the newest tokens' queries q [T][Hq][D] over the quantized
+    pools, causal; row offsets cu_new_lens int32 [B + 1] (None: one row per sequence).  With
+    `window` a row sees that many last tokens and the first `num_sinks` (see vq_chunk_attention)."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    f16, i32, u8 = torch.float16, torch.int32, torch.uint8
+    T, D, H, dev, P = q.shape[0], layout.head_dim, layout.num_kv_heads, q.device, layout.page_size
+    B = seq_lens.shape[0]
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B][max_pages]")
+    kr, vr = row_bytes(layout)
+    pages = k_pool.shape[0]
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, layout.num_q_heads, D), dtype=f16, device=dev)
+        if workspace is None:
+            workspace = alloc_chunk_workspace(layout, B, T, max_seq_len, max_new_len, dev)
+        vq_chunk_attention(
+            layout, B, T, _arg(q, f16, "q", dev, (T, layout.num_q_heads, D)),
+            _arg(lambda_, torch.float32, "lambda", dev, (H, D)),
+            _arg(codebook_k, f16, "codebook_k", dev, (1 << layout.k_bits, layout.k_sub)),
+            _arg(codebook_v, f16, "codebook_v", dev, (1 << layout.v_bits, layout.v_sub)),
+            _arg(k_pool, u8, "k_pool", dev, (pages, H, P, kr)),
+            _arg(v_pool, u8, "v_pool", dev, (pages, H, P, vr)), pages,
+            _arg(page_table, i32, "page_table", dev, (B, page_table.shape[1])),
+            page_table.shape[1], _arg(seq_lens, i32, "seq_lens", dev, (B,)), max_seq_len,
+            _arg(cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)), max_new_len, window, num_sinks,
+            softmax_scale, _arg(out, f16, "out", dev, (T, layout.num_q_heads, D)),
+            _arg(workspace, u8, "workspace", dev), workspace.numel(),
+            _arg(status, i32, "status", dev, (1,)), st)
+    return out
 
 
 class AppendedSlots(NamedTuple):

@@ -1087,3 +1087,129 @@ vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const in
 }
 
 }  // extern "C"
+
+// ---- attention of several new tokens per sequence --------------------------------
+namespace {
+
+// Tile height of a call: all rows of a (sequence, KV head) where 8 hold them.
+int chunk_tile_rows(const vq_layout& L, int max_new_len) {
+  const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
+  return rows <= 8 ? 8 : 16;
+}
+
+struct ChunkWs {
+  size_t o_off, ml_off, rec_off, total;
+};
+
+// Two partials and a record per CTA.
+ChunkWs chunk_ws(const vq_layout& L, int max_new_len, int grid) {
+  ChunkWs w;
+  const size_t rows = 2 * static_cast<size_t>(grid) * chunk_tile_rows(L, max_new_len);
+  w.o_off = 0;
+  w.ml_off = rows * 128 * sizeof(float);
+  w.rec_off = (w.ml_off + rows * sizeof(float2) + 255) & ~size_t(255);
+  w.total = (w.rec_off + grid * sizeof(vqk::ChunkRecord) + 255) & ~size_t(255);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                                int32_t max_seq_len, int32_t max_new_len, int32_t num_sms) {
+  if (check_layout_impl(layout, 1) != VQ_OK || batch < 0 || num_tokens < 0 || max_seq_len < 0 || max_new_len < 0)
+    return 0;
+  const int sms = num_sms > 0 ? num_sms : device_sms();
+  if (sms <= 0) return 0;
+  return chunk_ws(*layout, max_new_len, sms).total;
+}
+
+vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                             const void* q, const float* lambda, const void* codebook_k,
+                             const void* codebook_v, const void* k_pool, const void* v_pool,
+                             int64_t num_pages, const int32_t* page_table,
+                             int32_t max_pages_per_seq, const int32_t* seq_lens,
+                             int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
+                             int32_t window, int32_t num_sinks, float softmax_scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream) {
+  vq_status st = check_layout_impl(layout, 1);
+  if (st != VQ_OK) return st;
+  const vq_layout& L = *layout;
+  if (batch < 0) return fail(VQ_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (batch > vqk::kChunkMaxBatch) return fail(VQ_ERR_UNSUPPORTED, "batch %d > %d", batch, vqk::kChunkMaxBatch);
+  if (num_tokens < 0) return fail(VQ_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (max_new_len < 0) return fail(VQ_ERR_INVALID_ARG, "max_new_len %d < 0", max_new_len);
+  if (window < 0 || num_sinks < 0) return fail(VQ_ERR_INVALID_ARG, "window %d or num_sinks %d < 0", window, num_sinks);
+  if (num_sinks > 0 && window == 0) return fail(VQ_ERR_INVALID_ARG, "num_sinks %d without a window", num_sinks);
+  if (!std::isfinite(softmax_scale)) return fail(VQ_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (batch == 0 || num_tokens == 0 || max_new_len == 0) return VQ_OK;
+  if (!cu_new_lens && num_tokens < batch)
+    return fail(VQ_ERR_INVALID_ARG, "num_tokens %d < batch %d without cu_new_lens", num_tokens, batch);
+  const void* ptrs[] = {q, lambda, codebook_k, codebook_v, k_pool, v_pool, page_table, seq_lens, out, workspace, cu_new_lens};
+  const char* names[] = {"q", "lambda", "codebook_k", "codebook_v", "k_pool", "v_pool", "page_table",
+                         "seq_lens", "out", "workspace", "cu_new_lens"};
+  for (int i = 0; i < 11; ++i) {
+    if (!ptrs[i] && i < 10) return fail(VQ_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if (!aligned16(ptrs[i])) return fail(VQ_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  if (num_pages < 1) return fail(VQ_ERR_INVALID_ARG, "num_pages %lld < 1", (long long)num_pages);
+  if (max_pages_per_seq < 1) return fail(VQ_ERR_INVALID_ARG, "max_pages_per_seq %d < 1", max_pages_per_seq);
+  if (max_seq_len < 0 || max_seq_len > (1 << 30))
+    return fail(VQ_ERR_INVALID_ARG, "max_seq_len %d not in 0..2^30", max_seq_len);
+  if (static_cast<long long>(max_seq_len) > static_cast<long long>(max_pages_per_seq) * L.page_size)
+    return fail(VQ_ERR_INVALID_ARG, "max_seq_len %d exceeds max_pages_per_seq * page_size", max_seq_len);
+  const size_t row_bytes = 2 * static_cast<size_t>(L.num_q_heads) * L.head_dim;
+  if (overlap(q, num_tokens * row_bytes, out, num_tokens * row_bytes))
+    return fail(VQ_ERR_INVALID_ARG, "out overlaps q");
+  const int sms = device_sms();
+  if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
+  const int grid = sms;
+  const ChunkWs ws = chunk_ws(L, max_new_len, grid);
+  if (workspace_bytes < ws.total)
+    return fail(VQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, ws.total);
+
+  vqk::ChunkParams p{};
+  p.q = q;
+  p.out = out;
+  p.lambda = lambda;
+  p.cb_k = codebook_k;
+  p.cb_v = codebook_v;
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.cu = cu_new_lens;
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(wsb + ws.o_off);
+  p.ws_ml = reinterpret_cast<float2*>(wsb + ws.ml_off);
+  p.records = reinterpret_cast<vqk::ChunkRecord*>(wsb + ws.rec_off);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.num_tokens = num_tokens;
+  p.hq = L.num_q_heads;
+  p.hkv = L.num_kv_heads;
+  p.group = L.num_q_heads / L.num_kv_heads;
+  p.page_size = L.page_size;
+  p.max_pages = max_pages_per_seq;
+  p.max_seq_len = max_seq_len;
+  p.max_new_len = max_new_len;
+  p.window = std::min(window, 1 << 30);  // no position is further back: the same as none
+  p.sinks = std::min(num_sinks, 1 << 30);
+  p.tile_rows = chunk_tile_rows(L, max_new_len);
+  p.tile_tok = p.tile_rows / p.group;
+  p.gap = 256;
+  p.min_range = 512;
+  const float scale = softmax_scale == 0.f ? 1.f / std::sqrt(static_cast<float>(L.head_dim)) : softmax_scale;
+  p.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 / std::sqrt(128.0));
+  cudaError_t e = vqk::launch_chunk_narrow(p, L.k_sub, L.k_bits, L.v_sub, L.v_bits, grid,
+                                           static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention launch");
+  e = vqk::launch_chunk_merge(p, grid, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention merge");
+  return VQ_OK;
+}
+
+}  // extern "C"

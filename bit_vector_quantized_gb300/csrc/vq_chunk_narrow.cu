@@ -1,0 +1,451 @@
+// vq_chunk_narrow.cu -- chunk attention for few query rows per (sequence, KV head) (sm_103a),
+// and the merge of the chunk kernels' partials.
+//
+// What is computed, per query row (VecInfer, section 方法细节 "注意力机制中的向量量化KV缓存", for
+// several new tokens at once):
+//   q~ = q diag(lambda) H_D,  s_p = q~ . VQ^-1(K~_p) * scale over the visible p,
+//   o = softmax(s) VQ^-1(V).
+//
+// A tile is 8 or 16 query rows.  Each warp takes every kWarps-th 16-token block
+// of the tile's keys and keeps its own online softmax (running maximum, sum
+// and 128-wide output); the warps join at the end of the piece.  Both
+// products are m16n8k16 warp mma with the query rows as rows and centroids
+// gathered from shared memory straight into the other operand:
+//   scores: the operand column of lane (g, c) = (lane / 4, lane % 4) is token
+//     g, its k-step j the dims 32c + 4j .. 32c + 4j + 3, one 8-byte gather;
+//   values: column g of output block nb is dim 16g + nb; the lane gathers the
+//     centroids of its four tokens (2c, 2c + 1, 2c + 8, 2c + 9) and pairs
+//     their elements, so a gather serves four blocks.
+// With 8 rows, rows 0..7 hold the high and rows 8..15 the low fp16 part of q~
+// and of p, and the two halves of each accumulator are added: both products
+// keep about fp32 accuracy at no extra mma.  With 16 rows q~ takes two mma
+// (high, low) and p is rounded to fp16 once (p <= 2^8: relative 2^-11, which
+// averages out over a row's tokens).  Sums and maxima are fp32.
+#include "vq_chunk_common.cuh"
+#include "vq_gather.cuh"
+
+namespace vqk {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kSlack = 8.f;    // the running maximum may lag by this much (log2 units): p <= 2^8
+constexpr int kNarrowWarps = 8;
+constexpr int kBlock = 16;       // tokens per block
+constexpr int kQStride = 132;    // halves between q~ rows in shared memory
+
+template <int DK, int BK, int DV, int BV>
+struct NarrowTable {
+  static constexpr bool kWide = DK == 8;
+  static constexpr int kRows = 1 << (BK > BV ? BK : BV);
+  static constexpr int kBytes = kWide ? 131072 : kRows * kTabRow;
+};
+
+// Codebooks into the gather table: 256-byte rows, K centroid j 16 (or 32)
+// times in bytes 0..127 and V centroid j in bytes 128..255; the 1.5-bit format
+// as two plain 64 KB tables.
+template <int DK, int BK, int DV, int BV>
+__device__ __forceinline__ void fill_table(const ChunkParams& p) {
+  using T = NarrowTable<DK, BK, DV, BV>;
+  uint4* tab = reinterpret_cast<uint4*>(g_smem);
+  const int tid = threadIdx.x, n = blockDim.x;
+  if constexpr (T::kWide) {
+    for (int i = tid; i < 4096; i += n) {
+      tab[i] = __ldg(static_cast<const uint4*>(p.cb_k) + i);
+      tab[4096 + i] = __ldg(static_cast<const uint4*>(p.cb_v) + i);
+    }
+  } else {
+    for (int i = tid; i < T::kRows * 16; i += n) {
+      const int row = i >> 4;
+      const bool v = (i & 8) != 0;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row < (v ? 1 << BV : 1 << BK)) {
+        if ((v ? DV : DK) == 4) {
+          const uint2 c = __ldg(static_cast<const uint2*>(v ? p.cb_v : p.cb_k) + row);
+          x = make_uint4(c.x, c.y, c.x, c.y);
+        } else {
+          const uint32_t c = __ldg(static_cast<const uint32_t*>(v ? p.cb_v : p.cb_k) + row);
+          x = make_uint4(c, c, c, c);
+        }
+      }
+      tab[i] = x;
+    }
+  }
+}
+
+// Elements e of two fp16 pairs as one operand register: (a.e, b.e).
+__device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+
+// kRows: 8 (high and low parts share an mma) or 16.
+template <int DK, int BK, int DV, int BV, int kRows>
+__global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(const ChunkParams p) {
+  using T = NarrowTable<DK, BK, DV, BV>;
+  constexpr bool kPacked = kRows == 8;
+  constexpr bool kWide = T::kWide;
+  constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
+  uint8_t* const sm = g_smem + T::kBytes;
+  long long* const pre = reinterpret_cast<long long*>(sm);                 // [kChunkMaxBatch + 1]
+  long long* const scratch = pre + kChunkMaxBatch + 1;                     // [32]
+  __half* const qs = reinterpret_cast<__half*>(scratch + 33);              // [2][kRows][kQStride] high, low
+  float* const mo = reinterpret_cast<float*>(qs + 2 * kRows * kQStride);   // [warps][kRows][128]
+  float2* const ml = reinterpret_cast<float2*>(mo + kNarrowWarps * kRows * kHeadDim);  // [warps][kRows]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  pdl_trigger();
+  fill_table<DK, BK, DV, BV>(p);
+  chunk_plan(p, pre, scratch);
+  ChunkWalk<kBlock> walk(p, pre);
+  const uint32_t lwk = kWide ? 0u : DK == 4 ? (lane & 15) * 8 : lane * 4;
+  const uint32_t lwv = kWide ? 65536u : 128u + (DV == 4 ? (lane & 15) * 8 : lane * 4);
+  const int G = p.group;
+  bool recorded = false;
+
+  ChunkPiece u;
+  while (walk.next(u)) {
+    const int i0 = u.tile * p.tile_tok;
+    const int rows = min(p.tile_tok, u.s.n - i0) * G;
+    // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
+    for (int r = warp; r < kRows; r += kNarrowWarps) {
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < rows) {
+        const long long row = static_cast<long long>(u.s.row0 + i0 + r / G) * p.hq + u.kvh * G + r % G;
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __half*>(p.q) + row * kHeadDim) + lane);
+        const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + u.kvh * kHeadDim) + lane);
+        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        x[0] = lo.x * lam.x;
+        x[1] = lo.y * lam.y;
+        x[2] = hi.x * lam.z;
+        x[3] = hi.y * lam.w;
+        fwht128_warp(x, lane);
+      }
+      uint2 vh, vl;
+      split_half2(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
+      split_half2(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
+      *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
+      *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
+    }
+    __syncthreads();
+    uint32_t qa[8][4], ql[kPacked ? 1 : 8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = 32 * c + 4 * j;
+      const uint2 h0 = *reinterpret_cast<const uint2*>(qs + g * kQStride + e);
+      const uint2 h1 = *reinterpret_cast<const uint2*>(qs + (g + 8) * kQStride + e);  // kPacked: the low part of row g
+      qa[j][0] = h0.x;
+      qa[j][1] = h1.x;
+      qa[j][2] = h0.y;
+      qa[j][3] = h1.y;
+      if constexpr (!kPacked) {
+        const uint2 l0 = *reinterpret_cast<const uint2*>(qs + (kRows + g) * kQStride + e);
+        const uint2 l1 = *reinterpret_cast<const uint2*>(qs + (kRows + g + 8) * kQStride + e);
+        ql[j][0] = l0.x;
+        ql[j][1] = l1.x;
+        ql[j][2] = l0.y;
+        ql[j][3] = l1.y;
+      }
+    }
+    // positions of the lane's rows g and g + 8 (rows past the tile see nothing)
+    constexpr int NR = kPacked ? 1 : 2;
+    int pos[NR];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int r = g + 8 * i;
+      pos[i] = r < rows ? u.s.base + i0 + r / G : -1;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    const int first_pos = u.s.base + i0, last_pos = u.s.base + min(i0 + p.tile_tok, u.s.n) - 1;
+    float o[16][4];
+#pragma unroll
+    for (int nb = 0; nb < 16; ++nb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nb][e] = 0.f;
+
+    KCodes<DK> kc[2];
+    VCodes<DV, BV> vc[4];
+    auto load = [&](int i, KCodes<DK>(&kx)[2], VCodes<DV, BV>(&vx)[4]) {  // false: no such page
+      const int t0 = u.k.block(i) * kBlock;
+      const int lp = t0 / p.page_size;
+      const int pg = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + lp);
+      if (pg < 0 || pg >= p.num_pages) {
+        if (lane == 0) report(p.status, kDevBadPage);
+        return false;
+      }
+      const long long row = (static_cast<long long>(pg) * p.hkv + u.kvh) * p.page_size + (t0 - lp * p.page_size);
+      const uint8_t* kr = p.k_pool + row * KROW;
+      const uint8_t* vr = p.v_pool + row * VROW;
+      kx[0].load(kr + g * KROW, c);
+      kx[1].load(kr + (g + 8) * KROW, c);
+      vx[0].load(vr + (2 * c) * VROW, g);
+      vx[1].load(vr + (2 * c + 1) * VROW, g);
+      vx[2].load(vr + (2 * c + 8) * VROW, g);
+      vx[3].load(vr + (2 * c + 9) * VROW, g);
+      return true;
+    };
+    bool have = false;
+    if (u.blk0 + warp < u.blk1) have = load(u.blk0 + warp, kc, vc);
+    for (int i = u.blk0 + warp; i < u.blk1; i += kNarrowWarps) {
+      KCodes<DK> kn[2];
+      VCodes<DV, BV> vn[4];
+      bool have_n = false;
+      if (i + kNarrowWarps < u.blk1) have_n = load(i + kNarrowWarps, kn, vn);
+      const int t0 = u.k.block(i) * kBlock;
+      if (have) {
+        // ---- scores: s[nb][..]: row g (and g + 8), tokens 8 nb + 2c, 2c + 1 ----------
+        float s[2][4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            uint32_t b[4];  // two k-steps
+            if constexpr (kWide) {
+              const uint4 w = tab128(kc[nb].off16(j >> 1, lwk));
+              b[0] = w.x, b[1] = w.y, b[2] = w.z, b[3] = w.w;
+            } else if constexpr (DK == 4) {
+              const uint2 w0 = tab64(kc[nb].off(j, lwk)), w1 = tab64(kc[nb].off(j + 1, lwk));
+              b[0] = w0.x, b[1] = w0.y, b[2] = w1.x, b[3] = w1.y;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] = tab32(kc[nb].off(2 * j + e, lwk));
+            }
+            mma16816(s[nb], qa[j][0], qa[j][1], qa[j][2], qa[j][3], b[0], b[1]);
+            mma16816(s[nb], qa[j + 1][0], qa[j + 1][1], qa[j + 1][2], qa[j + 1][3], b[2], b[3]);
+            if constexpr (!kPacked) {
+              mma16816(s[nb], ql[j][0], ql[j][1], ql[j][2], ql[j][3], b[0], b[1]);
+              mma16816(s[nb], ql[j + 1][0], ql[j + 1][1], ql[j + 1][2], ql[j + 1][3], b[2], b[3]);
+            }
+          }
+          if constexpr (kPacked) {
+            s[nb][0] += s[nb][2];
+            s[nb][1] += s[nb][3];
+          }
+        }
+        // ---- masks --------------------------------------------------------------------
+        const bool whole = t0 + kBlock - 1 <= first_pos && t0 + kBlock <= u.s.limit &&
+                           (p.window == 0 || t0 > last_pos - p.window || t0 + kBlock <= p.sinks);
+        if (!whole) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int t = t0 + 8 * nb + 2 * c + e;
+                const bool see = t <= pos[r] && t < u.s.limit &&
+                                 (p.window == 0 || t > pos[r] - p.window || t < p.sinks);
+                if (!see) s[nb][2 * r + e] = -INFINITY;
+              }
+        }
+        // ---- online softmax ------------------------------------------------------------
+        float pr[NR][4];  // the row's tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
+          const bool raise = mx > m[r] + kSlack || (m[r] == -INFINITY && mx > -INFINITY);
+          if (__any_sync(kAll, raise)) {
+            const float mn = raise ? mx : m[r];
+            const float a = raise ? fast_exp2(m[r] - mn) : 1.f;  // 0 while nothing is accumulated
+            m[r] = mn;
+            l[r] *= a;
+#pragma unroll
+            for (int nb = 0; nb < 16; ++nb) {
+              o[nb][2 * r] *= a;
+              o[nb][2 * r + 1] *= a;
+              if constexpr (kPacked) {
+                o[nb][2] *= a;
+                o[nb][3] *= a;
+              }
+            }
+          }
+          const float mu = m[r] == -INFINITY ? 0.f : m[r];
+          pr[r][0] = fast_exp2(s[0][2 * r] - mu);
+          pr[r][1] = fast_exp2(s[0][2 * r + 1] - mu);
+          pr[r][2] = fast_exp2(s[1][2 * r] - mu);
+          pr[r][3] = fast_exp2(s[1][2 * r + 1] - mu);
+          l[r] += (pr[r][0] + pr[r][1]) + (pr[r][2] + pr[r][3]);
+        }
+        uint32_t a0, a1, a2, a3;
+        if constexpr (kPacked) {
+          split_half2(pr[0][0], pr[0][1], a0, a1);
+          split_half2(pr[0][2], pr[0][3], a2, a3);
+        } else {
+          a0 = pack_half2(__float2half_rn(pr[0][0]), __float2half_rn(pr[0][1]));
+          a1 = pack_half2(__float2half_rn(pr[NR - 1][0]), __float2half_rn(pr[NR - 1][1]));
+          a2 = pack_half2(__float2half_rn(pr[0][2]), __float2half_rn(pr[0][3]));
+          a3 = pack_half2(__float2half_rn(pr[NR - 1][2]), __float2half_rn(pr[NR - 1][3]));
+        }
+        // ---- o += p V -------------------------------------------------------------------
+        auto pv = [&](int nb, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+          mma16816(o[nb], a0, a1, a2, a3, pair_lo(w0, w1), pair_lo(w2, w3));
+          mma16816(o[nb + 1], a0, a1, a2, a3, pair_hi(w0, w1), pair_hi(w2, w3));
+        };
+        if constexpr (kWide) {
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2) {
+            uint4 w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = tab128(vc[t].off16(i2, lwv));
+            pv(8 * i2, w[0].x, w[1].x, w[2].x, w[3].x);
+            pv(8 * i2 + 2, w[0].y, w[1].y, w[2].y, w[3].y);
+            pv(8 * i2 + 4, w[0].z, w[1].z, w[2].z, w[3].z);
+            pv(8 * i2 + 6, w[0].w, w[1].w, w[2].w, w[3].w);
+          }
+        } else if constexpr (DV == 4) {
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) {
+            uint2 w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = tab64(vc[t].off(i2, lwv));
+            pv(4 * i2, w[0].x, w[1].x, w[2].x, w[3].x);
+            pv(4 * i2 + 2, w[0].y, w[1].y, w[2].y, w[3].y);
+          }
+        } else {
+#pragma unroll
+          for (int i2 = 0; i2 < 8; ++i2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = tab32(vc[t].off(i2, lwv));
+            pv(2 * i2, w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      kc[0] = kn[0], kc[1] = kn[1];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) vc[t] = vn[t];
+      have = have_n;
+    }
+    // ---- the warps' partials join ------------------------------------------------------
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      l[r] += __shfl_xor_sync(kAll, l[r], 1);
+      l[r] += __shfl_xor_sync(kAll, l[r], 2);
+      if (c == 0) ml[warp * kRows + g + 8 * r] = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int nb = 0; nb < 16; ++nb) {
+        float* dst = mo + (warp * kRows + g + 8 * r) * kHeadDim;
+        dst[32 * c + nb] = kPacked ? o[nb][0] + o[nb][2] : o[nb][2 * r];
+        dst[32 * c + 16 + nb] = kPacked ? o[nb][1] + o[nb][3] : o[nb][2 * r + 1];
+      }
+    }
+    __syncthreads();
+    for (int r = warp; r < kRows; r += kNarrowWarps) {
+      if (r >= rows && u.slot < 0) continue;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kNarrowWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float Mu = M == -INFINITY ? 0.f : M;  // a row that sees nothing: sums of 0 (or of its NaN)
+#pragma unroll
+      for (int w = 0; w < kNarrowWarps; ++w) {
+        const float2 v = ml[w * kRows + r];
+        const float f = fast_exp2(v.x - Mu);
+        L = fmaf(f, v.y, L);
+        const float4 x = *reinterpret_cast<const float4*>(mo + (w * kRows + r) * kHeadDim + 4 * lane);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+      }
+      if (u.slot >= 0) {
+        const long long at = static_cast<long long>(u.slot) * kRows + r;
+        reinterpret_cast<float4*>(p.ws_o + at * kHeadDim)[lane] = acc;
+        if (lane == 0) p.ws_ml[at] = make_float2(M, L);
+      } else {
+        const float f = L == 0.f ? 0.f : 1.f / L;
+        const long long row = static_cast<long long>(u.s.row0 + i0 + r / G) * p.hq + u.kvh * G + r % G;
+        const __half2 h0 = __floats2half2_rn(acc.x * f, acc.y * f), h1 = __floats2half2_rn(acc.z * f, acc.w * f);
+        uint2 w;
+        w.x = *reinterpret_cast<const uint32_t*>(&h0);
+        w.y = *reinterpret_cast<const uint32_t*>(&h1);
+        reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row * kHeadDim)[lane] = w;
+      }
+    }
+    if (u.slot >= 0 && (u.slot & 1) && tid == 0) {
+      write_record(p, &u);
+      recorded = true;
+    }
+    __syncthreads();  // q~ and the join buffers are free again
+  }
+  if (tid == 0 && !recorded) write_record(p, nullptr);
+}
+
+template <int DK, int BK, int DV, int BV, int kRows>
+cudaError_t launch_narrow(const ChunkParams& p, int grid, cudaStream_t stream) {
+  static SmemOptIn opt;
+  constexpr size_t smem = NarrowTable<DK, BK, DV, BV>::kBytes + (kChunkMaxBatch + 34) * sizeof(long long) +
+                          2 * kRows * kQStride * sizeof(__half) + kNarrowWarps * kRows * (kHeadDim + 2) * sizeof(float);
+  cudaError_t e = ensure_smem(vq_chunk_narrow_kernel<DK, BK, DV, BV, kRows>, smem, opt);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(vq_chunk_narrow_kernel<DK, BK, DV, BV, kRows>, dim3(grid), dim3(kNarrowWarps * 32), smem, stream, p, false);
+}
+
+template <int DK, int BK, int DV, int BV>
+cudaError_t launch_narrow(const ChunkParams& p, int grid, cudaStream_t stream) {
+  return p.tile_rows == 8 ? launch_narrow<DK, BK, DV, BV, 8>(p, grid, stream) : launch_narrow<DK, BK, DV, BV, 16>(p, grid, stream);
+}
+
+// ---- merge of the pieces of tiles that several CTAs took -----------------------------
+// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the tile's pieces, in the CTAs' order.
+// blockIdx.x: the CTA that began the tile; one warp per row, four elements per lane.
+__global__ void __launch_bounds__(256) vq_chunk_merge_kernel(const ChunkParams p) {
+  pdl_wait();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.records + c0));
+  const int rows = rec.x;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+    auto at = [&](int cta) {
+      return static_cast<long long>(cta == c0 ? 2 * c0 + 1 : 2 * cta) * p.tile_rows + r;
+    };
+    float M = -INFINITY;
+    for (int cta = c0 + lane; cta <= rec.w; cta += 32) M = fmaxf(M, __ldcg(p.ws_ml + at(cta)).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    const float Mu = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+    for (int cta = c0; cta <= rec.w; ++cta) {
+      const float2 v = __ldcg(p.ws_ml + at(cta));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at(cta) * kHeadDim) + lane);
+      const float f = fast_exp2(v.x - Mu);
+      L = fmaf(f, v.y, L);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+    const float f = L == 0.f ? 0.f : 1.f / L;
+    const __half2 h0 = __floats2half2_rn(acc.x * f, acc.y * f), h1 = __floats2half2_rn(acc.z * f, acc.w * f);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t*>(&h0);
+    w.y = *reinterpret_cast<const uint32_t*>(&h1);
+    const long long row = static_cast<long long>(rec.y + r / p.group) * p.hq + rec.z * p.group + r % p.group;
+    reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row * kHeadDim)[lane] = w;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
+                                cudaStream_t stream) {
+  if (k_sub == 8 && k_bits == 12 && v_sub == 8 && v_bits == 12) return launch_narrow<8, 12, 8, 12>(p, grid, stream);
+  if (k_bits == 8 && (k_sub == 2 || k_sub == 4)) {
+    const bool k4 = k_sub == 4;
+    if (v_sub == 4 && v_bits == 8) return k4 ? launch_narrow<4, 8, 4, 8>(p, grid, stream) : launch_narrow<2, 8, 4, 8>(p, grid, stream);
+    if (v_sub == 4 && v_bits == 9) return k4 ? launch_narrow<4, 8, 4, 9>(p, grid, stream) : launch_narrow<2, 8, 4, 9>(p, grid, stream);
+    if (v_sub == 2 && v_bits == 8) return k4 ? launch_narrow<4, 8, 2, 8>(p, grid, stream) : launch_narrow<2, 8, 2, 8>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_chunk_merge(const ChunkParams& p, int grid, cudaStream_t stream) {
+  return launch_pdl(vq_chunk_merge_kernel, dim3(grid, (p.tile_rows + 15) / 16), dim3(256), 0, stream, p, true);
+}
+
+}  // namespace vqk

@@ -156,6 +156,37 @@ struct SlotsParams {
   int batch, max_pages, free_capacity, page_size, max_tokens;
 };
 
+// A tile of query rows whose keys more than one CTA of the chunk kernel took:
+// CTA c (the record's index) began it in slot 2c + 1, CTAs c + 1 .. last_cta
+// went on in their slots 2c'.  rows 0: none.
+struct __align__(16) ChunkRecord {
+  int rows, row0, kvh, last_cta;  // tile row r: token row0 + r / G, head kvh G + r % G
+};
+
+struct ChunkParams {
+  const void* q;              // fp16 [T][Hq][128]
+  void* out;                  // fp16 [T][Hq][128]
+  const float* lambda;        // fp32 [Hkv][128]
+  const void* cb_k;           // fp16 [2^bk][dk]
+  const void* cb_v;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const int32_t* page_table;  // [B][max_pages]
+  const int32_t* seq_lens;    // [B] tokens, the new ones among them
+  const int32_t* cu;          // [B + 1] row offsets, or NULL: one row per sequence
+  float* ws_o;                // [2 grid][tile_rows][128] unnormalised partials
+  float2* ws_ml;              // [2 grid][tile_rows] (maximum in log2 units, sum)
+  ChunkRecord* records;       // [grid]
+  int32_t* status;
+  long long num_pages;
+  int batch, num_tokens, hq, hkv, group;
+  int page_size, max_pages, max_seq_len, max_new_len;
+  int window, sinks;          // window 0: none
+  int tile_tok, tile_rows;    // tokens and (padded) rows of a tile
+  int gap, min_range;         // a tile's fixed cost and a CTA's least share, in tokens
+  float qscale;               // softmax scale * log2(e) / sqrt(128)
+};
+
 constexpr int kProducerWarps = 4;  // TMA-issuing warps (one in four stages each)
 constexpr int kMaxUnitsPerCta = 256;
 constexpr int kUnitTok = 32;       // split boundaries are multiples of this many tokens
@@ -316,5 +347,10 @@ int dequant_tokens_per_cta();
 cudaError_t launch_rotary(RotaryParams p, bool bf16, int sms, cudaStream_t stream);
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream);
 constexpr int kSlotsMaxBatch = 16384;
+// Chunk attention; rows: the tile height (8 or 16) of the narrow kernel.
+cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
+                                cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams& p, int grid, cudaStream_t stream);
+constexpr int kChunkMaxBatch = 1024;
 
 }  // namespace vqk

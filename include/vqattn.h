@@ -407,6 +407,59 @@ vq_status vq_decode_attention_residual(const vq_layout* layout, int32_t batch, c
                                        void* stream);
 
 /*
+ * Attention of each sequence's newest tokens over its quantized cache, causal,
+ * optionally with a sliding window and first tokens that stay visible
+ * ("sinks").  Serves chunks of a prompt, drafted tokens that are checked
+ * together, single decode tokens, and any mix of them in one batch.  For every
+ * new token exactly what vq_decode_attention computes for it (VecInfer,
+ * section 方法细节 "注意力机制中的向量量化KV缓存"), over the tokens it sees: the new
+ * tokens' own codes are in the cache already (vq_encode_kv).
+ *   The rows of sequence b are cu_new_lens[b] .. cu_new_lens[b + 1] - 1 of q
+ *   and out: its last n tokens, row i standing at position
+ *   t = seq_lens[b] - n + i.  It sees the cached tokens p with p <= t and,
+ *   with a window, p > t - window or p < num_sinks.  A row that sees
+ *   nothing (t < 0, pages out of range) is zero.
+ *   num_tokens    rows of q and out; rows from cu_new_lens[batch] on are left
+ *                 as they were.
+ *   q, out        fp16 [num_tokens][Hq][D], 16-byte aligned, not overlapping.
+ *   seq_lens      int32 [batch]: tokens of each sequence, the new ones among
+ *                 them, 0 .. max_seq_len.
+ *   cu_new_lens   int32 [batch + 1], not descending, or NULL: one row per
+ *                 sequence (num_tokens >= batch).
+ *   max_seq_len, max_new_len  host bounds of seq_lens and of the rows per
+ *                 sequence; the latter chooses the kernel.  A sequence
+ *                 outside its bounds, or with rows outside q, is left out (its
+ *                 rows are left as they were): VQ_DEV_BAD_LENGTH.
+ *   window        tokens a row sees at most besides the sinks, itself among
+ *                 them; 0: no window.
+ *   num_sinks     first tokens that every later row sees (only with a window).
+ *   softmax_scale 0 selects 1/sqrt(D).
+ *   workspace     vq_chunk_workspace_bytes(...) bytes with the same layout and
+ *                 bounds or larger ones, 256-byte aligned; no initialisation.  Calls
+ *                 that may run at the same time (other streams, graphs) need
+ *                 workspaces of their own.
+ *   lambda, codebooks, pools, page_table, status: as in vq_decode_attention;
+ *   the codebooks' values are finite.  Batches up to 1024, max_seq_len up
+ *   to 2^30.
+ * batch or num_tokens 0 is a no-op.  Every layout that vq_decode_attention
+ * supports.  Two kernels on `stream`; results do not vary from run to run.
+ */
+vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                             const void* q, const float* lambda, const void* codebook_k,
+                             const void* codebook_v, const void* k_pool, const void* v_pool,
+                             int64_t num_pages, const int32_t* page_table,
+                             int32_t max_pages_per_seq, const int32_t* seq_lens,
+                             int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
+                             int32_t window, int32_t num_sinks, float softmax_scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream);
+
+/* Workspace bytes of vq_chunk_attention (num_sms <= 0: the current device).
+ * Pure host arithmetic otherwise.  Returns 0 for invalid arguments. */
+size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                                int32_t max_seq_len, int32_t max_new_len, int32_t num_sms);
+
+/*
  * Page tables, slot map, positions and row offsets of one serving step, from
  * request lengths that live on the device: what vq_encode_kv (slot_mapping),
  * vq_rotary (positions), vq_chunk_attention (cu_new_lens, seq_lens,

@@ -58,3 +58,34 @@ def test_rotary_refusals():
         (dict(q_out=(1 << 24) + 1024), bad), (dict(k_out=1 << 25), bad), (dict(q_out=1 << 24, q_stride=640), bad),
         (dict(q_out=1 << 24, dtype=vq.VQ_BF16), bad), (dict(k_out=FAKE), bad)])
     vq.vq_rotary(**dict(args, num_tokens=0, positions=None, q=None, q_out=None, k=None, k_out=None))  # no tokens: no-op
+
+
+def test_chunk_attention_refusals():
+    L = vq.make_layout()
+    args = dict(layout=L, batch=2, num_tokens=4, q=1 << 24, lambda_=FAKE, codebook_k=FAKE, codebook_v=FAKE, k_pool=FAKE,
+                v_pool=FAKE, num_pages=4, page_table=FAKE, max_pages_per_seq=4, seq_lens=FAKE, max_seq_len=100,
+                cu_new_lens=FAKE, max_new_len=2, window=0, num_sinks=0, softmax_scale=0.0, out=1 << 26, workspace=FAKE,
+                workspace_bytes=1 << 30)
+    bad, unsupported = vq.VQ_ERR_INVALID_ARG, vq.VQ_ERR_UNSUPPORTED
+    refused(vq.vq_chunk_attention, args, [
+        (dict(batch=-1), bad), (dict(batch=1025), unsupported), (dict(num_tokens=-1), bad), (dict(max_new_len=-1), bad),
+        (dict(window=-1), bad), (dict(num_sinks=-1), bad), (dict(num_sinks=4), bad), (dict(softmax_scale=float("nan")), bad),
+        (dict(q=None), bad), (dict(lambda_=None), bad), (dict(codebook_k=None), bad), (dict(codebook_v=None), bad),
+        (dict(k_pool=None), bad), (dict(v_pool=None), bad), (dict(page_table=None), bad), (dict(seq_lens=None), bad),
+        (dict(out=None), bad), (dict(workspace=None), bad), (dict(cu_new_lens=FAKE + 4), bad), (dict(q=FAKE + 8), bad),
+        (dict(num_pages=0), bad), (dict(max_pages_per_seq=0), bad), (dict(max_seq_len=-1), bad), (dict(max_seq_len=1025), bad),
+        (dict(max_seq_len=(1 << 30) + 1, max_pages_per_seq=1 << 24), bad), (dict(out=(1 << 24) + 64), bad),
+        (dict(cu_new_lens=None, num_tokens=1), bad), (dict(layout=vq.make_layout(v_sub=8)), unsupported),
+        (dict(layout=vq.make_layout(page_size=8)), bad)])
+    for kw in (dict(batch=0), dict(num_tokens=0), dict(max_new_len=0)):  # nothing to do
+        vq.vq_chunk_attention(**dict(args, q=None, out=None, workspace=None, **kw))
+
+
+def test_chunk_workspace_bytes():
+    L = vq.make_layout()
+    n = vq.vq_chunk_workspace_bytes(L, 4, 4, 1000, 1, 152)
+    assert n > 0 and n % 256 == 0
+    assert vq.vq_chunk_workspace_bytes(L, 4, 400, 1000, 100, 152) >= n
+    for kw in ((-1, 4, 1000, 1), (4, -1, 1000, 1), (4, 4, -1, 1), (4, 4, 1000, -1)):
+        assert vq.vq_chunk_workspace_bytes(L, *kw, 152) == 0
+    assert vq.vq_chunk_workspace_bytes(vq.make_layout(v_sub=8), 4, 4, 1000, 1, 152) == 0
