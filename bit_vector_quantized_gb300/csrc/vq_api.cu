@@ -1091,10 +1091,17 @@ vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const in
 // ---- attention of several new tokens per sequence --------------------------------
 namespace {
 
-// Tile height of a call: all rows of a (sequence, KV head) where 8 hold them.
+// Tile height of a call, by the rows of its longest (sequence, KV head): all
+// of them where 8 or 16 hold them (warp mma), else 128 (tcgen05).
+// VQ_CHUNK_ROWS=16|128 selects a height explicitly (a tuning switch for
+// profiling).
 int chunk_tile_rows(const vq_layout& L, int max_new_len) {
   const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
-  return rows <= 8 ? 8 : 16;
+  if (const char* env = std::getenv("VQ_CHUNK_ROWS")) {
+    if (std::strcmp(env, "16") == 0) return 16;
+    if (std::strcmp(env, "128") == 0) return 128;
+  }
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
 }
 
 struct ChunkWs {
@@ -1200,12 +1207,14 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.sinks = std::min(num_sinks, 1 << 30);
   p.tile_rows = chunk_tile_rows(L, max_new_len);
   p.tile_tok = p.tile_rows / p.group;
-  p.gap = 256;
+  const bool wide = p.tile_rows == 128;
+  p.gap = wide ? 384 : 256;
   p.min_range = 512;
+  p.timeout_ns = 2000000000ULL;
   const float scale = softmax_scale == 0.f ? 1.f / std::sqrt(static_cast<float>(L.head_dim)) : softmax_scale;
   p.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 / std::sqrt(128.0));
-  cudaError_t e = vqk::launch_chunk_narrow(p, L.k_sub, L.k_bits, L.v_sub, L.v_bits, grid,
-                                           static_cast<cudaStream_t>(stream));
+  auto launch = wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;
+  cudaError_t e = launch(p, L.k_sub, L.k_bits, L.v_sub, L.v_bits, grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention launch");
   e = vqk::launch_chunk_merge(p, grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention merge");

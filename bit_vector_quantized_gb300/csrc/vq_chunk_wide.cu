@@ -1,0 +1,607 @@
+// vq_chunk_wide.cu -- chunk attention for many query rows per (sequence, KV head) (sm_103a).
+//
+// The mathematics of vq_chunk_narrow.cu for tiles of 128 query rows, on the
+// fifth-generation tensor cores: per block of 128 tokens
+//   S [128 x 128] = Q~ K~^T,  P = 2^(S - m),  O [128 x 128] += P V.
+// A block costs 2 x 128^3 multiply-adds for the scores (q~ in high and low fp16
+// parts, so that scores keep about fp32 accuracy) and 128^3 for the values;
+// the codes are 8 KB, so the kernel is bound by arithmetic: the tensor pipe
+// first, the softmax's exponentials and the expansion of the codes beside it.
+//
+//   * Eight warps expand codes: a thread takes one token's codes of 64 dims
+//     (loaded two blocks ahead, page first), gathers their centroids from the
+//     replicated, bank-conflict-free table and stores 16-byte pieces into the
+//     swizzled tiles that the tensor core reads (K rows of dims, V rows of
+//     dims with the token as k: one layout for both).  K runs one block ahead
+//     of V.
+//   * One thread issues the products: scores of block j + 1 before the values
+//     of block j, so the tensor pipe works while the softmax of block j runs.
+//   * Four warps hold one query row per thread: the Walsh-Hadamard transform
+//     of their q row in registers, the online softmax (maximum and sum in
+//     fp32; the maximum may lag by 2^8, so O is seldom rescaled), P rounded
+//     to fp16 once (p <= 2^8: relative 2^-11, averaging out over the tokens).
+//   * Tensor memory, all 512 columns: S twice (P overwrites its S, so the
+//     values read it from there), O, and Q~ high and low.
+//   * Every wait is bounded: on a timeout the CTA raises an abort flag,
+//     everybody leaves, the products in flight are drained and
+//     VQ_DEV_TIMEOUT is reported.
+#include "vq_chunk_common.cuh"
+#include "vq_gather.cuh"
+#include "vq_tcgen05.cuh"
+
+namespace vqk {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
+constexpr int kTile = 128;           // query rows of a tile, and tokens of a block
+constexpr int kSoftWarps = 4, kCodeWarps = 8;
+constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 1) * 32;
+constexpr int kTileBytes = kTile * kHeadDim * 2;
+constexpr int kKStages = 2;
+constexpr int kMasks = 4;            // token masks in flight (see the code warps)
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
+
+template <int DK, int BK, int DV, int BV>
+struct WideSmem {
+  static constexpr bool kWideCodes = DK == 8;      // 1.5-bit format: plain 64 KB tables
+  static constexpr bool kSplitTable = BV == 9;     // 128-byte rows, K then V; else 256-byte rows (K, V)
+  static constexpr int kTable = kWideCodes ? 131072 : kSplitTable ? (256 + 512) * 128 : 65536;
+  static constexpr int kVStages = kWideCodes ? 1 : 2;
+  static constexpr int kTiles = kTable;                             // K stages, then V stages
+  static constexpr int kMisc = kTiles + (kKStages + kVStages) * kTileBytes;
+  static constexpr int kTotal = kMisc + 512;
+  static_assert(kTotal <= 232448, "shared memory of one CTA");
+  static_assert((kChunkMaxBatch + 1 + 32) * 8 <= kTileBytes, "the plan shares a tile");
+};
+
+// Codes of one token's 64-dim half, and the table offset of code i.
+template <int D, int B>
+struct HalfCodes {
+  static constexpr int kCodes = 64 / D;
+  static constexpr int kWords = B == 9 ? 5 : kCodes * B / 32;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const uint8_t* row, int half) {
+    if constexpr (B == 8) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + half * kCodes) + i / 4);
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
+    } else if constexpr (B == 9) {  // 144 bits from bit 0 or bit 144 (word 4, bit 16)
+      const uint32_t* r = reinterpret_cast<const uint32_t*>(row) + 4 * half;
+      uint32_t x[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) x[i] = __ldg(r + i);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = __funnelshift_r(x[i], i < 4 ? x[i + 1] : 0u, 16 * half);
+    } else {  // 12-bit codes: 96 bits
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + kWords * half + i);
+    }
+  }
+  __device__ __forceinline__ uint32_t code(int i) const {
+    if constexpr (B == 8) {
+      return __byte_perm(w[i >> 2], 0u, 0x4440 | (i & 3));
+    } else {
+      const int bit = i * B, k = bit >> 5, s = bit & 31;
+      const uint32_t x = s + B > 32 ? __funnelshift_r(w[k], w[k + 1 < kWords ? k + 1 : k], s) : w[k] >> s;
+      return x & ((1u << B) - 1u);
+    }
+  }
+};
+
+// 16-byte piece c (dims 8c .. 8c + 7) of the half: its centroids.
+// row_shift: log2 of the table's row bytes; lane: the lane's byte in a row.
+template <int D, int B, int kRowShift>
+__device__ __forceinline__ uint4 gather_piece(const HalfCodes<D, B>& x, int c, uint32_t lane) {
+  auto off = [&](int i) {
+    if constexpr (B == 8 && kRowShift == 8) return row_addr(x.w[i >> 2], lane, i & 3);
+    else return (x.code(i) << kRowShift) + lane;
+  };
+  if constexpr (D == 8) {
+    return tab128(off(c));
+  } else if constexpr (D == 4) {
+    const uint2 a = tab64(off(2 * c)), b = tab64(off(2 * c + 1));
+    return make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+    return make_uint4(tab32(off(4 * c)), tab32(off(4 * c + 1)), tab32(off(4 * c + 2)), tab32(off(4 * c + 3)));
+  }
+}
+
+template <int DK, int BK, int DV, int BV>
+__device__ __forceinline__ void fill_wide_table(const ChunkParams& p) {
+  using W = WideSmem<DK, BK, DV, BV>;
+  uint4* tab = reinterpret_cast<uint4*>(g_smem);
+  auto replicas = [](const void* cb, int row, bool four) {
+    if (four) {
+      const uint2 c = __ldg(static_cast<const uint2*>(cb) + row);
+      return make_uint4(c.x, c.y, c.x, c.y);
+    }
+    const uint32_t c = __ldg(static_cast<const uint32_t*>(cb) + row);
+    return make_uint4(c, c, c, c);
+  };
+  for (int i = threadIdx.x; i < W::kTable / 16; i += blockDim.x) {
+    if constexpr (W::kWideCodes) {
+      tab[i] = i < 4096 ? __ldg(static_cast<const uint4*>(p.cb_k) + i) : __ldg(static_cast<const uint4*>(p.cb_v) + i - 4096);
+    } else if constexpr (W::kSplitTable) {
+      tab[i] = i < 2048 ? replicas(p.cb_k, i >> 3, DK == 4) : replicas(p.cb_v, (i - 2048) >> 3, DV == 4);
+    } else {
+      tab[i] = i & 8 ? replicas(p.cb_v, i >> 4, DV == 4) : replicas(p.cb_k, i >> 4, DK == 4);
+    }
+  }
+}
+
+// Unnormalised Walsh-Hadamard transform of 64 registers.
+__device__ __forceinline__ void fwht64(float (&x)[64]) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if (!(i & s)) {
+        const float a = x[i], b = x[i + s];
+        x[i] = a + b;
+        x[i + s] = a - b;
+      }
+}
+
+// A ring slot's position: phase flips each time the ring wraps.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <int DK, int BK, int DV, int BV>
+__global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
+  using W = WideSmem<DK, BK, DV, BV>;
+  constexpr int NV = W::kVStages;
+  constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
+  uint8_t* const tiles = g_smem + W::kTiles;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(g_smem + W::kMisc);
+  uint64_t* const k_full = bars;               // [2] code warps -> products
+  uint64_t* const k_empty = k_full + kKStages; // [2] products -> code warps
+  uint64_t* const v_full = k_empty + kKStages; // [NV]
+  uint64_t* const v_empty = v_full + 2;        // [NV]
+  uint64_t* const s_full = v_empty + 2;        // [2] scores done
+  uint64_t* const p_full = s_full + 2;         // [2] P stored
+  uint64_t* const o_full = p_full + 2;         // values of a block done
+  uint64_t* const q_full = o_full + 1;         // Q~ stored, O read
+  uint64_t* const drain = q_full + 1;
+  uint32_t* const masks = reinterpret_cast<uint32_t*>(bars + 24);  // [kMasks][4] tokens that have a page
+  uint32_t* const tmem_at = masks + kMasks * 4;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (smem_addr(tiles) & 1023u) {  // the swizzled tiles need it (and dynamic shared memory alone gives it)
+    if (tid == 0) {
+      report(p.status, kDevBadConfig);
+      write_record(p, nullptr);
+    }
+    return;
+  }
+  fill_wide_table<DK, BK, DV, BV>(p);
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(k_full + i, kCodeWarps);
+      mbar_init(k_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(v_full + i, kCodeWarps);
+      mbar_init(v_empty + i, 1);
+      mbar_init(s_full + i, 2);  // the products' commit, and the issuer's arrival after its own waits
+      mbar_init(p_full + i, kSoftWarps);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(q_full, kSoftWarps);
+    mbar_init(drain, 1);
+    mbar_init_fence();
+    *abort_flag = 0;
+  }
+  if (warp == kSoftWarps + kCodeWarps) tmem_alloc(tmem_at, kCols);
+  long long* const pre = reinterpret_cast<long long*>(tiles);  // the plan, before the first tile is written
+  tc_fence_before();
+  chunk_plan(p, pre, pre + kChunkMaxBatch + 1);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_at;
+  ChunkWalk<kTile> walk(p, pre);
+  __syncthreads();  // everybody has read the plan
+  ChunkPiece u;
+
+  // Bounded wait; on a timeout the CTA is given up.  The warps' form is uniform over the warp.
+  auto wait_one = [&](uint64_t* bar, uint32_t phase) {
+    if (mbar_wait_bounded(bar, phase, abort_flag, p.timeout_ns)) return true;
+    if (!*abort_flag) {
+      *abort_flag = 1;
+      report(p.status, kDevTimeout);
+    }
+    return false;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(kAll, wait_one(bar, phase)) != 0; };
+
+  if (warp < kSoftWarps) {
+    // ============================ one query row per thread ============================
+    const int r = tid, G = p.group;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t blocks = 0;  // blocks so far, over all pieces
+    bool recorded = false, ok = true;
+    while (ok && walk.next(u)) {
+      const int i0 = u.tile * p.tile_tok;
+      const int rows = min(p.tile_tok, u.s.n - i0) * G;
+      const bool live = r < rows;
+      const long long row = static_cast<long long>(u.s.row0 + i0 + (live ? r / G : 0)) * p.hq + u.kvh * G + (live ? r % G : 0);
+      const int nblk = u.blk1 - u.blk0;
+      float m = -INFINITY, l = 0.f;
+      if (nblk > 0) {
+        // ---- q~ = q diag(lambda) H: the first butterfly joins the halves, then 64 + 64 ----
+        const __half* q = static_cast<const __half*>(p.q) + row * kHeadDim;
+        const float* lam = p.lambda + u.kvh * kHeadDim;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float x[64];
+          const float sg = h ? -p.qscale : p.qscale;
+#pragma unroll
+          for (int i = 0; i < 64; i += 8) {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (live) {
+              a = __ldg(reinterpret_cast<const uint4*>(q + i));
+              b = __ldg(reinterpret_cast<const uint4*>(q + 64 + i));
+            }
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+              const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
+              const float2 la = __ldg(reinterpret_cast<const float2*>(lam + i) + e);
+              const float2 lb = __ldg(reinterpret_cast<const float2*>(lam + 64 + i) + e);
+              x[i + 2 * e] = fmaf(fb.x * lb.x, sg, fa.x * la.x * p.qscale);
+              x[i + 2 * e + 1] = fmaf(fb.y * lb.y, sg, fa.y * la.y * p.qscale);
+            }
+          }
+          fwht64(x);
+          __syncwarp();
+          uint32_t hi[32], lo[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) split_half2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+          tmem_st32(tmem + lanes + kColQ + 32 * h, hi);
+          tmem_st32(tmem + lanes + kColQ + 64 + 32 * h, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+
+        const int pos = live ? u.s.base + i0 + r / G : -1;
+        const int first_pos = u.s.base + i0, last_pos = u.s.base + min(i0 + p.tile_tok, u.s.n) - 1;
+        for (int j = 0; j < nblk; ++j, ++blocks) {
+          const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb;
+          ok = wait(s_full + sb, (blocks >> 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const int t0 = u.k.block(u.blk0 + j) * kTile;
+          uint32_t seen[4];
+          bool whole = t0 + kTile - 1 <= first_pos && (p.window == 0 || t0 > last_pos - p.window || t0 + kTile <= p.sinks);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            seen[i] = masks[(blocks % kMasks) * 4 + i];
+            whole = whole && seen[i] == kAll;
+          }
+          auto mask = [&](uint32_t(&s)[32], int c) {  // columns 32 c .. 32 c + 31
+            // (tokens past the sequence's end are not in `seen`)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int t = t0 + 32 * c + i;
+              const bool see = (seen[c] >> i & 1u) && t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
+              if (!see) s[i] = __float_as_uint(-INFINITY);
+            }
+          };
+          auto top = [&](const uint32_t(&s)[32]) {
+            float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) {
+              a = fmaxf(a, __uint_as_float(s[i]));
+              b = fmaxf(b, __uint_as_float(s[i + 1]));
+            }
+            return fmaxf(a, b);
+          };
+          // ---- the row's maximum, then p; columns 64 .. 127 stay in registers between the two ----
+          uint32_t s0[32], s1[32];
+          tmem_ld32(col_s, s0);
+          tmem_ld32(col_s + 32, s1);
+          tmem_wait_ld();
+          if (!whole) {
+            mask(s0, 0);
+            mask(s1, 1);
+          }
+          float mx = fmaxf(top(s0), top(s1));
+          tmem_ld32(col_s + 64, s0);
+          tmem_ld32(col_s + 96, s1);
+          tmem_wait_ld();
+          if (!whole) {
+            mask(s0, 2);
+            mask(s1, 3);
+          }
+          mx = fmaxf(mx, fmaxf(top(s0), top(s1)));
+          const bool raise = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
+          const float scale = raise ? fast_exp2(m - mx) : 1.f;  // 0 while nothing is accumulated
+          m = raise ? mx : m;
+          l *= scale;
+          const float mu = m == -INFINITY ? 0.f : m;
+          float sum0 = 0.f, sum1 = 0.f;
+          auto store_p = [&](const uint32_t(&s)[32], int c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float a = fast_exp2(__uint_as_float(s[2 * i]) - mu), b = fast_exp2(__uint_as_float(s[2 * i + 1]) - mu);
+              sum0 += a;
+              sum1 += b;
+              const __half2 h = __floats2half2_rn(a, b);
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tmem_st16(col_s + 32 * c, w);  // over its own scores
+          };
+          store_p(s0, 2);
+          store_p(s1, 3);
+          tmem_ld32(col_s, s0);
+          tmem_ld32(col_s + 32, s1);
+          tmem_wait_ld();
+          if (!whole) {
+            mask(s0, 0);
+            mask(s1, 1);
+          }
+          store_p(s0, 0);
+          store_p(s1, 1);
+          l += sum0 + sum1;
+          if (j > 0) {
+            // The values of block - 1 (they ran beside this softmax) are waited for in every
+            // block, so each phase of o_full is met once, in order.
+            ok = wait(o_full, (blocks - 1) & 1u);
+            if (!ok) break;
+            if (__any_sync(kAll, raise)) {  // O follows the maximum
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld32(tmem + lanes + kColO + 32 * c, s0);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
+                tmem_st32(tmem + lanes + kColO + 32 * c, s0);
+              }
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + sb);
+        }
+        if (!ok) break;
+        ok = wait(o_full, (blocks - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // ---- the piece's rows: to `out`, or as a partial to the workspace --------------------
+      const float f = u.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const long long at = static_cast<long long>(u.slot) * kTile + r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = 0u;
+        if (nblk > 0) {
+          tmem_ld32(tmem + lanes + kColO + 32 * c, s);
+          tmem_wait_ld();
+        }
+        if (live && u.slot >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.ws_o + at * kHeadDim + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + row * kHeadDim + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 h = __floats2half2_rn(__uint_as_float(s[8 * i + 2 * e]) * f, __uint_as_float(s[8 * i + 2 * e + 1]) * f);
+              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (u.slot >= 0) {
+        if (live) p.ws_ml[at] = make_float2(m, l);
+        if ((u.slot & 1) && tid == 0) {
+          write_record(p, &u);
+          recorded = true;
+        }
+      }
+      tc_fence_before();  // (O's reads, before the next piece's arrival on q_full)
+    }
+    if (tid == 0 && !recorded) write_record(p, nullptr);
+  } else if (warp < kSoftWarps + kCodeWarps) {
+    // ================================= code warps ======================================
+    const int w = warp - kSoftWarps, half = w & 1, tok = 32 * (w >> 1) + lane;
+    const uint32_t rep = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
+    const uint32_t lane_k = W::kWideCodes ? 0u : rep;
+    const uint32_t lane_v = W::kWideCodes ? 65536u : W::kSplitTable ? 32768u + rep_v : 128u + rep_v;
+    constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
+    const uint32_t dst = smem_addr(tiles) + half * (kTileBytes / 2) + tok * 128;
+    const uint32_t sw = tok & 7;
+    auto store = [&](uint32_t at, int c, uint4 v) {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((c ^ sw) << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    };
+    // Block iterator, two blocks ahead of the tiles: the thread's page; then its codes one ahead.
+    bool more = true;
+    int i = 0;
+    u.blk1 = 0;
+    struct Where {
+      int page, off, kvh;
+      bool in, any;  // the token exists; the block exists
+    };
+    auto advance = [&]() {
+      Where x = {0, 0, 0, false, false};
+      while (more && i >= u.blk1) {
+        more = walk.next(u);
+        i = more ? u.blk0 : 0;
+      }
+      if (!more) return x;
+      const int t = u.k.block(i++) * kTile + tok;
+      x.any = true;
+      x.in = t < u.s.limit;
+      x.kvh = u.kvh;
+      if (x.in) {
+        const int lp = t / p.page_size;
+        x.off = t - lp * p.page_size;
+        x.page = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + lp);
+      }
+      return x;
+    };
+    HalfCodes<DK, BK> kc;
+    HalfCodes<DV, BV> vc, vc_prev;
+    bool has = false, has_prev = false;  // the token can be read
+    auto fetch = [&](const Where& x, HalfCodes<DK, BK>& k, HalfCodes<DV, BV>& v) {
+      bool good = x.in && x.page >= 0 && x.page < p.num_pages;
+      if (x.in && !good) report(p.status, kDevBadPage);
+      if (good) {
+        const long long row = (static_cast<long long>(x.page) * p.hkv + x.kvh) * p.page_size + x.off;
+        k.load(p.k_pool + row * KROW, half);
+        v.load(p.v_pool + row * VROW, half);
+      }
+      return good;
+    };
+    Where now = advance(), ahead = advance();
+    if (now.any) has = fetch(now, kc, vc);
+    bool any = now.any, any_prev = false;
+    Ring rk, rv;
+    uint32_t blocks = 0;
+    while (any || any_prev) {
+      HalfCodes<DK, BK> kn;
+      HalfCodes<DV, BV> vn;
+      const Where next = ahead;
+      ahead = advance();
+      const bool has_n = next.any && fetch(next, kn, vn);
+      if (any) {
+        if (!wait(k_empty + rk.slot, rk.phase ^ 1u)) break;
+        const uint32_t at = dst + rk.slot * kTileBytes;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) store(at, c, has ? gather_piece<DK, BK, kShift>(kc, c, lane_k) : make_uint4(0, 0, 0, 0));
+        const uint32_t seen = __ballot_sync(kAll, has);
+        if (half == 0 && lane == 0) masks[(blocks % kMasks) * 4 + (w >> 1)] = seen;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + rk.slot);
+        rk.next(kKStages);
+        ++blocks;
+      }
+      if (any_prev) {
+        if (!wait(v_empty + rv.slot, rv.phase ^ 1u)) break;
+        const uint32_t at = dst + (kKStages + rv.slot) * kTileBytes;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          store(at, c, has_prev ? gather_piece<DV, BV, kShift>(vc_prev, c, lane_v) : make_uint4(0, 0, 0, 0));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full + rv.slot);
+        rv.next(NV);
+      }
+      vc_prev = vc;
+      has_prev = has;
+      any_prev = any;
+      kc = kn;
+      vc = vn;
+      has = has_n;
+      any = next.any;
+    }
+  } else if (lane == 0) {
+    // ================================= the products ====================================
+    constexpr uint32_t kScores = tc_idesc(kTile, kTile, false), kValues = tc_idesc(kTile, kHeadDim, true);
+    const uint32_t tile0 = smem_addr(tiles);
+    Ring rk, rv;
+    uint32_t blocks = 0, pieces = 0;
+    bool ok = true;
+    while (ok && walk.next(u)) {
+      const int nblk = u.blk1 - u.blk0;
+      if (nblk <= 0) continue;
+      ok = wait_one(q_full, pieces++ & 1u);
+      for (int j = 0; ok && j <= nblk; ++j) {
+        if (j < nblk) {  // scores of block j
+          const uint32_t sb = (blocks + j) & 1u;
+          if (!(ok = wait_one(k_full + rk.slot, rk.phase))) break;
+          tc_fence_after();
+          const uint32_t kt = tile0 + rk.slot * kTileBytes;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)  // high and low part of q~
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma_ts(tmem + kColS + 128 * sb, tmem + kColQ + 64 * part + 8 * ks,
+                        tc_desc(kt + (ks >> 2) * (kTileBytes / 2) + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
+          tc_commit(s_full + sb);
+          mbar_arrive(s_full + sb);
+          tc_commit(k_empty + rk.slot);
+          rk.next(kKStages);
+        }
+        if (j > 0) {  // values of block j - 1
+          const uint32_t blk = blocks + j - 1, sb = blk & 1u;
+          if (!(ok = wait_one(p_full + sb, (blk >> 1) & 1u))) break;
+          if (!(ok = wait_one(v_full + rv.slot, rv.phase))) break;
+          tc_fence_after();
+          const uint32_t vt = tile0 + (kKStages + rv.slot) * kTileBytes;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
+            tc_mma_ts(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
+                      tc_desc(vt + ks * 2048, kTileBytes / 2), kValues, j > 1 || ks > 0);
+          tc_commit(v_empty + rv.slot);
+          tc_commit(o_full);
+          rv.next(NV);
+        }
+      }
+      blocks += nblk;
+    }
+    if (!ok) {  // given up: the products in flight end before the tensor memory goes back
+      tc_commit(drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < p.timeout_ns) {
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + kCodeWarps) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, kCols);
+  }
+}
+
+template <int DK, int BK, int DV, int BV>
+cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
+  static SmemOptIn opt;
+  constexpr size_t smem = WideSmem<DK, BK, DV, BV>::kTotal;
+  cudaError_t e = ensure_smem(vq_chunk_wide_kernel<DK, BK, DV, BV>, smem, opt);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(vq_chunk_wide_kernel<DK, BK, DV, BV>, dim3(grid), dim3(kWideThreads), smem, stream, p, false);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
+                              cudaStream_t stream) {
+  if (k_sub == 8 && k_bits == 12 && v_sub == 8 && v_bits == 12) return launch_wide<8, 12, 8, 12>(p, grid, stream);
+  if (k_bits == 8 && (k_sub == 2 || k_sub == 4)) {
+    const bool k4 = k_sub == 4;
+    if (v_sub == 4 && v_bits == 8) return k4 ? launch_wide<4, 8, 4, 8>(p, grid, stream) : launch_wide<2, 8, 4, 8>(p, grid, stream);
+    if (v_sub == 4 && v_bits == 9) return k4 ? launch_wide<4, 8, 4, 9>(p, grid, stream) : launch_wide<2, 8, 4, 9>(p, grid, stream);
+    if (v_sub == 2 && v_bits == 8) return k4 ? launch_wide<4, 8, 2, 8>(p, grid, stream) : launch_wide<2, 8, 2, 8>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace vqk

@@ -185,6 +185,7 @@ struct ChunkParams {
   int tile_tok, tile_rows;    // tokens and (padded) rows of a tile
   int gap, min_range;         // a tile's fixed cost and a CTA's least share, in tokens
   float qscale;               // softmax scale * log2(e) / sqrt(128)
+  unsigned long long timeout_ns;
 };
 
 constexpr int kProducerWarps = 4;  // TMA-issuing warps (one in four stages each)
@@ -347,9 +348,11 @@ int dequant_tokens_per_cta();
 cudaError_t launch_rotary(RotaryParams p, bool bf16, int sms, cudaStream_t stream);
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream);
 constexpr int kSlotsMaxBatch = 16384;
-// Chunk attention; rows: the tile height (8 or 16) of the narrow kernel.
+// Chunk attention, tile_rows 8 or 16 (narrow) and 128 (wide); the merge of either.
 cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
                                 cudaStream_t stream);
+cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
+                              cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int grid, cudaStream_t stream);
 constexpr int kChunkMaxBatch = 1024;
 
