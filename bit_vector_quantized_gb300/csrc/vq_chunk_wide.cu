@@ -35,11 +35,13 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
 constexpr int kTile = 128;           // query rows of a tile, and tokens of a block
-constexpr int kSoftWarps = 4, kCodeWarps = 8;
-constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 1) * 32;
+constexpr int kSoftWarps = 8, kCodeWarps = 8;
+constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has one busy warp
+// Registers per thread: 96 at the launch (640 threads), then 256 x 128 + 256 x 80 + 128 x 56 <= 640 x 96.
+constexpr int kSoftRegs = 128, kCodeRegs = 80, kIssueRegs = 56;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kKStages = 2;
-constexpr int kMasks = 4;            // token masks in flight (see the code warps)
+constexpr int kMasks = 4;            // token masks in flight: a slot comes round after the softmax of its block
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
 
 template <int DK, int BK, int DV, int BV>
@@ -50,7 +52,7 @@ struct WideSmem {
   static constexpr int kVStages = kWideCodes ? 1 : 2;
   static constexpr int kTiles = kTable;                             // K stages, then V stages
   static constexpr int kMisc = kTiles + (kKStages + kVStages) * kTileBytes;
-  static constexpr int kTotal = kMisc + 512;
+  static constexpr int kTotal = kMisc + 640 + 2 * 2 * kTile * 4;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
   static_assert((kChunkMaxBatch + 1 + 32) * 8 <= kTileBytes, "the plan shares a tile");
 };
@@ -145,6 +147,29 @@ __device__ __forceinline__ void fwht64(float (&x)[64]) {
       }
 }
 
+// The warpgroup's registers per thread from here on (all four warps call it).
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Maximum of three (fp32 bits), and a packed pair of fp32 additions.
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+__device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+
 // A ring slot's position: phase flips each time the ring wraps.
 struct Ring {
   uint32_t slot = 0, phase = 0;
@@ -155,6 +180,31 @@ struct Ring {
     }
   }
 };
+
+// One piece of a tile as the planning warp hands it to the others.
+struct __align__(16) WidePiece {
+  int b, kvh;
+  int row0, rows;            // the tile's first row in q and out, and its rows (tokens x G)
+  int first_pos, last_pos;   // positions of its first and last token
+  int limit;                 // keys end here
+  int sink, lo, blk0, blk1;  // blocks [blk0, blk1) of its keys (ChunkKeys)
+  int slot;                  // partial slot or -1
+  int more;                  // 0: there is no piece, the range is done
+  int pad[3];
+  __device__ __forceinline__ int block(int i) const { return i < sink ? i : lo + (i - sink); }
+};
+static_assert(sizeof(WidePiece) == 64, "the pieces' place in shared memory");
+// Pieces under way.  The code warps look two blocks ahead of the one they store,
+// whose values' tile is still one behind: four pieces of one block each are
+// all that can lie between the last to read a piece and the first (pieces
+// without a block are not handed out).
+constexpr uint32_t kPieces = 4;
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 
 template <int DK, int BK, int DV, int BV>
 __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
@@ -172,9 +222,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   uint64_t* const o_full = p_full + 2;         // values of a block done
   uint64_t* const q_full = o_full + 1;         // Q~ stored, O read
   uint64_t* const drain = q_full + 1;
+  uint64_t* const piece_full = drain + 1;              // [kPieces] planning warp -> everybody
+  uint64_t* const piece_empty = piece_full + kPieces;  // [kPieces]
+  WidePiece* const pieces = reinterpret_cast<WidePiece*>(bars + 48);  // [kPieces]
   uint32_t* const masks = reinterpret_cast<uint32_t*>(bars + 24);  // [kMasks][4] tokens that have a page
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+  float* const tops = reinterpret_cast<float*>(g_smem + W::kMisc + 640);  // [2][2][128] maxima of a row's two halves
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -200,6 +254,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     mbar_init(o_full, 1);
     mbar_init(q_full, kSoftWarps);
     mbar_init(drain, 1);
+    for (int i = 0; i < static_cast<int>(kPieces); ++i) {
+      mbar_init(piece_full + i, 1);
+      mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 1);
+    }
     mbar_init_fence();
     *abort_flag = 0;
   }
@@ -208,10 +266,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   tc_fence_before();
   chunk_plan(p, pre, pre + kChunkMaxBatch + 1);
   tc_fence_after();
-  const uint32_t tmem = *tmem_at;
-  ChunkWalk<kTile> walk(p, pre);
-  __syncthreads();  // everybody has read the plan
-  ChunkPiece u;
+  // All 512 columns are this CTA's, so they start at column 0; the constant keeps the
+  // products' operands in uniform registers.
+  constexpr uint32_t tmem = 0;
+  if (*tmem_at != tmem) {
+    if (tid == 0) report(p.status, kDevBadConfig);
+    if (tid == 0) write_record(p, nullptr);
+    __syncthreads();
+    if (warp == kSoftWarps + kCodeWarps) tmem_free(*tmem_at, kCols);
+    return;
+  }
 
   // Bounded wait; on a timeout the CTA is given up.  The warps' form is uniform over the warp.
   auto wait_one = [&](uint64_t* bar, uint32_t phase) {
@@ -223,179 +287,177 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     return false;
   };
   auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(kAll, wait_one(bar, phase)) != 0; };
+  // The next piece (whole warps); false when there is none or the CTA was given up.
+  Ring rp;
+  auto next_piece = [&](WidePiece& u) {
+    if (!wait(piece_full + rp.slot, rp.phase)) return false;
+    u = pieces[rp.slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(piece_empty + rp.slot);
+    rp.next(kPieces);
+    return u.more != 0;
+  };
+  WidePiece u;
 
   if (warp < kSoftWarps) {
-    // ============================ one query row per thread ============================
-    const int r = tid, G = p.group;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // ====== two threads per query row: columns (and dims) 0 .. 63 and 64 .. 127 of a block ======
+    reg_inc<kSoftRegs>();
+    const int r = tid & (kTile - 1), g = tid >> 7, G = p.group;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // the two warps of a row meet here
+    auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
     uint32_t blocks = 0;  // blocks so far, over all pieces
-    bool recorded = false, ok = true;
-    while (ok && walk.next(u)) {
-      const int i0 = u.tile * p.tile_tok;
-      const int rows = min(p.tile_tok, u.s.n - i0) * G;
-      const bool live = r < rows;
-      const long long row = static_cast<long long>(u.s.row0 + i0 + (live ? r / G : 0)) * p.hq + u.kvh * G + (live ? r % G : 0);
+    bool ok = true;
+    while (ok && next_piece(u)) {
+      const bool live = r < u.rows;
+      const int token = live ? r / G : 0;
+      const long long row = static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (live ? r - token * G : 0);
       const int nblk = u.blk1 - u.blk0;
       float m = -INFINITY, l = 0.f;
-      if (nblk > 0) {
-        // ---- q~ = q diag(lambda) H: the first butterfly joins the halves, then 64 + 64 ----
+      // ---- q~ = q diag(lambda) H: the first butterfly joins the halves, then 64 of this half ----
+      {
         const __half* q = static_cast<const __half*>(p.q) + row * kHeadDim;
         const float* lam = p.lambda + u.kvh * kHeadDim;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float x[64];
-          const float sg = h ? -p.qscale : p.qscale;
+        float x[64];
+        const float sg = g ? -p.qscale : p.qscale;
 #pragma unroll
-          for (int i = 0; i < 64; i += 8) {
-            uint4 a = make_uint4(0, 0, 0, 0), b = a;
-            if (live) {
-              a = __ldg(reinterpret_cast<const uint4*>(q + i));
-              b = __ldg(reinterpret_cast<const uint4*>(q + 64 + i));
+        for (int i = 0; i < 64; i += 8) {
+          uint4 a = make_uint4(0, 0, 0, 0), b = a;
+          if (live) {
+            a = __ldg(reinterpret_cast<const uint4*>(q + i));
+            b = __ldg(reinterpret_cast<const uint4*>(q + 64 + i));
+          }
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
+            const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
+            const float2 la = __ldg(reinterpret_cast<const float2*>(lam + i) + e);
+            const float2 lb = __ldg(reinterpret_cast<const float2*>(lam + 64 + i) + e);
+            x[i + 2 * e] = fmaf(fb.x * lb.x, sg, fa.x * la.x * p.qscale);
+            x[i + 2 * e + 1] = fmaf(fb.y * lb.y, sg, fa.y * la.y * p.qscale);
+          }
+        }
+        fwht64(x);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) split_half2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1], hi[i], lo[i]);
+          tmem_st16(tmem + lanes + kColQ + 32 * g + 16 * c, hi);
+          tmem_st16(tmem + lanes + kColQ + 64 + 32 * g + 16 * c, lo);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      const int pos = live ? u.first_pos + token : -1;
+      for (int j = 0; j < nblk; ++j, ++blocks) {
+        const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb + 64 * g;
+        ok = wait(s_full + sb, (blocks >> 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s0[32], s1[32];
+        tmem_ld32(col_s, s0);
+        tmem_ld32(col_s + 32, s1);
+        const int t0 = u.block(u.blk0 + j) * kTile;
+        const uint4 seen = *reinterpret_cast<const uint4*>(masks + (blocks % kMasks) * 4);
+        const bool whole = t0 + kTile - 1 <= u.first_pos && (p.window == 0 || t0 > u.last_pos - p.window || t0 + kTile <= p.sinks) &&
+                           (seen.x & seen.y & seen.z & seen.w) == kAll;
+        tmem_wait_ld();
+        if (!whole) {
+          auto mask = [&](uint32_t(&s)[32], int t_first, uint32_t here) {
+            // (tokens past the sequence's end are not in `seen`)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int t = t_first + i;
+              const bool see = (here >> i & 1u) && t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
+              if (!see) s[i] = __float_as_uint(-INFINITY);
             }
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+          };
+          mask(s0, t0 + 64 * g, g ? seen.z : seen.x);
+          mask(s1, t0 + 64 * g + 32, g ? seen.w : seen.y);
+        }
+        // ---- the row's maximum, from both halves ------------------------------------------
+        float a[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
-              const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
-              const float2 la = __ldg(reinterpret_cast<const float2*>(lam + i) + e);
-              const float2 lb = __ldg(reinterpret_cast<const float2*>(lam + 64 + i) + e);
-              x[i + 2 * e] = fmaf(fb.x * lb.x, sg, fa.x * la.x * p.qscale);
-              x[i + 2 * e + 1] = fmaf(fb.y * lb.y, sg, fa.y * la.y * p.qscale);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t* x = k < 2 ? s0 + 16 * k : s1 + 16 * (k - 2);
+          a[k] = max3(x[0], x[1], x[2]);
+#pragma unroll
+          for (int i = 3; i < 15; i += 2) a[k] = max3(__float_as_uint(a[k]), x[i], x[i + 1]);
+          a[k] = fmaxf(a[k], __uint_as_float(x[15]));
+        }
+        float mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+        float* const meet = tops + sb * 2 * kTile;
+        meet[g * kTile + r] = mx;
+        row_sync();
+        mx = fmaxf(mx, meet[(g ^ 1) * kTile + r]);
+        const bool raise = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
+        const float scale = raise ? fast_exp2(m - mx) : 1.f;  // 0 while nothing is accumulated
+        m = raise ? mx : m;
+        l *= scale;
+        // ---- p, its sum, and P in fp16 over its own scores --------------------------------
+        const float mu = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        auto store_p = [&](const uint32_t(&s)[32], uint32_t at) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+            add2(x0, x1, mu, mu);
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x0, x1);
+            const __half2 h = __floats2half2_rn(x0, x1);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(at, w);
+        };
+        store_p(s0, col_s);
+        store_p(s1, col_s + 32);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (j > 0) {
+          // The values of block - 1 (they ran beside this softmax) are waited for in every
+          // block, so each phase of o_full is met once, in order.
+          ok = wait(o_full, (blocks - 1) & 1u);
+          if (!ok) break;
+          if (__any_sync(kAll, raise)) {  // O follows the maximum
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
+              tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
             }
           }
-          fwht64(x);
-          __syncwarp();
-          uint32_t hi[32], lo[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) split_half2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
-          tmem_st32(tmem + lanes + kColQ + 32 * h, hi);
-          tmem_st32(tmem + lanes + kColQ + 64 + 32 * h, lo);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-
-        const int pos = live ? u.s.base + i0 + r / G : -1;
-        const int first_pos = u.s.base + i0, last_pos = u.s.base + min(i0 + p.tile_tok, u.s.n) - 1;
-        for (int j = 0; j < nblk; ++j, ++blocks) {
-          const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb;
-          ok = wait(s_full + sb, (blocks >> 1) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const int t0 = u.k.block(u.blk0 + j) * kTile;
-          uint32_t seen[4];
-          bool whole = t0 + kTile - 1 <= first_pos && (p.window == 0 || t0 > last_pos - p.window || t0 + kTile <= p.sinks);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            seen[i] = masks[(blocks % kMasks) * 4 + i];
-            whole = whole && seen[i] == kAll;
-          }
-          auto mask = [&](uint32_t(&s)[32], int c) {  // columns 32 c .. 32 c + 31
-            // (tokens past the sequence's end are not in `seen`)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int t = t0 + 32 * c + i;
-              const bool see = (seen[c] >> i & 1u) && t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
-              if (!see) s[i] = __float_as_uint(-INFINITY);
-            }
-          };
-          auto top = [&](const uint32_t(&s)[32]) {
-            float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
-#pragma unroll
-            for (int i = 2; i < 32; i += 2) {
-              a = fmaxf(a, __uint_as_float(s[i]));
-              b = fmaxf(b, __uint_as_float(s[i + 1]));
-            }
-            return fmaxf(a, b);
-          };
-          // ---- the row's maximum, then p; columns 64 .. 127 stay in registers between the two ----
-          uint32_t s0[32], s1[32];
-          tmem_ld32(col_s, s0);
-          tmem_ld32(col_s + 32, s1);
-          tmem_wait_ld();
-          if (!whole) {
-            mask(s0, 0);
-            mask(s1, 1);
-          }
-          float mx = fmaxf(top(s0), top(s1));
-          tmem_ld32(col_s + 64, s0);
-          tmem_ld32(col_s + 96, s1);
-          tmem_wait_ld();
-          if (!whole) {
-            mask(s0, 2);
-            mask(s1, 3);
-          }
-          mx = fmaxf(mx, fmaxf(top(s0), top(s1)));
-          const bool raise = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
-          const float scale = raise ? fast_exp2(m - mx) : 1.f;  // 0 while nothing is accumulated
-          m = raise ? mx : m;
-          l *= scale;
-          const float mu = m == -INFINITY ? 0.f : m;
-          float sum0 = 0.f, sum1 = 0.f;
-          auto store_p = [&](const uint32_t(&s)[32], int c) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = fast_exp2(__uint_as_float(s[2 * i]) - mu), b = fast_exp2(__uint_as_float(s[2 * i + 1]) - mu);
-              sum0 += a;
-              sum1 += b;
-              const __half2 h = __floats2half2_rn(a, b);
-              w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            tmem_st16(col_s + 32 * c, w);  // over its own scores
-          };
-          store_p(s0, 2);
-          store_p(s1, 3);
-          tmem_ld32(col_s, s0);
-          tmem_ld32(col_s + 32, s1);
-          tmem_wait_ld();
-          if (!whole) {
-            mask(s0, 0);
-            mask(s1, 1);
-          }
-          store_p(s0, 0);
-          store_p(s1, 1);
-          l += sum0 + sum1;
-          if (j > 0) {
-            // The values of block - 1 (they ran beside this softmax) are waited for in every
-            // block, so each phase of o_full is met once, in order.
-            ok = wait(o_full, (blocks - 1) & 1u);
-            if (!ok) break;
-            if (__any_sync(kAll, raise)) {  // O follows the maximum
-              tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                tmem_ld32(tmem + lanes + kColO + 32 * c, s0);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
-                tmem_st32(tmem + lanes + kColO + 32 * c, s0);
-              }
-            }
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + sb);
-        }
-        if (!ok) break;
-        ok = wait(o_full, (blocks - 1) & 1u);
-        if (!ok) break;
-        tc_fence_after();
+        if (lane == 0) mbar_arrive(p_full + sb);
       }
+      if (!ok) break;
+      ok = wait(o_full, (blocks - 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
       // ---- the piece's rows: to `out`, or as a partial to the workspace --------------------
+      float* const sums = tops + (blocks & 1u) * 2 * kTile;  // (not the last block's maxima)
+      sums[g * kTile + r] = l;
+      row_sync();
+      l = sums[r] + sums[kTile + r];  // (the same order in both threads)
       const float f = u.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const long long at = static_cast<long long>(u.slot) * kTile + r;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 2 * g; c < 2 * g + 2; ++c) {
         uint32_t s[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = 0u;
-        if (nblk > 0) {
-          tmem_ld32(tmem + lanes + kColO + 32 * c, s);
-          tmem_wait_ld();
-        }
+        tmem_ld32(tmem + lanes + kColO + 32 * c, s);
+        tmem_wait_ld();
         if (live && u.slot >= 0) {
           uint4* dst = reinterpret_cast<uint4*>(p.ws_o + at * kHeadDim + 32 * c);
 #pragma unroll
@@ -415,86 +477,101 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         }
         __syncwarp();
       }
-      if (u.slot >= 0) {
-        if (live) p.ws_ml[at] = make_float2(m, l);
-        if ((u.slot & 1) && tid == 0) {
-          write_record(p, &u);
-          recorded = true;
-        }
-      }
+      if (u.slot >= 0 && live && g == 0) p.ws_ml[at] = make_float2(m, l);
+      row_sync();         // `sums` is free again
       tc_fence_before();  // (O's reads, before the next piece's arrival on q_full)
     }
-    if (tid == 0 && !recorded) write_record(p, nullptr);
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
-    const int w = warp - kSoftWarps, half = w & 1, tok = 32 * (w >> 1) + lane;
+    reg_dec<kCodeRegs>();
+    const int w = warp - kSoftWarps, half = w & 1, quarter = w >> 1;
+    const int tok = 32 * quarter + lane;
     const uint32_t rep = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
     const uint32_t lane_k = W::kWideCodes ? 0u : rep;
     const uint32_t lane_v = W::kWideCodes ? 65536u : W::kSplitTable ? 32768u + rep_v : 128u + rep_v;
     constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
-    const uint32_t dst = smem_addr(tiles) + half * (kTileBytes / 2) + tok * 128;
-    const uint32_t sw = tok & 7;
+    const uint32_t dst = smem_addr(tiles) + half * (kTileBytes / 2) + tok * 128 + ((tok & 7) << 4);  // (piece 0, swizzled)
     auto store = [&](uint32_t at, int c, uint4 v) {
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((c ^ sw) << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
     };
     // Block iterator, two blocks ahead of the tiles: the thread's page; then its codes one ahead.
+    // The token's page and offset follow from the block before, by 128 tokens, where blocks adjoin.
+    const int step_page = kTile / p.page_size, step_off = kTile - step_page * p.page_size;
     bool more = true;
-    int i = 0;
+    int i = 0, t = 0, lp = 0, off = 0;
     u.blk1 = 0;
+    u.sink = -1;
     struct Where {
       int page, off, kvh;
       bool in, any;  // the token exists; the block exists
     };
     auto advance = [&]() {
       Where x = {0, 0, 0, false, false};
+      bool jump = i == u.sink;
       while (more && i >= u.blk1) {
-        more = walk.next(u);
+        more = next_piece(u);
         i = more ? u.blk0 : 0;
+        jump = true;
       }
       if (!more) return x;
-      const int t = u.k.block(i++) * kTile + tok;
-      x.any = true;
-      x.in = t < u.s.limit;
-      x.kvh = u.kvh;
-      if (x.in) {
-        const int lp = t / p.page_size;
-        x.off = t - lp * p.page_size;
-        x.page = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + lp);
+      if (jump) {
+        t = u.block(i) * kTile + tok;
+        lp = t / p.page_size;
+        off = t - lp * p.page_size;
+      } else {
+        t += kTile;
+        lp += step_page;
+        off += step_off;
+        if (off >= p.page_size) {
+          off -= p.page_size;
+          ++lp;
+        }
       }
+      ++i;
+      x.any = true;
+      x.in = t < u.limit;
+      x.kvh = u.kvh;
+      x.off = off;
+      if (x.in) x.page = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + lp);
       return x;
     };
-    HalfCodes<DK, BK> kc;
-    HalfCodes<DV, BV> vc, vc_prev;
-    bool has = false, has_prev = false;  // the token can be read
-    auto fetch = [&](const Where& x, HalfCodes<DK, BK>& k, HalfCodes<DV, BV>& v) {
-      bool good = x.in && x.page >= 0 && x.page < p.num_pages;
-      if (x.in && !good) report(p.status, kDevBadPage);
-      if (good) {
-        const long long row = (static_cast<long long>(x.page) * p.hkv + x.kvh) * p.page_size + x.off;
-        k.load(p.k_pool + row * KROW, half);
-        v.load(p.v_pool + row * VROW, half);
-      }
-      return good;
+    struct Codes {
+      HalfCodes<DK, BK> k;
+      HalfCodes<DV, BV> v;
+      bool has;  // the token can be read
     };
-    Where now = advance(), ahead = advance();
-    if (now.any) has = fetch(now, kc, vc);
-    bool any = now.any, any_prev = false;
+    auto fetch = [&](const Where& x, Codes& y) {
+      y.has = x.in && x.page >= 0 && x.page < p.num_pages;
+      if (x.in && !y.has) report(p.status, kDevBadPage);
+      if (y.has) {
+        const long long row = (static_cast<long long>(x.page) * p.hkv + x.kvh) * p.page_size + x.off;
+        y.k.load(p.k_pool + row * KROW, half);
+        y.v.load(p.v_pool + row * VROW, half);
+      }
+    };
+    Codes now, next;
+    HalfCodes<DV, BV> v_prev;
+    bool has_prev = false, any_prev = false;
+    const Where first = advance();
+    Where ahead = advance();
+    bool any = first.any;
+    now.has = next.has = false;
+    if (any) fetch(first, now);
     Ring rk, rv;
     uint32_t blocks = 0;
     while (any || any_prev) {
-      HalfCodes<DK, BK> kn;
-      HalfCodes<DV, BV> vn;
-      const Where next = ahead;
+      const Where then = ahead;
       ahead = advance();
-      const bool has_n = next.any && fetch(next, kn, vn);
+      next.has = false;
+      if (then.any) fetch(then, next);
       if (any) {
         if (!wait(k_empty + rk.slot, rk.phase ^ 1u)) break;
         const uint32_t at = dst + rk.slot * kTileBytes;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) store(at, c, has ? gather_piece<DK, BK, kShift>(kc, c, lane_k) : make_uint4(0, 0, 0, 0));
-        const uint32_t seen = __ballot_sync(kAll, has);
-        if (half == 0 && lane == 0) masks[(blocks % kMasks) * 4 + (w >> 1)] = seen;
+        for (int c = 0; c < 8; ++c) store(at, c, now.has ? gather_piece<DK, BK, kShift>(now.k, c, lane_k) : make_uint4(0, 0, 0, 0));
+        const uint32_t seen = __ballot_sync(kAll, now.has);
+        if (half == 0 && lane == 0) masks[(blocks % kMasks) * 4 + quarter] = seen;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + rk.slot);
@@ -506,70 +583,127 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         const uint32_t at = dst + (kKStages + rv.slot) * kTileBytes;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          store(at, c, has_prev ? gather_piece<DV, BV, kShift>(vc_prev, c, lane_v) : make_uint4(0, 0, 0, 0));
+          store(at, c, has_prev ? gather_piece<DV, BV, kShift>(v_prev, c, lane_v) : make_uint4(0, 0, 0, 0));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full + rv.slot);
         rv.next(NV);
       }
-      vc_prev = vc;
-      has_prev = has;
+      v_prev = now.v;
+      has_prev = now.has;
       any_prev = any;
-      kc = kn;
-      vc = vn;
-      has = has_n;
-      any = next.any;
+      now = next;
+      any = then.any;
     }
-  } else if (lane == 0) {
+  } else {
     // ================================= the products ====================================
-    constexpr uint32_t kScores = tc_idesc(kTile, kTile, false), kValues = tc_idesc(kTile, kHeadDim, true);
-    const uint32_t tile0 = smem_addr(tiles);
-    Ring rk, rv;
-    uint32_t blocks = 0, pieces = 0;
-    bool ok = true;
-    while (ok && walk.next(u)) {
-      const int nblk = u.blk1 - u.blk0;
-      if (nblk <= 0) continue;
-      ok = wait_one(q_full, pieces++ & 1u);
-      for (int j = 0; ok && j <= nblk; ++j) {
-        if (j < nblk) {  // scores of block j
-          const uint32_t sb = (blocks + j) & 1u;
-          if (!(ok = wait_one(k_full + rk.slot, rk.phase))) break;
-          tc_fence_after();
-          const uint32_t kt = tile0 + rk.slot * kTileBytes;
+    reg_dec<kIssueRegs>();
+    if (warp == kSoftWarps + kCodeWarps) {
+      constexpr uint32_t kScores = tc_idesc(kTile, kTile, false), kValues = tc_idesc(kTile, kHeadDim, true);
+      const uint32_t tile0 = smem_addr(tiles);
+      Ring rk, rv;
+      uint32_t blocks = 0, tiles_done = 0;
+      bool ok = true;
+      while (ok && next_piece(u)) {
+        const int nblk = u.blk1 - u.blk0;
+        ok = wait(q_full, tiles_done++ & 1u);
+        for (int j = 0; ok && j <= nblk; ++j) {
+          if (j < nblk) {  // scores of block j
+            const uint32_t sb = (blocks + j) & 1u;
+            if (!(ok = wait(k_full + rk.slot, rk.phase))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t kt = tile0 + rk.slot * kTileBytes;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)  // high and low part of q~
+              for (int part = 0; part < 2; ++part)  // high and low part of q~
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              tc_mma_ts(tmem + kColS + 128 * sb, tmem + kColQ + 64 * part + 8 * ks,
-                        tc_desc(kt + (ks >> 2) * (kTileBytes / 2) + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
-          tc_commit(s_full + sb);
-          mbar_arrive(s_full + sb);
-          tc_commit(k_empty + rk.slot);
-          rk.next(kKStages);
+                for (int ks = 0; ks < 8; ++ks)
+                  tc_mma_ts(tmem + kColS + 128 * sb, tmem + kColQ + 64 * part + 8 * ks,
+                            tc_desc(kt + (ks >> 2) * (kTileBytes / 2) + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
+              tc_commit(s_full + sb);
+              mbar_arrive(s_full + sb);
+              tc_commit(k_empty + rk.slot);
+            }
+            __syncwarp();
+            rk.next(kKStages);
+          }
+          if (j > 0) {  // values of block j - 1
+            const uint32_t blk = blocks + j - 1, sb = blk & 1u;
+            if (!(ok = wait(v_full + rv.slot, rv.phase))) break;
+            if (!(ok = wait(p_full + sb, (blk >> 1) & 1u))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vt = tile0 + (kKStages + rv.slot) * kTileBytes;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
+                tc_mma_ts(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
+                          tc_desc(vt + ks * 2048, kTileBytes / 2), kValues, j > 1 || ks > 0);
+              tc_commit(v_empty + rv.slot);
+              tc_commit(o_full);
+            }
+            __syncwarp();
+            rv.next(NV);
+          }
         }
-        if (j > 0) {  // values of block j - 1
-          const uint32_t blk = blocks + j - 1, sb = blk & 1u;
-          if (!(ok = wait_one(p_full + sb, (blk >> 1) & 1u))) break;
-          if (!(ok = wait_one(v_full + rv.slot, rv.phase))) break;
-          tc_fence_after();
-          const uint32_t vt = tile0 + (kKStages + rv.slot) * kTileBytes;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
-            tc_mma_ts(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
-                      tc_desc(vt + ks * 2048, kTileBytes / 2), kValues, j > 1 || ks > 0);
-          tc_commit(v_empty + rv.slot);
-          tc_commit(o_full);
-          rv.next(NV);
-        }
+        blocks += nblk;
       }
-      blocks += nblk;
-    }
-    if (!ok) {  // given up: the products in flight end before the tensor memory goes back
-      tc_commit(drain);
+      // (given up or not) the products in flight end before the tensor memory goes back
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < p.timeout_ns) {
       }
+    } else if (warp == kSoftWarps + kCodeWarps + 1) {
+      // ================================== planning =======================================
+      ChunkWalk<kTile> walk(p, pre);  // (the tiles over the plan wait for the first piece)
+      ChunkPiece q;
+      Ring ro;
+      bool recorded = false;
+      for (bool more = true; more;) {
+        more = walk.next(q);
+        const int i0 = q.tile * p.tile_tok, n = more ? min(p.tile_tok, q.s.n - i0) : 0;
+        if (more && q.slot >= 0 && (q.slot & 1)) {
+          if (lane == 0) write_record(p, &q);
+          recorded = true;
+        }
+        if (more && q.blk0 >= q.blk1) {  // rows that see nothing here: zero, or an empty partial
+          for (int r = 0; r < n * p.group; ++r) {
+            if (q.slot >= 0) {
+              const long long at = static_cast<long long>(q.slot) * kTile + r;
+              reinterpret_cast<float4*>(p.ws_o + at * kHeadDim)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (lane == 0) p.ws_ml[at] = make_float2(-INFINITY, 0.f);
+            } else {
+              const long long row = static_cast<long long>(q.s.row0 + i0 + r / p.group) * p.hq + q.kvh * p.group + r % p.group;
+              reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row * kHeadDim)[lane] = make_uint2(0, 0);
+            }
+          }
+          continue;
+        }
+        if (!wait(piece_empty + ro.slot, ro.phase ^ 1u)) break;
+        if (lane == 0) {
+          WidePiece w = {};
+          w.more = more;
+          if (more) {
+            w.b = q.b;
+            w.kvh = q.kvh;
+            w.row0 = q.s.row0 + i0;
+            w.rows = n * p.group;
+            w.first_pos = q.s.base + i0;
+            w.last_pos = q.s.base + i0 + n - 1;
+            w.limit = q.s.limit;
+            w.sink = q.k.sink;
+            w.lo = q.k.lo;
+            w.blk0 = q.blk0;
+            w.blk1 = q.blk1;
+            w.slot = q.slot;
+          }
+          pieces[ro.slot] = w;
+          mbar_arrive(piece_full + ro.slot);
+        }
+        __syncwarp();
+        ro.next(kPieces);
+      }
+      if (!recorded && lane == 0) write_record(p, nullptr);
     }
   }
   tc_fence_before();
