@@ -562,50 +562,53 @@ def decode_step(layout: vq_layout, q, k_new, v_new, lambda_, codebook_k, codeboo
 # ------------------------------------------------- torch layer: serving step ---
 # These calls run on the device of their tensors whatever the current one is, and
 # make the outputs and workspaces that they are not given on the stream they run on.
+# A decode step's calls take a few microseconds on the GPU, so the checks keep a
+# short path: one comparison per property, and errors are told apart only on failure.
 
-class _Launch:
-    """Device and stream of one call: enters the tensors' device and, where `stream` is given,
-    that stream, so that what the call allocates belongs to it."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        self.ctx = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return _torch().cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+def _launch(device, stream, call):
+    """call(raw stream) on `device` and `stream` (None: the device's current one); where either
+    is not the current one it is entered first, so that what `call` allocates belongs to it."""
+    torch = _torch()
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch's own short form
+        return call(raw(index) if raw else torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _arg(t, dtype, name, device, shape=None):
     """data_ptr of a tensor argument (contiguous, of this type and shape, on this device)."""
-    if t is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return _dev_ptr(t, dtype, name, shape)
+    if t is None:
+        return None
+    if not (hasattr(t, "data_ptr") and t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        _dev_ptr(t, dtype, name, shape)  # raises for all but the device
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _need(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.device
 
 
 def alloc_chunk_workspace(layout: vq_layout, batch: int, num_tokens: int, max_seq_len: int,
                           max_new_len: int, device="cuda"):
     torch = _torch()
-    device = torch.device(device)
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            n = vq_chunk_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len)
-    else:
+    with torch.cuda.device(device):
         n = vq_chunk_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len)
-    if n == 0:
-        raise VQError(VQ_ERR_INVALID_ARG, "cannot size the workspace")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+        if n == 0:
+            raise VQError(VQ_ERR_INVALID_ARG, "cannot size the workspace")
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
 
 
 def chunk_attention(layout: vq_layout, q, lambda_, codebook_k, codebook_v, k_pool, v_pool,
@@ -616,34 +619,36 @@ def chunk_attention(layout: vq_layout, q, lambda_, codebook_k, codebook_v, k_poo
     pools, causal; row offsets cu_new_lens int32 [B + 1] (None: one row per sequence).  With
     `window` a row sees that many last tokens and the first `num_sinks` (see vq_chunk_attention)."""
     torch = _torch()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
+    dev = _need(q, "q")
     f16, i32, u8 = torch.float16, torch.int32, torch.uint8
-    T, D, H, dev, P = q.shape[0], layout.head_dim, layout.num_kv_heads, q.device, layout.page_size
-    B = seq_lens.shape[0]
+    T, B, pages = q.shape[0], seq_lens.shape[0], k_pool.shape[0]
+    L = layout
+    D, H, P = L.head_dim, L.num_kv_heads, L.page_size
+    rows = (T, L.num_q_heads, D)
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B][max_pages]")
-    kr, vr = row_bytes(layout)
-    pages = k_pool.shape[0]
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, layout.num_q_heads, D), dtype=f16, device=dev)
-        if workspace is None:
-            workspace = alloc_chunk_workspace(layout, B, T, max_seq_len, max_new_len, dev)
-        vq_chunk_attention(
-            layout, B, T, _arg(q, f16, "q", dev, (T, layout.num_q_heads, D)),
-            _arg(lambda_, torch.float32, "lambda", dev, (H, D)),
-            _arg(codebook_k, f16, "codebook_k", dev, (1 << layout.k_bits, layout.k_sub)),
-            _arg(codebook_v, f16, "codebook_v", dev, (1 << layout.v_bits, layout.v_sub)),
-            _arg(k_pool, u8, "k_pool", dev, (pages, H, P, kr)),
-            _arg(v_pool, u8, "v_pool", dev, (pages, H, P, vr)), pages,
-            _arg(page_table, i32, "page_table", dev, (B, page_table.shape[1])),
-            page_table.shape[1], _arg(seq_lens, i32, "seq_lens", dev, (B,)), max_seq_len,
+    width = page_table.shape[1]
+    args = (_arg(q, f16, "q", dev, rows), _arg(lambda_, torch.float32, "lambda", dev, (H, D)),
+            _arg(codebook_k, f16, "codebook_k", dev, (1 << L.k_bits, L.k_sub)),
+            _arg(codebook_v, f16, "codebook_v", dev, (1 << L.v_bits, L.v_sub)),
+            _arg(k_pool, u8, "k_pool", dev, (pages, H, P, (D // L.k_sub * L.k_bits + 31) // 32 * 4)),
+            _arg(v_pool, u8, "v_pool", dev, (pages, H, P, (D // L.v_sub * L.v_bits + 31) // 32 * 4)),
+            pages, _arg(page_table, i32, "page_table", dev, (B, width)), width,
+            _arg(seq_lens, i32, "seq_lens", dev, (B,)), max_seq_len,
             _arg(cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)), max_new_len, window, num_sinks,
-            softmax_scale, _arg(out, f16, "out", dev, (T, layout.num_q_heads, D)),
-            _arg(workspace, u8, "workspace", dev), workspace.numel(),
-            _arg(status, i32, "status", dev, (1,)), st)
-    return out
+            softmax_scale)
+
+    def call(st):
+        o = torch.empty(rows, dtype=f16, device=dev) if out is None else out
+        w = workspace
+        if w is None:
+            w = alloc_chunk_workspace(layout, B, T, max_seq_len, max_new_len, dev)
+        _check(lib().vq_chunk_attention(ctypes.byref(layout), B, T, *args, _arg(o, f16, "out", dev, rows),
+                                        _arg(w, u8, "workspace", dev), w.numel(),
+                                        _arg(status, i32, "status", dev, (1,)), st))
+        return o
+
+    return _launch(dev, stream, call)
 
 
 class AppendedSlots(NamedTuple):
@@ -661,47 +666,49 @@ def append_slots(seq_lens, new_lens, page_table, free_pages, num_free, page_size
     """Page tables, slots, positions and row offsets of one step (see vq_append_slots):
     page_table [B][max_pages] is extended in place with pages off the free stack."""
     torch = _torch()
-    if not isinstance(seq_lens, torch.Tensor) or not seq_lens.is_cuda:
-        raise TypeError("seq_lens must be a CUDA tensor")
-    B, dev, i32 = seq_lens.shape[0], seq_lens.device, torch.int32
+    dev, i32, i64 = _need(seq_lens, "seq_lens"), torch.int32, torch.int64
+    B = seq_lens.shape[0]
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B][max_pages]")
-    with _Launch(dev, stream) as st:
-        new = lambda t, n, dt: torch.empty(n, dtype=dt, device=dev) if t is None else t  # noqa: E731
-        r = AppendedSlots(new(seq_lens_out, B, i32), new(num_free_out, 1, i32),
-                          new(cu_new_lens, B + 1, i32), new(slot_mapping, max_tokens, torch.int64),
-                          new(positions, max_tokens, i32))
-        vq_append_slots(B, _arg(seq_lens, i32, "seq_lens", dev, (B,)),
-                        _arg(new_lens, i32, "new_lens", dev, (B,)),
-                        _arg(page_table, i32, "page_table", dev, (B, page_table.shape[1])),
-                        page_table.shape[1],
-                        _arg(free_pages, i32, "free_pages", dev, (free_pages.numel(),)),
-                        free_pages.numel(), _arg(num_free, i32, "num_free", dev, (1,)), page_size,
-                        num_pages, max_tokens, _arg(r.seq_lens, i32, "seq_lens_out", dev, (B,)),
-                        _arg(r.num_free, i32, "num_free_out", dev, (1,)),
-                        _arg(r.cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)),
-                        _arg(r.slot_mapping, torch.int64, "slot_mapping", dev, (max_tokens,)),
-                        _arg(r.positions, i32, "positions", dev, (max_tokens,)),
-                        _arg(status, i32, "status", dev, (1,)), st)
-    return r
+    width, free = page_table.shape[1], free_pages.numel()
+    args = (_arg(seq_lens, i32, "seq_lens", dev, (B,)), _arg(new_lens, i32, "new_lens", dev, (B,)),
+            _arg(page_table, i32, "page_table", dev, (B, width)), width,
+            _arg(free_pages, i32, "free_pages", dev, (free,)), free,
+            _arg(num_free, i32, "num_free", dev, (1,)), page_size, num_pages, max_tokens)
+
+    def call(st):
+        empty = torch.empty
+        r = AppendedSlots(empty(B, dtype=i32, device=dev) if seq_lens_out is None else seq_lens_out,
+                          empty(1, dtype=i32, device=dev) if num_free_out is None else num_free_out,
+                          empty(B + 1, dtype=i32, device=dev) if cu_new_lens is None else cu_new_lens,
+                          empty(max_tokens, dtype=i64, device=dev) if slot_mapping is None else slot_mapping,
+                          empty(max_tokens, dtype=i32, device=dev) if positions is None else positions)
+        _check(lib().vq_append_slots(B, *args, _arg(r[0], i32, "seq_lens_out", dev, (B,)),
+                                     _arg(r[1], i32, "num_free_out", dev, (1,)),
+                                     _arg(r[2], i32, "cu_new_lens", dev, (B + 1,)),
+                                     _arg(r[3], i64, "slot_mapping", dev, (max_tokens,)),
+                                     _arg(r[4], i32, "positions", dev, (max_tokens,)),
+                                     _arg(status, i32, "status", dev, (1,)), st))
+        return r
+
+    return _launch(dev, stream, call)
 
 
 def _rows_arg(t, dtype, name, device, tokens, head_dim):
-    """(data_ptr, token stride) of [T][heads][D] rows whose heads are contiguous."""
+    """(data_ptr, token stride, heads) of [T][heads][D] rows whose heads are contiguous."""
     if t is None:
-        return None, 0
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device != device:
+        return None, 0, 0
+    if _need(t, name) != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != head_dim:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({tokens}, heads, {head_dim})")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim)):
+    heads = t.shape[1]
+    s0, s1, s2 = t.stride()
+    if tokens and heads and (s2 != 1 or (heads > 1 and s1 != head_dim)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if tokens > 1 else max(t.shape[1] * head_dim, 8)
+    return t.data_ptr(), s0 if tokens > 1 else heads * head_dim, heads
 
 
 def rotary(config: vq_rotary_config, positions, q=None, k=None, v=None, q_out=None, k_out=None,
@@ -713,25 +720,34 @@ def rotary(config: vq_rotary_config, positions, q=None, k=None, v=None, q_out=No
     some = q if q is not None else k if k is not None else v
     if some is None:
         raise ValueError("q, k and v are all None")
-    if some.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"q, k and v must be float16 or bfloat16, got {some.dtype}")
-    T, D, dev = positions.shape[0], config.head_dim, some.device
-    if k is not None and v is not None and k.shape[1] != v.shape[1]:
+    dt, f16, dev = some.dtype, torch.float16, _need(some, "q, k or v")
+    if dt is not f16 and dt is not torch.bfloat16:
+        raise TypeError(f"q, k and v must be float16 or bfloat16, got {dt}")
+    T, D = positions.shape[0], config.head_dim
+    qp, qs, qh = _rows_arg(q, dt, "q", dev, T, D)
+    kp, ks, kh = _rows_arg(k, dt, "k", dev, T, D)
+    vp, vs, vh = _rows_arg(v, dt, "v", dev, T, D)
+    if k is not None and v is not None and kh != vh:
         raise ValueError("k and v have different numbers of heads")
-    with _Launch(dev, stream) as st:
-        a, out = [], []
-        for x, o, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
-            a.append(_rows_arg(x, some.dtype, name, dev, T, D))
-            if x is not None and o is None:
-                o = torch.empty((T, x.shape[1], D), dtype=torch.float16, device=dev)
-            elif x is None and o is not None:
-                raise ValueError(f"{name}_out is given without {name}")
-            out.append(o)
-        kv = k if k is not None else v
-        ptr = [None if o is None else _arg(o, torch.float16, n, dev, (T, x.shape[1], D))
-               for o, x, n in zip(out, (q, k, v), ("q_out", "k_out", "v_out"))]
-        vq_rotary(config, T, _arg(positions, torch.int32, "positions", dev, (T,)),
-                  VQ_BF16 if some.dtype == torch.bfloat16 else VQ_FP16, a[0][0], a[0][1],
-                  0 if q is None else q.shape[1], ptr[0], a[1][0], a[1][1], a[2][0], a[2][1],
-                  0 if kv is None else kv.shape[1], ptr[1], ptr[2], st)
-    return tuple(out)
+    for x, o, name in ((q, q_out, "q"), (k, k_out, "k"), (v, v_out, "v")):
+        if x is None and o is not None:
+            raise ValueError(f"{name}_out is given without {name}")
+    pos = _arg(positions, torch.int32, "positions", dev, (T,))
+
+    def call(st):
+        def make(x, o, heads, name):
+            if x is None:
+                return None, None
+            shape = (T, heads, D)
+            if o is None:
+                o = torch.empty(shape, dtype=f16, device=dev)
+                return o, o.data_ptr()
+            return o, _arg(o, f16, name, dev, shape)
+        qo, qop = make(q, q_out, qh, "q_out")
+        ko, kop = make(k, k_out, kh, "k_out")
+        vo, vop = make(v, v_out, vh, "v_out")
+        _check(lib().vq_rotary(ctypes.byref(config), T, pos, VQ_FP16 if dt is f16 else VQ_BF16, qp, qs, qh,
+                               qop, kp, ks, vp, vs, kh or vh, kop, vop, st))
+        return qo, ko, vo
+
+    return _launch(dev, stream, call)
