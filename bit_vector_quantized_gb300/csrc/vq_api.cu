@@ -1200,6 +1200,9 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.hkv = L.num_kv_heads;
   p.group = L.num_q_heads / L.num_kv_heads;
   p.page_size = L.page_size;
+  p.page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (L.page_size == 1 << i) p.page_shift = i;
   p.max_pages = max_pages_per_seq;
   p.max_seq_len = max_seq_len;
   p.max_new_len = max_new_len;

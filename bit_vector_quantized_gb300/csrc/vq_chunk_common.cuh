@@ -98,17 +98,16 @@ struct ChunkPiece {
   int last_cta;    // the CTA that ends the tile (slot 2c + 1 only)
 };
 
-// Walks the pieces of this CTA's range; every thread holds the same state.
+// Walks the pieces of this CTA's range (one thread does, for all).
 template <int CW>
 struct ChunkWalk {
-  const ChunkParams& p;
-  const long long* pre;  // [B + 1] estimated length of the sequences before b, all KV heads
   long long x, x1, W;    // position, end of the range, range per CTA
   long long tile_x;      // where the current tile begins
   int b, kvh, tile, tiles;
   ChunkSeq s;
 
-  __device__ __forceinline__ ChunkWalk(const ChunkParams& p_, const long long* pre_) : p(p_), pre(pre_) {
+  // pre: [B + 1] estimated length of the sequences before b, all KV heads
+  __device__ __forceinline__ void start(const ChunkParams& p, const long long* pre) {
     const long long total = pre[p.batch];
     W = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(p.min_range));
     x = min(W * blockIdx.x, total);
@@ -138,7 +137,7 @@ struct ChunkWalk {
   }
 
   // The next piece; false when the range is done.
-  __device__ __forceinline__ bool next(ChunkPiece& q) {
+  __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPiece& q) {
     if (x >= x1) return false;
     const long long w = chunk_sum(p, s, tile + 1) - chunk_sum(p, s, tile);
     const long long o0 = x - tile_x, o1 = min(w, o0 + (x1 - x));

@@ -6,21 +6,25 @@
 //   q~ = q diag(lambda) H_D,  s_p = q~ . VQ^-1(K~_p) * scale over the visible p,
 //   o = softmax(s) VQ^-1(V).
 //
-// A tile is 8 or 16 query rows.  Each warp takes every kWarps-th 16-token block
-// of the tile's keys and keeps its own online softmax (running maximum, sum
-// and 128-wide output); the warps join at the end of the piece.  Both
-// products are m16n8k16 warp mma with the query rows as rows and centroids
-// gathered from shared memory straight into the other operand:
-//   scores: the operand column of lane (g, c) = (lane / 4, lane % 4) is token
-//     g, its k-step j the dims 32c + 4j .. 32c + 4j + 3, one 8-byte gather;
-//   values: column g of output block nb is dim 16g + nb; the lane gathers the
-//     centroids of its four tokens (2c, 2c + 1, 2c + 8, 2c + 9) and pairs
-//     their elements, so a gather serves four blocks.
-// With 8 rows, rows 0..7 hold the high and rows 8..15 the low fp16 part of q~
-// and of p, and the two halves of each accumulator are added: both products
-// keep about fp32 accuracy at no extra mma.  With 16 rows q~ takes two mma
-// (high, low) and p is rounded to fp16 once (p <= 2^8: relative 2^-11, which
-// averages out over a row's tokens).  Sums and maxima are fp32.
+// Each warp takes every n-th 16-token block of a tile's keys and keeps its own
+// online softmax (running maximum, sum and 128-wide output); the warps join at
+// the end of the piece.  Both products are m16n8k16 warp mma, with centroids
+// gathered from the replicated, bank-conflict-free table straight into one
+// operand.  Two kernels:
+//
+//   * 8 rows and fewer (single decode tokens, a few drafted ones): tokens as
+//     rows, scores^T [16 tok x 8] = K~ q~^T and o^T [128 x 8] += V^T p^T, the
+//     form with the fewest products (16 or 24 per block) and registers (32 of
+//     output), so 16 warps share an SM and hide the latency of the codes.
+//     With 4 rows and fewer, columns 2h and 2h + 1 hold the high and low fp16
+//     parts of q~ and of p, and both products keep about fp32 accuracy.
+//   * up to 16 rows: the query rows as rows, the centroids as columns; a
+//     gather of a V centroid serves four output blocks.
+//
+// q~ is split into high and low fp16 parts everywhere (scores keep about fp32
+// accuracy); p is rounded to fp16 once where it is not split (p <= 2^8:
+// relative 2^-11, which averages out over a row's tokens).  Sums and maxima
+// are fp32.
 #include "vq_chunk_common.cuh"
 #include "vq_gather.cuh"
 
@@ -29,7 +33,8 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;    // the running maximum may lag by this much (log2 units): p <= 2^8
-constexpr int kNarrowWarps = 8;
+constexpr int kNarrowWarps = 8;  // of the 16-row kernel
+constexpr int kFewWarps = 16;    // of the kernel for 8 rows and fewer
 constexpr int kBlock = 16;       // tokens per block
 constexpr int kQStride = 132;    // halves between q~ rows in shared memory
 
@@ -72,36 +77,94 @@ __device__ __forceinline__ void fill_table(const ChunkParams& p) {
   }
 }
 
+// Shared memory of both kernels before q~ and the join buffers.
+struct NarrowHead {
+  long long pre[kChunkMaxBatch + 1];
+  long long scratch[33];
+  ChunkWalk<kBlock> walk;  // thread 0's
+  ChunkPiece piece[2];     // the piece under way and the next one
+  int more[2];
+};
+static_assert(sizeof(NarrowHead) % 8 == 0, "what follows is aligned by hand");
+constexpr size_t kHeadBytes = (sizeof(NarrowHead) + 15) / 16 * 16;
+
+// The next piece, into the buffer after piece k's.
+__device__ __forceinline__ void plan_next(const ChunkParams& p, NarrowHead* h, int k) {
+  h->more[k & 1] = h->walk.next(p, h->piece[k & 1]);
+}
+
 // Elements e of two fp16 pairs as one operand register: (a.e, b.e).
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
-// kRows: 8 (high and low parts share an mma) or 16.
-template <int DK, int BK, int DV, int BV, int kRows>
+// Row r of a piece from its warps' partials (one warp; mo [warps][rows][128], ml [warps][rows]): to
+// `out`, or as one partial to the workspace.
+template <int kWarps, int kRows>
+__device__ __forceinline__ void join_row(const ChunkParams& p, const ChunkPiece& u, const float* mo, const float2* ml, int r,
+                                         bool live, int slot_rows, int lane) {
+  if (!live) return;
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float Mu = M == -INFINITY ? 0.f : M;  // a row that sees nothing: sums of 0 (or of its NaN)
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float2 v = ml[w * kRows + r];
+    const float f = fast_exp2(v.x - Mu);
+    L = fmaf(f, v.y, L);
+    const float4 x = *reinterpret_cast<const float4*>(mo + (w * kRows + r) * kHeadDim + 4 * lane);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+  if (u.slot >= 0) {
+    const long long at = static_cast<long long>(u.slot) * slot_rows + r;
+    reinterpret_cast<float4*>(p.ws_o + at * kHeadDim)[lane] = acc;
+    if (lane == 0) p.ws_ml[at] = make_float2(M, L);
+  } else {
+    const float f = L == 0.f ? 0.f : 1.f / L;
+    const long long row = static_cast<long long>(u.s.row0 + u.tile * p.tile_tok + r / p.group) * p.hq + u.kvh * p.group + r % p.group;
+    const __half2 h0 = __floats2half2_rn(acc.x * f, acc.y * f), h1 = __floats2half2_rn(acc.z * f, acc.w * f);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t*>(&h0);
+    w.y = *reinterpret_cast<const uint32_t*>(&h1);
+    reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row * kHeadDim)[lane] = w;
+  }
+}
+
+// ---- up to 16 rows: the query rows as the rows of the products --------------------------------
+template <int DK, int BK, int DV, int BV>
 __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(const ChunkParams p) {
   using T = NarrowTable<DK, BK, DV, BV>;
-  constexpr bool kPacked = kRows == 8;
+  constexpr int kRows = 16;
   constexpr bool kWide = T::kWide;
   constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
   uint8_t* const sm = g_smem + T::kBytes;
-  long long* const pre = reinterpret_cast<long long*>(sm);                 // [kChunkMaxBatch + 1]
-  long long* const scratch = pre + kChunkMaxBatch + 1;                     // [32]
-  __half* const qs = reinterpret_cast<__half*>(scratch + 33);              // [2][kRows][kQStride] high, low
+  NarrowHead* const head = reinterpret_cast<NarrowHead*>(sm);
+  __half* const qs = reinterpret_cast<__half*>(sm + kHeadBytes);           // [2][kRows][kQStride] high, low
   float* const mo = reinterpret_cast<float*>(qs + 2 * kRows * kQStride);   // [warps][kRows][128]
   float2* const ml = reinterpret_cast<float2*>(mo + kNarrowWarps * kRows * kHeadDim);  // [warps][kRows]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_trigger();
   fill_table<DK, BK, DV, BV>(p);
-  chunk_plan(p, pre, scratch);
-  ChunkWalk<kBlock> walk(p, pre);
+  chunk_plan(p, head->pre, head->scratch);
+  if (tid == 0) {
+    head->walk.start(p, head->pre);
+    plan_next(p, head, 0);
+  }
+  __syncthreads();
   const uint32_t lwk = kWide ? 0u : DK == 4 ? (lane & 15) * 8 : lane * 4;
   const uint32_t lwv = kWide ? 65536u : 128u + (DV == 4 ? (lane & 15) * 8 : lane * 4);
   const int G = p.group;
   bool recorded = false;
 
-  ChunkPiece u;
-  while (walk.next(u)) {
+  for (int k = 0; head->more[k & 1]; ++k) {
+    const ChunkPiece& u = head->piece[k & 1];
+    const ChunkKeys keys = u.k;
+    const int blk1 = u.blk1, limit = u.s.limit;
     const int i0 = u.tile * p.tile_tok;
     const int rows = min(p.tile_tok, u.s.n - i0) * G;
     // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
@@ -126,27 +189,26 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
       *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
     }
     __syncthreads();
-    uint32_t qa[8][4], ql[kPacked ? 1 : 8][4];
+    if (tid == 0) plan_next(p, head, k + 1);
+    uint32_t qa[8][4], ql[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = 32 * c + 4 * j;
       const uint2 h0 = *reinterpret_cast<const uint2*>(qs + g * kQStride + e);
-      const uint2 h1 = *reinterpret_cast<const uint2*>(qs + (g + 8) * kQStride + e);  // kPacked: the low part of row g
+      const uint2 h1 = *reinterpret_cast<const uint2*>(qs + (g + 8) * kQStride + e);
       qa[j][0] = h0.x;
       qa[j][1] = h1.x;
       qa[j][2] = h0.y;
       qa[j][3] = h1.y;
-      if constexpr (!kPacked) {
-        const uint2 l0 = *reinterpret_cast<const uint2*>(qs + (kRows + g) * kQStride + e);
-        const uint2 l1 = *reinterpret_cast<const uint2*>(qs + (kRows + g + 8) * kQStride + e);
-        ql[j][0] = l0.x;
-        ql[j][1] = l1.x;
-        ql[j][2] = l0.y;
-        ql[j][3] = l1.y;
-      }
+      const uint2 l0 = *reinterpret_cast<const uint2*>(qs + (kRows + g) * kQStride + e);
+      const uint2 l1 = *reinterpret_cast<const uint2*>(qs + (kRows + g + 8) * kQStride + e);
+      ql[j][0] = l0.x;
+      ql[j][1] = l1.x;
+      ql[j][2] = l0.y;
+      ql[j][3] = l1.y;
     }
     // positions of the lane's rows g and g + 8 (rows past the tile see nothing)
-    constexpr int NR = kPacked ? 1 : 2;
+    constexpr int NR = 2;
     int pos[NR];
     float m[NR], l[NR];
 #pragma unroll
@@ -166,7 +228,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
     KCodes<DK> kc[2];
     VCodes<DV, BV> vc[4];
     auto load = [&](int i, KCodes<DK>(&kx)[2], VCodes<DV, BV>(&vx)[4]) {  // false: no such page
-      const int t0 = u.k.block(i) * kBlock;
+      const int t0 = keys.block(i) * kBlock;
       const int lp = t0 / p.page_size;
       const int pg = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + lp);
       if (pg < 0 || pg >= p.num_pages) {
@@ -185,13 +247,13 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
       return true;
     };
     bool have = false;
-    if (u.blk0 + warp < u.blk1) have = load(u.blk0 + warp, kc, vc);
-    for (int i = u.blk0 + warp; i < u.blk1; i += kNarrowWarps) {
+    if (u.blk0 + warp < blk1) have = load(u.blk0 + warp, kc, vc);
+    for (int i = u.blk0 + warp; i < blk1; i += kNarrowWarps) {
       KCodes<DK> kn[2];
       VCodes<DV, BV> vn[4];
       bool have_n = false;
-      if (i + kNarrowWarps < u.blk1) have_n = load(i + kNarrowWarps, kn, vn);
-      const int t0 = u.k.block(i) * kBlock;
+      if (i + kNarrowWarps < blk1) have_n = load(i + kNarrowWarps, kn, vn);
+      const int t0 = keys.block(i) * kBlock;
       if (have) {
         // ---- scores: s[nb][..]: row g (and g + 8), tokens 8 nb + 2c, 2c + 1 ----------
         float s[2][4];
@@ -214,18 +276,12 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
             }
             mma16816(s[nb], qa[j][0], qa[j][1], qa[j][2], qa[j][3], b[0], b[1]);
             mma16816(s[nb], qa[j + 1][0], qa[j + 1][1], qa[j + 1][2], qa[j + 1][3], b[2], b[3]);
-            if constexpr (!kPacked) {
-              mma16816(s[nb], ql[j][0], ql[j][1], ql[j][2], ql[j][3], b[0], b[1]);
-              mma16816(s[nb], ql[j + 1][0], ql[j + 1][1], ql[j + 1][2], ql[j + 1][3], b[2], b[3]);
-            }
-          }
-          if constexpr (kPacked) {
-            s[nb][0] += s[nb][2];
-            s[nb][1] += s[nb][3];
+            mma16816(s[nb], ql[j][0], ql[j][1], ql[j][2], ql[j][3], b[0], b[1]);
+            mma16816(s[nb], ql[j + 1][0], ql[j + 1][1], ql[j + 1][2], ql[j + 1][3], b[2], b[3]);
           }
         }
         // ---- masks --------------------------------------------------------------------
-        const bool whole = t0 + kBlock - 1 <= first_pos && t0 + kBlock <= u.s.limit &&
+        const bool whole = t0 + kBlock - 1 <= first_pos && t0 + kBlock <= limit &&
                            (p.window == 0 || t0 > last_pos - p.window || t0 + kBlock <= p.sinks);
         if (!whole) {
 #pragma unroll
@@ -235,7 +291,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int t = t0 + 8 * nb + 2 * c + e;
-                const bool see = t <= pos[r] && t < u.s.limit &&
+                const bool see = t <= pos[r] && t < limit &&
                                  (p.window == 0 || t > pos[r] - p.window || t < p.sinks);
                 if (!see) s[nb][2 * r + e] = -INFINITY;
               }
@@ -257,10 +313,6 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
             for (int nb = 0; nb < 16; ++nb) {
               o[nb][2 * r] *= a;
               o[nb][2 * r + 1] *= a;
-              if constexpr (kPacked) {
-                o[nb][2] *= a;
-                o[nb][3] *= a;
-              }
             }
           }
           const float mu = m[r] == -INFINITY ? 0.f : m[r];
@@ -270,16 +322,10 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
           pr[r][3] = fast_exp2(s[1][2 * r + 1] - mu);
           l[r] += (pr[r][0] + pr[r][1]) + (pr[r][2] + pr[r][3]);
         }
-        uint32_t a0, a1, a2, a3;
-        if constexpr (kPacked) {
-          split_half2(pr[0][0], pr[0][1], a0, a1);
-          split_half2(pr[0][2], pr[0][3], a2, a3);
-        } else {
-          a0 = pack_half2(__float2half_rn(pr[0][0]), __float2half_rn(pr[0][1]));
-          a1 = pack_half2(__float2half_rn(pr[NR - 1][0]), __float2half_rn(pr[NR - 1][1]));
-          a2 = pack_half2(__float2half_rn(pr[0][2]), __float2half_rn(pr[0][3]));
-          a3 = pack_half2(__float2half_rn(pr[NR - 1][2]), __float2half_rn(pr[NR - 1][3]));
-        }
+        const uint32_t a0 = pack_half2(__float2half_rn(pr[0][0]), __float2half_rn(pr[0][1]));
+        const uint32_t a1 = pack_half2(__float2half_rn(pr[1][0]), __float2half_rn(pr[1][1]));
+        const uint32_t a2 = pack_half2(__float2half_rn(pr[0][2]), __float2half_rn(pr[0][3]));
+        const uint32_t a3 = pack_half2(__float2half_rn(pr[1][2]), __float2half_rn(pr[1][3]));
         // ---- o += p V -------------------------------------------------------------------
         auto pv = [&](int nb, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
           mma16816(o[nb], a0, a1, a2, a3, pair_lo(w0, w1), pair_lo(w2, w3));
@@ -329,65 +375,360 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
 #pragma unroll
       for (int nb = 0; nb < 16; ++nb) {
         float* dst = mo + (warp * kRows + g + 8 * r) * kHeadDim;
-        dst[32 * c + nb] = kPacked ? o[nb][0] + o[nb][2] : o[nb][2 * r];
-        dst[32 * c + 16 + nb] = kPacked ? o[nb][1] + o[nb][3] : o[nb][2 * r + 1];
+        dst[32 * c + nb] = o[nb][2 * r];
+        dst[32 * c + 16 + nb] = o[nb][2 * r + 1];
       }
     }
     __syncthreads();
-    for (int r = warp; r < kRows; r += kNarrowWarps) {
-      if (r >= rows && u.slot < 0) continue;
-      float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kNarrowWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float Mu = M == -INFINITY ? 0.f : M;  // a row that sees nothing: sums of 0 (or of its NaN)
-#pragma unroll
-      for (int w = 0; w < kNarrowWarps; ++w) {
-        const float2 v = ml[w * kRows + r];
-        const float f = fast_exp2(v.x - Mu);
-        L = fmaf(f, v.y, L);
-        const float4 x = *reinterpret_cast<const float4*>(mo + (w * kRows + r) * kHeadDim + 4 * lane);
-        acc.x = fmaf(f, x.x, acc.x);
-        acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z);
-        acc.w = fmaf(f, x.w, acc.w);
+    for (int r = warp; r < kRows; r += kNarrowWarps)
+      join_row<kNarrowWarps, kRows>(p, u, mo, ml, r, r < rows, kRows, lane);
+    if (u.slot >= 0 && (u.slot & 1) && tid == 0) {
+      write_record(p, &u);
+      recorded = true;
+    }
+    __syncthreads();  // q~ and the join buffers are free again; the next piece is known
+  }
+  if (tid == 0 && !recorded) write_record(p, nullptr);
+}
+
+// ---- 8 rows or fewer per (sequence, KV head): tokens as the rows of the products ---------------
+// kPair: up to 4 query rows, columns 2h and 2h + 1 of the 8-wide operand being the high and low
+// fp16 parts of row h; else up to 8 rows, a column each, and two mma per step for q~.
+template <int DK, int BK, int DV, int BV, bool kPair>
+__global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const ChunkParams p) {
+  using T = NarrowTable<DK, BK, DV, BV>;
+  constexpr bool kWide = T::kWide;
+  constexpr int kRows = 8;                 // rows of a tile's slots in the workspace
+  constexpr int NR = kPair ? 1 : 2;        // rows of one lane
+  constexpr int kTileRows = kPair ? 4 : 8;
+  constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
+  uint8_t* const sm = g_smem + T::kBytes;
+  NarrowHead* const head = reinterpret_cast<NarrowHead*>(sm);
+  __half* const qs = reinterpret_cast<__half*>(sm + kHeadBytes);           // [2][kRows][kQStride] high, low
+  float* const mo = reinterpret_cast<float*>(qs + 2 * kRows * kQStride);   // [warps][kTileRows][128]
+  float2* const ml = reinterpret_cast<float2*>(mo + kFewWarps * kTileRows * kHeadDim);  // [warps][kTileRows]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  pdl_trigger();
+  fill_table<DK, BK, DV, BV>(p);
+  chunk_plan(p, head->pre, head->scratch);
+  if (tid == 0) {
+    head->walk.start(p, head->pre);
+    plan_next(p, head, 0);
+  }
+  __syncthreads();
+  const uint32_t lwk = kWide ? 0u : DK == 4 ? (lane & 15) * 8 : lane * 4;
+  const uint32_t lwv = kWide ? 65536u : 128u + (DV == 4 ? (lane & 15) * 8 : lane * 4);
+  const int G = p.group;
+  bool recorded = false;
+
+  for (int k = 0; head->more[k & 1]; ++k) {
+    const ChunkPiece& u = head->piece[k & 1];
+    const ChunkKeys keys = u.k;
+    const int blk1 = u.blk1, limit = u.s.limit;
+    const int i0 = u.tile * p.tile_tok;
+    const int rows = min(p.tile_tok, u.s.n - i0) * G;
+    const int32_t* const pages = p.page_table + static_cast<long long>(u.b) * p.max_pages;
+    // The pipeline of a warp's blocks (every kFewWarps-th): codes in registers one block ahead, their
+    // rows' first cache lines asked for two ahead, the page looked up three ahead.
+    auto page_of = [&](int i) {  // -1: no such block
+      if (i >= blk1) return -1;
+      return __ldg(pages + (p.page_shift >= 0 ? (keys.block(i) * kBlock) >> p.page_shift : (keys.block(i) * kBlock) / p.page_size));
+    };
+    auto row_of = [&](int i, int pg) -> long long {  // row of the block's first token in the pools, or -1
+      if (i >= blk1) return -1;
+      if (pg < 0 || pg >= p.num_pages) {
+        if (lane == 0) report(p.status, kDevBadPage);
+        return -1;
       }
-      if (u.slot >= 0) {
-        const long long at = static_cast<long long>(u.slot) * kRows + r;
-        reinterpret_cast<float4*>(p.ws_o + at * kHeadDim)[lane] = acc;
-        if (lane == 0) p.ws_ml[at] = make_float2(M, L);
-      } else {
-        const float f = L == 0.f ? 0.f : 1.f / L;
+      const int t0 = keys.block(i) * kBlock;
+      const int off = p.page_shift >= 0 ? t0 & (p.page_size - 1) : t0 % p.page_size;
+      return (static_cast<long long>(pg) * p.hkv + u.kvh) * p.page_size + off;
+    };
+    auto touch = [&](long long row) {  // one 128-byte line per lane
+      if (row < 0) return;
+      constexpr int kLines = (kBlock * KROW + 127) / 128, vLines = (kBlock * VROW + 127) / 128;
+      const uint8_t* at = lane < kLines ? p.k_pool + row * KROW + 128 * lane : p.v_pool + row * VROW + 128 * (lane - kLines);
+      if (lane < kLines + vLines) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    };
+    KCodes<DK> kc[2];
+    VCodes<DV, BV> vc[4];
+    auto load = [&](long long row, KCodes<DK>(&kx)[2], VCodes<DV, BV>(&vx)[4]) {
+      if (row < 0) return;
+      const uint8_t* kr = p.k_pool + row * KROW;
+      const uint8_t* vr = p.v_pool + row * VROW;
+      kx[0].load(kr + g * KROW, c);
+      kx[1].load(kr + (g + 8) * KROW, c);
+      vx[0].load(vr + (2 * c) * VROW, g);
+      vx[1].load(vr + (2 * c + 1) * VROW, g);
+      vx[2].load(vr + (2 * c + 8) * VROW, g);
+      vx[3].load(vr + (2 * c + 9) * VROW, g);
+    };
+    const int first = u.blk0 + warp;
+    long long row0, row1, row2;
+    int pg3;
+    {
+      const int pg0 = page_of(first), pg1 = page_of(first + kFewWarps), pg2 = page_of(first + 2 * kFewWarps);
+      pg3 = page_of(first + 3 * kFewWarps);
+      row0 = row_of(first, pg0);
+      load(row0, kc, vc);
+      row1 = row_of(first + kFewWarps, pg1);
+      touch(row1);
+      row2 = row_of(first + 2 * kFewWarps, pg2);
+      touch(row2);
+    }
+    // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
+    if (warp < kTileRows) {
+      const int r = warp;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < rows) {
         const long long row = static_cast<long long>(u.s.row0 + i0 + r / G) * p.hq + u.kvh * G + r % G;
-        const __half2 h0 = __floats2half2_rn(acc.x * f, acc.y * f), h1 = __floats2half2_rn(acc.z * f, acc.w * f);
-        uint2 w;
-        w.x = *reinterpret_cast<const uint32_t*>(&h0);
-        w.y = *reinterpret_cast<const uint32_t*>(&h1);
-        reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row * kHeadDim)[lane] = w;
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __half*>(p.q) + row * kHeadDim) + lane);
+        const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + u.kvh * kHeadDim) + lane);
+        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+        x[0] = lo.x * lam.x;
+        x[1] = lo.y * lam.y;
+        x[2] = hi.x * lam.z;
+        x[3] = hi.y * lam.w;
+        fwht128_warp(x, lane);
       }
+      uint2 vh, vl;
+      split_half2(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
+      split_half2(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
+      *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
+      *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
+    }
+    __syncthreads();
+    if (tid == 0) plan_next(p, head, k + 1);
+    uint32_t qb[8][2], ql[kPair ? 1 : 8][2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = (kPair ? (g & 1) * kRows + (g >> 1) : g) * kQStride + 32 * c + 4 * j;
+      const uint2 h = *reinterpret_cast<const uint2*>(qs + at);
+      qb[j][0] = h.x;
+      qb[j][1] = h.y;
+      if constexpr (!kPair) {
+        const uint2 w = *reinterpret_cast<const uint2*>(qs + kRows * kQStride + at);
+        ql[j][0] = w.x;
+        ql[j][1] = w.y;
+      }
+    }
+    int pos[NR];  // positions of the lane's rows (rows past the tile see nothing)
+    float m[NR], l[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int r = kPair ? c : 2 * c + i;
+      pos[i] = r < rows ? u.s.base + i0 + r / G : -1;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    const int first_pos = u.s.base + i0, last_pos = u.s.base + min(i0 + p.tile_tok, u.s.n) - 1;
+    float o[8][4];  // dims 16 g + 2 mb and + 1, columns 2c and 2c + 1
+#pragma unroll
+    for (int mb = 0; mb < 8; ++mb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[mb][e] = 0.f;
+
+    for (int i = first; i < blk1; i += kFewWarps) {
+      KCodes<DK> kn[2];
+      VCodes<DV, BV> vn[4];
+      load(row1, kn, vn);
+      const long long row3 = row_of(i + 3 * kFewWarps, pg3);
+      touch(row3);
+      pg3 = page_of(i + 4 * kFewWarps);
+      if (row0 >= 0) {
+        const int t0 = keys.block(i) * kBlock;
+        // ---- scores: tokens g and g + 8 ------------------------------------------------
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          uint32_t a[2][4];  // two k-steps
+          if constexpr (kWide) {
+            const uint4 w0 = tab128(kc[0].off16(j >> 1, lwk)), w1 = tab128(kc[1].off16(j >> 1, lwk));
+            a[0][0] = w0.x, a[0][1] = w1.x, a[0][2] = w0.y, a[0][3] = w1.y;
+            a[1][0] = w0.z, a[1][1] = w1.z, a[1][2] = w0.w, a[1][3] = w1.w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if constexpr (DK == 4) {
+                const uint2 w0 = tab64(kc[0].off(j + e, lwk)), w1 = tab64(kc[1].off(j + e, lwk));
+                a[e][0] = w0.x, a[e][1] = w1.x, a[e][2] = w0.y, a[e][3] = w1.y;
+              } else {
+                a[e][0] = tab32(kc[0].off(2 * (j + e), lwk));
+                a[e][1] = tab32(kc[1].off(2 * (j + e), lwk));
+                a[e][2] = tab32(kc[0].off(2 * (j + e) + 1, lwk));
+                a[e][3] = tab32(kc[1].off(2 * (j + e) + 1, lwk));
+              }
+            }
+          }
+          mma16816(s, a[0][0], a[0][1], a[0][2], a[0][3], qb[j][0], qb[j][1]);
+          mma16816(s2, a[1][0], a[1][1], a[1][2], a[1][3], qb[j + 1][0], qb[j + 1][1]);
+          if constexpr (!kPair) {
+            mma16816(s, a[0][0], a[0][1], a[0][2], a[0][3], ql[j][0], ql[j][1]);
+            mma16816(s2, a[1][0], a[1][1], a[1][2], a[1][3], ql[j + 1][0], ql[j + 1][1]);
+          }
+        }
+        float x[NR][2];  // the lane's rows, tokens g and g + 8
+        if constexpr (kPair) {
+          x[0][0] = (s[0] + s2[0]) + (s[1] + s2[1]);
+          x[0][1] = (s[2] + s2[2]) + (s[3] + s2[3]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            x[r][0] = s[r] + s2[r];
+            x[r][1] = s[2 + r] + s2[2 + r];
+          }
+        }
+        const bool whole = t0 + kBlock - 1 <= first_pos && t0 + kBlock <= limit &&
+                           (p.window == 0 || t0 > last_pos - p.window || t0 + kBlock <= p.sinks);
+        if (!whole) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int t = t0 + g + 8 * e;
+              const bool see = t <= pos[r] && t < limit && (p.window == 0 || t > pos[r] - p.window || t < p.sinks);
+              if (!see) x[r][e] = -INFINITY;
+            }
+        }
+        // ---- online softmax: the maxima move only when a score passes them by kSlack ----------
+        bool over = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float mx = fmaxf(x[r][0], x[r][1]);
+          over |= mx > m[r] + kSlack || (m[r] == -INFINITY && mx > -INFINITY);
+        }
+        if (__any_sync(kAll, over)) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float mx = fmaxf(fmaxf(x[r][0], x[r][1]), m[r]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
+            const float a = mx == m[r] ? 1.f : fast_exp2(m[r] - mx);  // 0 while nothing is accumulated
+            m[r] = mx;
+            l[r] *= a;
+#pragma unroll
+            for (int mb = 0; mb < 8; ++mb) {
+              o[mb][r] *= a;
+              o[mb][2 + r] *= a;
+              if constexpr (kPair) {
+                o[mb][1] *= a;
+                o[mb][3] *= a;
+              }
+            }
+          }
+        }
+        uint32_t b[2];  // tokens 0..7 and 8..15
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float pr[NR];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            pr[r] = fast_exp2(x[r][e] - (m[r] == -INFINITY ? 0.f : m[r]));
+            l[r] += pr[r];
+          }
+          uint32_t w;
+          if constexpr (kPair) {
+            const __half h = __float2half_rn(pr[0]);
+            w = pack_half2(h, __float2half_rn(pr[0] - __half2float(h)));
+          } else {
+            w = pack_half2(__float2half_rn(pr[0]), __float2half_rn(pr[NR - 1]));
+          }
+          b[e] = movmatrix_trans(w);
+        }
+        // ---- o^T += V^T p ------------------------------------------------------------------
+        auto pv = [&](int mb, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+          mma16816(o[mb], pair_lo(w0, w1), pair_hi(w0, w1), pair_lo(w2, w3), pair_hi(w2, w3), b[0], b[1]);
+        };
+        if constexpr (kWide) {
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2) {
+            uint4 w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = tab128(vc[t].off16(i2, lwv));
+            pv(4 * i2, w[0].x, w[1].x, w[2].x, w[3].x);
+            pv(4 * i2 + 1, w[0].y, w[1].y, w[2].y, w[3].y);
+            pv(4 * i2 + 2, w[0].z, w[1].z, w[2].z, w[3].z);
+            pv(4 * i2 + 3, w[0].w, w[1].w, w[2].w, w[3].w);
+          }
+        } else if constexpr (DV == 4) {
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) {
+            uint2 w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = tab64(vc[t].off(i2, lwv));
+            pv(2 * i2, w[0].x, w[1].x, w[2].x, w[3].x);
+            pv(2 * i2 + 1, w[0].y, w[1].y, w[2].y, w[3].y);
+          }
+        } else {
+#pragma unroll
+          for (int i2 = 0; i2 < 8; ++i2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) w[t] = tab32(vc[t].off(i2, lwv));
+            pv(i2, w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      kc[0] = kn[0], kc[1] = kn[1];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) vc[t] = vn[t];
+      row0 = row1;
+      row1 = row2;
+      row2 = row3;
+    }
+    // ---- the warps' partials join ------------------------------------------------------
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(kAll, l[r], d);
+      const int row = kPair ? c : 2 * c + r;
+      if (g == 0) ml[warp * kTileRows + row] = make_float2(m[r], l[r]);
+      float* dst = mo + (warp * kTileRows + row) * kHeadDim + 16 * g;
+#pragma unroll
+      for (int mb = 0; mb < 8; ++mb) {
+        float2 v;
+        v.x = kPair ? o[mb][0] + o[mb][1] : o[mb][r];
+        v.y = kPair ? o[mb][2] + o[mb][3] : o[mb][2 + r];
+        *reinterpret_cast<float2*>(dst + 2 * mb) = v;
+      }
+    }
+    __syncthreads();
+    if (warp < kTileRows) {
+      const int r = warp;
+      join_row<kFewWarps, kTileRows>(p, u, mo, ml, r, r < rows, kRows, lane);
     }
     if (u.slot >= 0 && (u.slot & 1) && tid == 0) {
       write_record(p, &u);
       recorded = true;
     }
-    __syncthreads();  // q~ and the join buffers are free again
+    __syncthreads();  // q~ and the join buffers are free again; the next piece is known
   }
   if (tid == 0 && !recorded) write_record(p, nullptr);
 }
 
-template <int DK, int BK, int DV, int BV, int kRows>
-cudaError_t launch_narrow(const ChunkParams& p, int grid, cudaStream_t stream) {
+template <int DK, int BK, int DV, int BV, bool kPair>
+cudaError_t launch_few(const ChunkParams& p, int grid, cudaStream_t stream) {
   static SmemOptIn opt;
-  constexpr size_t smem = NarrowTable<DK, BK, DV, BV>::kBytes + (kChunkMaxBatch + 34) * sizeof(long long) +
-                          2 * kRows * kQStride * sizeof(__half) + kNarrowWarps * kRows * (kHeadDim + 2) * sizeof(float);
-  cudaError_t e = ensure_smem(vq_chunk_narrow_kernel<DK, BK, DV, BV, kRows>, smem, opt);
+  constexpr size_t smem = NarrowTable<DK, BK, DV, BV>::kBytes + kHeadBytes +
+                          2 * 8 * kQStride * sizeof(__half) + kFewWarps * (kPair ? 4 : 8) * (kHeadDim + 2) * sizeof(float);
+  cudaError_t e = ensure_smem(vq_chunk_few_kernel<DK, BK, DV, BV, kPair>, smem, opt);
   if (e != cudaSuccess) return e;
-  return launch_pdl(vq_chunk_narrow_kernel<DK, BK, DV, BV, kRows>, dim3(grid), dim3(kNarrowWarps * 32), smem, stream, p, false);
+  return launch_pdl(vq_chunk_few_kernel<DK, BK, DV, BV, kPair>, dim3(grid), dim3(kFewWarps * 32), smem, stream, p, false);
 }
 
 template <int DK, int BK, int DV, int BV>
 cudaError_t launch_narrow(const ChunkParams& p, int grid, cudaStream_t stream) {
-  return p.tile_rows == 8 ? launch_narrow<DK, BK, DV, BV, 8>(p, grid, stream) : launch_narrow<DK, BK, DV, BV, 16>(p, grid, stream);
+  if (p.tile_rows == 8)
+    return p.tile_tok * p.group <= 4 ? launch_few<DK, BK, DV, BV, true>(p, grid, stream)
+                                     : launch_few<DK, BK, DV, BV, false>(p, grid, stream);
+  static SmemOptIn opt;
+  constexpr size_t smem = NarrowTable<DK, BK, DV, BV>::kBytes + kHeadBytes +
+                          2 * 16 * kQStride * sizeof(__half) + kNarrowWarps * 16 * (kHeadDim + 2) * sizeof(float);
+  cudaError_t e = ensure_smem(vq_chunk_narrow_kernel<DK, BK, DV, BV>, smem, opt);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(vq_chunk_narrow_kernel<DK, BK, DV, BV>, dim3(grid), dim3(kNarrowWarps * 32), smem, stream, p, false);
 }
 
 // ---- merge of the pieces of tiles that several CTAs took -----------------------------

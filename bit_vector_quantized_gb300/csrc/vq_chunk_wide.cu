@@ -655,12 +655,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       }
     } else if (warp == kSoftWarps + kCodeWarps + 1) {
       // ================================== planning =======================================
-      ChunkWalk<kTile> walk(p, pre);  // (the tiles over the plan wait for the first piece)
+      ChunkWalk<kTile> walk;
+      walk.start(p, pre);  // (the tiles over the plan wait for the first piece)
       ChunkPiece q;
       Ring ro;
       bool recorded = false;
       for (bool more = true; more;) {
-        more = walk.next(q);
+        more = walk.next(p, q);
         const int i0 = q.tile * p.tile_tok, n = more ? min(p.tile_tok, q.s.n - i0) : 0;
         if (more && q.slot >= 0 && (q.slot & 1)) {
           if (lane == 0) write_record(p, &q);

@@ -181,6 +181,7 @@ struct ChunkParams {
   long long num_pages;
   int batch, num_tokens, hq, hkv, group;
   int page_size, max_pages, max_seq_len, max_new_len;
+  int page_shift;             // log2 of page_size, or -1
   int window, sinks;          // window 0: none
   int tile_tok, tile_rows;    // tokens and (padded) rows of a tile
   int gap, min_range;         // a tile's fixed cost and a CTA's least share, in tokens
