@@ -1108,14 +1108,17 @@ struct ChunkWs {
   size_t o_off, ml_off, rec_off, total;
 };
 
-// Two partials and a record per CTA.
-ChunkWs chunk_ws(const vq_layout& L, int max_new_len, int grid) {
+// Workers of a launch over `grid` CTAs.
+int chunk_workers(int tile_rows, int grid) { return tile_rows == 8 ? vqk::kFewGroups * grid : grid; }
+
+// Two partials and a record per worker.
+ChunkWs chunk_ws(int tile_rows, int grid) {
   ChunkWs w;
-  const size_t rows = 2 * static_cast<size_t>(grid) * chunk_tile_rows(L, max_new_len);
+  const size_t workers = chunk_workers(tile_rows, grid), rows = 2 * workers * tile_rows;
   w.o_off = 0;
   w.ml_off = rows * 128 * sizeof(float);
   w.rec_off = (w.ml_off + rows * sizeof(float2) + 255) & ~size_t(255);
-  w.total = (w.rec_off + grid * sizeof(vqk::ChunkRecord) + 255) & ~size_t(255);
+  w.total = (w.rec_off + workers * sizeof(vqk::ChunkRecord) + 255) & ~size_t(255);
   return w;
 }
 
@@ -1129,7 +1132,8 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
     return 0;
   const int sms = num_sms > 0 ? num_sms : device_sms();
   if (sms <= 0) return 0;
-  return chunk_ws(*layout, max_new_len, sms).total;
+    // a call with smaller bounds may take a lower tile, whose slots are more
+  return std::max(chunk_ws(chunk_tile_rows(*layout, max_new_len), sms).total, chunk_ws(8, sms).total);
 }
 
 vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
@@ -1173,7 +1177,8 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   const int sms = device_sms();
   if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
   const int grid = sms;
-  const ChunkWs ws = chunk_ws(L, max_new_len, grid);
+  const int tile_rows = chunk_tile_rows(L, max_new_len);
+  const ChunkWs ws = chunk_ws(tile_rows, grid);
   if (workspace_bytes < ws.total)
     return fail(VQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, ws.total);
 
@@ -1208,7 +1213,7 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.max_new_len = max_new_len;
   p.window = std::min(window, 1 << 30);  // no position is further back: the same as none
   p.sinks = std::min(num_sinks, 1 << 30);
-  p.tile_rows = chunk_tile_rows(L, max_new_len);
+  p.tile_rows = tile_rows;
   p.tile_tok = p.tile_rows / p.group;
   const bool wide = p.tile_rows == 128;
   p.gap = wide ? 384 : 256;
@@ -1219,7 +1224,7 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   auto launch = wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;
   cudaError_t e = launch(p, L.k_sub, L.k_bits, L.v_sub, L.v_bits, grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention launch");
-  e = vqk::launch_chunk_merge(p, grid, static_cast<cudaStream_t>(stream));
+  e = vqk::launch_chunk_merge(p, chunk_workers(tile_rows, grid), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention merge");
   return VQ_OK;
 }

@@ -9,15 +9,16 @@
 // blocks, then the window's.
 //
 // Work division.  The tiles are laid end to end, each as long as an estimate
-// of its keys plus a fixed cost, and CTA c takes [c W, (c + 1) W), whatever
-// the mix of lengths, so that the last CTA ends with the others.  The
+// of its keys plus a fixed cost, and worker c (a CTA, or a group of its warps)
+// takes [c W, (c + 1) W), whatever the mix of lengths, so that the last
+// worker ends with the others.  The
 // estimate is min(len - n + (t + 1) TT, cap) for tile t, whose sums have a
-// closed form: a CTA finds its first tile by two binary searches, without a
+// closed form: a worker finds its first tile by two binary searches, without a
 // list of tiles.  A cut inside a tile falls on a block; the tile's pieces
-// leave unnormalised partials in the workspace: a CTA has at most one tile
+// leave unnormalised partials in the workspace: a worker has at most one tile
 // that began before it (slot 2c) and one that it begins but does not end
-// (slot 2c + 1), so 2 slots per CTA are enough for any batch.  The CTA that
-// begins such a tile writes its record, and the merge kernel joins the
+// (slot 2c + 1), so 2 slots per worker are enough for any batch.  The worker
+// that begins such a tile writes its record, and the merge kernel joins the
 // pieces, in order.
 #pragma once
 
@@ -95,22 +96,24 @@ struct ChunkPiece {
   ChunkKeys k;
   int blk0, blk1;  // blocks [blk0, blk1) of the tile's keys
   int slot;        // partial slot, or -1: the piece is the whole tile
-  int last_cta;    // the CTA that ends the tile (slot 2c + 1 only)
+  int last;        // the worker that ends the tile (slot 2c + 1 only)
 };
 
-// Walks the pieces of this CTA's range (one thread does, for all).
+// Walks the pieces of worker `me` of `workers` (one thread does, for all of it).
 template <int CW>
 struct ChunkWalk {
   long long x, x1, W;    // position, end of the range, range per CTA
   long long tile_x;      // where the current tile begins
+  int me;
   int b, kvh, tile, tiles;
   ChunkSeq s;
 
   // pre: [B + 1] estimated length of the sequences before b, all KV heads
-  __device__ __forceinline__ void start(const ChunkParams& p, const long long* pre) {
+  __device__ __forceinline__ void start(const ChunkParams& p, const long long* pre, int me_, int workers) {
+    me = me_;
     const long long total = pre[p.batch];
-    W = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x), static_cast<long long>(p.min_range));
-    x = min(W * blockIdx.x, total);
+    W = max((total + workers - 1) / static_cast<long long>(workers), static_cast<long long>(p.min_range));
+    x = min(W * me, total);
     x1 = min(x + W, total);
     if (x >= x1) return;
     int lo = 0, hi = p.batch;  // the last b with pre[b] <= x; its own length is not 0
@@ -148,8 +151,8 @@ struct ChunkWalk {
     q.k = chunk_keys<CW>(p, s, tile);
     q.blk0 = o0 == 0 ? 0 : static_cast<int>(o0 * q.k.count / w);
     q.blk1 = o1 == w ? q.k.count : static_cast<int>(o1 * q.k.count / w);
-    q.slot = o0 > 0 ? 2 * static_cast<int>(blockIdx.x) : o1 < w ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
-    q.last_cta = static_cast<int>((tile_x + w - 1) / W);
+    q.slot = o0 > 0 ? 2 * me : o1 < w ? 2 * me + 1 : -1;
+    q.last = static_cast<int>((tile_x + w - 1) / W);
     x += o1 - o0;
     if (o1 == w) {  // on to the next tile
       tile_x += w;
@@ -200,16 +203,16 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, long long* pre,
   __syncthreads();
 }
 
-// The record of the tile that CTA c begins and does not end (or none).
-__device__ __forceinline__ void write_record(const ChunkParams& p, const ChunkPiece* q) {
+// The record of the tile that a worker begins and does not end (or none).
+__device__ __forceinline__ void write_record(const ChunkParams& p, int worker, const ChunkPiece* q) {
   ChunkRecord r = {};
   if (q) {
     r.rows = min(p.tile_tok, q->s.n - q->tile * p.tile_tok) * p.group;
     r.row0 = q->s.row0 + q->tile * p.tile_tok;
     r.kvh = q->kvh;
-    r.last_cta = q->last_cta;
+    r.last = q->last;
   }
-  *reinterpret_cast<int4*>(p.records + blockIdx.x) = *reinterpret_cast<const int4*>(&r);
+  *reinterpret_cast<int4*>(p.records + worker) = *reinterpret_cast<const int4*>(&r);
 }
 
 }  // namespace

@@ -35,6 +35,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;    // the running maximum may lag by this much (log2 units): p <= 2^8
 constexpr int kNarrowWarps = 8;  // of the 16-row kernel
 constexpr int kFewWarps = 16;    // of the kernel for 8 rows and fewer
+constexpr int kGroupWarps = kFewWarps / kFewGroups, kGroupThreads = kGroupWarps * 32;
 constexpr int kBlock = 16;       // tokens per block
 constexpr int kQStride = 132;    // halves between q~ rows in shared memory
 
@@ -78,20 +79,19 @@ __device__ __forceinline__ void fill_table(const ChunkParams& p) {
 }
 
 // Shared memory of both kernels before q~ and the join buffers.
+struct NarrowWorker {
+  ChunkWalk<kBlock> walk;  // its first thread's
+  ChunkPiece piece[2];     // the piece under way and the next one
+  int more[2];
+  // piece k, into its buffer
+  __device__ __forceinline__ void plan(const ChunkParams& p, int k) { more[k & 1] = walk.next(p, piece[k & 1]); }
+};
 struct NarrowHead {
   long long pre[kChunkMaxBatch + 1];
   long long scratch[33];
-  ChunkWalk<kBlock> walk;  // thread 0's
-  ChunkPiece piece[2];     // the piece under way and the next one
-  int more[2];
+  NarrowWorker worker[kFewGroups];
 };
-static_assert(sizeof(NarrowHead) % 8 == 0, "what follows is aligned by hand");
 constexpr size_t kHeadBytes = (sizeof(NarrowHead) + 15) / 16 * 16;
-
-// The next piece, into the buffer after piece k's.
-__device__ __forceinline__ void plan_next(const ChunkParams& p, NarrowHead* h, int k) {
-  h->more[k & 1] = h->walk.next(p, h->piece[k & 1]);
-}
 
 // Elements e of two fp16 pairs as one operand register: (a.e, b.e).
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
   pdl_trigger();
   fill_table<DK, BK, DV, BV>(p);
   chunk_plan(p, head->pre, head->scratch);
+  NarrowWorker* const me = head->worker;
   if (tid == 0) {
-    head->walk.start(p, head->pre);
-    plan_next(p, head, 0);
+    me->walk.start(p, head->pre, blockIdx.x, gridDim.x);
+    me->plan(p, 0);
   }
   __syncthreads();
   const uint32_t lwk = kWide ? 0u : DK == 4 ? (lane & 15) * 8 : lane * 4;
@@ -161,8 +162,8 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
   const int G = p.group;
   bool recorded = false;
 
-  for (int k = 0; head->more[k & 1]; ++k) {
-    const ChunkPiece& u = head->piece[k & 1];
+  for (int k = 0; me->more[k & 1]; ++k) {
+    const ChunkPiece& u = me->piece[k & 1];
     const ChunkKeys keys = u.k;
     const int blk1 = u.blk1, limit = u.s.limit;
     const int i0 = u.tile * p.tile_tok;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
       *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
     }
     __syncthreads();
-    if (tid == 0) plan_next(p, head, k + 1);
+    if (tid == 0) me->plan(p, k + 1);
     uint32_t qa[8][4], ql[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -383,13 +384,100 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
     for (int r = warp; r < kRows; r += kNarrowWarps)
       join_row<kNarrowWarps, kRows>(p, u, mo, ml, r, r < rows, kRows, lane);
     if (u.slot >= 0 && (u.slot & 1) && tid == 0) {
-      write_record(p, &u);
+      write_record(p, blockIdx.x, &u);
       recorded = true;
     }
     __syncthreads();  // q~ and the join buffers are free again; the next piece is known
   }
-  if (tid == 0 && !recorded) write_record(p, nullptr);
+  if (tid == 0 && !recorded) write_record(p, blockIdx.x, nullptr);
 }
+
+// A lane's code words as they lie in the pools, loaded ahead of their use: the loads are volatile, so
+// that they stay where they are issued, and nothing is computed from the words until get().
+__device__ __forceinline__ uint32_t ld_words1(const uint8_t* at) {
+  uint32_t x;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(at));
+  return x;
+}
+template <int DK>
+struct KWords;
+template <>
+struct KWords<4> {
+  KCodes<4> k;
+  __device__ __forceinline__ void load(const uint8_t* row, int c) {
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(k.w.x), "=r"(k.w.y) : "l"(row + 8 * c));
+  }
+  __device__ __forceinline__ KCodes<4> get(int) const { return k; }
+};
+template <>
+struct KWords<2> {
+  KCodes<2> k;
+  __device__ __forceinline__ void load(const uint8_t* row, int c) {
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(k.w.x), "=r"(k.w.y), "=r"(k.w.z), "=r"(k.w.w)
+                 : "l"(row + 16 * c));
+  }
+  __device__ __forceinline__ KCodes<2> get(int) const { return k; }
+};
+template <>
+struct KWords<8> {  // 48 bits from bit 48 c
+  uint32_t lo, hi;
+  __device__ __forceinline__ void load(const uint8_t* row, int c) {
+    const uint8_t* at = row + (48 * c) / 32 * 4;
+    lo = ld_words1(at);
+    hi = ld_words1(at + 4);
+  }
+  __device__ __forceinline__ KCodes<8> get(int c) const {
+    KCodes<8> k;
+    k.a = __funnelshift_r(lo, hi, (48 * c) & 31);
+    k.b = hi >> ((48 * c) & 31);
+    return k;
+  }
+};
+template <int DV, int BV>
+struct VWords;
+template <>
+struct VWords<4, 8> {
+  VCodes<4, 8> v;
+  __device__ __forceinline__ void load(const uint8_t* row, int r) { v.w = ld_words1(row + 4 * r); }
+  __device__ __forceinline__ VCodes<4, 8> get(int) const { return v; }
+};
+template <>
+struct VWords<2, 8> {
+  VCodes<2, 8> v;
+  __device__ __forceinline__ void load(const uint8_t* row, int r) {
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.w.x), "=r"(v.w.y) : "l"(row + 8 * r));
+  }
+  __device__ __forceinline__ VCodes<2, 8> get(int) const { return v; }
+};
+template <>
+struct VWords<4, 9> {  // 36 bits from bit 36 r
+  uint32_t lo, hi;
+  __device__ __forceinline__ void load(const uint8_t* row, int r) {
+    lo = ld_words1(row + 4 * r);
+    hi = ld_words1(row + 4 * r + 4);
+  }
+  __device__ __forceinline__ VCodes<4, 9> get(int r) const {
+    VCodes<4, 9> v;
+    v.a = __funnelshift_r(lo, hi, 4 * r);
+    v.b = hi >> (4 * r);
+    return v;
+  }
+};
+template <>
+struct VWords<8, 12> {  // 24 bits from bit 24 r; the last lane's lie in its first word
+  uint32_t lo, hi;
+  __device__ __forceinline__ void load(const uint8_t* row, int r) {
+    const uint8_t* at = row + (24 * r) / 32 * 4;
+    lo = ld_words1(at);
+    hi = ld_words1(r < 7 ? at + 4 : at);
+  }
+  __device__ __forceinline__ VCodes<8, 12> get(int r) const {
+    VCodes<8, 12> v;
+    v.x = __funnelshift_r(lo, hi, (24 * r) & 31);
+    return v;
+  }
+};
 
 // ---- 8 rows or fewer per (sequence, KV head): tokens as the rows of the products ---------------
 // kPair: up to 4 query rows, columns 2h and 2h + 1 of the 8-wide operand being the high and low
@@ -404,17 +492,24 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
   constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
   uint8_t* const sm = g_smem + T::kBytes;
   NarrowHead* const head = reinterpret_cast<NarrowHead*>(sm);
-  __half* const qs = reinterpret_cast<__half*>(sm + kHeadBytes);           // [2][kRows][kQStride] high, low
-  float* const mo = reinterpret_cast<float*>(qs + 2 * kRows * kQStride);   // [warps][kTileRows][128]
-  float2* const ml = reinterpret_cast<float2*>(mo + kFewWarps * kTileRows * kHeadDim);  // [warps][kTileRows]
+  // The CTA's warps work in groups, each with pieces of its own, so that one group's waits (page, codes,
+  // join) pass under the others' products.
+  const int group = threadIdx.x / kGroupThreads, tid = threadIdx.x % kGroupThreads;
+  const int worker = group * gridDim.x + blockIdx.x;  // (few pieces go to different SMs)
+  __half* const qs = reinterpret_cast<__half*>(sm + kHeadBytes) + group * 2 * kRows * kQStride;  // [2][kRows][kQStride] high, low
+  float* const mo = reinterpret_cast<float*>(sm + kHeadBytes + kFewGroups * 2 * kRows * kQStride * sizeof(__half)) +
+                    group * kGroupWarps * kTileRows * (kHeadDim + 2);                     // [warps][kTileRows][128]
+  float2* const ml = reinterpret_cast<float2*>(mo + kGroupWarps * kTileRows * kHeadDim);  // [warps][kTileRows]
+  auto group_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupThreads) : "memory"); };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_trigger();
   fill_table<DK, BK, DV, BV>(p);
   chunk_plan(p, head->pre, head->scratch);
+  NarrowWorker* const me = head->worker + group;
   if (tid == 0) {
-    head->walk.start(p, head->pre);
-    plan_next(p, head, 0);
+    me->walk.start(p, head->pre, worker, kFewGroups * gridDim.x);
+    me->plan(p, 0);
   }
   __syncthreads();
   const uint32_t lwk = kWide ? 0u : DK == 4 ? (lane & 15) * 8 : lane * 4;
@@ -422,20 +517,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
   const int G = p.group;
   bool recorded = false;
 
-  for (int k = 0; head->more[k & 1]; ++k) {
-    const ChunkPiece& u = head->piece[k & 1];
+  for (int k = 0; me->more[k & 1]; ++k) {
+    const ChunkPiece& u = me->piece[k & 1];
     const ChunkKeys keys = u.k;
-    const int blk1 = u.blk1, limit = u.s.limit;
+    const int blk1 = u.blk1, limit = u.s.limit, kvh = u.kvh;
     const int i0 = u.tile * p.tile_tok;
     const int rows = min(p.tile_tok, u.s.n - i0) * G;
     const int32_t* const pages = p.page_table + static_cast<long long>(u.b) * p.max_pages;
-    // The pipeline of a warp's blocks (every kFewWarps-th): codes in registers one block ahead, their
+    // The pipeline of a warp's blocks (every kGroupWarps-th): codes in registers one block ahead, their
     // rows' first cache lines asked for two ahead, the page looked up three ahead.
     auto page_of = [&](int i) {  // -1: no such block
       if (i >= blk1) return -1;
       return __ldg(pages + (p.page_shift >= 0 ? (keys.block(i) * kBlock) >> p.page_shift : (keys.block(i) * kBlock) / p.page_size));
     };
-    auto row_of = [&](int i, int pg) -> long long {  // row of the block's first token in the pools, or -1
+    auto row_of = [&](int i, int pg) {  // the block's rows in the pools, in blocks of 16, or -1
       if (i >= blk1) return -1;
       if (pg < 0 || pg >= p.num_pages) {
         if (lane == 0) report(p.status, kDevBadPage);
@@ -443,20 +538,21 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
       }
       const int t0 = keys.block(i) * kBlock;
       const int off = p.page_shift >= 0 ? t0 & (p.page_size - 1) : t0 % p.page_size;
-      return (static_cast<long long>(pg) * p.hkv + u.kvh) * p.page_size + off;
+      return (pg * p.hkv + kvh) * (p.page_size / kBlock) + off / kBlock;
     };
-    auto touch = [&](long long row) {  // one 128-byte line per lane
+    auto touch = [&](int row) {  // one 128-byte line per lane
       if (row < 0) return;
       constexpr int kLines = (kBlock * KROW + 127) / 128, vLines = (kBlock * VROW + 127) / 128;
-      const uint8_t* at = lane < kLines ? p.k_pool + row * KROW + 128 * lane : p.v_pool + row * VROW + 128 * (lane - kLines);
+      const uint8_t* at = lane < kLines ? p.k_pool + static_cast<long long>(row) * (kBlock * KROW) + 128 * lane
+                                          : p.v_pool + static_cast<long long>(row) * (kBlock * VROW) + 128 * (lane - kLines);
       if (lane < kLines + vLines) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
     };
-    KCodes<DK> kc[2];
-    VCodes<DV, BV> vc[4];
-    auto load = [&](long long row, KCodes<DK>(&kx)[2], VCodes<DV, BV>(&vx)[4]) {
+    KWords<DK> kw[2];
+    VWords<DV, BV> vw[4];
+    auto load = [&](int row, KWords<DK>(&kx)[2], VWords<DV, BV>(&vx)[4]) {
       if (row < 0) return;
-      const uint8_t* kr = p.k_pool + row * KROW;
-      const uint8_t* vr = p.v_pool + row * VROW;
+      const uint8_t* kr = p.k_pool + static_cast<long long>(row) * (kBlock * KROW);
+      const uint8_t* vr = p.v_pool + static_cast<long long>(row) * (kBlock * VROW);
       kx[0].load(kr + g * KROW, c);
       kx[1].load(kr + (g + 8) * KROW, c);
       vx[0].load(vr + (2 * c) * VROW, g);
@@ -465,21 +561,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
       vx[3].load(vr + (2 * c + 9) * VROW, g);
     };
     const int first = u.blk0 + warp;
-    long long row0, row1, row2;
+    int row0, row1, row2;
     int pg3;
     {
-      const int pg0 = page_of(first), pg1 = page_of(first + kFewWarps), pg2 = page_of(first + 2 * kFewWarps);
-      pg3 = page_of(first + 3 * kFewWarps);
+      const int pg0 = page_of(first), pg1 = page_of(first + kGroupWarps), pg2 = page_of(first + 2 * kGroupWarps);
+      pg3 = page_of(first + 3 * kGroupWarps);
       row0 = row_of(first, pg0);
-      load(row0, kc, vc);
-      row1 = row_of(first + kFewWarps, pg1);
+      load(row0, kw, vw);
+      row1 = row_of(first + kGroupWarps, pg1);
       touch(row1);
-      row2 = row_of(first + 2 * kFewWarps, pg2);
+      row2 = row_of(first + 2 * kGroupWarps, pg2);
       touch(row2);
     }
     // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
-    if (warp < kTileRows) {
-      const int r = warp;
+    for (int r = warp; r < kTileRows; r += kGroupWarps) {
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       if (r < rows) {
         const long long row = static_cast<long long>(u.s.row0 + i0 + r / G) * p.hq + u.kvh * G + r % G;
@@ -499,20 +594,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
       *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
       *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
     }
-    __syncthreads();
-    if (tid == 0) plan_next(p, head, k + 1);
-    uint32_t qb[8][2], ql[kPair ? 1 : 8][2];
+    group_sync();
+    if (tid == 0) me->plan(p, k + 1);
+    uint32_t qb[8][2];  // (the low parts of more than 4 rows are read again for every block: registers are short)
+    const uint32_t ql_at = smem_addr(qs + (kRows + g) * kQStride + 32 * c);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int at = (kPair ? (g & 1) * kRows + (g >> 1) : g) * kQStride + 32 * c + 4 * j;
       const uint2 h = *reinterpret_cast<const uint2*>(qs + at);
       qb[j][0] = h.x;
       qb[j][1] = h.y;
-      if constexpr (!kPair) {
-        const uint2 w = *reinterpret_cast<const uint2*>(qs + kRows * kQStride + at);
-        ql[j][0] = w.x;
-        ql[j][1] = w.y;
-      }
     }
     int pos[NR];  // positions of the lane's rows (rows past the tile see nothing)
     float m[NR], l[NR];
@@ -530,13 +621,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[mb][e] = 0.f;
 
-    for (int i = first; i < blk1; i += kFewWarps) {
-      KCodes<DK> kn[2];
-      VCodes<DV, BV> vn[4];
-      load(row1, kn, vn);
-      const long long row3 = row_of(i + 3 * kFewWarps, pg3);
+    for (int i = first; i < blk1; i += kGroupWarps) {
+      const KCodes<DK> kc[2] = {kw[0].get(c), kw[1].get(c)};
+      const VCodes<DV, BV> vc[4] = {vw[0].get(g), vw[1].get(g), vw[2].get(g), vw[3].get(g)};
+      load(row1, kw, vw);
+      const int row3 = row_of(i + 3 * kGroupWarps, pg3);
       touch(row3);
-      pg3 = page_of(i + 4 * kFewWarps);
+      pg3 = page_of(i + 4 * kGroupWarps);
       if (row0 >= 0) {
         const int t0 = keys.block(i) * kBlock;
         // ---- scores: tokens g and g + 8 ------------------------------------------------
@@ -565,8 +656,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
           mma16816(s, a[0][0], a[0][1], a[0][2], a[0][3], qb[j][0], qb[j][1]);
           mma16816(s2, a[1][0], a[1][1], a[1][2], a[1][3], qb[j + 1][0], qb[j + 1][1]);
           if constexpr (!kPair) {
-            mma16816(s, a[0][0], a[0][1], a[0][2], a[0][3], ql[j][0], ql[j][1]);
-            mma16816(s2, a[1][0], a[1][1], a[1][2], a[1][3], ql[j + 1][0], ql[j + 1][1]);
+            uint32_t w[4];
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(ql_at + 8 * j));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(ql_at + 8 * j + 8));
+            mma16816(s, a[0][0], a[0][1], a[0][2], a[0][3], w[0], w[1]);
+            mma16816(s2, a[1][0], a[1][1], a[1][2], a[1][3], w[2], w[3]);
           }
         }
         float x[NR][2];  // the lane's rows, tokens g and g + 8
@@ -671,9 +765,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
           }
         }
       }
-      kc[0] = kn[0], kc[1] = kn[1];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) vc[t] = vn[t];
       row0 = row1;
       row1 = row2;
       row2 = row3;
@@ -694,25 +785,23 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
         *reinterpret_cast<float2*>(dst + 2 * mb) = v;
       }
     }
-    __syncthreads();
-    if (warp < kTileRows) {
-      const int r = warp;
-      join_row<kFewWarps, kTileRows>(p, u, mo, ml, r, r < rows, kRows, lane);
-    }
+    group_sync();
+    for (int r = warp; r < kTileRows; r += kGroupWarps)
+      join_row<kGroupWarps, kTileRows>(p, u, mo, ml, r, r < rows, kRows, lane);
     if (u.slot >= 0 && (u.slot & 1) && tid == 0) {
-      write_record(p, &u);
+      write_record(p, worker, &u);
       recorded = true;
     }
-    __syncthreads();  // q~ and the join buffers are free again; the next piece is known
+    group_sync();  // q~ and the join buffers are free again; the next piece is known
   }
-  if (tid == 0 && !recorded) write_record(p, nullptr);
+  if (tid == 0 && !recorded) write_record(p, worker, nullptr);
 }
 
 template <int DK, int BK, int DV, int BV, bool kPair>
 cudaError_t launch_few(const ChunkParams& p, int grid, cudaStream_t stream) {
   static SmemOptIn opt;
   constexpr size_t smem = NarrowTable<DK, BK, DV, BV>::kBytes + kHeadBytes +
-                          2 * 8 * kQStride * sizeof(__half) + kFewWarps * (kPair ? 4 : 8) * (kHeadDim + 2) * sizeof(float);
+                          kFewGroups * 2 * 8 * kQStride * sizeof(__half) + kFewWarps * (kPair ? 4 : 8) * (kHeadDim + 2) * sizeof(float);
   cudaError_t e = ensure_smem(vq_chunk_few_kernel<DK, BK, DV, BV, kPair>, smem, opt);
   if (e != cudaSuccess) return e;
   return launch_pdl(vq_chunk_few_kernel<DK, BK, DV, BV, kPair>, dim3(grid), dim3(kFewWarps * 32), smem, stream, p, false);
@@ -732,28 +821,28 @@ cudaError_t launch_narrow(const ChunkParams& p, int grid, cudaStream_t stream) {
 }
 
 // ---- merge of the pieces of tiles that several CTAs took -----------------------------
-// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the tile's pieces, in the CTAs' order.
-// blockIdx.x: the CTA that began the tile; one warp per row, four elements per lane.
+// o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the tile's pieces, in the workers' order.
+// blockIdx.x: the worker that began the tile; one warp per row, four elements per lane.
 __global__ void __launch_bounds__(256) vq_chunk_merge_kernel(const ChunkParams p) {
   pdl_wait();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.records + c0));
   const int rows = rec.x;
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
-    auto at = [&](int cta) {
-      return static_cast<long long>(cta == c0 ? 2 * c0 + 1 : 2 * cta) * p.tile_rows + r;
+    auto at = [&](int w) {
+      return static_cast<long long>(w == c0 ? 2 * c0 + 1 : 2 * w) * p.tile_rows + r;
     };
     float M = -INFINITY;
-    for (int cta = c0 + lane; cta <= rec.w; cta += 32) M = fmaxf(M, __ldcg(p.ws_ml + at(cta)).x);
+    for (int i = c0 + lane; i <= rec.w; i += 32) M = fmaxf(M, __ldcg(p.ws_ml + at(i)).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
     const float Mu = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-    for (int cta = c0; cta <= rec.w; ++cta) {
-      const float2 v = __ldcg(p.ws_ml + at(cta));
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at(cta) * kHeadDim) + lane);
+    for (int i = c0; i <= rec.w; ++i) {
+      const float2 v = __ldcg(p.ws_ml + at(i));
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at(i) * kHeadDim) + lane);
       const float f = fast_exp2(v.x - Mu);
       L = fmaf(f, v.y, L);
       acc.x = fmaf(f, x.x, acc.x);
@@ -785,8 +874,8 @@ cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_chunk_merge(const ChunkParams& p, int grid, cudaStream_t stream) {
-  return launch_pdl(vq_chunk_merge_kernel, dim3(grid, (p.tile_rows + 15) / 16), dim3(256), 0, stream, p, true);
+cudaError_t launch_chunk_merge(const ChunkParams& p, int workers, cudaStream_t stream) {
+  return launch_pdl(vq_chunk_merge_kernel, dim3(workers, (p.tile_rows + 15) / 16), dim3(256), 0, stream, p, true);
 }
 
 }  // namespace vqk

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   if (smem_addr(tiles) & 1023u) {  // the swizzled tiles need it (and dynamic shared memory alone gives it)
     if (tid == 0) {
       report(p.status, kDevBadConfig);
-      write_record(p, nullptr);
+      write_record(p, blockIdx.x, nullptr);
     }
     return;
   }
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   constexpr uint32_t tmem = 0;
   if (*tmem_at != tmem) {
     if (tid == 0) report(p.status, kDevBadConfig);
-    if (tid == 0) write_record(p, nullptr);
+    if (tid == 0) write_record(p, blockIdx.x, nullptr);
     __syncthreads();
     if (warp == kSoftWarps + kCodeWarps) tmem_free(*tmem_at, kCols);
     return;
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     } else if (warp == kSoftWarps + kCodeWarps + 1) {
       // ================================== planning =======================================
       ChunkWalk<kTile> walk;
-      walk.start(p, pre);  // (the tiles over the plan wait for the first piece)
+      walk.start(p, pre, blockIdx.x, gridDim.x);  // (the tiles over the plan wait for the first piece)
       ChunkPiece q;
       Ring ro;
       bool recorded = false;
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         more = walk.next(p, q);
         const int i0 = q.tile * p.tile_tok, n = more ? min(p.tile_tok, q.s.n - i0) : 0;
         if (more && q.slot >= 0 && (q.slot & 1)) {
-          if (lane == 0) write_record(p, &q);
+          if (lane == 0) write_record(p, blockIdx.x, &q);
           recorded = true;
         }
         if (more && q.blk0 >= q.blk1) {  // rows that see nothing here: zero, or an empty partial
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         __syncwarp();
         ro.next(kPieces);
       }
-      if (!recorded && lane == 0) write_record(p, nullptr);
+      if (!recorded && lane == 0) write_record(p, blockIdx.x, nullptr);
     }
   }
   tc_fence_before();

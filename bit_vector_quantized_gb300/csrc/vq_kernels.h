@@ -156,11 +156,11 @@ struct SlotsParams {
   int batch, max_pages, free_capacity, page_size, max_tokens;
 };
 
-// A tile of query rows whose keys more than one CTA of the chunk kernel took:
-// CTA c (the record's index) began it in slot 2c + 1, CTAs c + 1 .. last_cta
-// went on in their slots 2c'.  rows 0: none.
+// A tile of query rows whose keys more than one worker of the chunk kernel
+// took: worker c (the record's index) began it in slot 2c + 1, workers
+// c + 1 .. last went on in their slots 2c'.  rows 0: none.
 struct __align__(16) ChunkRecord {
-  int rows, row0, kvh, last_cta;  // tile row r: token row0 + r / G, head kvh G + r % G
+  int rows, row0, kvh, last;  // tile row r: token row0 + r / G, head kvh G + r % G
 };
 
 struct ChunkParams {
@@ -174,9 +174,9 @@ struct ChunkParams {
   const int32_t* page_table;  // [B][max_pages]
   const int32_t* seq_lens;    // [B] tokens, the new ones among them
   const int32_t* cu;          // [B + 1] row offsets, or NULL: one row per sequence
-  float* ws_o;                // [2 grid][tile_rows][128] unnormalised partials
-  float2* ws_ml;              // [2 grid][tile_rows] (maximum in log2 units, sum)
-  ChunkRecord* records;       // [grid]
+  float* ws_o;                // [2 workers][tile_rows][128] unnormalised partials
+  float2* ws_ml;              // [2 workers][tile_rows] (maximum in log2 units, sum)
+  ChunkRecord* records;       // [workers]
   int32_t* status;
   long long num_pages;
   int batch, num_tokens, hq, hkv, group;
@@ -184,7 +184,7 @@ struct ChunkParams {
   int page_shift;             // log2 of page_size, or -1
   int window, sinks;          // window 0: none
   int tile_tok, tile_rows;    // tokens and (padded) rows of a tile
-  int gap, min_range;         // a tile's fixed cost and a CTA's least share, in tokens
+  int gap, min_range;         // a tile's fixed cost and a worker's least share, in tokens
   float qscale;               // softmax scale * log2(e) / sqrt(128)
   unsigned long long timeout_ns;
 };
@@ -354,7 +354,8 @@ cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int
                                 cudaStream_t stream);
 cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
                               cudaStream_t stream);
-cudaError_t launch_chunk_merge(const ChunkParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams& p, int workers, cudaStream_t stream);
 constexpr int kChunkMaxBatch = 1024;
+constexpr int kFewGroups = 4;  // workers per CTA of the kernel for 8 rows and fewer
 
 }  // namespace vqk
