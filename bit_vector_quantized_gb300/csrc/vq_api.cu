@@ -1216,7 +1216,7 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.tile_rows = tile_rows;
   p.tile_tok = p.tile_rows / p.group;
   const bool wide = p.tile_rows == 128;
-  p.gap = wide ? 384 : 256;
+  p.gap = wide ? 640 : 256;
   p.min_range = 512;
   p.timeout_ns = 2000000000ULL;
   const float scale = softmax_scale == 0.f ? 1.f / std::sqrt(static_cast<float>(L.head_dim)) : softmax_scale;

@@ -316,26 +316,31 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       float m = -INFINITY, l = 0.f;
       // ---- q~ = q diag(lambda) H: the first butterfly joins the halves, then 64 of this half ----
       {
-        const __half* q = static_cast<const __half*>(p.q) + row * kHeadDim;
-        const float* lam = p.lambda + u.kvh * kHeadDim;
-        float x[64];
-        const float sg = g ? -p.qscale : p.qscale;
+        // lambda by way of shared memory (the maxima's place); the row itself in one round trip
+        float* const lam = tops;
+        if (tid < kHeadDim) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
+        uint4 raw[16];
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) + row * kHeadDim);
 #pragma unroll
-        for (int i = 0; i < 64; i += 8) {
-          uint4 a = make_uint4(0, 0, 0, 0), b = a;
-          if (live) {
-            a = __ldg(reinterpret_cast<const uint4*>(q + i));
-            b = __ldg(reinterpret_cast<const uint4*>(q + 64 + i));
-          }
-          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        for (int i = 0; i < 16; ++i) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (live) raw[i] = __ldg(q + i);
+        }
+        asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");
+        float x[64];
+        const float sg = g ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t aw[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const uint32_t bw[4] = {raw[8 + i].x, raw[8 + i].y, raw[8 + i].z, raw[8 + i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
             const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
-            const float2 la = __ldg(reinterpret_cast<const float2*>(lam + i) + e);
-            const float2 lb = __ldg(reinterpret_cast<const float2*>(lam + 64 + i) + e);
-            x[i + 2 * e] = fmaf(fb.x * lb.x, sg, fa.x * la.x * p.qscale);
-            x[i + 2 * e + 1] = fmaf(fb.y * lb.y, sg, fa.y * la.y * p.qscale);
+            const float2 la = *reinterpret_cast<const float2*>(lam + 8 * i + 2 * e);
+            const float2 lb = *reinterpret_cast<const float2*>(lam + 64 + 8 * i + 2 * e);
+            x[8 * i + 2 * e] = fmaf(fb.x * lb.x, sg, fa.x * la.x);
+            x[8 * i + 2 * e + 1] = fmaf(fb.y * lb.y, sg, fa.y * la.y);
           }
         }
         fwht64(x);
@@ -348,6 +353,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
           tmem_st16(tmem + lanes + kColQ + 32 * g + 16 * c, hi);
           tmem_st16(tmem + lanes + kColQ + 64 + 32 * g + 16 * c, lo);
         }
+        asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");  // lambda is read: maxima from here on
       }
       tmem_wait_st();
       tc_fence_before();
@@ -369,14 +375,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
                            (seen.x & seen.y & seen.z & seen.w) == kAll;
         tmem_wait_ld();
         if (!whole) {
-          auto mask = [&](uint32_t(&s)[32], int t_first, uint32_t here) {
+          // the row sees tokens up to pos, from `from` on, and the sinks: as bits of a half's two words
+          const int from = p.window > 0 ? pos - p.window + 1 : 0;
+          auto bits = [](int lo, int hi) {  // bits lo .. hi - 1 of 32, whatever the two are
+            const uint32_t up = hi >= 32 ? kAll : hi <= 0 ? 0u : (1u << hi) - 1u;
+            const uint32_t down = lo >= 32 ? kAll : lo <= 0 ? 0u : (1u << lo) - 1u;
+            return up & ~down;
+          };
+          auto mask = [&](uint32_t(&s)[32], int t, uint32_t here) {
             // (tokens past the sequence's end are not in `seen`)
+            const uint32_t see = here & bits(0, pos + 1 - t) & (bits(from - t, 32) | bits(0, p.sinks - t));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int t = t_first + i;
-              const bool see = (here >> i & 1u) && t <= pos && (p.window == 0 || t > pos - p.window || t < p.sinks);
-              if (!see) s[i] = __float_as_uint(-INFINITY);
-            }
+            for (int i = 0; i < 32; ++i) s[i] = see >> i & 1u ? s[i] : __float_as_uint(-INFINITY);
           };
           mask(s0, t0 + 64 * g, g ? seen.z : seen.x);
           mask(s1, t0 + 64 * g + 32, g ? seen.w : seen.y);
