@@ -28,6 +28,16 @@
 namespace vqk {
 namespace {
 
+// fp32 pair -> fp16 pairs of the high and low parts, hi + lo == x to about 2^-22 relative
+// (split_half2's values, by packed conversions: half the instructions).
+__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
 struct ChunkSeq {
   int row0;   // first row (new token) in q and out
   int n;      // new tokens (0: nothing to do)
@@ -83,11 +93,11 @@ __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, const Chun
 
 // Estimated length of tiles 0 .. j-1 of one (sequence, KV head): each
 // kGap + clamp(base + (t + 1) TT, 0, cap).
-__device__ __forceinline__ long long chunk_sum(const ChunkParams& p, const ChunkSeq& s, long long j) {
-  const long long TT = p.tile_tok, base = max(s.base, 0), cap = p.window > 0 ? min(static_cast<long long>(s.limit), static_cast<long long>(p.window) + p.sinks + TT) : s.limit;
-  long long rise = cap > base ? (cap - base) / TT : 0;  // tiles below the cap
-  rise = min(rise, j);
-  return j * p.gap + rise * base + TT * (rise * (rise + 1) / 2) + (j - rise) * cap;
+__device__ __forceinline__ long long chunk_sum(const ChunkParams& p, const ChunkSeq& s, int j) {
+  const int TT = p.tile_tok, base = max(s.base, 0);
+  const int cap = p.window > 0 ? static_cast<int>(min(static_cast<long long>(s.limit), static_cast<long long>(p.window) + p.sinks + TT)) : s.limit;
+  const long long rise = min(cap > base ? static_cast<int>(static_cast<unsigned>(cap - base) / static_cast<unsigned>(TT)) : 0, j);  // tiles below the cap
+  return static_cast<long long>(j) * p.gap + rise * base + TT * (rise * (rise + 1) / 2) + (j - rise) * cap;
 }
 
 struct ChunkPiece {

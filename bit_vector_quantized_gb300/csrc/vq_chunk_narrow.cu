@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
         fwht128_warp(x, lane);
       }
       uint2 vh, vl;
-      split_half2(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
-      split_half2(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
+      split_pair(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
+      split_pair(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
       *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
       *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
     }
@@ -323,10 +323,12 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
           pr[r][3] = fast_exp2(s[1][2 * r + 1] - mu);
           l[r] += (pr[r][0] + pr[r][1]) + (pr[r][2] + pr[r][3]);
         }
-        const uint32_t a0 = pack_half2(__float2half_rn(pr[0][0]), __float2half_rn(pr[0][1]));
-        const uint32_t a1 = pack_half2(__float2half_rn(pr[1][0]), __float2half_rn(pr[1][1]));
-        const uint32_t a2 = pack_half2(__float2half_rn(pr[0][2]), __float2half_rn(pr[0][3]));
-        const uint32_t a3 = pack_half2(__float2half_rn(pr[1][2]), __float2half_rn(pr[1][3]));
+        auto pack = [](float a, float b) {
+          const __half2 h = __floats2half2_rn(a, b);
+          return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        const uint32_t a0 = pack(pr[0][0], pr[0][1]), a1 = pack(pr[1][0], pr[1][1]);
+        const uint32_t a2 = pack(pr[0][2], pr[0][3]), a3 = pack(pr[1][2], pr[1][3]);
         // ---- o += p V -------------------------------------------------------------------
         auto pv = [&](int nb, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
           mma16816(o[nb], a0, a1, a2, a3, pair_lo(w0, w1), pair_lo(w2, w3));
@@ -589,8 +591,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
         fwht128_warp(x, lane);
       }
       uint2 vh, vl;
-      split_half2(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
-      split_half2(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
+      split_pair(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
+      split_pair(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
       *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
       *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
     }
@@ -714,22 +716,25 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
           }
         }
         uint32_t b[2];  // tokens 0..7 and 8..15
+        float pr[NR][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float pr[NR];
+        for (int r = 0; r < NR; ++r) {
+          const float mu = m[r] == -INFINITY ? 0.f : m[r];
+          pr[r][0] = fast_exp2(x[r][0] - mu);
+          pr[r][1] = fast_exp2(x[r][1] - mu);
+          l[r] += pr[r][0] + pr[r][1];
+        }
+        if constexpr (kPair) {
+          uint32_t hi, lo;
+          split_pair(pr[0][0], pr[0][1], hi, lo);
+          b[0] = movmatrix_trans(pair_lo(hi, lo));
+          b[1] = movmatrix_trans(pair_hi(hi, lo));
+        } else {
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            pr[r] = fast_exp2(x[r][e] - (m[r] == -INFINITY ? 0.f : m[r]));
-            l[r] += pr[r];
+          for (int e = 0; e < 2; ++e) {
+            const __half2 h = __floats2half2_rn(pr[0][e], pr[NR - 1][e]);
+            b[e] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));
           }
-          uint32_t w;
-          if constexpr (kPair) {
-            const __half h = __float2half_rn(pr[0]);
-            w = pack_half2(h, __float2half_rn(pr[0] - __half2float(h)));
-          } else {
-            w = pack_half2(__float2half_rn(pr[0]), __float2half_rn(pr[NR - 1]));
-          }
-          b[e] = movmatrix_trans(w);
         }
         // ---- o^T += V^T p ------------------------------------------------------------------
         auto pv = [&](int mb, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {

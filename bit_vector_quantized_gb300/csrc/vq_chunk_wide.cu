@@ -8,7 +8,7 @@
 // the codes are 8 KB, so the kernel is bound by arithmetic: the tensor pipe
 // first, the softmax's exponentials and the expansion of the codes beside it.
 //
-//   * Eight warps expand codes: a thread takes one token's codes of 64 dims
+//   * Sixteen warps expand codes: a thread takes one token's codes of 32 dims
 //     (loaded two blocks ahead, page first), gathers their centroids from the
 //     replicated, bank-conflict-free table and stores 16-byte pieces into the
 //     swizzled tiles that the tensor core reads (K rows of dims, V rows of
@@ -16,7 +16,7 @@
 //     of V.
 //   * One thread issues the products: scores of block j + 1 before the values
 //     of block j, so the tensor pipe works while the softmax of block j runs.
-//   * Four warps hold one query row per thread: the Walsh-Hadamard transform
+//   * Eight warps hold half a query row per thread: the Walsh-Hadamard transform
 //     of their q row in registers, the online softmax (maximum and sum in
 //     fp32; the maximum may lag by 2^8, so O is seldom rescaled), P rounded
 //     to fp16 once (p <= 2^8: relative 2^-11, averaging out over the tokens).
@@ -35,10 +35,10 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
 constexpr int kTile = 128;           // query rows of a tile, and tokens of a block
-constexpr int kSoftWarps = 8, kCodeWarps = 8;
-constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has one busy warp
-// Registers per thread: 96 at the launch (640 threads), then 256 x 128 + 256 x 80 + 128 x 56 <= 640 x 96.
-constexpr int kSoftRegs = 128, kCodeRegs = 80, kIssueRegs = 56;
+constexpr int kSoftWarps = 8, kCodeWarps = 16;
+constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
+// Registers per thread: 72 at the launch (896 threads), then 256 x 112 + 512 x 56 + 128 x 56 = 896 x 72.
+constexpr int kSoftRegs = 112, kCodeRegs = 56, kIssueRegs = 56;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kKStages = 2;
 constexpr int kMasks = 4;            // token masks in flight: a slot comes round after the softmax of its block
@@ -57,29 +57,38 @@ struct WideSmem {
   static_assert((kChunkMaxBatch + 1 + 32) * 8 <= kTileBytes, "the plan shares a tile");
 };
 
-// Codes of one token's 64-dim half, and the table offset of code i.
+// Codes of one token's 32 dims (quarter 0 .. 3 of the head), loaded ahead of their use: the loads are
+// volatile, so that they stay where they are issued, and nothing is computed from the words before
+// align().
+__device__ __forceinline__ uint32_t ld_word(const uint8_t* at) {
+  uint32_t x;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(at));
+  return x;
+}
 template <int D, int B>
-struct HalfCodes {
-  static constexpr int kCodes = 64 / D;
-  static constexpr int kWords = B == 9 ? 5 : kCodes * B / 32;
+struct QuarterCodes {
+  static constexpr int kCodes = 32 / D;
+  static constexpr int kWords = (kCodes * B + 31) / 32;  // 9- and 12-bit codes start inside their first word
   uint32_t w[kWords];
-  __device__ __forceinline__ void load(const uint8_t* row, int half) {
-    if constexpr (B == 8) {
+  __device__ __forceinline__ void load(const uint8_t* row, int quarter) {
+    if constexpr (B == 8 && kWords == 4) {
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(row + 16 * quarter));
+    } else if constexpr (B == 8) {
+      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(row + 8 * quarter));
+    } else {
+      const uint8_t* at = row + quarter * kCodes * B / 32 * 4;
 #pragma unroll
-      for (int i = 0; i < kWords; i += 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + half * kCodes) + i / 4);
-        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-      }
-    } else if constexpr (B == 9) {  // 144 bits from bit 0 or bit 144 (word 4, bit 16)
-      const uint32_t* r = reinterpret_cast<const uint32_t*>(row) + 4 * half;
-      uint32_t x[5];
+      for (int i = 0; i < kWords; ++i) w[i] = ld_word(at + 4 * i);
+    }
+  }
+  // Code 0 to bit 0.
+  __device__ __forceinline__ void align(int quarter) {
+    if constexpr (B != 8) {
+      const int s = quarter * kCodes * B & 31;
 #pragma unroll
-      for (int i = 0; i < 5; ++i) x[i] = __ldg(r + i);
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = __funnelshift_r(x[i], i < 4 ? x[i + 1] : 0u, 16 * half);
-    } else {  // 12-bit codes: 96 bits
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + kWords * half + i);
+      for (int i = 0; i < kWords; ++i) w[i] = i + 1 < kWords ? __funnelshift_r(w[i], w[i + 1], s) : w[i] >> s;
     }
   }
   __device__ __forceinline__ uint32_t code(int i) const {
@@ -92,11 +101,12 @@ struct HalfCodes {
     }
   }
 };
+static_assert(QuarterCodes<4, 9>::kWords == 3 && QuarterCodes<8, 12>::kWords == 2, "72 + 24 and 48 + 16 bits");
 
-// 16-byte piece c (dims 8c .. 8c + 7) of the half: its centroids.
+// 16-byte piece c (dims 8c .. 8c + 7) of the quarter: its centroids.
 // row_shift: log2 of the table's row bytes; lane: the lane's byte in a row.
 template <int D, int B, int kRowShift>
-__device__ __forceinline__ uint4 gather_piece(const HalfCodes<D, B>& x, int c, uint32_t lane) {
+__device__ __forceinline__ uint4 gather_piece(const QuarterCodes<D, B>& x, int c, uint32_t lane) {
   auto off = [&](int i) {
     if constexpr (B == 8 && kRowShift == 8) return row_addr(x.w[i >> 2], lane, i & 3);
     else return (x.code(i) << kRowShift) + lane;
@@ -314,46 +324,60 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       const long long row = static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (live ? r - token * G : 0);
       const int nblk = u.blk1 - u.blk0;
       float m = -INFINITY, l = 0.f;
-      // ---- q~ = q diag(lambda) H: the first butterfly joins the halves, then 64 of this half ----
+      // ---- q~ = q diag(lambda) H: 64 elements here, then the butterfly of the two halves --------
       {
-        // lambda by way of shared memory (the maxima's place); the row itself in one round trip
+        // lambda by way of shared memory (the maxima's place), this thread's 64 elements in one round trip
         float* const lam = tops;
         if (tid < kHeadDim) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
-        uint4 raw[16];
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) + row * kHeadDim);
+        uint4 raw[8];
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) + row * kHeadDim + 64 * g);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           raw[i] = make_uint4(0, 0, 0, 0);
           if (live) raw[i] = __ldg(q + i);
         }
         asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");
         float x[64];
-        const float sg = g ? -1.f : 1.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t aw[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          const uint32_t bw[4] = {raw[8 + i].x, raw[8 + i].y, raw[8 + i].z, raw[8 + i].w};
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&aw[e]));
-            const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&bw[e]));
-            const float2 la = *reinterpret_cast<const float2*>(lam + 8 * i + 2 * e);
-            const float2 lb = *reinterpret_cast<const float2*>(lam + 64 + 8 * i + 2 * e);
-            x[8 * i + 2 * e] = fmaf(fb.x * lb.x, sg, fa.x * la.x);
-            x[8 * i + 2 * e + 1] = fmaf(fb.y * lb.y, sg, fa.y * la.y);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+            const float2 v = *reinterpret_cast<const float2*>(lam + 64 * g + 8 * i + 2 * e);
+            x[8 * i + 2 * e] = f.x * v.x;
+            x[8 * i + 2 * e + 1] = f.y * v.y;
           }
         }
         fwht64(x);
         __syncwarp();
+        // the last butterfly joins the row's two threads, by way of the scores' columns (free by now)
+        {
+          uint32_t y[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[16], lo[16];
+          for (int c = 0; c < 2; ++c) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) split_half2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1], hi[i], lo[i]);
-          tmem_st16(tmem + lanes + kColQ + 32 * g + 16 * c, hi);
-          tmem_st16(tmem + lanes + kColQ + 64 + 32 * g + 16 * c, lo);
+            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[32 * c + i]);
+            tmem_st32(tmem + lanes + kColS + 64 * g + 32 * c, y);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          row_sync();
+          tc_fence_after();
+          const float sg = g ? -1.f : 1.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(tmem + lanes + kColS + 64 * (g ^ 1) + 32 * c, y);
+            tmem_wait_ld();
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              split_pair(fmaf(x[32 * c + 2 * i], sg, __uint_as_float(y[2 * i])),
+                          fmaf(x[32 * c + 2 * i + 1], sg, __uint_as_float(y[2 * i + 1])), hi[i], lo[i]);
+            tmem_st16(tmem + lanes + kColQ + 32 * g + 16 * c, hi);
+            tmem_st16(tmem + lanes + kColQ + 64 + 32 * g + 16 * c, lo);
+          }
         }
-        asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");  // lambda is read: maxima from here on
       }
       tmem_wait_st();
       tc_fence_before();
@@ -494,13 +518,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
     reg_dec<kCodeRegs>();
-    const int w = warp - kSoftWarps, half = w & 1, quarter = w >> 1;
-    const int tok = 32 * quarter + lane;
+    const int w = warp - kSoftWarps, quarter = w & 3, tok = 32 * (w >> 2) + lane;  // dims and token of the thread
     const uint32_t rep = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
     const uint32_t lane_k = W::kWideCodes ? 0u : rep;
     const uint32_t lane_v = W::kWideCodes ? 65536u : W::kSplitTable ? 32768u + rep_v : 128u + rep_v;
     constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
-    const uint32_t dst = smem_addr(tiles) + half * (kTileBytes / 2) + tok * 128 + ((tok & 7) << 4);  // (piece 0, swizzled)
+    // the quarter's first 16-byte piece, swizzled (the quarter's four: this address ^ (c << 4))
+    const uint32_t dst = smem_addr(tiles) + (quarter >> 1) * (kTileBytes / 2) + tok * 128 + (((tok & 7) ^ (4 * (quarter & 1))) << 4);
     auto store = [&](uint32_t at, int c, uint4 v) {
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
@@ -547,8 +571,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       return x;
     };
     struct Codes {
-      HalfCodes<DK, BK> k;
-      HalfCodes<DV, BV> v;
+      QuarterCodes<DK, BK> k;
+      QuarterCodes<DV, BV> v;
       bool has;  // the token can be read
     };
     auto fetch = [&](const Where& x, Codes& y) {
@@ -556,12 +580,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       if (x.in && !y.has) report(p.status, kDevBadPage);
       if (y.has) {
         const long long row = (static_cast<long long>(x.page) * p.hkv + x.kvh) * p.page_size + x.off;
-        y.k.load(p.k_pool + row * KROW, half);
-        y.v.load(p.v_pool + row * VROW, half);
+        y.k.load(p.k_pool + row * KROW, quarter);
+        y.v.load(p.v_pool + row * VROW, quarter);
       }
     };
     Codes now, next;
-    HalfCodes<DV, BV> v_prev;
+    QuarterCodes<DV, BV> v_prev;
     bool has_prev = false, any_prev = false;
     const Where first = advance();
     Where ahead = advance();
@@ -578,10 +602,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       if (any) {
         if (!wait(k_empty + rk.slot, rk.phase ^ 1u)) break;
         const uint32_t at = dst + rk.slot * kTileBytes;
+        now.k.align(quarter);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) store(at, c, now.has ? gather_piece<DK, BK, kShift>(now.k, c, lane_k) : make_uint4(0, 0, 0, 0));
+        for (int c = 0; c < 4; ++c) store(at, c, now.has ? gather_piece<DK, BK, kShift>(now.k, c, lane_k) : make_uint4(0, 0, 0, 0));
         const uint32_t seen = __ballot_sync(kAll, now.has);
-        if (half == 0 && lane == 0) masks[(blocks % kMasks) * 4 + quarter] = seen;
+        if (quarter == 0 && lane == 0) masks[(blocks % kMasks) * 4 + (w >> 2)] = seen;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(k_full + rk.slot);
@@ -591,8 +616,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       if (any_prev) {
         if (!wait(v_empty + rv.slot, rv.phase ^ 1u)) break;
         const uint32_t at = dst + (kKStages + rv.slot) * kTileBytes;
+        v_prev.align(quarter);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < 4; ++c)
           store(at, c, has_prev ? gather_piece<DV, BV, kShift>(v_prev, c, lane_v) : make_uint4(0, 0, 0, 0));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -689,6 +715,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
             }
           }
           continue;
+        }
+        if (more) {  // the tile's query rows, for the softmax warps a piece later
+          const char* rows = reinterpret_cast<const char*>(static_cast<const __half*>(p.q) +
+                                                           (static_cast<long long>(q.s.row0 + i0) * p.hq + q.kvh * p.group) * kHeadDim);
+          const int lines = 2 * p.group;  // a token's rows, 128 bytes each line
+          for (int i = lane; i < n * lines; i += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + static_cast<long long>(i / lines) * p.hq * (kHeadDim * 2) + (i % lines) * 128));
         }
         if (!wait(piece_empty + ro.slot, ro.phase ^ 1u)) break;
         if (lane == 0) {
