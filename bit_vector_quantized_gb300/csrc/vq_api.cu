@@ -1092,16 +1092,17 @@ vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const in
 namespace {
 
 // Tile height of a call, by the rows of its longest (sequence, KV head): all
-// of them where 8 or 16 hold them (warp mma), else 128 (tcgen05).
-// VQ_CHUNK_ROWS=16|128 selects a height explicitly (a tuning switch for
+// of them where 8 or 16 hold them (warp mma), else 128 (tcgen05) or 256 (a
+// pair of CTAs on one product).  VQ_CHUNK_ROWS=16|128|256 selects a height explicitly (a tuning switch for
 // profiling).
 int chunk_tile_rows(const vq_layout& L, int max_new_len) {
   const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
   if (const char* env = std::getenv("VQ_CHUNK_ROWS")) {
     if (std::strcmp(env, "16") == 0) return 16;
     if (std::strcmp(env, "128") == 0) return 128;
+    if (std::strcmp(env, "256") == 0) return 256;
   }
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 128;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
 }
 
 struct ChunkWs {
@@ -1109,7 +1110,9 @@ struct ChunkWs {
 };
 
 // Workers of a launch over `grid` CTAs.
-int chunk_workers(int tile_rows, int grid) { return tile_rows == 8 ? vqk::kFewGroups * grid : grid; }
+int chunk_workers(int tile_rows, int grid) {
+  return tile_rows == 8 ? vqk::kFewGroups * grid : tile_rows == 256 ? grid / 2 : grid;
+}
 
 // Two partials and a record per worker.
 ChunkWs chunk_ws(int tile_rows, int grid) {
@@ -1132,8 +1135,12 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
     return 0;
   const int sms = num_sms > 0 ? num_sms : device_sms();
   if (sms <= 0) return 0;
-    // a call with smaller bounds may take a lower tile, whose slots are more
-  return std::max(chunk_ws(chunk_tile_rows(*layout, max_new_len), sms).total, chunk_ws(8, sms).total);
+  // a call with smaller bounds may take a lower tile, whose slots may be more
+  size_t most = 0;
+  const int need = chunk_tile_rows(*layout, max_new_len);
+  for (int rows : {8, 16, 128, 256})
+    if (rows <= need) most = std::max(most, chunk_ws(rows, sms).total);
+  return most;
 }
 
 vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
@@ -1176,8 +1183,8 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
     return fail(VQ_ERR_INVALID_ARG, "out overlaps q");
   const int sms = device_sms();
   if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
-  const int grid = sms;
   const int tile_rows = chunk_tile_rows(L, max_new_len);
+  const int grid = tile_rows == 256 ? std::max(sms & ~1, 2) : sms;
   const ChunkWs ws = chunk_ws(tile_rows, grid);
   if (workspace_bytes < ws.total)
     return fail(VQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, ws.total);
@@ -1214,8 +1221,8 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.window = std::min(window, 1 << 30);  // no position is further back: the same as none
   p.sinks = std::min(num_sinks, 1 << 30);
   p.tile_rows = tile_rows;
-  p.tile_tok = p.tile_rows / p.group;
-  const bool wide = p.tile_rows == 128;
+  p.tile_tok = p.tile_rows == 256 ? 2 * (128 / p.group) : p.tile_rows / p.group;
+  const bool wide = p.tile_rows >= 128;
   p.gap = wide ? 640 : 256;
   p.min_range = 512;
   p.timeout_ns = 2000000000ULL;

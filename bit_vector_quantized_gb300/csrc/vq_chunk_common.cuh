@@ -217,7 +217,7 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, long long* pre,
 __device__ __forceinline__ void write_record(const ChunkParams& p, int worker, const ChunkPiece* q) {
   ChunkRecord r = {};
   if (q) {
-    r.rows = min(p.tile_tok, q->s.n - q->tile * p.tile_tok) * p.group;
+    r.tokens = min(p.tile_tok, q->s.n - q->tile * p.tile_tok);
     r.row0 = q->s.row0 + q->tile * p.tile_tok;
     r.kvh = q->kvh;
     r.last = q->last;

@@ -832,8 +832,11 @@ __global__ void __launch_bounds__(256) vq_chunk_merge_kernel(const ChunkParams p
   pdl_wait();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.records + c0));
-  const int rows = rec.x;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+  const int half = p.tile_rows == 256 ? 128 : p.tile_rows, half_tok = p.tile_tok * half / p.tile_rows;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < p.tile_rows; r += gridDim.y * 8) {
+    // row r: of 256 rows, each 128 hold half of the tile's tokens
+    const int in_half = r % half, token = r / half * half_tok + in_half / p.group;
+    if (in_half >= half_tok * p.group || token >= rec.x) continue;
     auto at = [&](int w) {
       return static_cast<long long>(w == c0 ? 2 * c0 + 1 : 2 * w) * p.tile_rows + r;
     };
@@ -860,7 +863,7 @@ __global__ void __launch_bounds__(256) vq_chunk_merge_kernel(const ChunkParams p
     uint2 w;
     w.x = *reinterpret_cast<const uint32_t*>(&h0);
     w.y = *reinterpret_cast<const uint32_t*>(&h1);
-    const long long row = static_cast<long long>(rec.y + r / p.group) * p.hq + rec.z * p.group + r % p.group;
+    const long long row = static_cast<long long>(rec.y + token) * p.hq + rec.z * p.group + in_half % p.group;
     reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + row * kHeadDim)[lane] = w;
   }
 }

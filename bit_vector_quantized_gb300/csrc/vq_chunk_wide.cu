@@ -34,27 +34,38 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
-constexpr int kTile = 128;           // query rows of a tile, and tokens of a block
-constexpr int kSoftWarps = 8, kCodeWarps = 16;
-constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
-// Registers per thread: 72 at the launch (896 threads), then 256 x 112 + 512 x 56 + 128 x 56 = 896 x 72.
-constexpr int kSoftRegs = 112, kCodeRegs = 56, kIssueRegs = 56;
-constexpr int kTileBytes = kTile * kHeadDim * 2;
-constexpr int kKStages = 2;
-constexpr int kMasks = 4;            // token masks in flight: a slot comes round after the softmax of its block
+constexpr int kTile = 128;           // query rows of a CTA's tile, and tokens of a block
+constexpr int kSoftWarps = 8;
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
 
-template <int DK, int BK, int DV, int BV>
+// One CTA alone, or the two CTAs of a pair that share a block's tiles.
+template <bool kPair>
+struct WideShape {
+  static constexpr int kCodeWarps = kPair ? 8 : 16;
+  static constexpr int kThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
+  // Registers per thread.  Alone: 72 at the launch (896 threads), then 256 x 112 + 512 x 56 + 128 x 56
+  // = 896 x 72.  Pair: 96 (640 threads), then 256 x 128 + 256 x 80 + 128 x 56 <= 640 x 96.
+  static constexpr int kSoftRegs = kPair ? 128 : 112, kCodeRegs = kPair ? 80 : 56, kIssueRegs = 56;
+  static constexpr int kTileBytes = kTile * kHeadDim * 2 / (kPair ? 2 : 1);  // of K or V, this CTA's part
+  static constexpr int kKStages = kPair ? 3 : 2;
+  // Token masks in flight: block b's K tile is stored once the scores of block b - kKStages are done,
+  // and with them only the softmax of block b - kKStages - 2.
+  static constexpr int kMasks = kPair ? 8 : 4;
+  static_assert(kMasks >= kKStages + 2, "a mask's slot comes round after its reader");
+};
+
+template <int DK, int BK, int DV, int BV, bool kPair>
 struct WideSmem {
+  using Shape = WideShape<kPair>;
   static constexpr bool kWideCodes = DK == 8;      // 1.5-bit format: plain 64 KB tables
   static constexpr bool kSplitTable = BV == 9;     // 128-byte rows, K then V; else 256-byte rows (K, V)
   static constexpr int kTable = kWideCodes ? 131072 : kSplitTable ? (256 + 512) * 128 : 65536;
-  static constexpr int kVStages = kWideCodes ? 1 : 2;
+  static constexpr int kVStages = kPair ? 3 : kWideCodes ? 1 : 2;
   static constexpr int kTiles = kTable;                             // K stages, then V stages
-  static constexpr int kMisc = kTiles + (kKStages + kVStages) * kTileBytes;
-  static constexpr int kTotal = kMisc + 640 + 2 * 2 * kTile * 4;
+  static constexpr int kMisc = kTiles + (Shape::kKStages + kVStages) * Shape::kTileBytes;
+  static constexpr int kTotal = kMisc + 704 + 2 * 2 * kTile * 4;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
-  static_assert((kChunkMaxBatch + 1 + 32) * 8 <= kTileBytes, "the plan shares a tile");
+  static_assert((kChunkMaxBatch + 1 + 32) * 8 <= Shape::kTileBytes, "the plan shares a tile");
 };
 
 // Codes of one token's 32 dims (quarter 0 .. 3 of the head), loaded ahead of their use: the loads are
@@ -123,7 +134,7 @@ __device__ __forceinline__ uint4 gather_piece(const QuarterCodes<D, B>& x, int c
 
 template <int DK, int BK, int DV, int BV>
 __device__ __forceinline__ void fill_wide_table(const ChunkParams& p) {
-  using W = WideSmem<DK, BK, DV, BV>;
+  using W = WideSmem<DK, BK, DV, BV, false>;  // (the table is the same in a pair)
   uint4* tab = reinterpret_cast<uint4*>(g_smem);
   auto replicas = [](const void* cb, int row, bool four) {
     if (four) {
@@ -216,18 +227,21 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-template <int DK, int BK, int DV, int BV>
-__global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
-  using W = WideSmem<DK, BK, DV, BV>;
-  constexpr int NV = W::kVStages;
+template <int DK, int BK, int DV, int BV, bool kPair>
+__global__ void __launch_bounds__(WideShape<kPair>::kThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
+  using W = WideSmem<DK, BK, DV, BV, kPair>;
+  using Shape = WideShape<kPair>;
+  constexpr int NV = W::kVStages, kKStages = Shape::kKStages, kMasks = Shape::kMasks, kTileBytes = Shape::kTileBytes;
+  constexpr int kCodeWarps = Shape::kCodeWarps, kCtas = kPair ? 2 : 1;
   constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
   uint8_t* const tiles = g_smem + W::kTiles;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(g_smem + W::kMisc);
-  uint64_t* const k_full = bars;               // [2] code warps -> products
-  uint64_t* const k_empty = k_full + kKStages; // [2] products -> code warps
-  uint64_t* const v_full = k_empty + kKStages; // [NV]
-  uint64_t* const v_empty = v_full + 2;        // [NV]
-  uint64_t* const s_full = v_empty + 2;        // [2] scores done
+  // (In a pair the first CTA's thread issues for both: what it waits for is arrived on there, by both.)
+  uint64_t* const k_full = bars;               // [kKStages] code warps -> products
+  uint64_t* const k_empty = k_full + 3;        // [kKStages] products -> code warps
+  uint64_t* const v_full = k_empty + 3;        // [NV]
+  uint64_t* const v_empty = v_full + 3;        // [NV]
+  uint64_t* const s_full = v_empty + 3;        // [2] scores done
   uint64_t* const p_full = s_full + 2;         // [2] P stored
   uint64_t* const o_full = p_full + 2;         // values of a block done
   uint64_t* const q_full = o_full + 1;         // Q~ stored, O read
@@ -235,35 +249,39 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   uint64_t* const piece_full = drain + 1;              // [kPieces] planning warp -> everybody
   uint64_t* const piece_empty = piece_full + kPieces;  // [kPieces]
   WidePiece* const pieces = reinterpret_cast<WidePiece*>(bars + 48);  // [kPieces]
-  uint32_t* const masks = reinterpret_cast<uint32_t*>(bars + 24);  // [kMasks][4] tokens that have a page
+  uint64_t* const mask_full = bars + 80;       // [kMasks] code warps -> softmax
+  uint32_t* const masks = reinterpret_cast<uint32_t*>(bars + 28);  // [kMasks][4] tokens that have a page
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
-  float* const tops = reinterpret_cast<float*>(g_smem + W::kMisc + 640);  // [2][2][128] maxima of a row's two halves
+  float* const tops = reinterpret_cast<float*>(g_smem + W::kMisc + 704);  // [2][2][128] maxima of a row's two halves
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
+  const uint32_t rank = kPair ? cluster_rank() : 0u;
+  const int worker = static_cast<int>(blockIdx.x) / kCtas;
   if (smem_addr(tiles) & 1023u) {  // the swizzled tiles need it (and dynamic shared memory alone gives it)
-    if (tid == 0) {
-      report(p.status, kDevBadConfig);
-      write_record(p, blockIdx.x, nullptr);
-    }
+    if (tid == 0) report(p.status, kDevBadConfig);
+    if (tid == 0 && rank == 0) write_record(p, worker, nullptr);
     return;
   }
   fill_wide_table<DK, BK, DV, BV>(p);
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(k_full + i, kCodeWarps);
+      mbar_init(k_full + i, kCtas * kCodeWarps);
       mbar_init(k_empty + i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(v_full + i, kCodeWarps);
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(v_full + i, kCtas * kCodeWarps);
       mbar_init(v_empty + i, 1);
-      mbar_init(s_full + i, 2);  // the products' commit, and the issuer's arrival after its own waits
-      mbar_init(p_full + i, kSoftWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, kCtas * kSoftWarps);
     }
     mbar_init(o_full, 1);
-    mbar_init(q_full, kSoftWarps);
+    mbar_init(q_full, kCtas * kSoftWarps);
     mbar_init(drain, 1);
+    for (int i = 0; i < kMasks; ++i) mbar_init(mask_full + i, 4);
     for (int i = 0; i < static_cast<int>(kPieces); ++i) {
       mbar_init(piece_full + i, 1);
       mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 1);
@@ -271,7 +289,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     mbar_init_fence();
     *abort_flag = 0;
   }
-  if (warp == kSoftWarps + kCodeWarps) tmem_alloc(tmem_at, kCols);
+  if (warp == kSoftWarps + kCodeWarps) tmem_alloc<kPair>(tmem_at, kCols);
   long long* const pre = reinterpret_cast<long long*>(tiles);  // the plan, before the first tile is written
   tc_fence_before();
   chunk_plan(p, pre, pre + kChunkMaxBatch + 1);
@@ -279,13 +297,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   // All 512 columns are this CTA's, so they start at column 0; the constant keeps the
   // products' operands in uniform registers.
   constexpr uint32_t tmem = 0;
-  if (*tmem_at != tmem) {
+  if (*tmem_at != tmem) {  // (in both CTAs of a pair, which allocate together)
     if (tid == 0) report(p.status, kDevBadConfig);
-    if (tid == 0) write_record(p, blockIdx.x, nullptr);
+    if (tid == 0 && rank == 0) write_record(p, worker, nullptr);
     __syncthreads();
-    if (warp == kSoftWarps + kCodeWarps) tmem_free(*tmem_at, kCols);
+    if (warp == kSoftWarps + kCodeWarps) tmem_free<kPair>(*tmem_at, kCols);
     return;
   }
+  if constexpr (kPair) cluster_sync();  // the barriers of both are there before either arrives on the other's
 
   // Bounded wait; on a timeout the CTA is given up.  The warps' form is uniform over the warp.
   auto wait_one = [&](uint64_t* bar, uint32_t phase) {
@@ -297,6 +316,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     return false;
   };
   auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(kAll, wait_one(bar, phase)) != 0; };
+  // An arrival that the issuing thread waits for.
+  auto arrive_issuer = [&](uint64_t* bar) {
+    if constexpr (kPair) mbar_arrive_at(bar, 0);
+    else mbar_arrive(bar);
+  };
   // The next piece (whole warps); false when there is none or the CTA was given up.
   Ring rp;
   auto next_piece = [&](WidePiece& u) {
@@ -311,7 +335,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
 
   if (warp < kSoftWarps) {
     // ====== two threads per query row: columns (and dims) 0 .. 63 and 64 .. 127 of a block ======
-    reg_inc<kSoftRegs>();
+    reg_inc<Shape::kSoftRegs>();
     const int r = tid & (kTile - 1), g = tid >> 7, G = p.group;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the two warps of a row meet here
@@ -382,12 +406,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) arrive_issuer(q_full);
 
       const int pos = live ? u.first_pos + token : -1;
       for (int j = 0; j < nblk; ++j, ++blocks) {
         const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb + 64 * g;
-        ok = wait(s_full + sb, (blocks >> 1) & 1u);
+        ok = wait(mask_full + blocks % kMasks, (blocks / kMasks) & 1u) && wait(s_full + sb, (blocks >> 1) & 1u);
         if (!ok) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
@@ -474,7 +498,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + sb);
+        if (lane == 0) arrive_issuer(p_full + sb);
       }
       if (!ok) break;
       ok = wait(o_full, (blocks - 1) & 1u);
@@ -486,7 +510,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       row_sync();
       l = sums[r] + sums[kTile + r];  // (the same order in both threads)
       const float f = u.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      const long long at = static_cast<long long>(u.slot) * kTile + r;
+      const long long at = static_cast<long long>(u.slot) * (kCtas * kTile) + rank * kTile + r;
 #pragma unroll
       for (int c = 2 * g; c < 2 * g + 2; ++c) {
         uint32_t s[32];
@@ -517,31 +541,49 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     }
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
-    reg_dec<kCodeRegs>();
-    const int w = warp - kSoftWarps, quarter = w & 3, tok = 32 * (w >> 2) + lane;  // dims and token of the thread
+    reg_dec<Shape::kCodeRegs>();
+    // A thread takes 32 dims of a token of K and of V.  Alone, of the same token; in a pair this CTA has
+    // the K of half the block's tokens (B's columns) and half the dims of V (B's columns again).
+    const int w = warp - kSoftWarps;
+    const int tok_v = 32 * (kPair ? w & 3 : w >> 2) + lane;
+    const int tok_k = kPair ? static_cast<int>(64 * rank) + 32 * (w & 1) + lane : tok_v;
+    const int quarter_k = kPair ? w >> 1 : w & 3, quarter_v = kPair ? static_cast<int>(2 * rank) + (w >> 2) : w & 3;
     const uint32_t rep = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
     const uint32_t lane_k = W::kWideCodes ? 0u : rep;
     const uint32_t lane_v = W::kWideCodes ? 65536u : W::kSplitTable ? 32768u + rep_v : 128u + rep_v;
     constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
-    // the quarter's first 16-byte piece, swizzled (the quarter's four: this address ^ (c << 4))
-    const uint32_t dst = smem_addr(tiles) + (quarter >> 1) * (kTileBytes / 2) + tok * 128 + (((tok & 7) ^ (4 * (quarter & 1))) << 4);
+    // the first 16-byte piece, swizzled, of the thread's four (this address ^ (c << 4)); K rows: tokens by
+    // halves of the dims, V rows: tokens by halves of the dims (a pair's CTA: its half alone)
+    const int row_k = kPair ? tok_k & 63 : tok_k, block_k = kPair ? 64 * 128 : kTile * 128;
+    const uint32_t dst_k = smem_addr(tiles) + (quarter_k >> 1) * block_k + row_k * 128 + (((row_k & 7) ^ (4 * (quarter_k & 1))) << 4);
+    const uint32_t dst_v = smem_addr(tiles) + (kPair ? 0 : (quarter_v >> 1) * kTile * 128) + tok_v * 128 +
+                           (((tok_v & 7) ^ (4 * (quarter_v & 1))) << 4);
     auto store = [&](uint32_t at, int c, uint4 v) {
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
     };
-    // Block iterator, two blocks ahead of the tiles: the thread's page; then its codes one ahead.
-    // The token's page and offset follow from the block before, by 128 tokens, where blocks adjoin.
+    // Block iterator, two blocks ahead of the tiles: the token's page; then its codes one ahead.
+    // A token's page and offset follow from the block before, by 128 tokens, where blocks adjoin.
     const int step_page = kTile / p.page_size, step_off = kTile - step_page * p.page_size;
     bool more = true;
-    int i = 0, t = 0, lp = 0, off = 0;
+    int i = 0;
     u.blk1 = 0;
     u.sink = -1;
+    struct Token {  // of the block the iterator is at
+      int t, lp, off;
+    };
+    Token at_k = {}, at_v = {};
     struct Where {
-      int page, off, kvh;
-      bool in, any;  // the token exists; the block exists
+      int page, off;
+      bool in;  // the token exists
+    };
+    struct Block {
+      Where k, v;
+      int kvh;
+      bool any;  // the block exists
     };
     auto advance = [&]() {
-      Where x = {0, 0, 0, false, false};
+      Block x = {};
       bool jump = i == u.sink;
       while (more && i >= u.blk1) {
         more = next_piece(u);
@@ -549,93 +591,105 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         jump = true;
       }
       if (!more) return x;
-      if (jump) {
-        t = u.block(i) * kTile + tok;
-        lp = t / p.page_size;
-        off = t - lp * p.page_size;
-      } else {
-        t += kTile;
-        lp += step_page;
-        off += step_off;
-        if (off >= p.page_size) {
-          off -= p.page_size;
-          ++lp;
+      auto move = [&](Token& y, int tok) {
+        if (jump) {
+          y.t = u.block(i) * kTile + tok;
+          y.lp = y.t / p.page_size;
+          y.off = y.t - y.lp * p.page_size;
+        } else {
+          y.t += kTile;
+          y.lp += step_page;
+          y.off += step_off;
+          if (y.off >= p.page_size) {
+            y.off -= p.page_size;
+            ++y.lp;
+          }
         }
-      }
-      ++i;
-      x.any = true;
-      x.in = t < u.limit;
+        Where z = {0, y.off, y.t < u.limit};
+        if (z.in) z.page = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + y.lp);
+        return z;
+      };
+      x.v = move(at_v, tok_v);
+      x.k = kPair ? move(at_k, tok_k) : x.v;
       x.kvh = u.kvh;
-      x.off = off;
-      if (x.in) x.page = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + lp);
+      x.any = true;
+      ++i;
       return x;
     };
     struct Codes {
       QuarterCodes<DK, BK> k;
       QuarterCodes<DV, BV> v;
-      bool has;  // the token can be read
+      bool has_k, has_v;  // the token can be read
     };
-    auto fetch = [&](const Where& x, Codes& y) {
-      y.has = x.in && x.page >= 0 && x.page < p.num_pages;
-      if (x.in && !y.has) report(p.status, kDevBadPage);
-      if (y.has) {
-        const long long row = (static_cast<long long>(x.page) * p.hkv + x.kvh) * p.page_size + x.off;
-        y.k.load(p.k_pool + row * KROW, quarter);
-        y.v.load(p.v_pool + row * VROW, quarter);
-      }
+    auto fetch = [&](const Block& x, Codes& y) {
+      auto row = [&](const Where& z) {
+        return (static_cast<long long>(z.page) * p.hkv + x.kvh) * p.page_size + z.off;
+      };
+      y.has_v = x.v.in && x.v.page >= 0 && x.v.page < p.num_pages;
+      y.has_k = kPair ? x.k.in && x.k.page >= 0 && x.k.page < p.num_pages : y.has_v;
+      if (x.v.in && !y.has_v) report(p.status, kDevBadPage);
+      if (y.has_k) y.k.load(p.k_pool + row(x.k) * KROW, quarter_k);
+      if (y.has_v) y.v.load(p.v_pool + row(x.v) * VROW, quarter_v);
     };
     Codes now, next;
     QuarterCodes<DV, BV> v_prev;
     bool has_prev = false, any_prev = false;
-    const Where first = advance();
-    Where ahead = advance();
+    const Block first = advance();
+    Block ahead = advance();
     bool any = first.any;
-    now.has = next.has = false;
+    now.has_k = now.has_v = next.has_k = next.has_v = false;
     if (any) fetch(first, now);
     Ring rk, rv;
     uint32_t blocks = 0;
     while (any || any_prev) {
-      const Where then = ahead;
+      const Block then = ahead;
       ahead = advance();
-      next.has = false;
+      next.has_k = next.has_v = false;
       if (then.any) fetch(then, next);
       if (any) {
         if (!wait(k_empty + rk.slot, rk.phase ^ 1u)) break;
-        const uint32_t at = dst + rk.slot * kTileBytes;
-        now.k.align(quarter);
+        const uint32_t at = dst_k + rk.slot * kTileBytes;
+        now.k.align(quarter_k);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) store(at, c, now.has ? gather_piece<DK, BK, kShift>(now.k, c, lane_k) : make_uint4(0, 0, 0, 0));
-        const uint32_t seen = __ballot_sync(kAll, now.has);
-        if (quarter == 0 && lane == 0) masks[(blocks % kMasks) * 4 + (w >> 2)] = seen;
+        for (int c = 0; c < 4; ++c) store(at, c, now.has_k ? gather_piece<DK, BK, kShift>(now.k, c, lane_k) : make_uint4(0, 0, 0, 0));
+        const uint32_t seen = __ballot_sync(kAll, now.has_v);  // (the V tokens: all 128 of the block, by four warps)
+        if ((kPair ? w < 4 : quarter_v == 0) && lane == 0) {
+          masks[(blocks % kMasks) * 4 + (tok_v >> 5)] = seen;
+          mbar_arrive(mask_full + blocks % kMasks);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + rk.slot);
+        if (lane == 0) arrive_issuer(k_full + rk.slot);
         rk.next(kKStages);
         ++blocks;
       }
       if (any_prev) {
         if (!wait(v_empty + rv.slot, rv.phase ^ 1u)) break;
-        const uint32_t at = dst + (kKStages + rv.slot) * kTileBytes;
-        v_prev.align(quarter);
+        const uint32_t at = dst_v + (kKStages + rv.slot) * kTileBytes;
+        v_prev.align(quarter_v);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           store(at, c, has_prev ? gather_piece<DV, BV, kShift>(v_prev, c, lane_v) : make_uint4(0, 0, 0, 0));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + rv.slot);
+        if (lane == 0) arrive_issuer(v_full + rv.slot);
         rv.next(NV);
       }
       v_prev = now.v;
-      has_prev = now.has;
+      has_prev = now.has_v;
       any_prev = any;
       now = next;
       any = then.any;
     }
   } else {
     // ================================= the products ====================================
-    reg_dec<kIssueRegs>();
-    if (warp == kSoftWarps + kCodeWarps) {
-      constexpr uint32_t kScores = tc_idesc(kTile, kTile, false), kValues = tc_idesc(kTile, kHeadDim, true);
+    reg_dec<Shape::kIssueRegs>();
+    if (warp == kSoftWarps + kCodeWarps && rank != 0) {
+      while (next_piece(u)) {  // the first CTA issues
+      }
+    } else if (warp == kSoftWarps + kCodeWarps) {
+      constexpr uint32_t kScores = tc_idesc(kCtas * kTile, kTile, false), kValues = tc_idesc(kCtas * kTile, kHeadDim, true);
+      constexpr uint32_t kHalfBytes = kPair ? 64 * 128 : kTile * 128;  // K: 64 dims of this CTA's tokens
       const uint32_t tile0 = smem_addr(tiles);
       Ring rk, rv;
       uint32_t blocks = 0, tiles_done = 0;
@@ -654,11 +708,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
               for (int part = 0; part < 2; ++part)  // high and low part of q~
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                  tc_mma_ts(tmem + kColS + 128 * sb, tmem + kColQ + 64 * part + 8 * ks,
-                            tc_desc(kt + (ks >> 2) * (kTileBytes / 2) + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
-              tc_commit(s_full + sb);
-              mbar_arrive(s_full + sb);
-              tc_commit(k_empty + rk.slot);
+                  tc_mma_ts<kPair>(tmem + kColS + 128 * sb, tmem + kColQ + 64 * part + 8 * ks,
+                            tc_desc(kt + (ks >> 2) * kHalfBytes + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
+              tc_commit<kPair>(s_full + sb);
+              tc_commit<kPair>(k_empty + rk.slot);
             }
             __syncwarp();
             rk.next(kKStages);
@@ -672,10 +725,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
               const uint32_t vt = tile0 + (kKStages + rv.slot) * kTileBytes;
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
-                tc_mma_ts(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
-                          tc_desc(vt + ks * 2048, kTileBytes / 2), kValues, j > 1 || ks > 0);
-              tc_commit(v_empty + rv.slot);
-              tc_commit(o_full);
+                tc_mma_ts<kPair>(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
+                          tc_desc(vt + ks * 2048, kTile * 128), kValues, j > 1 || ks > 0);
+              tc_commit<kPair>(v_empty + rv.slot);
+              tc_commit<kPair>(o_full);
             }
             __syncwarp();
             rv.next(NV);
@@ -684,7 +737,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         blocks += nblk;
       }
       // (given up or not) the products in flight end before the tensor memory goes back
-      if (elect_one()) tc_commit(drain);
+      if (elect_one()) tc_commit<kPair>(drain);
       __syncwarp();
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < p.timeout_ns) {
@@ -692,21 +745,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     } else if (warp == kSoftWarps + kCodeWarps + 1) {
       // ================================== planning =======================================
       ChunkWalk<kTile> walk;
-      walk.start(p, pre, blockIdx.x, gridDim.x);  // (the tiles over the plan wait for the first piece)
+      walk.start(p, pre, worker, static_cast<int>(gridDim.x) / kCtas);  // (the tiles over the plan wait for the first piece)
       ChunkPiece q;
       Ring ro;
       bool recorded = false;
       for (bool more = true; more;) {
         more = walk.next(p, q);
-        const int i0 = q.tile * p.tile_tok, n = more ? min(p.tile_tok, q.s.n - i0) : 0;
+        // this CTA's tokens of the tile (a pair's second CTA may have none)
+        const int tokens = p.tile_tok / kCtas, i0 = q.tile * p.tile_tok + static_cast<int>(rank) * tokens;
+        const int n = more ? max(min(tokens, q.s.n - i0), 0) : 0;
         if (more && q.slot >= 0 && (q.slot & 1)) {
-          if (lane == 0) write_record(p, blockIdx.x, &q);
+          if (lane == 0 && rank == 0) write_record(p, worker, &q);
           recorded = true;
         }
         if (more && q.blk0 >= q.blk1) {  // rows that see nothing here: zero, or an empty partial
           for (int r = 0; r < n * p.group; ++r) {
             if (q.slot >= 0) {
-              const long long at = static_cast<long long>(q.slot) * kTile + r;
+              const long long at = static_cast<long long>(q.slot) * (kCtas * kTile) + rank * kTile + r;
               reinterpret_cast<float4*>(p.ws_o + at * kHeadDim)[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (lane == 0) p.ws_ml[at] = make_float2(-INFINITY, 0.f);
             } else {
@@ -747,25 +802,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         __syncwarp();
         ro.next(kPieces);
       }
-      if (!recorded && lane == 0) write_record(p, blockIdx.x, nullptr);
+      if (!recorded && lane == 0 && rank == 0) write_record(p, worker, nullptr);
     }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither leaves while the other's barriers or products need it
   if (warp == kSoftWarps + kCodeWarps) {
     __syncwarp();
     tc_fence_after();
-    tmem_free(tmem, kCols);
+    tmem_free<kPair>(tmem, kCols);
   }
+}
+
+template <int DK, int BK, int DV, int BV, bool kPair>
+cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
+  static SmemOptIn opt;
+  auto kern = vq_chunk_wide_kernel<DK, BK, DV, BV, kPair>;
+  constexpr size_t smem = WideSmem<DK, BK, DV, BV, kPair>::kTotal;
+  cudaError_t e = ensure_smem(kern, smem, opt);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(WideShape<kPair>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPair ? 2 : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int DK, int BK, int DV, int BV>
 cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
-  static SmemOptIn opt;
-  constexpr size_t smem = WideSmem<DK, BK, DV, BV>::kTotal;
-  cudaError_t e = ensure_smem(vq_chunk_wide_kernel<DK, BK, DV, BV>, smem, opt);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(vq_chunk_wide_kernel<DK, BK, DV, BV>, dim3(grid), dim3(kWideThreads), smem, stream, p, false);
+  return p.tile_rows == 2 * kTile ? launch_wide<DK, BK, DV, BV, true>(p, grid, stream)
+                                  : launch_wide<DK, BK, DV, BV, false>(p, grid, stream);
 }
 
 }  // namespace

@@ -158,9 +158,9 @@ struct SlotsParams {
 
 // A tile of query rows whose keys more than one worker of the chunk kernel
 // took: worker c (the record's index) began it in slot 2c + 1, workers
-// c + 1 .. last went on in their slots 2c'.  rows 0: none.
+// c + 1 .. last went on in their slots 2c'.  tokens 0: none.
 struct __align__(16) ChunkRecord {
-  int rows, row0, kvh, last;  // tile row r: token row0 + r / G, head kvh G + r % G
+  int tokens, row0, kvh, last;  // the tile's tokens, the first one's row, its KV head
 };
 
 struct ChunkParams {
@@ -183,7 +183,7 @@ struct ChunkParams {
   int page_size, max_pages, max_seq_len, max_new_len;
   int page_shift;             // log2 of page_size, or -1
   int window, sinks;          // window 0: none
-  int tile_tok, tile_rows;    // tokens and (padded) rows of a tile
+  int tile_tok, tile_rows;    // tokens and (padded) rows of a tile; of 256 rows, 128 have half the tokens
   int gap, min_range;         // a tile's fixed cost and a worker's least share, in tokens
   float qscale;               // softmax scale * log2(e) / sqrt(128)
   unsigned long long timeout_ns;
@@ -349,7 +349,7 @@ int dequant_tokens_per_cta();
 cudaError_t launch_rotary(RotaryParams p, bool bf16, int sms, cudaStream_t stream);
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream);
 constexpr int kSlotsMaxBatch = 16384;
-// Chunk attention, tile_rows 8 or 16 (narrow) and 128 (wide); the merge of either.
+// Chunk attention, tile_rows 8 or 16 (narrow), 128 or 256 (wide; 256: a pair of CTAs); the merge of either.
 cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
                                 cudaStream_t stream);
 cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
