@@ -8,12 +8,12 @@
 // the codes are 8 KB, so the kernel is bound by arithmetic: the tensor pipe
 // first, the softmax's exponentials and the expansion of the codes beside it.
 //
-//   * Sixteen warps expand codes: a thread takes one token's codes of 32 dims
-//     (loaded two blocks ahead, page first), gathers their centroids from the
-//     replicated, bank-conflict-free table and stores 16-byte pieces into the
-//     swizzled tiles that the tensor core reads (K rows of dims, V rows of
-//     dims with the token as k: one layout for both).  K runs one block ahead
-//     of V.
+//   * Sixteen warps expand codes, eight K and eight V: a thread takes one
+//     token's codes of 64 dims (loaded a block ahead, their page two ahead),
+//     gathers their centroids from the replicated, bank-conflict-free table
+//     and stores 16-byte pieces into the swizzled tiles that the tensor core
+//     reads (K rows of dims, V rows of dims with the token as k: one layout
+//     for both).
 //   * One thread issues the products: scores of block j + 1 before the values
 //     of block j, so the tensor pipe works while the softmax of block j runs.
 //   * Eight warps hold half a query row per thread: the Walsh-Hadamard transform
@@ -25,6 +25,8 @@
 //   * Every wait is bounded: on a timeout the CTA raises an abort flag,
 //     everybody leaves, the products in flight are drained and
 //     VQ_DEV_TIMEOUT is reported.
+#include <type_traits>
+
 #include "vq_chunk_common.cuh"
 #include "vq_gather.cuh"
 #include "vq_tcgen05.cuh"
@@ -35,23 +37,20 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
 constexpr int kTile = 128;           // query rows of a CTA's tile, and tokens of a block
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 8, kCodeWarps = 16;
+constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
+// Registers per thread: 72 at the launch (896 threads), then 256 x 112 + 512 x 56 + 128 x 56 = 896 x 72.
+constexpr int kSoftRegs = 112, kCodeRegs = 56, kIssueRegs = 56;
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
 
 // One CTA alone, or the two CTAs of a pair that share a block's tiles.
 template <bool kPair>
 struct WideShape {
-  static constexpr int kCodeWarps = kPair ? 8 : 16;
-  static constexpr int kThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
-  // Registers per thread.  Alone: 72 at the launch (896 threads), then 256 x 112 + 512 x 56 + 128 x 56
-  // = 896 x 72.  Pair: 96 (640 threads), then 256 x 128 + 256 x 80 + 128 x 56 <= 640 x 96.
-  static constexpr int kSoftRegs = kPair ? 128 : 112, kCodeRegs = kPair ? 80 : 56, kIssueRegs = 56;
   static constexpr int kTileBytes = kTile * kHeadDim * 2 / (kPair ? 2 : 1);  // of K or V, this CTA's part
   static constexpr int kKStages = kPair ? 3 : 2;
-  // Token masks in flight: block b's K tile is stored once the scores of block b - kKStages are done,
-  // and with them only the softmax of block b - kKStages - 2.
-  static constexpr int kMasks = kPair ? 8 : 4;
-  static_assert(kMasks >= kKStages + 2, "a mask's slot comes round after its reader");
+  // Token masks in flight: block b's is written when the V tile of block b - 1 has been, so the values of
+  // block b - 1 - (V stages) are done, and the softmax of that block.
+  static constexpr int kMasks = 4;
 };
 
 template <int DK, int BK, int DV, int BV, bool kPair>
@@ -64,40 +63,39 @@ struct WideSmem {
   static constexpr int kTiles = kTable;                             // K stages, then V stages
   static constexpr int kMisc = kTiles + (Shape::kKStages + kVStages) * Shape::kTileBytes;
   static constexpr int kTotal = kMisc + 704 + 2 * 2 * kTile * 4;
+  static_assert(Shape::kMasks >= kVStages + 1, "a mask's slot comes round after its reader");
   static_assert(kTotal <= 232448, "shared memory of one CTA");
   static_assert((kChunkMaxBatch + 1 + 32) * 8 <= Shape::kTileBytes, "the plan shares a tile");
 };
 
-// Codes of one token's 32 dims (quarter 0 .. 3 of the head), loaded ahead of their use: the loads are
-// volatile, so that they stay where they are issued, and nothing is computed from the words before
-// align().
-__device__ __forceinline__ uint32_t ld_word(const uint8_t* at) {
-  uint32_t x;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(x) : "l"(at));
-  return x;
-}
-template <int D, int B>
-struct QuarterCodes {
-  static constexpr int kCodes = 32 / D;
-  static constexpr int kWords = (kCodes * B + 31) / 32;  // 9- and 12-bit codes start inside their first word
+// Codes of kDims dims of a token (32 or 64; part 0 .. 128 / kDims - 1), loaded ahead of their use: the
+// loads are volatile, so that they stay where they are issued, and nothing is computed from the words
+// before align().
+template <int D, int B, int kDims>
+struct PartCodes {
+  static constexpr int kBits = B, kSub = D, kPieces = kDims / 8;  // 16-byte pieces of centroids
+  static constexpr int kCodes = kDims / D;
+  static constexpr int kWords = (kCodes * B + 31) / 32;  // (9- and 12-bit codes may start inside their first word)
   uint32_t w[kWords];
-  __device__ __forceinline__ void load(const uint8_t* row, int quarter) {
-    if constexpr (B == 8 && kWords == 4) {
-      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "l"(row + 16 * quarter));
-    } else if constexpr (B == 8) {
-      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(row + 8 * quarter));
-    } else {
-      const uint8_t* at = row + quarter * kCodes * B / 32 * 4;
+  static __device__ __forceinline__ int first_byte(int part) { return part * kCodes * B / 32 * 4; }
+  __device__ __forceinline__ void load(const uint8_t* at) {
+    if constexpr (B == 8 && kWords % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = ld_word(at + 4 * i);
+      for (int i = 0; i < kWords; i += 4)
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                     : "l"(at + 4 * i));
+    } else if constexpr (B == 8) {
+      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(at));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[i]) : "l"(at + 4 * i));
     }
   }
   // Code 0 to bit 0.
-  __device__ __forceinline__ void align(int quarter) {
-    if constexpr (B != 8) {
-      const int s = quarter * kCodes * B & 31;
+  __device__ __forceinline__ void align(int part) {
+    if constexpr (kCodes * B % 32) {
+      const int s = part * kCodes * B & 31;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) w[i] = i + 1 < kWords ? __funnelshift_r(w[i], w[i + 1], s) : w[i] >> s;
     }
@@ -112,14 +110,17 @@ struct QuarterCodes {
     }
   }
 };
-static_assert(QuarterCodes<4, 9>::kWords == 3 && QuarterCodes<8, 12>::kWords == 2, "72 + 24 and 48 + 16 bits");
+static_assert(PartCodes<4, 9, 32>::kWords == 3 && PartCodes<4, 9, 64>::kWords == 5 && PartCodes<8, 12, 32>::kWords == 2 &&
+                  PartCodes<8, 12, 64>::kWords == 3,
+              "72 + 24, 144 + 16, 48 + 16 and 96 bits");
 
-// 16-byte piece c (dims 8c .. 8c + 7) of the quarter: its centroids.
-// row_shift: log2 of the table's row bytes; lane: the lane's byte in a row.
-template <int D, int B, int kRowShift>
-__device__ __forceinline__ uint4 gather_piece(const QuarterCodes<D, B>& x, int c, uint32_t lane) {
+// 16-byte piece c (dims 8c .. 8c + 7) of the part: its centroids.
+// kRowShift: log2 of the table's row bytes; lane: the lane's byte in a row.
+template <typename Codes, int kRowShift>
+__device__ __forceinline__ uint4 gather_piece(const Codes& x, int c, uint32_t lane) {
+  constexpr int D = Codes::kSub;
   auto off = [&](int i) {
-    if constexpr (B == 8 && kRowShift == 8) return row_addr(x.w[i >> 2], lane, i & 3);
+    if constexpr (Codes::kBits == 8 && kRowShift == 8) return row_addr(x.w[i >> 2], lane, i & 3);
     else return (x.code(i) << kRowShift) + lane;
   };
   if constexpr (D == 8) {
@@ -216,9 +217,9 @@ struct __align__(16) WidePiece {
 };
 static_assert(sizeof(WidePiece) == 64, "the pieces' place in shared memory");
 // Pieces under way.  The code warps look two blocks ahead of the one they store,
-// whose values' tile is still one behind: four pieces of one block each are
-// all that can lie between the last to read a piece and the first (pieces
-// without a block are not handed out).
+// while the issuer may still wait for that one: of pieces of one block each,
+// the issuer has read the stored block's, and two more are needed ahead of
+// it (pieces without a block are not handed out).
 constexpr uint32_t kPieces = 4;
 
 __device__ __forceinline__ bool elect_one() {
@@ -228,11 +229,11 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int DK, int BK, int DV, int BV, bool kPair>
-__global__ void __launch_bounds__(WideShape<kPair>::kThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
   using W = WideSmem<DK, BK, DV, BV, kPair>;
   using Shape = WideShape<kPair>;
   constexpr int NV = W::kVStages, kKStages = Shape::kKStages, kMasks = Shape::kMasks, kTileBytes = Shape::kTileBytes;
-  constexpr int kCodeWarps = Shape::kCodeWarps, kCtas = kPair ? 2 : 1;
+  constexpr int kCtas = kPair ? 2 : 1;
   constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
   uint8_t* const tiles = g_smem + W::kTiles;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(g_smem + W::kMisc);
@@ -267,11 +268,11 @@ __global__ void __launch_bounds__(WideShape<kPair>::kThreads, 1) vq_chunk_wide_k
   fill_wide_table<DK, BK, DV, BV>(p);
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(k_full + i, kCtas * kCodeWarps);
+      mbar_init(k_full + i, kCtas * kCodeWarps / 2);
       mbar_init(k_empty + i, 1);
     }
     for (int i = 0; i < NV; ++i) {
-      mbar_init(v_full + i, kCtas * kCodeWarps);
+      mbar_init(v_full + i, kCtas * kCodeWarps / 2);
       mbar_init(v_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(WideShape<kPair>::kThreads, 1) vq_chunk_wide_k
 
   if (warp < kSoftWarps) {
     // ====== two threads per query row: columns (and dims) 0 .. 63 and 64 .. 127 of a block ======
-    reg_inc<Shape::kSoftRegs>();
+    reg_inc<kSoftRegs>();
     const int r = tid & (kTile - 1), g = tid >> 7, G = p.group;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the two warps of a row meet here
@@ -541,149 +542,130 @@ __global__ void __launch_bounds__(WideShape<kPair>::kThreads, 1) vq_chunk_wide_k
     }
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
-    reg_dec<Shape::kCodeRegs>();
-    // A thread takes 32 dims of a token of K and of V.  Alone, of the same token; in a pair this CTA has
-    // the K of half the block's tokens (B's columns) and half the dims of V (B's columns again).
-    const int w = warp - kSoftWarps;
-    const int tok_v = 32 * (kPair ? w & 3 : w >> 2) + lane;
-    const int tok_k = kPair ? static_cast<int>(64 * rank) + 32 * (w & 1) + lane : tok_v;
-    const int quarter_k = kPair ? w >> 1 : w & 3, quarter_v = kPair ? static_cast<int>(2 * rank) + (w >> 2) : w & 3;
-    const uint32_t rep = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
-    const uint32_t lane_k = W::kWideCodes ? 0u : rep;
-    const uint32_t lane_v = W::kWideCodes ? 65536u : W::kSplitTable ? 32768u + rep_v : 128u + rep_v;
-    constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
-    // the first 16-byte piece, swizzled, of the thread's four (this address ^ (c << 4)); K rows: tokens by
-    // halves of the dims, V rows: tokens by halves of the dims (a pair's CTA: its half alone)
-    const int row_k = kPair ? tok_k & 63 : tok_k, block_k = kPair ? 64 * 128 : kTile * 128;
-    const uint32_t dst_k = smem_addr(tiles) + (quarter_k >> 1) * block_k + row_k * 128 + (((row_k & 7) ^ (4 * (quarter_k & 1))) << 4);
-    const uint32_t dst_v = smem_addr(tiles) + (kPair ? 0 : (quarter_v >> 1) * kTile * 128) + tok_v * 128 +
-                           (((tok_v & 7) ^ (4 * (quarter_v & 1))) << 4);
-    auto store = [&](uint32_t at, int c, uint4 v) {
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                   : "memory");
-    };
-    // Block iterator, two blocks ahead of the tiles: the token's page; then its codes one ahead.
-    // A token's page and offset follow from the block before, by 128 tokens, where blocks adjoin.
-    const int step_page = kTile / p.page_size, step_off = kTile - step_page * p.page_size;
-    bool more = true;
-    int i = 0;
-    u.blk1 = 0;
-    u.sink = -1;
-    struct Token {  // of the block the iterator is at
-      int t, lp, off;
-    };
-    Token at_k = {}, at_v = {};
-    struct Where {
-      int page, off;
-      bool in;  // the token exists
-    };
-    struct Block {
-      Where k, v;
-      int kvh;
-      bool any;  // the block exists
-    };
-    auto advance = [&]() {
-      Block x = {};
-      bool jump = i == u.sink;
-      while (more && i >= u.blk1) {
-        more = next_piece(u);
-        i = more ? u.blk0 : 0;
-        jump = true;
-      }
-      if (!more) return x;
-      auto move = [&](Token& y, int tok) {
+    reg_dec<kCodeRegs>();
+    // The first half of the warps expand K, the others V, each at its own pace.  Alone, a thread takes 64
+    // dims of a token; in a pair 32, and the CTA has the K of half the block's tokens (columns of B) and
+    // half the dims of V (columns of B again).
+    constexpr int kDims = kPair ? 32 : 64;
+    const int w = (warp - kSoftWarps) % (kCodeWarps / 2);
+    auto expand = [&](auto codes, auto row_bytes, const uint8_t* pool, int tok, int part, uint32_t dst, uint32_t table,
+                      uint32_t stages, uint64_t* full, uint64_t* empty, bool masking) {
+      using Codes = decltype(codes);
+      constexpr int kRow = decltype(row_bytes)::value;
+      constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
+      // Block iterator, two blocks ahead of the tiles: the token's page; then its codes one ahead.  The
+      // page and the offset in it follow from the block before, by 128 tokens, where blocks adjoin; rows are
+      // counted by 16 (a token's place among 16 is its own).
+      pool += (tok % 16) * kRow + Codes::first_byte(part);
+      const int per_page = p.page_size / 16, step_page = kTile / p.page_size, step_off = kTile / 16 - step_page * per_page;
+      bool more = true;
+      int i = 0, t = 0, lp = 0, off = 0;
+      const int32_t* pages = nullptr;
+      u.blk1 = 0;
+      u.sink = -1;
+      struct Where {
+        int page, off, kvh;
+        bool in, any;  // the token exists; the block exists
+      };
+      auto advance = [&]() {
+        Where x = {0, 0, 0, false, false};
+        bool jump = i == u.sink;
+        while (more && i >= u.blk1) {
+          more = next_piece(u);
+          i = more ? u.blk0 : 0;
+          jump = true;
+          pages = p.page_table + static_cast<long long>(u.b) * p.max_pages;
+        }
+        if (!more) return x;
         if (jump) {
-          y.t = u.block(i) * kTile + tok;
-          y.lp = y.t / p.page_size;
-          y.off = y.t - y.lp * p.page_size;
+          t = u.block(i) * kTile + tok;
+          lp = t / p.page_size;
+          off = (t - lp * p.page_size) / 16;
         } else {
-          y.t += kTile;
-          y.lp += step_page;
-          y.off += step_off;
-          if (y.off >= p.page_size) {
-            y.off -= p.page_size;
-            ++y.lp;
+          t += kTile;
+          lp += step_page;
+          off += step_off;
+          if (off >= per_page) {
+            off -= per_page;
+            ++lp;
           }
         }
-        Where z = {0, y.off, y.t < u.limit};
-        if (z.in) z.page = __ldg(p.page_table + static_cast<long long>(u.b) * p.max_pages + y.lp);
-        return z;
+        ++i;
+        x.any = true;
+        x.in = t < u.limit;
+        x.kvh = u.kvh;
+        x.off = off;
+        if (x.in) x.page = __ldg(pages + lp);
+        return x;
       };
-      x.v = move(at_v, tok_v);
-      x.k = kPair ? move(at_k, tok_k) : x.v;
-      x.kvh = u.kvh;
-      x.any = true;
-      ++i;
-      return x;
-    };
-    struct Codes {
-      QuarterCodes<DK, BK> k;
-      QuarterCodes<DV, BV> v;
-      bool has_k, has_v;  // the token can be read
-    };
-    auto fetch = [&](const Block& x, Codes& y) {
-      auto row = [&](const Where& z) {
-        return (static_cast<long long>(z.page) * p.hkv + x.kvh) * p.page_size + z.off;
+      bool has = false, has_next = false;  // the token can be read
+      Codes now, next;
+      auto fetch = [&](const Where& x, Codes& y) {
+        const bool good = x.in && static_cast<unsigned long long>(x.page) < static_cast<unsigned long long>(p.num_pages);
+        if (good) {
+          const uint32_t row16 = static_cast<uint32_t>(x.page * p.hkv + x.kvh) * per_page + x.off;
+          y.load(pool + static_cast<unsigned long long>(row16) * (16 * kRow));
+        } else if (x.in) {
+          report(p.status, kDevBadPage);
+        }
+        return good;
       };
-      y.has_v = x.v.in && x.v.page >= 0 && x.v.page < p.num_pages;
-      y.has_k = kPair ? x.k.in && x.k.page >= 0 && x.k.page < p.num_pages : y.has_v;
-      if (x.v.in && !y.has_v) report(p.status, kDevBadPage);
-      if (y.has_k) y.k.load(p.k_pool + row(x.k) * KROW, quarter_k);
-      if (y.has_v) y.v.load(p.v_pool + row(x.v) * VROW, quarter_v);
-    };
-    Codes now, next;
-    QuarterCodes<DV, BV> v_prev;
-    bool has_prev = false, any_prev = false;
-    const Block first = advance();
-    Block ahead = advance();
-    bool any = first.any;
-    now.has_k = now.has_v = next.has_k = next.has_v = false;
-    if (any) fetch(first, now);
-    Ring rk, rv;
-    uint32_t blocks = 0;
-    while (any || any_prev) {
-      const Block then = ahead;
-      ahead = advance();
-      next.has_k = next.has_v = false;
-      if (then.any) fetch(then, next);
-      if (any) {
-        if (!wait(k_empty + rk.slot, rk.phase ^ 1u)) break;
-        const uint32_t at = dst_k + rk.slot * kTileBytes;
-        now.k.align(quarter_k);
+      const Where first = advance();
+      Where ahead = advance();
+      bool any = first.any;
+      if (any) has = fetch(first, now);
+      Ring ring;
+      uint32_t blocks = 0;
+      while (any) {
+        const Where then = ahead;
+        ahead = advance();
+        has_next = then.any && fetch(then, next);
+        if (masking) {  // the tokens of the block that can be read
+          const uint32_t seen = __ballot_sync(kAll, has);
+          if (lane == 0) {
+            masks[(blocks % kMasks) * 4 + tok / 32] = seen;
+            mbar_arrive(mask_full + blocks % kMasks);
+          }
+        }
+        if (!wait(empty + ring.slot, ring.phase ^ 1u)) break;
+        const uint32_t at = dst + ring.slot * kTileBytes;
+        now.align(part);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) store(at, c, now.has_k ? gather_piece<DK, BK, kShift>(now.k, c, lane_k) : make_uint4(0, 0, 0, 0));
-        const uint32_t seen = __ballot_sync(kAll, now.has_v);  // (the V tokens: all 128 of the block, by four warps)
-        if ((kPair ? w < 4 : quarter_v == 0) && lane == 0) {
-          masks[(blocks % kMasks) * 4 + (tok_v >> 5)] = seen;
-          mbar_arrive(mask_full + blocks % kMasks);
+        for (int c = 0; c < Codes::kPieces; ++c) {
+          const uint4 v = has ? gather_piece<Codes, kShift>(now, c, table) : make_uint4(0, 0, 0, 0);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_issuer(k_full + rk.slot);
-        rk.next(kKStages);
+        if (lane == 0) arrive_issuer(full + ring.slot);
+        ring.next(stages);
         ++blocks;
+        now = next;
+        has = has_next;
+        any = then.any;
       }
-      if (any_prev) {
-        if (!wait(v_empty + rv.slot, rv.phase ^ 1u)) break;
-        const uint32_t at = dst_v + (kKStages + rv.slot) * kTileBytes;
-        v_prev.align(quarter_v);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          store(at, c, has_prev ? gather_piece<DV, BV, kShift>(v_prev, c, lane_v) : make_uint4(0, 0, 0, 0));
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) arrive_issuer(v_full + rv.slot);
-        rv.next(NV);
-      }
-      v_prev = now.v;
-      has_prev = now.has_v;
-      any_prev = any;
-      now = next;
-      any = then.any;
+    };
+    // The first 16-byte piece of the thread's part, swizzled (its others: this address ^ (c << 4)).
+    auto place = [&](int row, int rows, int part) {
+      const int first = part * (kDims / 8);
+      return smem_addr(tiles) + first / 8 * (rows * 128) + row * 128 + (((row & 7) ^ (first & 7)) << 4);
+    };
+    const uint32_t rep_k = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
+    if (warp < kSoftWarps + kCodeWarps / 2) {
+      const int row = kPair ? 32 * (w & 1) + lane : 32 * (w >> 1) + lane, part = kPair ? w >> 1 : w & 1;
+      expand(PartCodes<DK, BK, kDims>{}, std::integral_constant<int, KROW>{}, p.k_pool,
+             static_cast<int>(64 * rank) + row, part, place(row, kPair ? 64 : kTile, part), W::kWideCodes ? 0u : rep_k, kKStages,
+             k_full, k_empty, false);
+    } else {
+      const int row = kPair ? 32 * (w & 3) + lane : 32 * (w >> 1) + lane, part = kPair ? w >> 2 : w & 1;
+      expand(PartCodes<DV, BV, kDims>{}, std::integral_constant<int, VROW>{}, p.v_pool, row,
+             (kPair ? static_cast<int>(2 * rank) : 0) + part, place(row, kTile, part) + kKStages * kTileBytes,
+             W::kWideCodes ? 65536u : (W::kSplitTable ? 32768u : 128u) + rep_v, NV, v_full, v_empty, part == 0);
     }
   } else {
     // ================================= the products ====================================
-    reg_dec<Shape::kIssueRegs>();
+    reg_dec<kIssueRegs>();
     if (warp == kSoftWarps + kCodeWarps && rank != 0) {
       while (next_piece(u)) {  // the first CTA issues
       }
@@ -824,7 +806,7 @@ cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(WideShape<kPair>::kThreads);
+  cfg.blockDim = dim3(kWideThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
