@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   uint64_t* const v_empty = v_full + 3;        // [NV]
   uint64_t* const s_full = v_empty + 3;        // [2] scores done
   uint64_t* const p_full = s_full + 2;         // [2] P stored
-  uint64_t* const o_full = p_full + 2;         // values of a block done
-  uint64_t* const q_full = o_full + 1;         // Q~ stored, O read
+  uint64_t* const o_full = p_full + 2;         // [2] values of a block done
+  uint64_t* const q_full = o_full + 2;         // Q~ stored, O read
   uint64_t* const drain = q_full + 1;
   uint64_t* const piece_full = drain + 1;              // [kPieces] planning warp -> everybody
   uint64_t* const piece_empty = piece_full + kPieces;  // [kPieces]
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, kCtas * kSoftWarps);
+      mbar_init(o_full + i, 1);
     }
-    mbar_init(o_full, 1);
     mbar_init(q_full, kCtas * kSoftWarps);
     mbar_init(drain, 1);
     for (int i = 0; i < kMasks; ++i) mbar_init(mask_full + i, 4);
@@ -341,7 +341,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the two warps of a row meet here
     auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
-    uint32_t blocks = 0;  // blocks so far, over all pieces
+    uint32_t blocks = 0;            // blocks so far, over all pieces
+    uint32_t done0 = 0, done1 = 0;  // even and odd blocks whose values are known to be done
+    // Waits until the values of all blocks below `end` are done.  Each phase of the two barriers is met
+    // once, in order, before the block after the next stores its P, so none can be taken for another.
+    auto values_done = [&](uint32_t end) {
+      bool good = true;
+      if (done0 < (end + 1) >> 1) good = wait(o_full, done0++ & 1u);
+      if (good && done1 < end >> 1) good = wait(o_full + 1, done1++ & 1u);
+      return good;
+    };
     bool ok = true;
     while (ok && next_piece(u)) {
       const bool live = r < u.rows;
@@ -412,7 +421,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       const int pos = live ? u.first_pos + token : -1;
       for (int j = 0; j < nblk; ++j, ++blocks) {
         const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb + 64 * g;
-        ok = wait(mask_full + blocks % kMasks, (blocks / kMasks) & 1u) && wait(s_full + sb, (blocks >> 1) & 1u);
+        // the block's tokens, the values of block - 2 (which run before these scores), and the scores
+        ok = wait(mask_full + blocks % kMasks, (blocks / kMasks) & 1u) && (j < 2 || values_done(blocks - 1)) &&
+             wait(s_full + sb, (blocks >> 1) & 1u);
         if (!ok) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
@@ -479,21 +490,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         store_p(s0, col_s);
         store_p(s1, col_s + 32);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (j > 0) {
-          // The values of block - 1 (they ran beside this softmax) are waited for in every
-          // block, so each phase of o_full is met once, in order.
-          ok = wait(o_full, (blocks - 1) & 1u);
+        if (j > 0 && __any_sync(kAll, raise)) {  // O follows the maximum, once the values of block - 1 are in
+          ok = values_done(blocks);
           if (!ok) break;
-          if (__any_sync(kAll, raise)) {  // O follows the maximum
-            tc_fence_after();
+          tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
-              tmem_wait_ld();
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
-              tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
-            }
+            for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
+            tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
           }
         }
         tmem_wait_st();
@@ -502,7 +509,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         if (lane == 0) arrive_issuer(p_full + sb);
       }
       if (!ok) break;
-      ok = wait(o_full, (blocks - 1) & 1u);
+      ok = values_done(blocks);
       if (!ok) break;
       tc_fence_after();
       // ---- the piece's rows: to `out`, or as a partial to the workspace --------------------
@@ -679,42 +686,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       while (ok && next_piece(u)) {
         const int nblk = u.blk1 - u.blk0;
         ok = wait(q_full, tiles_done++ & 1u);
-        for (int j = 0; ok && j <= nblk; ++j) {
-          if (j < nblk) {  // scores of block j
-            const uint32_t sb = (blocks + j) & 1u;
-            if (!(ok = wait(k_full + rk.slot, rk.phase))) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t kt = tile0 + rk.slot * kTileBytes;
+        auto scores = [&](uint32_t blk) {  // of block blk, whose K tile is there
+          if (elect_one()) {
+            const uint32_t kt = tile0 + rk.slot * kTileBytes;
 #pragma unroll
-              for (int part = 0; part < 2; ++part)  // high and low part of q~
+            for (int part = 0; part < 2; ++part)  // high and low part of q~
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  tc_mma_ts<kPair>(tmem + kColS + 128 * sb, tmem + kColQ + 64 * part + 8 * ks,
-                            tc_desc(kt + (ks >> 2) * kHalfBytes + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
-              tc_commit<kPair>(s_full + sb);
-              tc_commit<kPair>(k_empty + rk.slot);
-            }
-            __syncwarp();
-            rk.next(kKStages);
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_ts<kPair>(tmem + kColS + 128 * (blk & 1u), tmem + kColQ + 64 * part + 8 * ks,
+                                 tc_desc(kt + (ks >> 2) * kHalfBytes + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
+            tc_commit<kPair>(s_full + (blk & 1u));
+            tc_commit<kPair>(k_empty + rk.slot);
           }
-          if (j > 0) {  // values of block j - 1
-            const uint32_t blk = blocks + j - 1, sb = blk & 1u;
-            if (!(ok = wait(v_full + rv.slot, rv.phase))) break;
-            if (!(ok = wait(p_full + sb, (blk >> 1) & 1u))) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t vt = tile0 + (kKStages + rv.slot) * kTileBytes;
+          __syncwarp();
+          rk.next(kKStages);
+        };
+        // scores of blocks 0 and 1, then values of block j and scores of block j + 2 (into j's columns)
+        for (int j = 0; ok && j < min(nblk, 2); ++j) {
+          ok = wait(k_full + rk.slot, rk.phase);
+          tc_fence_after();
+          if (ok) scores(blocks + j);
+        }
+        for (int j = 0; ok && j < nblk; ++j) {
+          const uint32_t blk = blocks + j, sb = blk & 1u;
+          // (P last: what follows it is issued in one go)
+          ok = wait(v_full + rv.slot, rv.phase) && (j + 2 >= nblk || wait(k_full + rk.slot, rk.phase)) &&
+               wait(p_full + sb, (blk >> 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vt = tile0 + (kKStages * kTileBytes) + rv.slot * kTileBytes;
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
-                tc_mma_ts<kPair>(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
-                          tc_desc(vt + ks * 2048, kTile * 128), kValues, j > 1 || ks > 0);
-              tc_commit<kPair>(v_empty + rv.slot);
-              tc_commit<kPair>(o_full);
-            }
-            __syncwarp();
-            rv.next(NV);
+            for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
+              tc_mma_ts<kPair>(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
+                               tc_desc(vt + ks * 2048, kTile * 128), kValues, j > 0 || ks > 0);
+            tc_commit<kPair>(v_empty + rv.slot);
+            tc_commit<kPair>(o_full + sb);
           }
+          __syncwarp();
+          rv.next(NV);
+          if (j + 2 < nblk) scores(blk + 2);
         }
         blocks += nblk;
       }
