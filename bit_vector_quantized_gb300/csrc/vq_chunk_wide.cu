@@ -237,20 +237,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
   uint8_t* const tiles = g_smem + W::kTiles;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(g_smem + W::kMisc);
+  // A wait costs 100 to 300 cycles here, ready or not (mbarrier operations queue behind the code warps'
+  // shared-memory accesses), so what is needed together is collected on one barrier.
   // (In a pair the first CTA's thread issues for both: what it waits for is arrived on there, by both.)
-  uint64_t* const k_full = bars;               // [kKStages] code warps -> products
-  uint64_t* const k_empty = k_full + 3;        // [kKStages] products -> code warps
-  uint64_t* const v_full = k_empty + 3;        // [NV]
-  uint64_t* const v_empty = v_full + 3;        // [NV]
-  uint64_t* const s_full = v_empty + 3;        // [2] scores done
-  uint64_t* const p_full = s_full + 2;         // [2] P stored
-  uint64_t* const o_full = p_full + 2;         // [2] values of a block done
-  uint64_t* const q_full = o_full + 2;         // Q~ stored, O read
+  uint64_t* const ready = bars;            // [4] by block b: P of b, the V tile of b, the K tile of b + 2
+  uint64_t* const start = ready + 4;       // K tiles of blocks 0 and 1
+  uint64_t* const k_empty = start + 1;     // [kKStages] scores done, the tile is free
+  uint64_t* const v_empty = k_empty + 3;   // [NV]
+  uint64_t* const s_full = v_empty + 3;    // [4] by block: the scores are done, the tokens' masks are there
+  uint64_t* const o_full = s_full + 4;     // [2] values of a piece's last block but one, and of its last
+  uint64_t* const q_full = o_full + 2;     // Q~ stored, O read
   uint64_t* const drain = q_full + 1;
   uint64_t* const piece_full = drain + 1;              // [kPieces] planning warp -> everybody
   uint64_t* const piece_empty = piece_full + kPieces;  // [kPieces]
   WidePiece* const pieces = reinterpret_cast<WidePiece*>(bars + 48);  // [kPieces]
-  uint64_t* const mask_full = bars + 80;       // [kMasks] code warps -> softmax
   uint32_t* const masks = reinterpret_cast<uint32_t*>(bars + 28);  // [kMasks][4] tokens that have a page
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
@@ -267,22 +267,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   }
   fill_wide_table<DK, BK, DV, BV>(p);
   if (tid == 0) {
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(k_full + i, kCtas * kCodeWarps / 2);
-      mbar_init(k_empty + i, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(ready + i, kCtas * (kSoftWarps + kCodeWarps));
+      mbar_init(s_full + i, 1 + 4);
     }
-    for (int i = 0; i < NV; ++i) {
-      mbar_init(v_full + i, kCtas * kCodeWarps / 2);
-      mbar_init(v_empty + i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, kCtas * kSoftWarps);
-      mbar_init(o_full + i, 1);
-    }
+    mbar_init(start, kCtas * kCodeWarps);  // (the K warps, for two blocks each)
+    for (int i = 0; i < kKStages; ++i) mbar_init(k_empty + i, 1);
+    for (int i = 0; i < NV; ++i) mbar_init(v_empty + i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(o_full + i, 1);
     mbar_init(q_full, kCtas * kSoftWarps);
     mbar_init(drain, 1);
-    for (int i = 0; i < kMasks; ++i) mbar_init(mask_full + i, 4);
     for (int i = 0; i < static_cast<int>(kPieces); ++i) {
       mbar_init(piece_full + i, 1);
       mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 1);
@@ -319,7 +313,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(kAll, wait_one(bar, phase)) != 0; };
   // An arrival that the issuing thread waits for.
   auto arrive_issuer = [&](uint64_t* bar) {
-    if constexpr (kPair) mbar_arrive_at(bar, 0);
+    if (kPair && rank != 0) mbar_arrive_at(bar, 0);
     else mbar_arrive(bar);
   };
   // The next piece (whole warps); false when there is none or the CTA was given up.
@@ -341,16 +335,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the two warps of a row meet here
     auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
-    uint32_t blocks = 0;            // blocks so far, over all pieces
-    uint32_t done0 = 0, done1 = 0;  // even and odd blocks whose values are known to be done
-    // Waits until the values of all blocks below `end` are done.  Each phase of the two barriers is met
-    // once, in order, before the block after the next stores its P, so none can be taken for another.
-    auto values_done = [&](uint32_t end) {
-      bool good = true;
-      if (done0 < (end + 1) >> 1) good = wait(o_full, done0++ & 1u);
-      if (good && done1 < end >> 1) good = wait(o_full + 1, done1++ & 1u);
-      return good;
-    };
+    uint32_t blocks = 0;  // blocks so far, over all pieces
+    uint32_t ends0 = 0, ends1 = 0;  // phases of o_full so far
     bool ok = true;
     while (ok && next_piece(u)) {
       const bool live = r < u.rows;
@@ -421,9 +407,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       const int pos = live ? u.first_pos + token : -1;
       for (int j = 0; j < nblk; ++j, ++blocks) {
         const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb + 64 * g;
-        // the block's tokens, the values of block - 2 (which run before these scores), and the scores
-        ok = wait(mask_full + blocks % kMasks, (blocks / kMasks) & 1u) && (j < 2 || values_done(blocks - 1)) &&
-             wait(s_full + sb, (blocks >> 1) & 1u);
+        ok = wait(s_full + (blocks & 3u), (blocks >> 2) & 1u);
         if (!ok) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
@@ -464,16 +448,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         float mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
         float* const meet = tops + sb * 2 * kTile;
         meet[g * kTile + r] = mx;
-        row_sync();
-        mx = fmaxf(mx, meet[(g ^ 1) * kTile + r]);
-        const bool raise = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
-        const float scale = raise ? fast_exp2(m - mx) : 1.f;  // 0 while nothing is accumulated
-        m = raise ? mx : m;
-        l *= scale;
         // ---- p, its sum, and P in fp16 over its own scores --------------------------------
-        const float mu = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        auto store_p = [&](const uint32_t(&s)[32], uint32_t at) {
+        // With the maximum so far, which nearly always stays: whether the other half of the row passes it is
+        // seen on the way.
+        auto passes = [&](float x) { return x > m + kSlack || (m == -INFINITY && x > -INFINITY); };
+        float sum[4];
+        auto store_p = [&](const uint32_t(&s)[32], uint32_t at, float mu) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -487,29 +467,45 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
           }
           tmem_st16(at, w);
         };
-        store_p(s0, col_s);
-        store_p(s1, col_s + 32);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (j > 0 && __any_sync(kAll, raise)) {  // O follows the maximum, once the values of block - 1 are in
-          ok = values_done(blocks);
-          if (!ok) break;
-          tc_fence_after();
+        bool again = __any_sync(kAll, passes(mx));
+        sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+        if (!again) store_p(s0, col_s, m == -INFINITY ? 0.f : -m);
+        row_sync();
+        const float other = meet[(g ^ 1) * kTile + r];
+        if (!again) store_p(s1, col_s + 32, m == -INFINITY ? 0.f : -m);
+        again = again || __any_sync(kAll, passes(other));
+        if (again) {  // (both warps of the rows come here)
+          mx = fmaxf(mx, other);
+          const float m_new = passes(mx) ? mx : m;
+          const float scale = m_new == m ? 1.f : fast_exp2(m - m_new);  // 0 while nothing is accumulated
+          m = m_new;
+          l *= scale;
+          sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+          const float mu = m == -INFINITY ? 0.f : -m;
+          store_p(s0, col_s, mu);
+          store_p(s1, col_s + 32, mu);
+          if (j > 0) {  // O follows the maximum, once the values of block - 1 are in (the next scores come after them)
+            ok = j + 1 < nblk ? wait(s_full + ((blocks + 1) & 3u), ((blocks + 1) >> 2) & 1u) : wait(o_full, ends0 & 1u);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
-            tmem_wait_ld();
+            for (int c = 0; c < 2; ++c) {
+              tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
-            tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+              for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
+              tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+            }
           }
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_issuer(p_full + sb);
+        if (lane == 0) arrive_issuer(ready + (blocks & 3u));
       }
       if (!ok) break;
-      ok = values_done(blocks);
+      ok = (nblk < 2 || wait(o_full, ends0++ & 1u)) && wait(o_full + 1, ends1++ & 1u);
       if (!ok) break;
       tc_fence_after();
       // ---- the piece's rows: to `out`, or as a partial to the workspace --------------------
@@ -556,7 +552,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     constexpr int kDims = kPair ? 32 : 64;
     const int w = (warp - kSoftWarps) % (kCodeWarps / 2);
     auto expand = [&](auto codes, auto row_bytes, const uint8_t* pool, int tok, int part, uint32_t dst, uint32_t table,
-                      uint32_t stages, uint64_t* full, uint64_t* empty, bool masking) {
+                      uint32_t stages, uint64_t* empty, bool is_k, bool masking) {
       using Codes = decltype(codes);
       constexpr int kRow = decltype(row_bytes)::value;
       constexpr int kShift = W::kWideCodes ? 4 : W::kSplitTable ? 7 : 8;
@@ -631,7 +627,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
           const uint32_t seen = __ballot_sync(kAll, has);
           if (lane == 0) {
             masks[(blocks % kMasks) * 4 + tok / 32] = seen;
-            mbar_arrive(mask_full + blocks % kMasks);
+            mbar_arrive(s_full + (blocks & 3u));
           }
         }
         if (!wait(empty + ring.slot, ring.phase ^ 1u)) break;
@@ -645,12 +641,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_issuer(full + ring.slot);
+        if (lane == 0) arrive_issuer(!is_k ? ready + (blocks & 3u) : blocks < 2 ? start : ready + ((blocks - 2) & 3u));
         ring.next(stages);
         ++blocks;
         now = next;
         has = has_next;
         any = then.any;
+      }
+      // The last two blocks have no K tile to wait for; its arrivals come in their turn all the same (unless
+      // the CTA was given up).
+      if (is_k && !any) {
+        for (uint32_t end = blocks + 2; blocks < end; ++blocks) {
+          if (!wait(empty + ring.slot, ring.phase ^ 1u)) break;
+          if (lane == 0) arrive_issuer(blocks < 2 ? start : ready + ((blocks - 2) & 3u));
+          ring.next(stages);
+        }
       }
     };
     // The first 16-byte piece of the thread's part, swizzled (its others: this address ^ (c << 4)).
@@ -663,12 +668,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       const int row = kPair ? 32 * (w & 1) + lane : 32 * (w >> 1) + lane, part = kPair ? w >> 1 : w & 1;
       expand(PartCodes<DK, BK, kDims>{}, std::integral_constant<int, KROW>{}, p.k_pool,
              static_cast<int>(64 * rank) + row, part, place(row, kPair ? 64 : kTile, part), W::kWideCodes ? 0u : rep_k, kKStages,
-             k_full, k_empty, false);
+             k_empty, true, false);
     } else {
       const int row = kPair ? 32 * (w & 3) + lane : 32 * (w >> 1) + lane, part = kPair ? w >> 2 : w & 1;
       expand(PartCodes<DV, BV, kDims>{}, std::integral_constant<int, VROW>{}, p.v_pool, row,
              (kPair ? static_cast<int>(2 * rank) : 0) + part, place(row, kTile, part) + kKStages * kTileBytes,
-             W::kWideCodes ? 65536u : (W::kSplitTable ? 32768u : 128u) + rep_v, NV, v_full, v_empty, part == 0);
+             W::kWideCodes ? 65536u : (W::kSplitTable ? 32768u : 128u) + rep_v, NV, v_empty, false, part == 0);
     }
   } else {
     // ================================= the products ====================================
@@ -695,23 +700,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
               for (int ks = 0; ks < 8; ++ks)
                 tc_mma_ts<kPair>(tmem + kColS + 128 * (blk & 1u), tmem + kColQ + 64 * part + 8 * ks,
                                  tc_desc(kt + (ks >> 2) * kHalfBytes + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
-            tc_commit<kPair>(s_full + (blk & 1u));
+            tc_commit<kPair>(s_full + (blk & 3u));
             tc_commit<kPair>(k_empty + rk.slot);
           }
           __syncwarp();
           rk.next(kKStages);
         };
-        // scores of blocks 0 and 1, then values of block j and scores of block j + 2 (into j's columns)
-        for (int j = 0; ok && j < min(nblk, 2); ++j) {
-          ok = wait(k_full + rk.slot, rk.phase);
-          tc_fence_after();
-          if (ok) scores(blocks + j);
-        }
+        // scores of blocks 0 and 1 (their K tiles were there with the blocks before), then values of block j
+        // and scores of block j + 2 (into j's columns)
+        if (ok && blocks == 0) ok = wait(start, 0);
+        tc_fence_after();
+        for (int j = 0; ok && j < min(nblk, 2); ++j) scores(blocks + j);
         for (int j = 0; ok && j < nblk; ++j) {
           const uint32_t blk = blocks + j, sb = blk & 1u;
-          // (P last: what follows it is issued in one go)
-          ok = wait(v_full + rv.slot, rv.phase) && (j + 2 >= nblk || wait(k_full + rk.slot, rk.phase)) &&
-               wait(p_full + sb, (blk >> 1) & 1u);
+          ok = wait(ready + (blk & 3u), (blk >> 2) & 1u);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -721,7 +723,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
               tc_mma_ts<kPair>(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
                                tc_desc(vt + ks * 2048, kTile * 128), kValues, j > 0 || ks > 0);
             tc_commit<kPair>(v_empty + rv.slot);
-            tc_commit<kPair>(o_full + sb);
+            if (j + 2 >= nblk) tc_commit<kPair>(o_full + (j + 1 == nblk));
           }
           __syncwarp();
           rv.next(NV);
