@@ -526,28 +526,40 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
     const int i0 = u.tile * p.tile_tok;
     const int rows = min(p.tile_tok, u.s.n - i0) * G;
     const int32_t* const pages = p.page_table + static_cast<long long>(u.b) * p.max_pages;
-    // The pipeline of a warp's blocks (every kGroupWarps-th): codes in registers one block ahead, their
-    // rows' first cache lines asked for two ahead, the page looked up three ahead.
-    auto page_of = [&](int i) {  // -1: no such block
-      if (i >= blk1) return -1;
-      return __ldg(pages + (p.page_shift >= 0 ? (keys.block(i) * kBlock) >> p.page_shift : (keys.block(i) * kBlock) / p.page_size));
+    // The pipeline of a warp's blocks (every kGroupWarps-th): codes in registers one block ahead, the page
+    // looked up two ahead.  A block's page and offset follow from the block before, by 64 tokens, where
+    // blocks adjoin; rows are counted by 16.
+    const int per_page = p.page_size / kBlock, step_page = kGroupWarps / per_page, step_off = kGroupWarps - step_page * per_page;
+    int at = u.blk0 + warp, lp = 0, off = 0;  // the iterator's block, its page and its offset in blocks
+    bool fresh = true;
+    struct Where {
+      int page, off;  // page -1: no block, or none that can be read
     };
-    auto row_of = [&](int i, int pg) {  // the block's rows in the pools, in blocks of 16, or -1
-      if (i >= blk1) return -1;
-      if (pg < 0 || pg >= p.num_pages) {
-        if (lane == 0) report(p.status, kDevBadPage);
-        return -1;
+    auto advance = [&]() {
+      Where x = {-1, 0};
+      if (at >= blk1) return x;
+      if (fresh) {
+        const int b = keys.block(at);
+        lp = p.page_shift >= 0 ? b >> (p.page_shift - 4) : b / per_page;
+        off = b - lp * per_page;
       }
-      const int t0 = keys.block(i) * kBlock;
-      const int off = p.page_shift >= 0 ? t0 & (p.page_size - 1) : t0 % p.page_size;
-      return (pg * p.hkv + kvh) * (p.page_size / kBlock) + off / kBlock;
+      // (volatile: the load is to be issued here, ahead of its use)
+      asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(x.page) : "l"(pages + lp));
+      x.off = off;
+      fresh = at < keys.sink && at + kGroupWarps >= keys.sink;  // on from the sinks to the window
+      at += kGroupWarps;
+      lp += step_page;
+      off += step_off;
+      if (off >= per_page) {
+        off -= per_page;
+        ++lp;
+      }
+      return x;
     };
-    auto touch = [&](int row) {  // one 128-byte line per lane
-      if (row < 0) return;
-      constexpr int kLines = (kBlock * KROW + 127) / 128, vLines = (kBlock * VROW + 127) / 128;
-      const uint8_t* at = lane < kLines ? p.k_pool + static_cast<long long>(row) * (kBlock * KROW) + 128 * lane
-                                          : p.v_pool + static_cast<long long>(row) * (kBlock * VROW) + 128 * (lane - kLines);
-      if (lane < kLines + vLines) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    auto row_of = [&](const Where& x, bool there) {  // the block's rows in the pools, in blocks of 16, or -1
+      if (static_cast<unsigned long long>(x.page) < static_cast<unsigned long long>(p.num_pages)) return (x.page * p.hkv + kvh) * per_page + x.off;
+      if (there && lane == 0) report(p.status, kDevBadPage);
+      return -1;
     };
     KWords<DK> kw[2];
     VWords<DV, BV> vw[4];
@@ -563,18 +575,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
       vx[3].load(vr + (2 * c + 9) * VROW, g);
     };
     const int first = u.blk0 + warp;
-    int row0, row1, row2;
-    int pg3;
-    {
-      const int pg0 = page_of(first), pg1 = page_of(first + kGroupWarps), pg2 = page_of(first + 2 * kGroupWarps);
-      pg3 = page_of(first + 3 * kGroupWarps);
-      row0 = row_of(first, pg0);
-      load(row0, kw, vw);
-      row1 = row_of(first + kGroupWarps, pg1);
-      touch(row1);
-      row2 = row_of(first + 2 * kGroupWarps, pg2);
-      touch(row2);
-    }
+    const Where w0 = advance();
+    Where ahead = advance();
+    int row0 = row_of(w0, first < blk1);
+    load(row0, kw, vw);
     // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
     for (int r = warp; r < kTileRows; r += kGroupWarps) {
       float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -626,10 +630,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
     for (int i = first; i < blk1; i += kGroupWarps) {
       const KCodes<DK> kc[2] = {kw[0].get(c), kw[1].get(c)};
       const VCodes<DV, BV> vc[4] = {vw[0].get(g), vw[1].get(g), vw[2].get(g), vw[3].get(g)};
+      const int row1 = row_of(ahead, i + kGroupWarps < blk1);
       load(row1, kw, vw);
-      const int row3 = row_of(i + 3 * kGroupWarps, pg3);
-      touch(row3);
-      pg3 = page_of(i + 4 * kGroupWarps);
+      ahead = advance();
       if (row0 >= 0) {
         const int t0 = keys.block(i) * kBlock;
         // ---- scores: tokens g and g + 8 ------------------------------------------------
@@ -771,8 +774,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
         }
       }
       row0 = row1;
-      row1 = row2;
-      row2 = row3;
     }
     // ---- the warps' partials join ------------------------------------------------------
 #pragma unroll

@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         x.in = t < u.limit;
         x.kvh = u.kvh;
         x.off = off;
-        if (x.in) x.page = __ldg(pages + lp);
+        // (volatile like the codes' loads: it is to be under way an iteration before its use)
+        if (x.in) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(x.page) : "l"(pages + lp));
         return x;
       };
       bool has = false, has_next = false;  // the token can be read
