@@ -62,7 +62,12 @@ struct WideSmem {
   static constexpr int kVStages = kPair ? 3 : kWideCodes ? 1 : 2;
   static constexpr int kTiles = kTable;                             // K stages, then V stages
   static constexpr int kMisc = kTiles + (Shape::kKStages + kVStages) * Shape::kTileBytes;
-  static constexpr int kTotal = kMisc + 704 + 2 * 2 * kTile * 4;
+  static constexpr int kEnd = kMisc + 704 + 2 * 2 * kTile * 4;
+  // 4 KB per softmax warp, where they fit (all but the 1.5-bit format, and the split table alone): its 32
+  // rows' half of q and of the output pass through, so that global accesses are whole 128-byte lines.
+  static constexpr bool kStaged = kEnd + 128 + kSoftWarps * 4096 <= 232448;
+  static constexpr int kStage = (kEnd + 127) / 128 * 128;
+  static constexpr int kTotal = kStaged ? kStage + kSoftWarps * 4096 : kEnd;
   static_assert(Shape::kMasks >= kVStages + 1, "a mask's slot comes round after its reader");
   static_assert(kTotal <= 232448, "shared memory of one CTA");
   static_assert((kChunkMaxBatch + 1 + 32) * 8 <= Shape::kTileBytes, "the plan shares a tile");
@@ -326,7 +331,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     rp.next(kPieces);
     return u.more != 0;
   };
-  WidePiece u;
+  WidePiece u = {};
 
   if (warp < kSoftWarps) {
     // ====== two threads per query row: columns (and dims) 0 .. 63 and 64 .. 127 of a block ======
@@ -337,11 +342,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     auto row_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory"); };
     uint32_t blocks = 0;  // blocks so far, over all pieces
     uint32_t ends0 = 0, ends1 = 0;  // phases of o_full so far
+    // Staging: 128 bytes of each of the warp's rows, 16-byte piece c of row i at piece c ^ (i & 7).  A warp
+    // moves pieces (row 4 k + lane / 8, piece lane % 8) between it and global memory, k = 0 .. 7.
+    uint8_t* const stage = g_smem + W::kStage + warp * 4096;
+    const int row_k = lane >> 3, piece = lane & 7;
+    auto staged = [&](int i, int c) { return reinterpret_cast<uint4*>(stage + i * 128 + ((c ^ (i & 7)) << 4)); };
+    const uint32_t inv_g = 65536u / G + 1u;  // r / G = r * inv_g >> 16 for r < 128
+    auto row_of = [&](int i) {  // row of q and out of tile row i
+      const int token = static_cast<int>(i * inv_g >> 16);
+      return static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (i - token * G);
+    };
     bool ok = true;
     while (ok && next_piece(u)) {
       const bool live = r < u.rows;
-      const int token = live ? r / G : 0;
-      const long long row = static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (live ? r - token * G : 0);
+      const long long row = row_of(live ? r : 0);
       const int nblk = u.blk1 - u.blk0;
       float m = -INFINITY, l = 0.f;
       // ---- q~ = q diag(lambda) H: 64 elements here, then the butterfly of the two halves --------
@@ -350,11 +364,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         float* const lam = tops;
         if (tid < kHeadDim) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
         uint4 raw[8];
-        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) + row * kHeadDim + 64 * g);
+        const __half* const q = static_cast<const __half*>(p.q) + 64 * g;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          const int at = W::kStaged ? (warp & 3) * 32 + 4 * i + row_k : r;
           raw[i] = make_uint4(0, 0, 0, 0);
-          if (live) raw[i] = __ldg(q + i);
+          if (at < u.rows) raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (W::kStaged ? row_of(at) : row) * kHeadDim) + (W::kStaged ? piece : i));
+        }
+        if constexpr (W::kStaged) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *staged(4 * i + row_k, piece) = raw[i];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) raw[i] = *staged(lane, i);
         }
         asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");
         float x[64];
@@ -404,7 +426,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       __syncwarp();
       if (lane == 0) arrive_issuer(q_full);
 
-      const int pos = live ? u.first_pos + token : -1;
+      const int pos = live ? u.first_pos + static_cast<int>(r * inv_g >> 16) : -1;
       for (int j = 0; j < nblk; ++j, ++blocks) {
         const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb + 64 * g;
         ok = wait(s_full + (blocks & 3u), (blocks >> 2) & 1u);
@@ -515,17 +537,37 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       l = sums[r] + sums[kTile + r];  // (the same order in both threads)
       const float f = u.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const long long at = static_cast<long long>(u.slot) * (kCtas * kTile) + rank * kTile + r;
+      __half* const out = static_cast<__half*>(p.out);
+      if (u.slot >= 0) {
+        float* const ws = p.ws_o + (at - r) * kHeadDim + 64 * g;  // of the tile's row 0
 #pragma unroll
-      for (int c = 2 * g; c < 2 * g + 2; ++c) {
-        uint32_t s[32];
-        tmem_ld32(tmem + lanes + kColO + 32 * c, s);
-        tmem_wait_ld();
-        if (live && u.slot >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.ws_o + at * kHeadDim + 32 * c);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[32];
+          tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s);
+          tmem_wait_ld();
+          if constexpr (W::kStaged) {
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(p.out) + row * kHeadDim + 32 * c);
+            for (int i = 0; i < 8; ++i) *staged(lane, i) = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int k = 4 * i + row_k;
+              reinterpret_cast<uint4*>(ws + ((warp & 3) * 32 + k) * kHeadDim + 32 * c)[piece] = *staged(k, piece);
+            }
+          } else if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(ws + r * kHeadDim + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[32];
+          tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
@@ -534,10 +576,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
               const __half2 h = __floats2half2_rn(__uint_as_float(s[8 * i + 2 * e]) * f, __uint_as_float(s[8 * i + 2 * e + 1]) * f);
               w[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (W::kStaged) *staged(lane, 4 * c + i) = v;
+            else if (live) reinterpret_cast<uint4*>(out + row * kHeadDim + 64 * g)[4 * c + i] = v;
           }
+          __syncwarp();
         }
-        __syncwarp();
+        if constexpr (W::kStaged) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = 4 * i + row_k, tile_row = (warp & 3) * 32 + k;
+            if (tile_row < u.rows) reinterpret_cast<uint4*>(out + row_of(tile_row) * kHeadDim + 64 * g)[piece] = *staged(k, piece);
+          }
+          __syncwarp();
+        }
       }
       if (u.slot >= 0 && live && g == 0) p.ws_ml[at] = make_float2(m, l);
       row_sync();         // `sums` is free again
