@@ -1221,7 +1221,9 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.window = std::min(window, 1 << 30);  // no position is further back: the same as none
   p.sinks = std::min(num_sinks, 1 << 30);
   p.tile_rows = tile_rows;
-  p.tile_tok = p.tile_rows == 256 ? 2 * (128 / p.group) : p.tile_rows / p.group;
+  // (of 8 rows, 4 where they are enough: the kernel then holds high and low parts side by side)
+  const bool few = p.tile_rows == 8 && static_cast<long long>(max_new_len) * p.group <= 4;
+  p.tile_tok = p.tile_rows == 256 ? 2 * (128 / p.group) : (few ? 4 : p.tile_rows) / p.group;
   const bool wide = p.tile_rows >= 128;
   p.gap = wide ? 640 : 256;
   p.min_range = 512;
