@@ -884,7 +884,7 @@ cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, int workers, cudaStream_t stream) {
-  return launch_pdl(vq_chunk_merge_kernel, dim3(workers, (p.tile_rows + 15) / 16), dim3(256), 0, stream, p, true);
+  return launch_pdl(vq_chunk_merge_kernel, dim3(workers, (p.tile_rows + 7) / 8), dim3(256), 0, stream, p, true);
 }
 
 }  // namespace vqk

@@ -39,13 +39,17 @@ constexpr float kSlack = 8.f;        // the running maximum may lag by this much
 constexpr int kTile = 128;           // query rows of a CTA's tile, and tokens of a block
 constexpr int kSoftWarps = 8, kCodeWarps = 16;
 constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
-// Registers per thread: 72 at the launch (896 threads), then 256 x 112 + 512 x 56 + 128 x 56 = 896 x 72.
-constexpr int kSoftRegs = 112, kCodeRegs = 56, kIssueRegs = 56;
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
 
 // One CTA alone, or the two CTAs of a pair that share a block's tiles.
 template <bool kPair>
 struct WideShape {
+  // Registers per thread: 72 at the launch (896 threads), then 256 soft + 512 code + 128 issue = 896 x 72
+  // (112, 56, 56 or 104, 64, 40).  Alone, a code thread's 64 dims need the 64: with 56 it spills, and
+  // spilled registers go to L2 beside this much shared memory (5 drafted tokens, batch 16: 174 -> 158 us).
+  // In a pair its 32 dims do not, and the others use theirs (chunks of 1000, window 1024: 131 against 142 us).
+  static constexpr int kSoftRegs = kPair ? 112 : 104, kCodeRegs = kPair ? 56 : 64, kIssueRegs = kPair ? 56 : 40;
+  static_assert(8 * kSoftRegs + 16 * kCodeRegs + 4 * kIssueRegs <= 28 * 72, "the block's registers at the launch");
   static constexpr int kTileBytes = kTile * kHeadDim * 2 / (kPair ? 2 : 1);  // of K or V, this CTA's part
   static constexpr int kKStages = kPair ? 3 : 2;
   // Token masks in flight: block b's is written when the V tile of block b - 1 has been, so the values of
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
 
   if (warp < kSoftWarps) {
     // ====== two threads per query row: columns (and dims) 0 .. 63 and 64 .. 127 of a block ======
-    reg_inc<kSoftRegs>();
+    reg_inc<Shape::kSoftRegs>();
     const int r = tid & (kTile - 1), g = tid >> 7, G = p.group;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the two warps of a row meet here
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     }
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
-    reg_dec<kCodeRegs>();
+    reg_dec<Shape::kCodeRegs>();
     // The first half of the warps expand K, the others V, each at its own pace.  Alone, a thread takes 64
     // dims of a token; in a pair 32, and the CTA has the K of half the block's tokens (columns of B) and
     // half the dims of V (columns of B again).
@@ -730,7 +734,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     }
   } else {
     // ================================= the products ====================================
-    reg_dec<kIssueRegs>();
+    reg_dec<Shape::kIssueRegs>();
     if (warp == kSoftWarps + kCodeWarps && rank != 0) {
       while (next_piece(u)) {  // the first CTA issues
       }
