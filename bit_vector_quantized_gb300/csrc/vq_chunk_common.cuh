@@ -20,6 +20,18 @@
 // (slot 2c + 1), so 2 slots per worker are enough for any batch.  The worker
 // that begins such a tile writes its record, and the merge kernel joins the
 // pieces, in order.
+//
+// W is total / workers, but at least 512 tokens and the root of 32 times the
+// mean length of a (sequence, KV head).  A smaller W shortens the scan and
+// lengthens the merge, which walks a tile's length / W pieces, so the best W
+// grows as the root of that length.  Device time of one new token of one
+// sequence (32 heads of 8 KV heads), W at least 512 | 768 | 1024 | 2048:
+// 4K tokens 18.5 | 19.3 | 21.4 | 28.9 us, 16K 27.0 | 24.6 | 25.6 | 30.7, 32K
+// 38.8 | 33.6 | 31.7 | 33.5; no constant is best at all three.  The root as
+// built: 18.8, 25.9, 32.0.  The root of the
+// total work instead (2 sqrt(total)) took four sequences of 32K from 40.6 to
+// 44.1.  (total / (hkv batch) is taken over idle sequences too: they lower W,
+// towards 512.)
 #pragma once
 
 #include "vq_device.cuh"
@@ -123,6 +135,7 @@ struct ChunkWalk {
     me = me_;
     const long long total = pre[p.batch];
     W = max((total + workers - 1) / static_cast<long long>(workers), static_cast<long long>(p.min_range));
+    W = max(W, static_cast<long long>(sqrtf(32.0f * static_cast<float>(total / (static_cast<long long>(p.hkv) * p.batch)))));
     x = min(W * me, total);
     x1 = min(x + W, total);
     if (x >= x1) return;

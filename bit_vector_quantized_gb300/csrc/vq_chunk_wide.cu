@@ -1,30 +1,50 @@
 // vq_chunk_wide.cu -- chunk attention for many query rows per (sequence, KV head) (sm_103a).
 //
-// The mathematics of vq_chunk_narrow.cu for tiles of 128 query rows, on the
-// fifth-generation tensor cores: per block of 128 tokens
+// The mathematics of vq_chunk_narrow.cu for tiles of 128 query rows per CTA, on
+// the fifth-generation tensor cores: per block of 128 tokens
 //   S [128 x 128] = Q~ K~^T,  P = 2^(S - m),  O [128 x 128] += P V.
-// A block costs 2 x 128^3 multiply-adds for the scores (q~ in high and low fp16
-// parts, so that scores keep about fp32 accuracy) and 128^3 for the values;
-// the codes are 8 KB, so the kernel is bound by arithmetic: the tensor pipe
-// first, the softmax's exponentials and the expansion of the codes beside it.
+//
+// Two shapes.  Alone, a CTA expands a block's codes for its 128 rows.  With
+// more than 128 rows two CTAs form a pair (cta_group::2): one product of 256
+// rows, each CTA holding half of the expanded tile (K of 64 of the block's
+// tokens, 64 dims of V), so each expands, stores and reads half as much.
 //
 //   * Sixteen warps expand codes, eight K and eight V: a thread takes one
-//     token's codes of 64 dims (loaded a block ahead, their page two ahead),
-//     gathers their centroids from the replicated, bank-conflict-free table
-//     and stores 16-byte pieces into the swizzled tiles that the tensor core
-//     reads (K rows of dims, V rows of dims with the token as k: one layout
-//     for both).
-//   * One thread issues the products: scores of block j + 1 before the values
-//     of block j, so the tensor pipe works while the softmax of block j runs.
+//     token's codes of 64 dims (32 in a pair; loaded a block ahead, their page
+//     two ahead), gathers their centroids from the replicated,
+//     bank-conflict-free table and stores 16-byte pieces into the swizzled
+//     tiles that the tensor core reads (K rows of dims, V rows of dims with
+//     the token as k: one layout for both).
+//   * One thread issues the products, values of block j and then scores of
+//     block j + 2 into the same columns; the tensor pipe works on one block
+//     while the softmax works on the next.  Operands are uniform (an elected
+//     lane of a converged warp): from a divergent branch an issue took 190
+//     cycles in a loop of products alone, 68 from uniform operands.
 //   * Eight warps hold half a query row per thread: the Walsh-Hadamard transform
 //     of their q row in registers, the online softmax (maximum and sum in
 //     fp32; the maximum may lag by 2^8, so O is seldom rescaled), P rounded
 //     to fp16 once (p <= 2^8: relative 2^-11, averaging out over the tokens).
+//   * One warp walks the CTA's pieces and hands them to the others, so that
+//     none of them carries the walk in registers.
 //   * Tensor memory, all 512 columns: S twice (P overwrites its S, so the
 //     values read it from there), O, and Q~ high and low.
 //   * Every wait is bounded: on a timeout the CTA raises an abort flag,
 //     everybody leaves, the products in flight are drained and
 //     VQ_DEV_TIMEOUT is reported.
+//
+// What bounds it.  A block costs 24 products of 64 cycles (16 for the scores,
+// q~ in high and low fp16 parts so that they keep about fp32 accuracy, and 8
+// for the values): 1536 cycles, against which the floor of 4 D operations per
+// (row, token) is 1024.  Measured (2048 new tokens in 32K, 32 heads of 8 KV
+// heads, 64 B of codes per token): 968 us, 1.10 PFLOP/s of the floor's
+// operations (0.58 of the measured 1.889), tensor pipe 71 % busy; what is
+// missing is the way from scores to P and back (two blocks of scores are all
+// that tensor memory holds).  The same alone: 1056 us; there a block's gathers, stores and
+// product reads are about 1800 cycles of shared memory, by count (no counter
+// was read for that shape).  A tile's start and end (q~, first scores, output)
+// take 12 000 to 15 000 cycles by clock reads in an earlier state of the
+// kernel, which short contexts feel: 131 to 137 us for chunks of 1000 with a
+// window of 1024 (floor 34).
 #include <type_traits>
 
 #include "vq_chunk_common.cuh"
