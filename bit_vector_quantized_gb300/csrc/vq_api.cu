@@ -1237,7 +1237,9 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   const bool wide = p.tile_rows >= 128;
   p.gap = wide ? 640 : 256;
   p.min_range = 512;
-  p.timeout_ns = 2000000000ULL;
+  // Two seconds, and time for one piece: some waits span a whole one, up to max_seq_len tokens (9 ns per
+  // token measured in tiles of 128 and 256 rows; 40 leaves room for slower formats and clocks).
+  p.timeout_ns = 2000000000ULL + 40ULL * max_seq_len;
   const float scale = softmax_scale == 0.f ? 1.f / std::sqrt(static_cast<float>(L.head_dim)) : softmax_scale;
   p.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 / std::sqrt(128.0));
   auto launch = wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;

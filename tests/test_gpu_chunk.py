@@ -63,6 +63,31 @@ def test_chunk_of_a_long_prompt():
     Case(FORMATS[0], 4, 1, 256, [2500, 700], [600, 700], seed=3).check(300, 33)
 
 
+@pytest.mark.parametrize("n", [1, 2, 4, 20, 50])
+def test_pools_past_32_bits(n):
+    """The same codes on the last pages of pools of more than 2^32 bytes: the same bits."""
+    c = Case(FORMATS[0], 8, 2, 64, [700, 130], [n, n], seed=11)
+    want = c.check()
+    pages = (1 << 32) // (c.hkv * c.page * c.k_pool.shape[3]) + 1000
+    at = pages - c.k_pool.shape[0]
+    pools = {}
+    for name, small in (("k_pool", c.k_pool), ("v_pool", c.v_pool)):
+        big = torch.empty((pages,) + small.shape[1:], dtype=torch.uint8, device="cuda")
+        big[at:] = torch.from_numpy(small).cuda()
+        assert big[:at].numel() > 1 << 32
+        pools[name] = big
+    table = torch.from_numpy(np.where(c.table >= 0, c.table + at, -1).astype(np.int32)).cuda()
+    assert np.array_equal(c.run(page_table=table, **pools), want)
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 20, 50])
+def test_the_largest_batch(n):
+    rng = np.random.default_rng(n)
+    news = np.where(rng.random(1024) < 0.5, 0, rng.integers(1, n + 1, 1024))
+    news[[0, 1023]] = n
+    Case(FORMATS[0], 4, 1, 16, news + rng.integers(0, 60, 1024), news, seed=n).check()
+
+
 @pytest.mark.parametrize("n", [1, 100])
 def test_large_scores_and_scale(n):
     Case(FORMATS[0], 8, 2, 64, [500, 100], [n, n], seed=5, q_scale=6.0).check()
