@@ -1093,14 +1093,20 @@ namespace {
 
 // Tile height of a call, by the rows of its longest (sequence, KV head): all
 // of them where 8 or 16 hold them (warp mma), else 128 (tcgen05) or 256 (a
-// pair of CTAs on one product).  Measured (4 heads per KV head):
+// pair of CTAs on one product).  Where three tiles of 128 hold the rows, the
+// pair's second tile is mostly empty and one CTA is faster, but for the 1.5-bit
+// format.  Measured (4 heads per KV head):
 //   5 rows (5 heads), 64 windows of 4096: 95 us at height 8, 214 at 16
 //   12 rows, batch 8, 8K contexts: 45 us at 16, 52 at 128
 //   32 rows, the same: 70 us at 16, 53 at 128, 73 at 256
-//   400 rows, the same: 114 us at 128, 122 at 256 (256 loses: 1.6 tiles of it)
+//   192 rows, the same: 86 us at 128, 80 at 256
+//   260 to 384 rows, the same: 109 to 114 us at 128, 125 to 129 at 256; one
+//     sequence of 32K: 77 and 88; (2,8) keys, batch 16: 174 to 184 and 182 to
+//     188; 1.5 bit, one sequence of 8K: 51 and 47 to 51
+//   512 rows, batch 8: 139 us at 128, 129 at 256; 640 rows: 165 and 176, but
+//     with (2,8) keys, batch 16: 285 and 268 (left to 256); ragged chunks of
+//     1 to 100 tokens (400 rows), batch 16: 150 and 170 (left to 256 too)
 //   2048 rows, one chunk of 512 tokens in 8K: 95 us at 128, 90 at 256
-//   ragged chunks of 1 to 509 tokens, batch 16: 620 us at 128, 525 at 256
-// The rule looks at the bound alone, so it takes 256 for 400 rows too.
 // VQ_CHUNK_ROWS=16|128|256 selects a height explicitly (a tuning switch for
 // profiling).
 int chunk_tile_rows(const vq_layout& L, int max_new_len) {
@@ -1110,7 +1116,9 @@ int chunk_tile_rows(const vq_layout& L, int max_new_len) {
     if (std::strcmp(env, "128") == 0) return 128;
     if (std::strcmp(env, "256") == 0) return 256;
   }
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+  const int per_tile = 128 / (L.num_q_heads / L.num_kv_heads);  // tokens of 128 rows
+  const bool three = max_new_len > 2 * per_tile && max_new_len <= 3 * per_tile && L.k_bits != 12;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 || three ? 128 : 256;
 }
 
 struct ChunkWs {
@@ -1143,11 +1151,11 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
     return 0;
   const int sms = num_sms > 0 ? num_sms : device_sms();
   if (sms <= 0) return 0;
-  // a call with smaller bounds may take a lower tile, whose slots may be more
+  // a call with smaller bounds may take another tile (of 128 rows also 256), whose slots may be more
   size_t most = 0;
   const int need = chunk_tile_rows(*layout, max_new_len);
   for (int rows : {8, 16, 128, 256})
-    if (rows <= need) most = std::max(most, chunk_ws(rows, sms).total);
+    if (rows <= need || need == 128) most = std::max(most, chunk_ws(rows, sms).total);
   return most;
 }
 

@@ -5,6 +5,8 @@ import random
 
 import pytest
 
+import bit_vector_quantized_gb300 as vq
+
 
 class Plan:
     def __init__(self, tile_tok, block, gap, min_range, window, sinks, hkv, workers, seqs):
@@ -107,3 +109,12 @@ def test_tiles_are_divided_without_gap_or_overlap(seed):
                     assert records[first] == ((b, h, t), got[-1][2])
                     assert [(x[2], x[3]) for x in got] == [(first, 2 * first + 1)] + [(first + i, 2 * (first + i)) for i in range(1, len(got))]
     assert not taken
+
+
+@pytest.mark.parametrize("fmt", [(4, 8, 4, 8), (2, 8, 4, 9), (8, 12, 8, 12)])
+@pytest.mark.parametrize("group", [1, 3, 4, 5, 8])
+@pytest.mark.parametrize("sms", [1, 2, 151, 152])
+def test_a_workspace_of_larger_bounds_serves_smaller_ones(fmt, group, sms):
+    layout = vq.make_layout(128, 2 * group, 2, *fmt, 64)
+    sizes = [vq.vq_chunk_workspace_bytes(layout, 4, 4 * n, 1 << 20, n, sms) for n in range(1, 600)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:])) and sizes[0] > 0
