@@ -268,7 +268,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   uint64_t* const bars = reinterpret_cast<uint64_t*>(g_smem + W::kMisc);
   // A wait costs 100 to 300 cycles here, ready or not (mbarrier operations queue behind the code warps'
   // shared-memory accesses), so what is needed together is collected on one barrier.
-  // (In a pair the first CTA's thread issues for both: what it waits for is arrived on there, by both.)
+  // In a pair the first CTA's thread issues for both.  The second CTA's Q~ and P are arrived on there directly.
+  // Its tiles are arrived on at home, and a warp passes each phase on as one arrival that releases them to the
+  // cluster: the release takes 500 to 800 cycles, which tiles, ready blocks ahead, have and P has not (chunk of
+  // 2048 in 32K, one input: 961 us; with Q~ and P passed on as well 1117).
   uint64_t* const ready = bars;            // [4] by block b: P of b, the V tile of b, the K tile of b + 2
   uint64_t* const start = ready + 4;       // K tiles of blocks 0 and 1
   uint64_t* const k_empty = start + 1;     // [kKStages] scores done, the tile is free
@@ -289,6 +292,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   pdl_trigger();
   const uint32_t rank = kPair ? cluster_rank() : 0u;
   const int worker = static_cast<int>(blockIdx.x) / kCtas;
+  const bool lead = rank == 0;
+  const uint32_t passed = kPair && lead ? 1u : 0u;       // the arrival that stands for the second CTA's tiles
+  const uint32_t soft = lead ? kCtas * kSoftWarps : 0u;  // softmax warps that arrive here
   if (smem_addr(tiles) & 1023u) {  // the swizzled tiles need it (and dynamic shared memory alone gives it)
     if (tid == 0) report(p.status, kDevBadConfig);
     if (tid == 0 && rank == 0) write_record(p, worker, nullptr);
@@ -297,10 +303,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   fill_wide_table<DK, BK, DV, BV>(p);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(ready + i, kCtas * (kSoftWarps + kCodeWarps));
+      mbar_init(ready + i, soft + kCodeWarps + passed);
       mbar_init(s_full + i, 1 + 4);
     }
-    mbar_init(start, kCtas * kCodeWarps);  // (the K warps, for two blocks each)
+    mbar_init(start, kCodeWarps + passed);  // (the K warps, for two blocks each)
     for (int i = 0; i < kKStages; ++i) mbar_init(k_empty + i, 1);
     for (int i = 0; i < NV; ++i) mbar_init(v_empty + i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(o_full + i, 1);
@@ -331,18 +337,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   if constexpr (kPair) cluster_sync();  // the barriers of both are there before either arrives on the other's
 
   // Bounded wait; on a timeout the CTA is given up.  The warps' form is uniform over the warp.
-  auto wait_one = [&](uint64_t* bar, uint32_t phase) {
-    if (mbar_wait_bounded(bar, phase, abort_flag, p.timeout_ns)) return true;
+  auto wait_one = [&](uint64_t* bar, uint32_t phase, auto cluster) {
+    if (mbar_wait_bounded<decltype(cluster)::value>(bar, phase, abort_flag, p.timeout_ns)) return true;
     if (!*abort_flag) {
       *abort_flag = 1;
       report(p.status, kDevTimeout);
     }
     return false;
   };
-  auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(kAll, wait_one(bar, phase)) != 0; };
-  // An arrival that the issuing thread waits for.
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(kAll, wait_one(bar, phase, std::false_type{})) != 0; };
+  // (the issuer's, for what both CTAs of a pair have ready)
+  auto wait_both = [&](uint64_t* bar, uint32_t phase) {
+    return __all_sync(kAll, wait_one(bar, phase, std::integral_constant<bool, kPair>{})) != 0;
+  };
+  // An arrival for what a softmax warp did in tensor memory, which the issuing thread waits for.
   auto arrive_issuer = [&](uint64_t* bar) {
-    if (kPair && rank != 0) mbar_arrive_at(bar, 0);
+    if (kPair && !lead) mbar_arrive_at_tmem(bar, 0);
     else mbar_arrive(bar);
   };
   // The next piece (whole warps); false when there is none or the CTA was given up.
@@ -718,7 +728,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive_issuer(!is_k ? ready + (blocks & 3u) : blocks < 2 ? start : ready + ((blocks - 2) & 3u));
+        if (lane == 0) mbar_arrive(!is_k ? ready + (blocks & 3u) : blocks < 2 ? start : ready + ((blocks - 2) & 3u));
         ring.next(stages);
         ++blocks;
         now = next;
@@ -730,7 +740,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       if (is_k && !any) {
         for (uint32_t end = blocks + 2; blocks < end; ++blocks) {
           if (!wait(empty + ring.slot, ring.phase ^ 1u)) break;
-          if (lane == 0) arrive_issuer(blocks < 2 ? start : ready + ((blocks - 2) & 3u));
+          if (lane == 0) mbar_arrive(blocks < 2 ? start : ready + ((blocks - 2) & 3u));
           ring.next(stages);
         }
       }
@@ -756,7 +766,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     // ================================= the products ====================================
     reg_dec<Shape::kIssueRegs>();
     if (warp == kSoftWarps + kCodeWarps && rank != 0) {
-      while (next_piece(u)) {  // the first CTA issues
+      // The first CTA issues; this one's tiles are passed on.
+      uint32_t blocks = 0;
+      auto pass = [&](uint64_t* bar, uint32_t phase) {
+        if (!wait(bar, phase)) return false;
+        if (lane == 0) mbar_arrive_at(bar, 0);
+        return true;
+      };
+      bool ok = true;
+      while (ok && next_piece(u)) {
+        if (blocks == 0) ok = pass(start, 0);
+        for (int j = u.blk0; ok && j < u.blk1; ++j, ++blocks) ok = pass(ready + (blocks & 3u), (blocks >> 2) & 1u);
       }
     } else if (warp == kSoftWarps + kCodeWarps) {
       constexpr uint32_t kScores = tc_idesc(kCtas * kTile, kTile, false), kValues = tc_idesc(kCtas * kTile, kHeadDim, true);
@@ -767,7 +787,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       bool ok = true;
       while (ok && next_piece(u)) {
         const int nblk = u.blk1 - u.blk0;
-        ok = wait(q_full, tiles_done++ & 1u);
+        ok = wait_both(q_full, tiles_done++ & 1u);
         auto scores = [&](uint32_t blk) {  // of block blk, whose K tile is there
           if (elect_one()) {
             const uint32_t kt = tile0 + rk.slot * kTileBytes;
@@ -785,12 +805,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         };
         // scores of blocks 0 and 1 (their K tiles were there with the blocks before), then values of block j
         // and scores of block j + 2 (into j's columns)
-        if (ok && blocks == 0) ok = wait(start, 0);
+        if (ok && blocks == 0) ok = wait_both(start, 0);
         tc_fence_after();
         for (int j = 0; ok && j < min(nblk, 2); ++j) scores(blocks + j);
         for (int j = 0; ok && j < nblk; ++j) {
           const uint32_t blk = blocks + j, sb = blk & 1u;
-          ok = wait(ready + (blk & 3u), (blk >> 2) & 1u);
+          ok = wait_both(ready + (blk & 3u), (blk >> 2) & 1u);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {

@@ -65,17 +65,29 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 // One bounded wait for phase `parity` of `bar`: the warp may be suspended by
 // the hardware until the phase completes or about `suspend_ns` nanoseconds
-// pass, whichever comes first; true when the phase completed.
+// pass, whichever comes first; true when the phase completed.  kCluster: what
+// threads of the cluster's other CTAs wrote before their arrivals
+// (mbar_arrive_at) is seen too; else what this CTA's threads wrote.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity,
                                               uint32_t suspend_ns = 0x10000u) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(suspend_ns)
-      : "memory");
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(suspend_ns)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(suspend_ns)
+        : "memory");
   return ok != 0;
 }
 
@@ -89,13 +101,14 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // nanoseconds (or soon after *abort is set by another warp).  Each try may
 // park the warp for up to ~65 us, so a waiting warp costs almost no issue
 // slots.  Returns false when it gave up; the caller then treats the stage as
-// empty.
+// empty.  kCluster: as in mbar_try_wait.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
                                                   volatile int* abort, uint64_t timeout_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait<kCluster>(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<kCluster>(bar, parity)) return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > timeout_ns) return false;
   }
