@@ -28,9 +28,11 @@
 //     none of them carries the walk in registers.
 //   * Tensor memory, all 512 columns: S twice (P overwrites its S, so the
 //     values read it from there), O, and Q~ high and low.
-//   * Every wait is bounded: on a timeout the CTA raises an abort flag,
-//     everybody leaves, the products in flight are drained and
-//     VQ_DEV_TIMEOUT is reported.
+//   * Every wait on an mbarrier is bounded: on a timeout the CTA raises an abort
+//     flag, everybody leaves, the products in flight are drained and
+//     VQ_DEV_TIMEOUT is reported.  The softmax warps also meet at barriers
+//     without a limit; vq_chunk_soft.cuh has the order in which none of them
+//     leaves another there.
 //
 // What bounds it.  A block costs 24 products of 64 cycles (16 for the scores,
 // q~ in high and low fp16 parts so that they keep about fp32 accuracy, and 8
@@ -48,6 +50,7 @@
 #include <type_traits>
 
 #include "vq_chunk_common.cuh"
+#include "vq_chunk_soft.cuh"
 #include "vq_gather.cuh"
 #include "vq_tcgen05.cuh"
 
@@ -386,189 +389,205 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       const int token = static_cast<int>(i * inv_g >> 16);
       return static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (i - token * G);
     };
-    bool ok = true;
-    while (ok && next_piece(u)) {
-      const bool live = r < u.rows;
-      const long long row = row_of(live ? r : 0);
-      const int nblk = u.blk1 - u.blk0;
-      float m = -INFINITY, l = 0.f;
-      // ---- q~ = q diag(lambda) H: 64 elements here, then the butterfly of the two halves --------
-      {
-        // lambda by way of shared memory (the maxima's place), this thread's 64 elements in one round trip
-        float* const lam = tops;
-        if (tid < kHeadDim) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
-        uint4 raw[8];
-        const __half* const q = static_cast<const __half*>(p.q) + 64 * g;
+    // What a warp does between its waits and barriers, whose order (and the way out when a wait gave up)
+    // is soft_warp's.
+    bool live = false;  // the thread has a row of the tile
+    long long row = 0;
+    int pos = -1;
+    float m = -INFINITY, l = 0.f;
+    uint4 raw[8];             // the thread's half of its q row
+    float x[64];              // and of its q~
+    uint32_t s0[32], s1[32];  // its half of a row of scores
+    float mx = 0.f, sum[4];
+    bool again = false;
+    float* const lam = tops;  // lambda by way of shared memory (the maxima's place), 64 elements in one round trip
+    auto take = [&]() { return next_piece(u); };
+    auto load_query = [&]() {  // (without a piece: an empty one's, or once more the last one's)
+      live = r < u.rows;
+      row = row_of(live ? r : 0);
+      m = -INFINITY;
+      l = 0.f;
+      if (tid < kHeadDim) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
+      const __half* const q = static_cast<const __half*>(p.q) + 64 * g;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = W::kStaged ? (warp & 3) * 32 + 4 * i + row_k : r;
-          raw[i] = make_uint4(0, 0, 0, 0);
-          if (at < u.rows) raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (W::kStaged ? row_of(at) : row) * kHeadDim) + (W::kStaged ? piece : i));
-        }
-        if constexpr (W::kStaged) {
+      for (int i = 0; i < 8; ++i) {
+        const int at = W::kStaged ? (warp & 3) * 32 + 4 * i + row_k : r;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (at < u.rows) raw[i] = __ldg(reinterpret_cast<const uint4*>(q + (W::kStaged ? row_of(at) : row) * kHeadDim) + (W::kStaged ? piece : i));
+      }
+      if constexpr (W::kStaged) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) *staged(4 * i + row_k, piece) = raw[i];
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) raw[i] = *staged(lane, i);
-        }
-        asm volatile("bar.sync 5, %0;" ::"n"(kSoftWarps * 32) : "memory");
-        float x[64];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-            const float2 v = *reinterpret_cast<const float2*>(lam + 64 * g + 8 * i + 2 * e);
-            x[8 * i + 2 * e] = f.x * v.x;
-            x[8 * i + 2 * e + 1] = f.y * v.y;
-          }
-        }
-        fwht64(x);
+        for (int i = 0; i < 8; ++i) *staged(4 * i + row_k, piece) = raw[i];
         __syncwarp();
-        // the last butterfly joins the row's two threads, by way of the scores' columns (free by now)
-        {
-          uint32_t y[32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 8; ++i) raw[i] = *staged(lane, i);
+      }
+    };
+    auto all_took = [&](bool took) {  // the eight warps meet: lambda is there, and all have the piece
+      uint32_t all;
+      asm volatile(
+          "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbar.red.and.pred b, 5, %2, a;\n\t"
+          "selp.u32 %0, 1, 0, b;\n\t}"
+          : "=r"(all)
+          : "r"(static_cast<uint32_t>(took)), "n"(kSoftWarps * 32)
+          : "memory");
+      return all != 0;
+    };
+    // ---- q~ = q diag(lambda) H: 64 elements here, then the butterfly of the two halves ----------
+    auto turn_half = [&]() {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[32 * c + i]);
-            tmem_st32(tmem + lanes + kColS + 64 * g + 32 * c, y);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          row_sync();
-          tc_fence_after();
-          const float sg = g ? -1.f : 1.f;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld32(tmem + lanes + kColS + 64 * (g ^ 1) + 32 * c, y);
-            tmem_wait_ld();
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              split_pair(fmaf(x[32 * c + 2 * i], sg, __uint_as_float(y[2 * i])),
-                          fmaf(x[32 * c + 2 * i + 1], sg, __uint_as_float(y[2 * i + 1])), hi[i], lo[i]);
-            tmem_st16(tmem + lanes + kColQ + 32 * g + 16 * c, hi);
-            tmem_st16(tmem + lanes + kColQ + 64 + 32 * g + 16 * c, lo);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+          const float2 v = *reinterpret_cast<const float2*>(lam + 64 * g + 8 * i + 2 * e);
+          x[8 * i + 2 * e] = f.x * v.x;
+          x[8 * i + 2 * e + 1] = f.y * v.y;
         }
+      }
+      fwht64(x);
+      __syncwarp();
+      // the last butterfly joins the row's two threads, by way of the scores' columns (free by now)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[32 * c + i]);
+        tmem_st32(tmem + lanes + kColS + 64 * g + 32 * c, y);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+    };
+    auto turn = [&]() {
+      tc_fence_after();
+      const float sg = g ? -1.f : 1.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t y[32];
+        tmem_ld32(tmem + lanes + kColS + 64 * (g ^ 1) + 32 * c, y);
+        tmem_wait_ld();
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          split_pair(fmaf(x[32 * c + 2 * i], sg, __uint_as_float(y[2 * i])),
+                     fmaf(x[32 * c + 2 * i + 1], sg, __uint_as_float(y[2 * i + 1])), hi[i], lo[i]);
+        tmem_st16(tmem + lanes + kColQ + 32 * g + 16 * c, hi);
+        tmem_st16(tmem + lanes + kColQ + 64 + 32 * g + 16 * c, lo);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_issuer(q_full);
-
-      const int pos = live ? u.first_pos + static_cast<int>(r * inv_g >> 16) : -1;
-      for (int j = 0; j < nblk; ++j, ++blocks) {
-        const uint32_t sb = blocks & 1u, col_s = tmem + lanes + kColS + 128 * sb + 64 * g;
-        ok = wait(s_full + (blocks & 3u), (blocks >> 2) & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s0[32], s1[32];
-        tmem_ld32(col_s, s0);
-        tmem_ld32(col_s + 32, s1);
-        const int t0 = u.block(u.blk0 + j) * kTile;
-        const uint4 seen = *reinterpret_cast<const uint4*>(masks + (blocks % kMasks) * 4);
-        const bool whole = t0 + kTile - 1 <= u.first_pos && (p.window == 0 || t0 > u.last_pos - p.window || t0 + kTile <= p.sinks) &&
-                           (seen.x & seen.y & seen.z & seen.w) == kAll;
-        tmem_wait_ld();
-        if (!whole) {
-          // the row sees tokens up to pos, from `from` on, and the sinks: as bits of a half's two words
-          const int from = p.window > 0 ? pos - p.window + 1 : 0;
-          auto bits = [](int lo, int hi) {  // bits lo .. hi - 1 of 32, whatever the two are
-            const uint32_t up = hi >= 32 ? kAll : hi <= 0 ? 0u : (1u << hi) - 1u;
-            const uint32_t down = lo >= 32 ? kAll : lo <= 0 ? 0u : (1u << lo) - 1u;
-            return up & ~down;
-          };
-          auto mask = [&](uint32_t(&s)[32], int t, uint32_t here) {
-            // (tokens past the sequence's end are not in `seen`)
-            const uint32_t see = here & bits(0, pos + 1 - t) & (bits(from - t, 32) | bits(0, p.sinks - t));
+      pos = live ? u.first_pos + static_cast<int>(r * inv_g >> 16) : -1;
+      return u.blk1 - u.blk0;
+    };
+    // ---- a block: its scores, their masks and maximum, P with the maximum so far -----------------
+    auto passes = [&](float v) { return v > m + kSlack || (m == -INFINITY && v > -INFINITY); };
+    auto col_s = [&]() { return tmem + lanes + kColS + 128 * (blocks & 1u) + 64 * g; };
+    auto meet = [&]() { return tops + (blocks & 1u) * 2 * kTile; };
+    // p, its sum, and P in fp16 over its own scores
+    auto store_p = [&](const uint32_t(&s)[32], uint32_t at, float mu) {
+      uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = see >> i & 1u ? s[i] : __float_as_uint(-INFINITY);
-          };
-          mask(s0, t0 + 64 * g, g ? seen.z : seen.x);
-          mask(s1, t0 + 64 * g + 32, g ? seen.w : seen.y);
-        }
-        // ---- the row's maximum, from both halves ------------------------------------------
-        float a[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t* x = k < 2 ? s0 + 16 * k : s1 + 16 * (k - 2);
-          a[k] = max3(x[0], x[1], x[2]);
-#pragma unroll
-          for (int i = 3; i < 15; i += 2) a[k] = max3(__float_as_uint(a[k]), x[i], x[i + 1]);
-          a[k] = fmaxf(a[k], __uint_as_float(x[15]));
-        }
-        float mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
-        float* const meet = tops + sb * 2 * kTile;
-        meet[g * kTile + r] = mx;
-        // ---- p, its sum, and P in fp16 over its own scores --------------------------------
-        // With the maximum so far, which nearly always stays: whether the other half of the row passes it is
-        // seen on the way.
-        auto passes = [&](float x) { return x > m + kSlack || (m == -INFINITY && x > -INFINITY); };
-        float sum[4];
-        auto store_p = [&](const uint32_t(&s)[32], uint32_t at, float mu) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
-            add2(x0, x1, mu, mu);
-            x0 = fast_exp2(x0);
-            x1 = fast_exp2(x1);
-            add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x0, x1);
-            const __half2 h = __floats2half2_rn(x0, x1);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          tmem_st16(at, w);
-        };
-        bool again = __any_sync(kAll, passes(mx));
-        sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
-        if (!again) store_p(s0, col_s, m == -INFINITY ? 0.f : -m);
-        row_sync();
-        const float other = meet[(g ^ 1) * kTile + r];
-        if (!again) store_p(s1, col_s + 32, m == -INFINITY ? 0.f : -m);
-        again = again || __any_sync(kAll, passes(other));
-        if (again) {  // (both warps of the rows come here)
-          mx = fmaxf(mx, other);
-          const float m_new = passes(mx) ? mx : m;
-          const float scale = m_new == m ? 1.f : fast_exp2(m - m_new);  // 0 while nothing is accumulated
-          m = m_new;
-          l *= scale;
-          sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
-          const float mu = m == -INFINITY ? 0.f : -m;
-          store_p(s0, col_s, mu);
-          store_p(s1, col_s + 32, mu);
-          if (j > 0) {  // O follows the maximum, once the values of block - 1 are in (the next scores come after them)
-            ok = j + 1 < nblk ? wait(s_full + ((blocks + 1) & 3u), ((blocks + 1) >> 2) & 1u) : wait(o_full, ends0 & 1u);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
-              tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
-            }
-          }
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_issuer(ready + (blocks & 3u));
+      for (int i = 0; i < 16; ++i) {
+        float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+        add2(x0, x1, mu, mu);
+        x0 = fast_exp2(x0);
+        x1 = fast_exp2(x1);
+        add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x0, x1);
+        const __half2 h = __floats2half2_rn(x0, x1);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      if (!ok) break;
-      ok = (nblk < 2 || wait(o_full, ends0++ & 1u)) && wait(o_full + 1, ends1++ & 1u);
-      if (!ok) break;
+      tmem_st16(at, w);
+    };
+    auto scores_wait = [&]() { return wait(s_full + (blocks & 3u), (blocks >> 2) & 1u); };
+    auto block_half = [&](int j) {
       tc_fence_after();
-      // ---- the piece's rows: to `out`, or as a partial to the workspace --------------------
-      float* const sums = tops + (blocks & 1u) * 2 * kTile;  // (not the last block's maxima)
-      sums[g * kTile + r] = l;
-      row_sync();
-      l = sums[r] + sums[kTile + r];  // (the same order in both threads)
+      tmem_ld32(col_s(), s0);
+      tmem_ld32(col_s() + 32, s1);
+      const int t0 = u.block(u.blk0 + j) * kTile;
+      const uint4 seen = *reinterpret_cast<const uint4*>(masks + (blocks % kMasks) * 4);
+      const bool whole = t0 + kTile - 1 <= u.first_pos && (p.window == 0 || t0 > u.last_pos - p.window || t0 + kTile <= p.sinks) &&
+                         (seen.x & seen.y & seen.z & seen.w) == kAll;
+      tmem_wait_ld();
+      if (!whole) {
+        // the row sees tokens up to pos, from `from` on, and the sinks: as bits of a half's two words
+        const int from = p.window > 0 ? pos - p.window + 1 : 0;
+        auto bits = [](int lo, int hi) {  // bits lo .. hi - 1 of 32, whatever the two are
+          const uint32_t up = hi >= 32 ? kAll : hi <= 0 ? 0u : (1u << hi) - 1u;
+          const uint32_t down = lo >= 32 ? kAll : lo <= 0 ? 0u : (1u << lo) - 1u;
+          return up & ~down;
+        };
+        auto mask = [&](uint32_t(&s)[32], int t, uint32_t here) {
+          // (tokens past the sequence's end are not in `seen`)
+          const uint32_t see = here & bits(0, pos + 1 - t) & (bits(from - t, 32) | bits(0, p.sinks - t));
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = see >> i & 1u ? s[i] : __float_as_uint(-INFINITY);
+        };
+        mask(s0, t0 + 64 * g, g ? seen.z : seen.x);
+        mask(s1, t0 + 64 * g + 32, g ? seen.w : seen.y);
+      }
+      float a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t* v = k < 2 ? s0 + 16 * k : s1 + 16 * (k - 2);
+        a[k] = max3(v[0], v[1], v[2]);
+#pragma unroll
+        for (int i = 3; i < 15; i += 2) a[k] = max3(__float_as_uint(a[k]), v[i], v[i + 1]);
+        a[k] = fmaxf(a[k], __uint_as_float(v[15]));
+      }
+      mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+      meet()[g * kTile + r] = mx;
+      // The maximum so far nearly always stays; whether the other half of the row passes it is seen on the way.
+      again = __any_sync(kAll, passes(mx));
+      sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+      if (!again) store_p(s0, col_s(), m == -INFINITY ? 0.f : -m);
+    };
+    // (false: the wait for O's values gave up)
+    auto block = [&](int j, int nblk) {
+      const float other = meet()[(g ^ 1) * kTile + r];
+      if (!again) store_p(s1, col_s() + 32, m == -INFINITY ? 0.f : -m);
+      again = again || __any_sync(kAll, passes(other));
+      if (again) {  // (both warps of the rows come here)
+        mx = fmaxf(mx, other);
+        const float m_new = passes(mx) ? mx : m;
+        const float scale = m_new == m ? 1.f : fast_exp2(m - m_new);  // 0 while nothing is accumulated
+        m = m_new;
+        l *= scale;
+        sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+        const float mu = m == -INFINITY ? 0.f : -m;
+        store_p(s0, col_s(), mu);
+        store_p(s1, col_s() + 32, mu);
+        if (j > 0) {  // O follows the maximum, once the values of block - 1 are in (the next scores come after them)
+          if (!(j + 1 < nblk ? wait(s_full + ((blocks + 1) & 3u), ((blocks + 1) >> 2) & 1u) : wait(o_full, ends0 & 1u))) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s0[i] = __float_as_uint(__uint_as_float(s0[i]) * scale);
+            tmem_st32(tmem + lanes + kColO + 64 * g + 32 * c, s0);
+          }
+        }
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_issuer(ready + (blocks & 3u));
+      ++blocks;
+      return true;
+    };
+    auto output_wait = [&](int nblk) { return (nblk < 2 || wait(o_full, ends0++ & 1u)) && wait(o_full + 1, ends1++ & 1u); };
+    auto put_sum = [&]() {
+      tc_fence_after();
+      meet()[g * kTile + r] = l;  // (not the last block's maxima)
+    };
+    // ---- the piece's rows: to `out`, or as a partial to the workspace ----------------------------
+    auto store = [&]() {
+      l = meet()[r] + meet()[kTile + r];  // (the same order in both threads)
       const float f = u.slot >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const long long at = static_cast<long long>(u.slot) * (kCtas * kTile) + rank * kTile + r;
       __half* const out = static_cast<__half*>(p.out);
@@ -626,9 +645,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         }
       }
       if (u.slot >= 0 && live && g == 0) p.ws_ml[at] = make_float2(m, l);
-      row_sync();         // `sums` is free again
       tc_fence_before();  // (O's reads, before the next piece's arrival on q_full)
-    }
+    };
+    soft_warp(take, load_query, all_took, turn_half, row_sync, turn, scores_wait, block_half, block, output_wait, put_sum, store);
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
     reg_dec<Shape::kCodeRegs>();
