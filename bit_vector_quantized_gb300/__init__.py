@@ -613,11 +613,18 @@ def alloc_chunk_workspace(layout: vq_layout, batch: int, num_tokens: int, max_se
 
 def chunk_attention(layout: vq_layout, q, lambda_, codebook_k, codebook_v, k_pool, v_pool,
                     page_table, seq_lens, max_seq_len: int, cu_new_lens=None,
-                    max_new_len: int = 1, window: int = 0, num_sinks: int = 0, out=None,
+                    max_new_len: Optional[int] = None, window: int = 0, num_sinks: int = 0, out=None,
                     workspace=None, softmax_scale: float = 0.0, status=None, stream=None):
     """fp16 [T][Hq][D] attention of the newest tokens' queries q [T][Hq][D] over the quantized
-    pools, causal; row offsets cu_new_lens int32 [B + 1] (None: one row per sequence).  With
+    pools, causal; row offsets cu_new_lens int32 [B + 1] (None: one row per sequence).
+    max_new_len bounds the rows of every sequence and is needed with row offsets: a sequence
+    with more is left out, which only `status` tells.  Rows that are left out, and rows behind
+    the last sequence, stay as they are in `out` (undefined where it is made here).  With
     `window` a row sees that many last tokens and the first `num_sinks` (see vq_chunk_attention)."""
+    if max_new_len is None:
+        if cu_new_lens is not None:
+            raise ValueError("max_new_len is needed with cu_new_lens")
+        max_new_len = 1
     torch = _torch()
     dev = _need(q, "q")
     f16, i32, u8 = torch.float16, torch.int32, torch.uint8

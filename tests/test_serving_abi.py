@@ -89,3 +89,9 @@ def test_chunk_workspace_bytes():
     for kw in ((-1, 4, 1000, 1), (4, -1, 1000, 1), (4, 4, -1, 1), (4, 4, 1000, -1)):
         assert vq.vq_chunk_workspace_bytes(L, *kw, 152) == 0
     assert vq.vq_chunk_workspace_bytes(vq.make_layout(v_sub=8), 4, 4, 1000, 1, 152) == 0
+
+
+def test_row_offsets_need_their_bound():
+    """Without it longer sequences would be left out of an output that nobody had written."""
+    with pytest.raises(ValueError, match="max_new_len"):
+        vq.chunk_attention(vq.make_layout(), None, None, None, None, None, None, None, None, 100, cu_new_lens=object())
