@@ -54,7 +54,9 @@ __global__ void __launch_bounds__(kSlotThreads) vq_slots_kernel(const SlotsParam
   __shared__ int bad;
   if (tid == 0) bad = kDevOk;
   __syncthreads();
-  auto fail = [&](int code) { atomicCAS(&bad, kDevOk, code); };
+  // Of several faults the same one is reported in every run: lengths, then too few pages, then pages.
+  static_assert(kDevOk < kDevBadPage && kDevBadPage < kDevBadLength && kDevBadLength < kDevNoPages, "the larger wins");
+  auto fail = [&](int code) { atomicMax(&bad, code); };
 
   // ---- lengths and their checks, this thread's run of sequences ----------------
   const int num_free = __ldg(p.num_free);
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kSlotThreads) vq_slots_kernel(const SlotsParam
   }
   if (tid == 0) {
     if (all_new > p.max_tokens) fail(kDevBadLength);
-    else if (all_take > num_free) fail(kDevNoPages);
+    else if (bad != kDevBadLength && all_take > num_free) fail(kDevNoPages);
   }
   for (int b = b0; b < b1; ++b) {  // (sums past int32 are never used: the step is refused)
     const int n = cu[b], k = first[b];

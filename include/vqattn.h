@@ -487,8 +487,8 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
  * more than max_tokens new tokens or num_free outside [0, free_capacity]
  * (VQ_DEV_BAD_LENGTH), too few free pages (VQ_DEV_NO_PAGES) or a page outside
  * [0, num_pages) among those the step uses (VQ_DEV_BAD_PAGE) report that
- * status, take no page, copy seq_lens and num_free through and leave every
- * row at -1 and every offset at 0.
+ * status (of several the first named here), take no page, copy seq_lens and
+ * num_free through and leave every row at -1 and every offset at 0.
  *   batch 0 .. 16384, max_tokens 0 .. 2^30, page_size as in vq_layout.
  * Outputs other than the two pairs named above must not overlap inputs.
  */

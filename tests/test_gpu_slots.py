@@ -142,6 +142,31 @@ def test_refused_steps_change_nothing(what, in_place):
     same(got, want)
 
 
+@pytest.mark.parametrize("faults", [("page", "length"), ("page", "tokens"), ("page", "few"), ("page", "few", "length"),
+                                    ("few", "num_free")])
+def test_of_several_faults_the_same_is_reported(faults):
+    """The old page's fault is met first, by the thread that meets the others too (two sequences per thread)."""
+    B, P = 1024, 16
+    lens, new, table, free, nf, P, pages = make(B, P, [5] * B, [20] * B, spare=0)
+    T = int(new.sum())
+    for f in faults:
+        if f == "page":
+            table[0, 0] = pages
+        elif f == "length":
+            lens[1] = -1
+        elif f == "tokens":
+            T -= 1
+        elif f == "few":
+            nf -= 1
+        elif f == "num_free":
+            nf = len(free) + 1
+    st, want = plain(lens, new, table, free, nf, P, pages, T)
+    for _ in range(5):
+        got_st, got = call(lens, new, table, free, nf, P, pages, T)
+        assert got_st == st
+        same(got, want)
+
+
 def test_sums_past_32_bits_are_refused():
     B = 8
     lens, new = np.zeros(B, np.int32), np.full(B, (1 << 31) - 1, np.int32)
