@@ -402,12 +402,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     bool again = false;
     float* const lam = tops;  // lambda by way of shared memory (the maxima's place), 64 elements in one round trip
     auto take = [&]() { return next_piece(u); };
-    auto load_query = [&]() {  // (without a piece: an empty one's, or once more the last one's)
+    auto load_query = [&]() {  // (without a piece: no row's, or once more the last piece's)
       live = r < u.rows;
       row = row_of(live ? r : 0);
       m = -INFINITY;
       l = 0.f;
-      if (tid < kHeadDim) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
+      if (tid < kHeadDim && u.more) lam[tid] = __ldg(p.lambda + u.kvh * kHeadDim + tid) * p.qscale;
       const __half* const q = static_cast<const __half*>(p.q) + 64 * g;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
