@@ -25,10 +25,6 @@ namespace {
 
 constexpr int kSlotThreads = 512;
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 __device__ __forceinline__ int pages_of(int tokens, int page_size) {
   return static_cast<int>((static_cast<unsigned>(tokens) + page_size - 1u) / page_size);
 }
@@ -130,7 +126,7 @@ __global__ void __launch_bounds__(kSlotThreads) vq_slots_kernel(const SlotsParam
   }
   __syncthreads();
   const bool ok = bad == kDevOk;
-  cluster_barrier();  // every CTA has read what the step may overwrite
+  cluster_sync();  // every CTA has read what the step may overwrite
 
   // ---- this CTA's share of the outputs ------------------------------------------
   const int nthreads = gridDim.x * kSlotThreads, gtid = blockIdx.x * kSlotThreads + tid;

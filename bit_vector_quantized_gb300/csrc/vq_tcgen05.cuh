@@ -77,9 +77,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Arrives on the barrier at this place in CTA `rank` of the cluster.  What this thread wrote, and what it
 // has seen of its own CTA's writes, comes before it for a thread there that waits by mbar_try_wait<true>:
 // release and acquire name the cluster, because without a scope they hold inside one CTA only.
