@@ -1095,18 +1095,24 @@ namespace {
 // of them where 8 or 16 hold them (warp mma), else 128 (tcgen05) or 256 (a
 // pair of CTAs on one product).  Where three tiles of 128 hold the rows, the
 // pair's second tile is mostly empty and one CTA is faster, but for the 1.5-bit
-// format.  Measured (4 heads per KV head):
-//   5 rows (5 heads), 64 windows of 4096: 95 us at height 8, 214 at 16
-//   12 rows, batch 8, 8K contexts: 45 us at 16, 52 at 128
-//   32 rows, the same: 70 us at 16, 53 at 128, 73 at 256
-//   192 rows, the same: 86 us at 128, 80 at 256
-//   260 to 384 rows, the same: 109 to 114 us at 128, 125 to 129 at 256; one
-//     sequence of 32K: 77 and 88; (2,8) keys, batch 16: 174 to 184 and 182 to
-//     188; 1.5 bit, one sequence of 8K: 51 and 47 to 51
-//   512 rows, batch 8: 139 us at 128, 129 at 256; 640 rows: 165 and 176, but
-//     with (2,8) keys, batch 16: 285 and 268 (left to 256); ragged chunks of
-//     1 to 100 tokens (400 rows), batch 16: 150 and 170 (left to 256 too)
-//   2048 rows, one chunk of 512 tokens in 8K: 95 us at 128, 90 at 256
+// format.  Measured on the device, merge included, from a cold L2 (4 heads per
+// KV head, (4,8) codes; batch 8: contexts of 4000 to 8000; batch 16: (2,8)
+// keys, 3000 to 6000):
+//   5 rows (5 heads), 64 windows of 4096: 99 us at height 8, 221 at 16
+//   12 to 16 rows, batch 8: 48 us at 16, 60 at 128
+//   20 to 32 rows, batch 8: 70 to 72 us at 16, 60 to 62 at 128; 32 rows 78 at 256
+//   128 rows, batch 8: 65 us at 128, 80 at 256; 192 rows: 89 and 83
+//   260 to 384 rows, batch 8: 116 to 121 us at 128, 127 to 130 at 256; one
+//     sequence of 32K: 83 to 84 and 91; batch 16: 182 to 188 and 185 to 188;
+//     1.5 bit, one sequence of 8K: 56 and 52 to 55
+//   512 rows, batch 8: 146 us at 128, 131 at 256; 640 rows: 170 and 178, but
+//     batch 16: 290 and 266 (left to 256); ragged chunks of 1 to 100 tokens
+//     (400 rows), batch 16 of 4096 to 8192: 158 and 168 (left to 256 too)
+//   2048 rows, one chunk of 512 tokens in 8K: 103 us at 128, 97 at 256
+// The height is the whole call's, from the bound of its longest chunk: many
+// single tokens beside one chunk pay for rows that they have not.  63 single
+// tokens (4000 to 16 000) and a chunk of 512: 668 us in one call, 144 and 97 in
+// two; 32 (4000 to 10 000) and a chunk of 5: 166, or 67 and 43.
 // VQ_CHUNK_ROWS=16|128|256 selects a height explicitly (a tuning switch for
 // profiling).
 int chunk_tile_rows(const vq_layout& L, int max_new_len) {

@@ -22,15 +22,25 @@
 //     gather of a V centroid serves four output blocks.
 //
 // q~ is split into high and low fp16 parts everywhere (scores keep about fp32
-// accuracy); p is rounded to fp16 once where it is not split (p <= 2^8:
-// relative 2^-11, which averages out over a row's tokens).  Sums and maxima
-// are fp32.
+// accuracy); p is rounded to fp16 once where it is not split (p <= 2^8,
+// relative 2^-11): a choice, which leaves the outputs off by 2.6e-4 to 2.8e-4
+// against 64 bits where their own rounding is 2.1e-4.  Splitting it for 5 to 8
+// rows too left 2.1e-4 and took 105 us instead of 97 in the case below.  Sums
+// and maxima are fp32.
 //
-// What bounds them: instructions and their latency (the few-row kernel issues
-// in 54 % of the cycles, its gathers take 52 % of the shared-memory pipe).
+// What bounds them: latency at 16 warps per SM (the table takes the shared
+// memory that more would need).  Nothing is full: the few-row kernel issues in
+// 54 % of the cycles, the shared-memory pipe is 65 % busy, DRAM 29 %; a warp
+// waits between two instructions first for the one before (1.9 cycles), then
+// for a gather (1.0), for its turn (0.9), for the tensor pipe (0.7) and for the
+// codes (0.5).
 // Measured for one token of each of 64 sequences with a window of 4096 and 4
 // sinks: 97 us for 40 heads of 8 KV heads and 100 B of codes per token (211 MB,
-// 2.2 TB/s, floor 31 us), 72 us for 32 heads and 64 B.  Groups of four warps
+// 2.2 TB/s, floor 31 us), 72 us for 32 heads and 64 B.  The 16-row kernel, 3
+// new tokens of each of 8 sequences of 4000 to 8000 tokens, 32 heads of 8 KV
+// heads and 64 B: 42 us and a merge of 8 (25 MB, floor 3.7 us).  It has 8 warps
+// and 216 registers a thread, so it is further from filling anything: issue
+// 30 %, shared memory 28 %, tensor pipe 22 %, DRAM 8 %.  Groups of four warps
 // with pieces of their own came together with the end of the spilled registers:
 // 146 to 104 us; which of the two did how much was not taken apart.
 

@@ -25,7 +25,8 @@
 // mean length of a (sequence, KV head).  A smaller W shortens the scan and
 // lengthens the merge, which walks a tile's length / W pieces, so the best W
 // grows as the root of that length.  Device time of one new token of one
-// sequence (32 heads of 8 KV heads), W at least 512 | 768 | 1024 | 2048:
+// sequence (32 heads of 8 KV heads; one graph replayed, so the codes were in
+// L2), W at least 512 | 768 | 1024 | 2048:
 // 4K tokens 18.5 | 19.3 | 21.4 | 28.9 us, 16K 27.0 | 24.6 | 25.6 | 30.7, 32K
 // 38.8 | 33.6 | 31.7 | 33.5; no constant is best at all three.  The root as
 // built: 18.8, 25.9, 32.0.  The root of the

@@ -23,7 +23,13 @@
 //   * Eight warps hold half a query row per thread: the Walsh-Hadamard transform
 //     of their q row in registers, the online softmax (maximum and sum in
 //     fp32; the maximum may lag by 2^8, so O is seldom rescaled), P rounded
-//     to fp16 once (p <= 2^8: relative 2^-11, averaging out over the tokens).
+//     to fp16 once (p <= 2^8, relative 2^-11).  That rounding is a choice: the
+//     outputs are off by 2.3e-4 to 2.9e-4 (relative, against 64 bits), their own
+//     rounding to fp16 being 2.1e-4 of it.  With P's low part as a second operand
+//     (tensor memory has its columns) 2.1e-4 is all that is left, but a block has
+//     32 products instead of 24: a chunk of 2048 in 32K took 1215 us instead of
+//     943, chunks of 1000 with a window of 1024 161 instead of 132, 5 drafted
+//     tokens 203 instead of 158.
 //   * One warp walks the CTA's pieces and hands them to the others, so that
 //     none of them carries the walk in registers.
 //   * Tensor memory, all 512 columns: S twice (P overwrites its S, so the
@@ -38,15 +44,21 @@
 // q~ in high and low fp16 parts so that they keep about fp32 accuracy, and 8
 // for the values): 1536 cycles, against which the floor of 4 D operations per
 // (row, token) is 1024.  Measured (2048 new tokens in 32K, 32 heads of 8 KV
-// heads, 64 B of codes per token): 968 us, 1.10 PFLOP/s of the floor's
-// operations (0.58 of the measured 1.889), tensor pipe 71 % busy; what is
+// heads, 64 B of codes per token): this kernel alone 946 us, 1.13 PFLOP/s of
+// the floor's operations (0.60 of the measured 1.889), tensor pipe 72 % busy;
+// the call on one input again and again 941 to 990 with the clock, on
+// changing inputs 1022 (1.04 PFLOP/s).  What is
 // missing is the way from scores to P and back (two blocks of scores are all
-// that tensor memory holds).  The same alone: 1056 us; there a block's gathers, stores and
-// product reads are about 1800 cycles of shared memory, by count (no counter
-// was read for that shape).  A tile's start and end (q~, first scores, output)
+// that tensor memory holds).  The same with one CTA per tile, in an earlier
+// state: 1056 us; there a block's gathers, stores and
+// product reads are about 1800 cycles of shared memory, by count (5 drafted
+// tokens, batch 16: its pipe is 55 % busy, the tensor pipe 43 %).  A tile's
+// start and end (q~, first scores, output)
 // take 12 000 to 15 000 cycles by clock reads in an earlier state of the
-// kernel, which short contexts feel: 131 to 137 us for chunks of 1000 with a
-// window of 1024 (floor 34).
+// kernel, which short contexts feel: 128 us, with the merge 132, for chunks
+// of 1000 with a window of 1024 (floor 34).  The 1.5-bit format's plain table,
+// whose gathers meet in the same banks, costs little beside that: prompts of
+// 512 to 8192 tokens take 3 to 12 % longer than at 8 bits.
 #include <type_traits>
 
 #include "vq_chunk_common.cuh"

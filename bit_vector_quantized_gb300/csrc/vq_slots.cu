@@ -9,8 +9,8 @@
 // position len_b + i and in slot page_table[b][pos / P] P + pos % P.
 //
 // One cluster of up to 8 CTAs does it in one launch.  Every CTA reads all
-// lengths and forms both prefix sums in shared memory (a few KB; cheaper than
-// a second launch), checks everything the step takes, and only after the
+// lengths and forms both prefix sums in shared memory (a few KB; instead of a
+// second launch, which was not tried), checks everything the step takes, and only after the
 // cluster's barrier writes its share, so seq_lens and num_free may be updated
 // in place and a step that cannot be served changes nothing.  A thread
 // finds its tokens' sequence by binary search in shared memory, four tokens

@@ -72,7 +72,8 @@ typedef enum vq_device_status {
   VQ_DEV_OK = 0,
   VQ_DEV_BAD_PAGE = 1,       /* page_table entry outside [0, num_pages): page skipped */
   VQ_DEV_BAD_SLOT = 2,       /* slot_mapping entry >= num_pages * page_size: token skipped */
-  VQ_DEV_TIMEOUT = 3,        /* an asynchronous-copy wait exceeded its time limit */
+  VQ_DEV_TIMEOUT = 3,        /* a wait inside a kernel (for a copy or a product) exceeded its
+                                time limit */
   VQ_DEV_BAD_CONFIG = 4,     /* launch parameters the kernel cannot honour: it did nothing
                                 (not reachable through this ABI's validated calls) */
   VQ_DEV_BAD_LENGTH = 5,     /* a length, count or row offset outside its range (see the call) */
@@ -410,10 +411,13 @@ vq_status vq_decode_attention_residual(const vq_layout* layout, int32_t batch, c
  * Attention of each sequence's newest tokens over its quantized cache, causal,
  * optionally with a sliding window and first tokens that stay visible
  * ("sinks").  Serves chunks of a prompt, drafted tokens that are checked
- * together, single decode tokens, and any mix of them in one batch.  For every
- * new token exactly what vq_decode_attention computes for it (VecInfer,
- * section 方法细节 "注意力机制中的向量量化KV缓存"), over the tokens it sees: the new
- * tokens' own codes are in the cache already (vq_encode_kv).
+ * together, single decode tokens, and any mix of them in one batch (many
+ * single tokens beside a few chunks are faster as two calls, because the
+ * kernel is chosen for the longest).  For every new token what
+ * vq_decode_attention computes for it (VecInfer, section 方法细节
+ * "注意力机制中的向量量化KV缓存"; sums in another order, so not bit for bit), over
+ * the tokens it sees: the new tokens' own codes are in the cache already
+ * (vq_encode_kv).
  *   The rows of sequence b are cu_new_lens[b] .. cu_new_lens[b + 1] - 1 of q
  *   and out: its last n tokens, row i standing at position
  *   t = seq_lens[b] - n + i.  It sees the cached tokens p with p <= t and,
@@ -441,8 +445,10 @@ vq_status vq_decode_attention_residual(const vq_layout* layout, int32_t batch, c
  *   lambda, codebooks, pools, page_table, status: as in vq_decode_attention;
  *   the codebooks' values are finite.  Batches up to 1024, max_seq_len up
  *   to 2^30.
- * batch or num_tokens 0 is a no-op.  Every layout that vq_decode_attention
- * supports.  Two kernels on `stream`; results do not vary from run to run.
+ * batch, num_tokens or max_new_len 0 is a no-op.  Every layout that
+ * vq_decode_attention supports.  Two kernels on `stream`; results do not vary
+ * from run to run.  Where a wait inside a kernel gave up (VQ_DEV_TIMEOUT) the
+ * rows of `out` are undefined.
  */
 vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
                              const void* q, const float* lambda, const void* codebook_k,
@@ -489,7 +495,8 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
  * [0, num_pages) among those the step uses (VQ_DEV_BAD_PAGE) report that
  * status (of several the first named here), take no page, copy seq_lens and
  * num_free through and leave every row at -1 and every offset at 0.
- *   batch 0 .. 16384, max_tokens 0 .. 2^30, page_size as in vq_layout.
+ *   batch 0 .. 16384 (vq_chunk_attention takes up to 1024 sequences a call),
+ *   max_tokens 0 .. 2^30, page_size as in vq_layout.
  * Outputs other than the two pairs named above must not overlap inputs.
  */
 vq_status vq_append_slots(int32_t batch, const int32_t* seq_lens, const int32_t* new_lens,
