@@ -116,6 +116,30 @@ constexpr size_t kHeadBytes = (sizeof(NarrowHead) + 15) / 16 * 16;
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
+// Row r of a tile's q~ (one warp) as high and low fp16 parts: rows r and kRows + r of qs; 0 where there is none.
+template <int kRows>
+__device__ __forceinline__ void query_row(const ChunkParams& p, const ChunkPiece& u, int r, bool live, __half* qs, int lane) {
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live) {
+    const int G = p.group;
+    const long long row = static_cast<long long>(u.s.row0 + u.tile * p.tile_tok + r / G) * p.hq + u.kvh * G + r % G;
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __half*>(p.q) + row * kHeadDim) + lane);
+    const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + u.kvh * kHeadDim) + lane);
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    x[0] = lo.x * lam.x;
+    x[1] = lo.y * lam.y;
+    x[2] = hi.x * lam.z;
+    x[3] = hi.y * lam.w;
+    fwht128_warp(x, lane);
+  }
+  uint2 vh, vl;
+  split_pair(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
+  split_pair(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
+  *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
+  *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
+}
+
 // Row r of a piece from its warps' partials (one warp; mo [warps][rows][128], ml [warps][rows]): to
 // `out`, or as one partial to the workspace.
 template <int kWarps, int kRows>
@@ -188,26 +212,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) vq_chunk_narrow_kernel(c
     const int i0 = u.tile * p.tile_tok;
     const int rows = min(p.tile_tok, u.s.n - i0) * G;
     // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
-    for (int r = warp; r < kRows; r += kNarrowWarps) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (r < rows) {
-        const long long row = static_cast<long long>(u.s.row0 + i0 + r / G) * p.hq + u.kvh * G + r % G;
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __half*>(p.q) + row * kHeadDim) + lane);
-        const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + u.kvh * kHeadDim) + lane);
-        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-        x[0] = lo.x * lam.x;
-        x[1] = lo.y * lam.y;
-        x[2] = hi.x * lam.z;
-        x[3] = hi.y * lam.w;
-        fwht128_warp(x, lane);
-      }
-      uint2 vh, vl;
-      split_pair(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
-      split_pair(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
-      *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
-      *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
-    }
+    for (int r = warp; r < kRows; r += kNarrowWarps) query_row<kRows>(p, u, r, r < rows, qs, lane);
     __syncthreads();
     if (tid == 0) me->plan(p, k + 1);
     uint32_t qa[8][4], ql[8][4];
@@ -599,26 +604,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) vq_chunk_few_kernel(const C
     int row0 = row_of(w0, first < blk1);
     load(row0, kw, vw);
     // ---- q~ of the tile's rows, as high and low fp16 parts ------------------------
-    for (int r = warp; r < kTileRows; r += kGroupWarps) {
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (r < rows) {
-        const long long row = static_cast<long long>(u.s.row0 + i0 + r / G) * p.hq + u.kvh * G + r % G;
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __half*>(p.q) + row * kHeadDim) + lane);
-        const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + u.kvh * kHeadDim) + lane);
-        const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-        const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-        x[0] = lo.x * lam.x;
-        x[1] = lo.y * lam.y;
-        x[2] = hi.x * lam.z;
-        x[3] = hi.y * lam.w;
-        fwht128_warp(x, lane);
-      }
-      uint2 vh, vl;
-      split_pair(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
-      split_pair(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
-      *reinterpret_cast<uint2*>(qs + r * kQStride + 4 * lane) = vh;
-      *reinterpret_cast<uint2*>(qs + (kRows + r) * kQStride + 4 * lane) = vl;
-    }
+    for (int r = warp; r < kTileRows; r += kGroupWarps) query_row<kRows>(p, u, r, r < rows, qs, lane);
     group_sync();
     if (tid == 0) me->plan(p, k + 1);
     uint32_t qb[8][2];  // (the low parts of more than 4 rows are read again for every block: registers are short)
