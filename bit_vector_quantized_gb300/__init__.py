@@ -5,7 +5,8 @@ in the library's CUDA kernels):
 
 * ``vq_*`` functions mirror the C ABI of include/vqattn.h one to one: they take
   device pointers as Python ints and raise :class:`VQError` on a non-OK status.
-* ``encode_kv`` / ``decode_attention`` / ``append_slots`` / ``rotary`` /
+* ``encode_kv`` / ``decode_attention`` / ``append_slots`` / ``rotary`` / ``append_kv`` /
+  ``tree_attention`` / ``keep_tokens`` /
   ``alloc_pools`` / ``alloc_workspace`` and their like accept torch tensors (PyTorch supplies device memory and streams), check
   dtypes, shapes and devices, and pass their pointers to the ``vq_*`` calls.
 
@@ -40,7 +41,8 @@ EXPORTED = ("vq_code_row_bytes", "vq_check_layout", "vq_encode_kv", "vq_decode_w
             "vq_decode_partial_method", "vq_decode_combine", "vq_decode_step", "vq_dequantize_kv",
             "vq_decode_residual_workspace_bytes", "vq_decode_attention_residual",
             "vq_decode_attention_static", "vq_static_scratch_bytes", "vq_chunk_attention",
-            "vq_chunk_workspace_bytes", "vq_append_slots", "vq_rotary", "vq_last_error", "vq_version")
+            "vq_chunk_workspace_bytes", "vq_append_slots", "vq_rotary", "vq_tree_attention",
+            "vq_tree_workspace_bytes", "vq_append_kv", "vq_keep_tokens", "vq_last_error", "vq_version")
 
 
 class VQError(RuntimeError):
@@ -128,6 +130,12 @@ def lib() -> ctypes.CDLL:
                                       P, P]),
             "vq_rotary": (I32, [ctypes.POINTER(vq_rotary_config), I32, P, I32, P, I64, I32, P, P,
                                 I64, P, I64, I32, P, P, P]),
+            "vq_tree_attention": (I32, [LP, I32, I32, P, P, P, P, P, P, I64, P, I32, P, I32, P, I32, P, I32, P,
+                                        I32, I32, ctypes.c_float, P, P, SZ, P, P]),
+            "vq_tree_workspace_bytes": (SZ, [LP, I32, I32, I32, I32, I32]),
+            "vq_append_kv": (I32, [LP, ctypes.POINTER(vq_rotary_config), I32, P, P, I32, P, I64, P, I64, P, I64,
+                                   P, P, P, P, P, P, I64, P, P]),
+            "vq_keep_tokens": (I32, [LP, I32, P, P, P, I32, P, P, I32, I64, I32, P, P, P, I32, P, P, P, P, P]),
             "vq_last_error": (ctypes.c_char_p, []),
             "vq_version": (ctypes.c_char_p, []),
         }
@@ -313,6 +321,44 @@ def vq_rotary(config, num_tokens, positions, dtype, q, q_stride, num_q_heads, q_
     _check(lib().vq_rotary(ctypes.byref(config), num_tokens, _ptr(positions), dtype, _ptr(q),
                            q_stride, num_q_heads, _ptr(q_out), _ptr(k), k_stride, _ptr(v),
                            v_stride, num_kv_heads, _ptr(k_out), _ptr(v_out), _ptr(stream)))
+
+
+def vq_tree_attention(layout, batch, num_tokens, q, lambda_, codebook_k, codebook_v, k_pool, v_pool, num_pages, page_table,
+                      max_pages_per_seq, seq_lens, max_seq_len, cu_new_lens, max_new_len, tree_masks, mask_words, positions,
+                      window, num_sinks, softmax_scale, out, workspace, workspace_bytes, status=None, stream=None) -> None:
+    _check(lib().vq_tree_attention(
+        ctypes.byref(layout), batch, num_tokens, _ptr(q), _ptr(lambda_), _ptr(codebook_k),
+        _ptr(codebook_v), _ptr(k_pool), _ptr(v_pool), num_pages, _ptr(page_table),
+        max_pages_per_seq, _ptr(seq_lens), max_seq_len, _ptr(cu_new_lens), max_new_len,
+        _ptr(tree_masks), mask_words, _ptr(positions), window, num_sinks, float(softmax_scale),
+        _ptr(out), _ptr(workspace), workspace_bytes, _ptr(status), _ptr(stream)))
+
+
+def vq_tree_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len, num_sms=0) -> int:
+    return int(lib().vq_tree_workspace_bytes(ctypes.byref(layout), batch, num_tokens, max_seq_len,
+                                             max_new_len, num_sms))
+
+
+def vq_append_kv(layout, config, num_tokens, positions, slot_mapping, dtype, q, q_stride, k, k_stride,
+                 v, v_stride, lambda_, codebook_k, codebook_v, q_out, k_pool, v_pool, num_pages,
+                 status=None, stream=None) -> None:
+    _check(lib().vq_append_kv(ctypes.byref(layout), ctypes.byref(config), num_tokens, _ptr(positions),
+                              _ptr(slot_mapping), dtype, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+                              v_stride, _ptr(lambda_), _ptr(codebook_k), _ptr(codebook_v), _ptr(q_out),
+                              _ptr(k_pool), _ptr(v_pool), num_pages, _ptr(status), _ptr(stream)))
+
+
+def vq_keep_tokens(layout, batch, seq_lens, cu_new_lens, keep, max_keep, keep_lens, page_table,
+                   max_pages_per_seq, num_pages, k_pools, v_pools, free_pages, free_capacity, num_free,
+                   seq_lens_out, num_free_out, status=None, stream=None) -> None:
+    """k_pools, v_pools: device pointers of the layers' pools, as many of the one as of the other."""
+    if len(k_pools) != len(v_pools):
+        raise ValueError("k_pools and v_pools have different numbers of layers")
+    kp, vp = ((ctypes.c_void_p * len(x))(*map(_ptr, x)) for x in (k_pools, v_pools))
+    _check(lib().vq_keep_tokens(ctypes.byref(layout), batch, _ptr(seq_lens), _ptr(cu_new_lens), _ptr(keep),
+                                max_keep, _ptr(keep_lens), _ptr(page_table), max_pages_per_seq, num_pages,
+                                len(k_pools), kp, vp, _ptr(free_pages), free_capacity, _ptr(num_free),
+                                _ptr(seq_lens_out), _ptr(num_free_out), _ptr(status), _ptr(stream)))
 
 
 def vq_last_error() -> str:
@@ -756,5 +802,156 @@ def rotary(config: vq_rotary_config, positions, q=None, k=None, v=None, q_out=No
         _check(lib().vq_rotary(ctypes.byref(config), T, pos, VQ_FP16 if dt is f16 else VQ_BF16, qp, qs, qh,
                                qop, kp, ks, vp, vs, kh or vh, kop, vop, st))
         return qo, ko, vo
+
+    return _launch(dev, stream, call)
+
+
+# ------------------------------------- torch layer: trees of drafted tokens ---
+
+def alloc_tree_workspace(layout: vq_layout, batch: int, num_tokens: int, max_seq_len: int,
+                         max_new_len: int, device="cuda"):
+    torch = _torch()
+    with torch.cuda.device(device):
+        n = vq_tree_workspace_bytes(layout, batch, num_tokens, max_seq_len, max_new_len)
+        if n == 0:
+            raise VQError(VQ_ERR_INVALID_ARG, "cannot size the workspace")
+        return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def tree_attention(layout: vq_layout, q, lambda_, codebook_k, codebook_v, k_pool, v_pool,
+                   page_table, seq_lens, max_seq_len: int, cu_new_lens, max_new_len: int, tree_masks,
+                   positions=None, window: int = 0, num_sinks: int = 0, out=None, workspace=None,
+                   softmax_scale: float = 0.0, status=None, stream=None):
+    """fp16 [T][Hq][D] attention of trees of drafted tokens, queries q [T][Hq][D], over the quantized
+    pools, which hold their codes already: each row sees the tokens before the drafted ones and of
+    these the ones that its bits name.  tree_masks int64 [T][words], bit j of a row (bit j % 64 of
+    word j // 64) for the sequence's j-th drafted token; up to max_new_len <= 256 per sequence.
+    With `window` positions (int32 [T]) are needed (see vq_tree_attention).  Rows that are left
+    out, and rows behind the last sequence, stay as they are in `out` (undefined where it is made
+    here)."""
+    torch = _torch()
+    dev = _need(q, "q")
+    f16, i32, u8 = torch.float16, torch.int32, torch.uint8
+    T, B, pages = q.shape[0], seq_lens.shape[0], k_pool.shape[0]
+    L = layout
+    D, H, P = L.head_dim, L.num_kv_heads, L.page_size
+    rows = (T, L.num_q_heads, D)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B][max_pages]")
+    if tree_masks.dim() != 2:
+        raise ValueError("tree_masks must be [T][words]")
+    width, words = page_table.shape[1], tree_masks.shape[1]
+    args = (_arg(q, f16, "q", dev, rows), _arg(lambda_, torch.float32, "lambda", dev, (H, D)),
+            _arg(codebook_k, f16, "codebook_k", dev, (1 << L.k_bits, L.k_sub)),
+            _arg(codebook_v, f16, "codebook_v", dev, (1 << L.v_bits, L.v_sub)),
+            _arg(k_pool, u8, "k_pool", dev, (pages, H, P, (D // L.k_sub * L.k_bits + 31) // 32 * 4)),
+            _arg(v_pool, u8, "v_pool", dev, (pages, H, P, (D // L.v_sub * L.v_bits + 31) // 32 * 4)),
+            pages, _arg(page_table, i32, "page_table", dev, (B, width)), width,
+            _arg(seq_lens, i32, "seq_lens", dev, (B,)), max_seq_len,
+            _arg(cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)), max_new_len,
+            _arg(tree_masks, torch.int64, "tree_masks", dev, (T, words)), words,
+            _arg(positions, i32, "positions", dev, (T,)), window, num_sinks, softmax_scale)
+
+    def call(st):
+        o = torch.empty(rows, dtype=f16, device=dev) if out is None else out
+        w = workspace
+        if w is None:
+            w = alloc_tree_workspace(layout, B, T, max_seq_len, max_new_len, dev)
+        _check(lib().vq_tree_attention(ctypes.byref(layout), B, T, *args, _arg(o, f16, "out", dev, rows),
+                                       _arg(w, u8, "workspace", dev), w.numel(),
+                                       _arg(status, i32, "status", dev, (1,)), st))
+        return o
+
+    return _launch(dev, stream, call)
+
+
+def append_kv(layout: vq_layout, config: vq_rotary_config, positions, slot_mapping, k, v, lambda_, codebook_k,
+              codebook_v, k_pool, v_pool, q=None, q_out=None, status=None, stream=None):
+    """Append k and v [T][Hkv][D] to the pools at slot_mapping (int64 [T]), keys turned by positions
+    (int32 [T]) on the way, and return q [T][Hq][D] turned (fp16; None without q): what rotary and
+    encode_kv do, in one launch and without rounding the turned keys.  Inputs are fp16 or bf16,
+    all of one type, and may be slices of one fused projection; q_out may be its own (fp16,
+    contiguous) q."""
+    torch = _torch()
+    dev, dt, f16, u8 = _need(k, "k"), k.dtype, torch.float16, torch.uint8
+    if dt is not f16 and dt is not torch.bfloat16:
+        raise TypeError(f"q, k and v must be float16 or bfloat16, got {dt}")
+    L = layout
+    T, D, H, P, pages = positions.shape[0], L.head_dim, L.num_kv_heads, L.page_size, k_pool.shape[0]
+    qp, qs, qh = _rows_arg(q, dt, "q", dev, T, D)
+    kp, ks, kh = _rows_arg(k, dt, "k", dev, T, D)
+    vp, vs, vh = _rows_arg(v, dt, "v", dev, T, D)
+    if kh != H or vh != H or (q is not None and qh != L.num_q_heads):
+        raise ValueError(f"q, k and v have {qh}, {kh} and {vh} heads, the layout has {L.num_q_heads} and {H}")
+    if q is None and q_out is not None:
+        raise ValueError("q_out is given without q")
+    head = (ctypes.byref(config), T, _arg(positions, torch.int32, "positions", dev, (T,)),
+            _arg(slot_mapping, torch.int64, "slot_mapping", dev, (T,)), VQ_FP16 if dt is f16 else VQ_BF16,
+            qp, qs, kp, ks, vp, vs, _arg(lambda_, torch.float32, "lambda", dev, (H, D)),
+            _arg(codebook_k, f16, "codebook_k", dev, (1 << L.k_bits, L.k_sub)),
+            _arg(codebook_v, f16, "codebook_v", dev, (1 << L.v_bits, L.v_sub)))
+    tail = (_arg(k_pool, u8, "k_pool", dev, (pages, H, P, (D // L.k_sub * L.k_bits + 31) // 32 * 4)),
+            _arg(v_pool, u8, "v_pool", dev, (pages, H, P, (D // L.v_sub * L.v_bits + 31) // 32 * 4)), pages,
+            _arg(status, torch.int32, "status", dev, (1,)))
+
+    def call(st):
+        o = q_out
+        if q is not None and o is None:
+            o = torch.empty((T, qh, D), dtype=f16, device=dev)
+        _check(lib().vq_append_kv(ctypes.byref(layout), *head,
+                                  None if q is None else _arg(o, f16, "q_out", dev, (T, qh, D)), *tail, st))
+        return o
+
+    return _launch(dev, stream, call)
+
+
+class KeptTokens(NamedTuple):
+    seq_lens: object  # int32 [B]
+    num_free: object  # int32 [1]
+
+
+def _layers_arg(pools, name, device, shape):
+    """Device pointers of the layers' pools: one tensor [layers][..], or one tensor per layer."""
+    torch = _torch()
+    if isinstance(pools, torch.Tensor):
+        first = _arg(pools, torch.uint8, name, device, (pools.shape[0],) + shape)
+        step = pools.stride(0)
+        return [first + i * step for i in range(pools.shape[0])]
+    return [_arg(x, torch.uint8, f"{name}[{i}]", device, shape) for i, x in enumerate(pools)]
+
+
+def keep_tokens(layout: vq_layout, seq_lens, cu_new_lens, keep, keep_lens, page_table, k_pools, v_pools, free_pages,
+                num_free, seq_lens_out=None, num_free_out=None, status=None, stream=None) -> KeptTokens:
+    """Keep the accepted ones of a step's drafted tokens: those with indices keep[b][:keep_lens[b]]
+    (int32 [B][max_keep], ascending) move together behind the context in the pools of all
+    layers, and emptied pages go back on the free stack (see vq_keep_tokens).  k_pools and
+    v_pools: one tensor [layers][pages][Hkv][P][row bytes], or a sequence of the layers' pools."""
+    torch = _torch()
+    dev, i32 = _need(seq_lens, "seq_lens"), torch.int32
+    L = layout
+    D, H, P, B = L.head_dim, L.num_kv_heads, L.page_size, seq_lens.shape[0]
+    if page_table.dim() != 2 or keep.dim() != 2:
+        raise ValueError("page_table and keep must be [B][max_pages] and [B][max_keep]")
+    if len(k_pools) != len(v_pools):
+        raise ValueError("k_pools and v_pools have different numbers of layers")
+    if len(k_pools) == 0:
+        raise ValueError("there are no pools")
+    width, most, free, pages = page_table.shape[1], keep.shape[1], free_pages.numel(), k_pools[0].shape[0]
+    kp = _layers_arg(k_pools, "k_pools", dev, (pages, H, P, (D // L.k_sub * L.k_bits + 31) // 32 * 4))
+    vp = _layers_arg(v_pools, "v_pools", dev, (pages, H, P, (D // L.v_sub * L.v_bits + 31) // 32 * 4))
+    layers = len(kp)
+    args = (_arg(seq_lens, i32, "seq_lens", dev, (B,)), _arg(cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)),
+            _arg(keep, i32, "keep", dev, (B, most)), most, _arg(keep_lens, i32, "keep_lens", dev, (B,)),
+            _arg(page_table, i32, "page_table", dev, (B, width)), width, pages, layers,
+            (ctypes.c_void_p * layers)(*kp), (ctypes.c_void_p * layers)(*vp),
+            _arg(free_pages, i32, "free_pages", dev, (free,)), free, _arg(num_free, i32, "num_free", dev, (1,)))
+
+    def call(st):
+        r = KeptTokens(torch.empty(B, dtype=i32, device=dev) if seq_lens_out is None else seq_lens_out,
+                       torch.empty(1, dtype=i32, device=dev) if num_free_out is None else num_free_out)
+        _check(lib().vq_keep_tokens(ctypes.byref(layout), B, *args, _arg(r[0], i32, "seq_lens_out", dev, (B,)),
+                                    _arg(r[1], i32, "num_free_out", dev, (1,)),
+                                    _arg(status, i32, "status", dev, (1,)), st))
+        return r
 
     return _launch(dev, stream, call)

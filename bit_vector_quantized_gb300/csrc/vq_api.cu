@@ -945,6 +945,31 @@ bool rotary_frequencies(const vq_rotary_config& c, unsigned long long (&freq)[64
   return true;
 }
 
+vq_status check_rotary_config(const vq_rotary_config* config, int32_t dtype) {
+  if (!config) return fail(VQ_ERR_INVALID_ARG, "config is NULL");
+  const vq_rotary_config& c = *config;
+  if (c.head_dim != 128)
+    return fail(VQ_ERR_UNSUPPORTED, "head_dim %d: this build implements head_dim 128", c.head_dim);
+  if (c.rotary_dim < 2 || c.rotary_dim > c.head_dim || c.rotary_dim % 2)
+    return fail(VQ_ERR_INVALID_ARG, "rotary_dim %d must be even and in 2..%d", c.rotary_dim, c.head_dim);
+  if (c.scaling < VQ_ROTARY_NONE || c.scaling > VQ_ROTARY_WAVELENGTH)
+    return fail(VQ_ERR_INVALID_ARG, "scaling %d is not a vq_rotary_scaling", c.scaling);
+  if (!(c.base >= 1.0) || !std::isfinite(c.base)) return fail(VQ_ERR_INVALID_ARG, "base must be finite and >= 1");
+  if (!(c.attention_factor > 0.0) || !std::isfinite(c.attention_factor))
+    return fail(VQ_ERR_INVALID_ARG, "attention_factor must be finite and > 0");
+  if (c.scaling != VQ_ROTARY_NONE && (!(c.factor > 0.0) || !std::isfinite(c.factor)))
+    return fail(VQ_ERR_INVALID_ARG, "factor must be finite and > 0");
+  if (c.scaling == VQ_ROTARY_PARTS || c.scaling == VQ_ROTARY_WAVELENGTH) {
+    if (!(c.original_len > 0.0) || !std::isfinite(c.original_len) || !(c.low_turns > 0.0) ||
+        !(c.high_turns > c.low_turns) || !std::isfinite(c.high_turns))
+      return fail(VQ_ERR_INVALID_ARG, "original_len > 0 and 0 < low_turns < high_turns are needed");
+    if (c.scaling == VQ_ROTARY_PARTS && !(c.base > 1.0))
+      return fail(VQ_ERR_INVALID_ARG, "scaling by parts needs a base > 1");
+  }
+  if (dtype != VQ_FP16 && dtype != VQ_BF16) return fail(VQ_ERR_INVALID_ARG, "dtype %d is not a vq_dtype", dtype);
+  return VQ_OK;
+}
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
@@ -1008,27 +1033,9 @@ vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const in
                     int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
                     void* q_out, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                     int32_t num_kv_heads, void* k_out, void* v_out, void* stream) {
-  if (!config) return fail(VQ_ERR_INVALID_ARG, "config is NULL");
+  vq_status checked = check_rotary_config(config, dtype);
+  if (checked != VQ_OK) return checked;
   const vq_rotary_config& c = *config;
-  if (c.head_dim != 128)
-    return fail(VQ_ERR_UNSUPPORTED, "head_dim %d: this build implements head_dim 128", c.head_dim);
-  if (c.rotary_dim < 2 || c.rotary_dim > c.head_dim || c.rotary_dim % 2)
-    return fail(VQ_ERR_INVALID_ARG, "rotary_dim %d must be even and in 2..%d", c.rotary_dim, c.head_dim);
-  if (c.scaling < VQ_ROTARY_NONE || c.scaling > VQ_ROTARY_WAVELENGTH)
-    return fail(VQ_ERR_INVALID_ARG, "scaling %d is not a vq_rotary_scaling", c.scaling);
-  if (!(c.base >= 1.0) || !std::isfinite(c.base)) return fail(VQ_ERR_INVALID_ARG, "base must be finite and >= 1");
-  if (!(c.attention_factor > 0.0) || !std::isfinite(c.attention_factor))
-    return fail(VQ_ERR_INVALID_ARG, "attention_factor must be finite and > 0");
-  if (c.scaling != VQ_ROTARY_NONE && (!(c.factor > 0.0) || !std::isfinite(c.factor)))
-    return fail(VQ_ERR_INVALID_ARG, "factor must be finite and > 0");
-  if (c.scaling == VQ_ROTARY_PARTS || c.scaling == VQ_ROTARY_WAVELENGTH) {
-    if (!(c.original_len > 0.0) || !std::isfinite(c.original_len) || !(c.low_turns > 0.0) ||
-        !(c.high_turns > c.low_turns) || !std::isfinite(c.high_turns))
-      return fail(VQ_ERR_INVALID_ARG, "original_len > 0 and 0 < low_turns < high_turns are needed");
-    if (c.scaling == VQ_ROTARY_PARTS && !(c.base > 1.0))
-      return fail(VQ_ERR_INVALID_ARG, "scaling by parts needs a base > 1");
-  }
-  if (dtype != VQ_FP16 && dtype != VQ_BF16) return fail(VQ_ERR_INVALID_ARG, "dtype %d is not a vq_dtype", dtype);
   if (num_tokens < 0) return fail(VQ_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
   if (num_tokens == 0) return VQ_OK;  // empty tensors may come with NULL pointers
   if (!positions || !aligned16(positions))
@@ -1147,33 +1154,25 @@ ChunkWs chunk_ws(int tile_rows, int grid) {
   return w;
 }
 
-}  // namespace
+// Tile height of a call over trees of drafted tokens.
+int tree_tile_rows(const vq_layout&, int) { return 256; }
 
-extern "C" {
+struct TreeArgs {
+  const uint64_t* masks;
+  int32_t mask_words;
+  const int32_t* positions;
+};
 
-size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t num_tokens,
-                                int32_t max_seq_len, int32_t max_new_len, int32_t num_sms) {
-  if (check_layout_impl(layout, 1) != VQ_OK || batch < 0 || num_tokens < 0 || max_seq_len < 0 || max_new_len < 0)
-    return 0;
-  const int sms = num_sms > 0 ? num_sms : device_sms();
-  if (sms <= 0) return 0;
-  // a call with smaller bounds may take another tile (of 128 rows also 256), whose slots may be more
-  size_t most = 0;
-  const int need = chunk_tile_rows(*layout, max_new_len);
-  for (int rows : {8, 16, 128, 256})
-    if (rows <= need || need == 128) most = std::max(most, chunk_ws(rows, sms).total);
-  return most;
-}
-
-vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
-                             const void* q, const float* lambda, const void* codebook_k,
-                             const void* codebook_v, const void* k_pool, const void* v_pool,
-                             int64_t num_pages, const int32_t* page_table,
-                             int32_t max_pages_per_seq, const int32_t* seq_lens,
-                             int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
-                             int32_t window, int32_t num_sinks, float softmax_scale, void* out,
-                             void* workspace, size_t workspace_bytes, int32_t* status,
-                             void* stream) {
+// vq_chunk_attention, or with `tree` vq_tree_attention.
+vq_status attention_of_rows(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                            const void* q, const float* lambda, const void* codebook_k,
+                            const void* codebook_v, const void* k_pool, const void* v_pool,
+                            int64_t num_pages, const int32_t* page_table,
+                            int32_t max_pages_per_seq, const int32_t* seq_lens,
+                            int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
+                            int32_t window, int32_t num_sinks, float softmax_scale, void* out,
+                            void* workspace, size_t workspace_bytes, int32_t* status,
+                            void* stream, const TreeArgs* tree) {
   vq_status st = check_layout_impl(layout, 1);
   if (st != VQ_OK) return st;
   const vq_layout& L = *layout;
@@ -1203,9 +1202,19 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   const size_t row_bytes = 2 * static_cast<size_t>(L.num_q_heads) * L.head_dim;
   if (overlap(q, num_tokens * row_bytes, out, num_tokens * row_bytes))
     return fail(VQ_ERR_INVALID_ARG, "out overlaps q");
+  if (tree) {
+    if (max_new_len > vqk::kTreeMaxTokens)
+      return fail(VQ_ERR_UNSUPPORTED, "max_new_len %d > %d drafted tokens", max_new_len, vqk::kTreeMaxTokens);
+    if (!cu_new_lens) return fail(VQ_ERR_INVALID_ARG, "cu_new_lens is NULL");
+    if (!tree->masks || !aligned16(tree->masks)) return fail(VQ_ERR_INVALID_ARG, "tree_masks is NULL or not 16-byte aligned");
+    if (tree->mask_words < (max_new_len + 63) / 64 || tree->mask_words > 64)
+      return fail(VQ_ERR_INVALID_ARG, "mask_words %d not in %d..64", tree->mask_words, (max_new_len + 63) / 64);
+    if (!tree->positions && window > 0) return fail(VQ_ERR_INVALID_ARG, "positions are needed with a window");
+    if (!aligned16(tree->positions)) return fail(VQ_ERR_INVALID_ARG, "positions is not 16-byte aligned");
+  }
   const int sms = device_sms();
   if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
-  const int tile_rows = chunk_tile_rows(L, max_new_len);
+  const int tile_rows = tree ? tree_tile_rows(L, max_new_len) : chunk_tile_rows(L, max_new_len);
   const int grid = tile_rows == 256 ? std::max(sms & ~1, 2) : sms;
   const ChunkWs ws = chunk_ws(tile_rows, grid);
   if (workspace_bytes < ws.total)
@@ -1240,8 +1249,8 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.max_pages = max_pages_per_seq;
   p.max_seq_len = max_seq_len;
   p.max_new_len = max_new_len;
-  p.window = std::min(window, 1 << 30);  // no position is further back: the same as none
-  p.sinks = std::min(num_sinks, 1 << 30);
+  p.window = tree ? window : std::min(window, 1 << 30);  // (without a tree no position is further back: the same as none)
+  p.sinks = tree ? num_sinks : std::min(num_sinks, 1 << 30);
   p.tile_rows = tile_rows;
   // (of 8 rows, 4 where they are enough: the kernel then holds high and low parts side by side)
   const bool few = p.tile_rows == 8 && static_cast<long long>(max_new_len) * p.group <= 4;
@@ -1256,11 +1265,230 @@ vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num
   p.timeout_ns = 2000000000ULL + 40ULL * max_seq_len;
   const float scale = softmax_scale == 0.f ? 1.f / std::sqrt(static_cast<float>(L.head_dim)) : softmax_scale;
   p.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 / std::sqrt(128.0));
-  auto launch = wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;
+  if (tree) {
+    p.masks = reinterpret_cast<const unsigned long long*>(tree->masks);
+    p.mask_words = tree->mask_words;
+    p.positions = tree->positions;
+  }
+  auto launch = tree ? vqk::launch_tree_wide : wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;
   cudaError_t e = launch(p, L.k_sub, L.k_bits, L.v_sub, L.v_bits, grid, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention launch");
+  if (e != cudaSuccess) return cuda_fail(e, tree ? "vq_tree_attention launch" : "vq_chunk_attention launch");
   e = vqk::launch_chunk_merge(p, chunk_workers(tile_rows, grid), static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "vq_chunk_attention merge");
+  if (e != cudaSuccess) return cuda_fail(e, tree ? "vq_tree_attention merge" : "vq_chunk_attention merge");
+  return VQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                                int32_t max_seq_len, int32_t max_new_len, int32_t num_sms) {
+  if (check_layout_impl(layout, 1) != VQ_OK || batch < 0 || num_tokens < 0 || max_seq_len < 0 || max_new_len < 0)
+    return 0;
+  const int sms = num_sms > 0 ? num_sms : device_sms();
+  if (sms <= 0) return 0;
+  // a call with smaller bounds may take another tile (of 128 rows also 256), whose slots may be more
+  size_t most = 0;
+  const int need = chunk_tile_rows(*layout, max_new_len);
+  for (int rows : {8, 16, 128, 256})
+    if (rows <= need || need == 128) most = std::max(most, chunk_ws(rows, sms).total);
+  return most;
+}
+
+vq_status vq_chunk_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                             const void* q, const float* lambda, const void* codebook_k,
+                             const void* codebook_v, const void* k_pool, const void* v_pool,
+                             int64_t num_pages, const int32_t* page_table,
+                             int32_t max_pages_per_seq, const int32_t* seq_lens,
+                             int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
+                             int32_t window, int32_t num_sinks, float softmax_scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream) {
+  return attention_of_rows(layout, batch, num_tokens, q, lambda, codebook_k, codebook_v, k_pool, v_pool, num_pages, page_table,
+                           max_pages_per_seq, seq_lens, max_seq_len, cu_new_lens, max_new_len, window, num_sinks, softmax_scale,
+                           out, workspace, workspace_bytes, status, stream, nullptr);
+}
+
+size_t vq_tree_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                               int32_t max_seq_len, int32_t max_new_len, int32_t num_sms) {
+  if (check_layout_impl(layout, 1) != VQ_OK || batch < 0 || num_tokens < 0 || max_seq_len < 0 || max_new_len < 0)
+    return 0;
+  const int sms = num_sms > 0 ? num_sms : device_sms();
+  if (sms <= 0) return 0;
+  return chunk_ws(tree_tile_rows(*layout, max_new_len), std::max(sms, 2)).total;
+}
+
+vq_status vq_tree_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                            const void* q, const float* lambda, const void* codebook_k,
+                            const void* codebook_v, const void* k_pool, const void* v_pool,
+                            int64_t num_pages, const int32_t* page_table,
+                            int32_t max_pages_per_seq, const int32_t* seq_lens,
+                            int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
+                            const uint64_t* tree_masks, int32_t mask_words,
+                            const int32_t* positions, int32_t window, int32_t num_sinks,
+                            float softmax_scale, void* out, void* workspace,
+                            size_t workspace_bytes, int32_t* status, void* stream) {
+  const TreeArgs tree = {tree_masks, mask_words, positions};
+  return attention_of_rows(layout, batch, num_tokens, q, lambda, codebook_k, codebook_v, k_pool, v_pool, num_pages, page_table,
+                           max_pages_per_seq, seq_lens, max_seq_len, cu_new_lens, max_new_len, window, num_sinks, softmax_scale,
+                           out, workspace, workspace_bytes, status, stream, &tree);
+}
+
+}  // extern "C"
+
+// ---- keys and values from a projection's rows, and accepted tokens ----------------
+extern "C" {
+
+vq_status vq_append_kv(const vq_layout* layout, const vq_rotary_config* config,
+                       int32_t num_tokens, const int32_t* positions,
+                       const int64_t* slot_mapping, int32_t dtype, const void* q,
+                       int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, const float* lambda, const void* codebook_k,
+                       const void* codebook_v, void* q_out, void* k_pool, void* v_pool,
+                       int64_t num_pages, int32_t* status, void* stream) {
+  vq_status st = check_layout_impl(layout, 1);
+  if (st != VQ_OK) return st;
+  const vq_layout& L = *layout;
+  st = check_rotary_config(config, dtype);
+  if (st != VQ_OK) return st;
+  const vq_rotary_config& c = *config;
+  if (num_tokens < 0) return fail(VQ_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_tokens == 0) return VQ_OK;  // empty tensors may come with NULL pointers
+  if (!q != !q_out) return fail(VQ_ERR_INVALID_ARG, "q and q_out go together");
+  const void* ptrs[] = {positions, slot_mapping, k, v, lambda, codebook_k, codebook_v, k_pool, v_pool, q, q_out};
+  const char* names[] = {"positions", "slot_mapping", "k", "v", "lambda", "codebook_k", "codebook_v", "k_pool", "v_pool", "q", "q_out"};
+  for (int i = 0; i < 11; ++i) {
+    if (!ptrs[i] && i < 9) return fail(VQ_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if (!aligned16(ptrs[i])) return fail(VQ_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  if (num_pages < 1) return fail(VQ_ERR_INVALID_ARG, "num_pages %lld < 1", (long long)num_pages);
+  if (L.num_q_heads > 4096) return fail(VQ_ERR_INVALID_ARG, "%d heads of q: 1..4096", L.num_q_heads);
+  const void* src[] = {q, k, v};
+  const int64_t stride[] = {q_stride, k_stride, v_stride};
+  const int32_t heads[] = {L.num_q_heads, L.num_kv_heads, L.num_kv_heads};
+  const char* row_names[] = {"q", "k", "v"};
+  size_t in_bytes[3] = {};
+  for (int i = 0; i < 3; ++i) {
+    if (!src[i]) continue;
+    const int64_t row = static_cast<int64_t>(heads[i]) * L.head_dim;
+    if (stride[i] < row || stride[i] % 8 || stride[i] > (1LL << 31))
+      return fail(VQ_ERR_INVALID_ARG, "%s_stride %lld must be a multiple of 8, at least %lld and at most 2^31", row_names[i],
+                  (long long)stride[i], (long long)row);
+    in_bytes[i] = 2 * (static_cast<size_t>(num_tokens - 1) * stride[i] + row);
+  }
+  vqk::AppendParams p{};
+  const size_t q_bytes = 2 * static_cast<size_t>(num_tokens) * L.num_q_heads * L.head_dim;
+  for (int i = 0; q && i < 3; ++i) {
+    const bool in_place = i == 0 && q_out == q && dtype == VQ_FP16 && in_bytes[0] == q_bytes;
+    if (!in_place && overlap(q_out, q_bytes, src[i], in_bytes[i])) return fail(VQ_ERR_INVALID_ARG, "q_out overlaps %s", row_names[i]);
+  }
+  if (q && (overlap(q_out, q_bytes, positions, 4 * static_cast<size_t>(num_tokens)) ||
+            overlap(q_out, q_bytes, slot_mapping, 8 * static_cast<size_t>(num_tokens))))
+    return fail(VQ_ERR_INVALID_ARG, "q_out overlaps positions or slot_mapping");
+  if (!rotary_frequencies(c, p.freq)) return fail(VQ_ERR_INVALID_ARG, "the frequencies are not finite");
+  const int sms = device_sms();
+  if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.lambda = lambda;
+  p.status = status;
+  p.num_slots = static_cast<long long>(num_pages) * L.page_size;
+  p.factor = c.attention_factor;
+  p.rotary_dim = c.rotary_dim;
+  p.interleaved = c.interleaved != 0;
+  p.bf16 = dtype == VQ_BF16;
+  p.num_tokens = num_tokens;
+  p.hkv = L.num_kv_heads;
+  p.page_size = L.page_size;
+  const void* cb[] = {codebook_k, codebook_v};
+  void* pool[] = {k_pool, v_pool};
+  const int32_t sub[] = {L.k_sub, L.v_sub}, bits[] = {L.k_bits, L.v_bits};
+  for (int i = 0; i < 2; ++i) {
+    p.src[i] = src[1 + i];
+    p.stride[i] = stride[1 + i];
+    p.cb[i] = cb[i];
+    p.pool[i] = static_cast<uint8_t*>(pool[i]);
+    p.sub[i] = sub[i];
+    p.bits[i] = bits[i];
+    p.row_bytes[i] = static_cast<int>(vq_code_row_bytes(L.head_dim, sub[i], bits[i]));
+  }
+  if (q) {
+    p.q.positions = positions;
+    p.q.src[0] = q;
+    p.q.dst[0] = q_out;
+    p.q.stride[0] = q_stride;
+    p.q.heads[0] = L.num_q_heads;
+    for (int i = 0; i < 64; ++i) p.q.freq[i] = p.freq[i];
+    p.q.factor = static_cast<float>(c.attention_factor);
+    p.q.rotary_dim = c.rotary_dim;
+    p.q.interleaved = c.interleaved != 0;
+    p.q.num_tokens = num_tokens;
+  }
+  cudaError_t e = vqk::launch_append(p, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vq_append_kv launch");
+  return VQ_OK;
+}
+
+vq_status vq_keep_tokens(const vq_layout* layout, int32_t batch, const int32_t* seq_lens,
+                         const int32_t* cu_new_lens, const int32_t* keep, int32_t max_keep,
+                         const int32_t* keep_lens, const int32_t* page_table,
+                         int32_t max_pages_per_seq, int64_t num_pages, int32_t num_layers,
+                         void* const* k_pools, void* const* v_pools, int32_t* free_pages,
+                         int32_t free_capacity, const int32_t* num_free, int32_t* seq_lens_out,
+                         int32_t* num_free_out, int32_t* status, void* stream) {
+  vq_status st = check_layout_impl(layout, 0);
+  if (st != VQ_OK) return st;
+  const vq_layout& L = *layout;
+  if (batch < 0) return fail(VQ_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (batch > vqk::kSlotsMaxBatch) return fail(VQ_ERR_UNSUPPORTED, "batch %d > %d", batch, vqk::kSlotsMaxBatch);
+  if (max_keep < 0) return fail(VQ_ERR_INVALID_ARG, "max_keep %d < 0", max_keep);
+  if (max_keep > vqk::kKeepMaxTokens) return fail(VQ_ERR_UNSUPPORTED, "max_keep %d > %d", max_keep, vqk::kKeepMaxTokens);
+  if (num_layers < 1) return fail(VQ_ERR_INVALID_ARG, "num_layers %d < 1", num_layers);
+  if (num_layers > vqk::kKeepMaxLayers) return fail(VQ_ERR_UNSUPPORTED, "num_layers %d > %d", num_layers, vqk::kKeepMaxLayers);
+  if (max_pages_per_seq < 1) return fail(VQ_ERR_INVALID_ARG, "max_pages_per_seq %d < 1", max_pages_per_seq);
+  if (num_pages < 1) return fail(VQ_ERR_INVALID_ARG, "num_pages %lld < 1", (long long)num_pages);
+  if (free_capacity < 0) return fail(VQ_ERR_INVALID_ARG, "free_capacity %d < 0", free_capacity);
+  if (batch == 0) return VQ_OK;
+  const void* ptrs[] = {seq_lens, cu_new_lens, keep_lens, page_table, num_free, seq_lens_out, num_free_out, k_pools, v_pools, keep, free_pages};
+  const char* names[] = {"seq_lens", "cu_new_lens", "keep_lens", "page_table", "num_free", "seq_lens_out", "num_free_out", "k_pools",
+                         "v_pools", "keep", "free_pages"};
+  for (int i = 0; i < 11; ++i) {
+    const bool may_be_null = i == 9 ? max_keep == 0 : i == 10 && free_capacity == 0;
+    if (!ptrs[i] && !may_be_null) return fail(VQ_ERR_INVALID_ARG, "%s is NULL", names[i]);
+    if (i != 7 && i != 8 && !aligned16(ptrs[i])) return fail(VQ_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  vqk::KeepParams p{};
+  for (int i = 0; i < num_layers; ++i) {
+    if (!k_pools[i] || !v_pools[i] || !aligned16(k_pools[i]) || !aligned16(v_pools[i]))
+      return fail(VQ_ERR_INVALID_ARG, "a pool of layer %d is NULL or not 16-byte aligned", i);
+    p.pool[0][i] = static_cast<uint8_t*>(k_pools[i]);
+    p.pool[1][i] = static_cast<uint8_t*>(v_pools[i]);
+  }
+  p.seq_lens = seq_lens;
+  p.cu = cu_new_lens;
+  p.keep = keep;
+  p.keep_lens = keep_lens;
+  p.page_table = page_table;
+  p.free_pages = free_pages;
+  p.num_free = num_free;
+  p.seq_lens_out = seq_lens_out;
+  p.num_free_out = num_free_out;
+  p.status = status;
+  p.num_pages = num_pages;
+  p.batch = batch;
+  p.max_keep = max_keep;
+  p.max_pages = max_pages_per_seq;
+  p.free_capacity = free_capacity;
+  p.page_size = L.page_size;
+  p.hkv = L.num_kv_heads;
+  p.layers = num_layers;
+  p.row_bytes[0] = static_cast<int>(vq_code_row_bytes(L.head_dim, L.k_sub, L.k_bits));
+  p.row_bytes[1] = static_cast<int>(vq_code_row_bytes(L.head_dim, L.v_sub, L.v_bits));
+  const int sms = device_sms();
+  if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
+  cudaError_t e = vqk::launch_keep(p, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "vq_keep_tokens launch");
   return VQ_OK;
 }
 

@@ -20,6 +20,7 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uin
 }
 
 // pre[b] for all sequences (all threads of the CTA; scratch: 32 long longs).
+template <bool kTree = false>
 __device__ __forceinline__ void chunk_plan(const ChunkParams& p, long long* pre, long long* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
   const int per = (p.batch + nthr - 1) / nthr;
@@ -27,9 +28,9 @@ __device__ __forceinline__ void chunk_plan(const ChunkParams& p, long long* pre,
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
     bool bad = false;
-    const ChunkSeq s = chunk_seq(p, b, bad);
+    const ChunkSeq s = chunk_seq<kTree>(p, b, bad);
     if (bad && blockIdx.x == 0) report(p.status, kDevBadLength);
-    const long long w = p.hkv * chunk_sum(p, s, (s.n + p.tile_tok - 1) / p.tile_tok);
+    const long long w = p.hkv * chunk_sum<kTree>(p, s, (s.n + p.tile_tok - 1) / p.tile_tok);
     pre[b] = w;
     sum += w;
   }

@@ -33,6 +33,11 @@
 // total work instead (2 sqrt(total)) took four sequences of 32K from 40.6 to
 // 44.1.  (total / (hkv batch) is taken over idle sequences too: they lower W,
 // towards 512.)
+//
+// kTree: the new tokens are a tree of drafted ones.  Every one of them sees the context
+// (tokens p < len - n, with a window those near its own position, which is len - n at
+// least), and of the new ones those that its bits name, so all tiles of a
+// sequence have the same keys.
 #pragma once
 
 #include "vq_kernels.h"
@@ -56,6 +61,7 @@ __host__ __device__ __forceinline__ int plan_load(const int32_t* at) {
 }
 
 // (bad: set where the sequence is outside its bounds and left out)
+template <bool kTree = false>
 __host__ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool& bad) {
   ChunkSeq s;
   const int len = plan_load(p.seq_lens + b);
@@ -68,7 +74,8 @@ __host__ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int
   s.n = 0;
   s.limit = 0;
   if (c1 != c0) {
-    if (len < 0 || len > p.max_seq_len || c0 < 0 || c1 < c0 || c1 > p.num_tokens || c1 - c0 > p.max_new_len) {
+    if (len < 0 || len > p.max_seq_len || c0 < 0 || c1 < c0 || c1 > p.num_tokens || c1 - c0 > p.max_new_len ||
+        (kTree && c1 - c0 > len)) {
       bad = true;
     } else {
       s.n = c1 - c0;
@@ -78,9 +85,10 @@ __host__ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int
   s.base = s.limit - s.n;
   return s;
 }
+template <bool kTree = false>
 __host__ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b) {
   bool bad = false;
-  return chunk_seq(p, b, bad);
+  return chunk_seq<kTree>(p, b, bad);
 }
 
 // The keys of tile t in blocks of CW tokens: `sink` blocks from token 0, then
@@ -90,10 +98,10 @@ struct ChunkKeys {
   __host__ __device__ __forceinline__ int block(int i) const { return i < sink ? i : lo + (i - sink); }
 };
 
-template <int CW>
+template <int CW, bool kTree = false>
 __host__ __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, const ChunkSeq& s, int t) {
   ChunkKeys k;
-  const int i0 = t * p.tile_tok, i1 = min(i0 + p.tile_tok, s.n);
+  const int i0 = kTree ? 0 : t * p.tile_tok, i1 = kTree ? s.n : min(i0 + p.tile_tok, s.n);
   const int hi = max(min(s.base + i1, s.limit), 0);
   int lo = 0;
   k.sink = 0;
@@ -108,7 +116,12 @@ __host__ __device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, c
 
 // Estimated length of tiles 0 .. j-1 of one (sequence, KV head): each
 // kGap + clamp(base + (t + 1) TT, 0, cap).
+template <bool kTree = false>
 __host__ __device__ __forceinline__ long long chunk_sum(const ChunkParams& p, const ChunkSeq& s, int j) {
+  if constexpr (kTree) {
+    const int keys = p.window > 0 ? static_cast<int>(min(static_cast<long long>(s.limit), static_cast<long long>(p.window) + p.sinks + s.n)) : s.limit;
+    return static_cast<long long>(j) * (p.gap + keys);
+  }
   const int TT = p.tile_tok, base = max(s.base, 0);
   const int cap = p.window > 0 ? static_cast<int>(min(static_cast<long long>(s.limit), static_cast<long long>(p.window) + p.sinks + TT)) : s.limit;
   const long long rise = min(cap > base ? static_cast<int>(static_cast<unsigned>(cap - base) / static_cast<unsigned>(TT)) : 0, j);  // tiles below the cap
@@ -125,7 +138,7 @@ struct ChunkPiece {
 };
 
 // Walks the pieces of worker `me` of `workers` (one thread does, for all of it).
-template <int CW>
+template <int CW, bool kTree = false>
 struct ChunkWalk {
   long long x, x1, W;    // position, end of the range, range per CTA
   long long tile_x;      // where the current tile begins
@@ -149,32 +162,32 @@ struct ChunkWalk {
       else hi = mid;
     }
     b = lo;
-    s = chunk_seq(p, b);
+    s = chunk_seq<kTree>(p, b);
     tiles = (s.n + p.tile_tok - 1) / p.tile_tok;
-    const long long per_head = chunk_sum(p, s, tiles);
+    const long long per_head = chunk_sum<kTree>(p, s, tiles);
     kvh = static_cast<int>((x - pre[b]) / per_head);
     const long long off = x - pre[b] - kvh * per_head;
     lo = 0;
     hi = tiles;  // the last tile with chunk_sum(tile) <= off
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (chunk_sum(p, s, mid) <= off) lo = mid;
+      if (chunk_sum<kTree>(p, s, mid) <= off) lo = mid;
       else hi = mid;
     }
     tile = lo;
-    tile_x = pre[b] + kvh * per_head + chunk_sum(p, s, tile);
+    tile_x = pre[b] + kvh * per_head + chunk_sum<kTree>(p, s, tile);
   }
 
   // The next piece; false when the range is done.
   __host__ __device__ __forceinline__ bool next(const ChunkParams& p, ChunkPiece& q) {
     if (x >= x1) return false;
-    const long long w = chunk_sum(p, s, tile + 1) - chunk_sum(p, s, tile);
+    const long long w = chunk_sum<kTree>(p, s, tile + 1) - chunk_sum<kTree>(p, s, tile);
     const long long o0 = x - tile_x, o1 = min(w, o0 + (x1 - x));
     q.b = b;
     q.kvh = kvh;
     q.tile = tile;
     q.s = s;
-    q.k = chunk_keys<CW>(p, s, tile);
+    q.k = chunk_keys<CW, kTree>(p, s, tile);
     q.blk0 = o0 == 0 ? 0 : static_cast<int>(o0 * q.k.count / w);
     q.blk1 = o1 == w ? q.k.count : static_cast<int>(o1 * q.k.count / w);
     q.slot = o0 > 0 ? 2 * me : o1 < w ? 2 * me + 1 : -1;
@@ -187,7 +200,7 @@ struct ChunkWalk {
         if (++kvh == p.hkv) {
           kvh = 0;
           if (x < x1) {
-            do s = chunk_seq(p, ++b);
+            do s = chunk_seq<kTree>(p, ++b);
             while (s.n == 0);
             tiles = (s.n + p.tile_tok - 1) / p.tile_tok;
           }

@@ -256,7 +256,8 @@ struct __align__(16) WidePiece {
   int sink, lo, blk0, blk1;  // blocks [blk0, blk1) of its keys (ChunkKeys)
   int slot;                  // partial slot or -1
   int more;                  // 0: there is no piece, the range is done
-  int pad[3];
+  int seq_row;               // (a tree:) row of the sequence's first drafted token; first_pos is the context's last token
+  int pad[2];
   __device__ __forceinline__ int block(int i) const { return i < sink ? i : lo + (i - sink); }
 };
 static_assert(sizeof(WidePiece) == 64, "the pieces' place in shared memory");
@@ -272,7 +273,29 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-template <int DK, int BK, int DV, int BV, bool kPair>
+// Which of tokens t .. t + 31 a row of a tree sees among the drafted ones, which begin at token `ctx` (its
+// bits, and with a window their positions against its own, pos).
+__device__ __forceinline__ uint32_t tree_bits(const ChunkParams& p, int row, int seq_row, int ctx, int t, int pos) {
+  const unsigned long long* const m = p.masks + static_cast<long long>(row) * p.mask_words;
+  const int at = t - ctx, w = at >> 6, s = at & 63;  // (at > -32; w -1 where the context's tokens come first)
+  unsigned long long x = w >= 0 && w < p.mask_words ? __ldg(m + w) >> s : 0ULL;
+  if (s > 32 && w + 1 < p.mask_words) x |= __ldg(m + w + 1) << (64 - s);
+  uint32_t see = static_cast<uint32_t>(x);
+  if (p.window > 0) {
+    uint32_t todo = see;
+    while (todo) {
+      const int i = __ffs(todo) - 1;
+      todo &= todo - 1u;
+      if (at + i < p.max_new_len && seq_row + at + i < p.num_tokens) {  // (a bit past the sequence names nothing: `seen` clears it)
+        const int its = max(__ldg(p.positions + seq_row + at + i), ctx);
+        if (its <= pos - p.window && its >= p.sinks) see &= ~(1u << i);
+      }
+    }
+  }
+  return see;
+}
+
+template <int DK, int BK, int DV, int BV, bool kPair, bool kTree>
 __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const ChunkParams p) {
   using W = WideSmem<DK, BK, DV, BV, kPair>;
   using Shape = WideShape<kPair>;
@@ -337,7 +360,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   if (warp == kSoftWarps + kCodeWarps) tmem_alloc<kPair>(tmem_at, kCols);
   long long* const pre = reinterpret_cast<long long*>(tiles);  // the plan, before the first tile is written
   tc_fence_before();
-  chunk_plan(p, pre, pre + kChunkMaxBatch + 1);
+  chunk_plan<kTree>(p, pre, pre + kChunkMaxBatch + 1);
   tc_fence_after();
   // All 512 columns are this CTA's, so they start at column 0; the constant keeps the
   // products' operands in uniform registers.
@@ -491,7 +514,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_issuer(q_full);
-      pos = live ? u.first_pos + static_cast<int>(r * inv_g >> 16) : -1;
+      const int token = static_cast<int>(r * inv_g >> 16);
+      if constexpr (kTree) pos = live && p.window > 0 ? max(__ldg(p.positions + u.row0 + token), u.first_pos + 1) : 0;
+      else pos = live ? u.first_pos + token : -1;
       return u.blk1 - u.blk0;
     };
     // ---- a block: its scores, their masks and maximum, P with the maximum so far -----------------
@@ -525,7 +550,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       tmem_wait_ld();
       if (!whole) {
         // the row sees tokens up to pos, from `from` on, and the sinks: as bits of a half's two words
-        const int from = p.window > 0 ? pos - p.window + 1 : 0;
+        const int from = p.window > 0 ? (kTree ? max(pos - p.window + 1, 0) : pos - p.window + 1) : 0;
         auto bits = [](int lo, int hi) {  // bits lo .. hi - 1 of 32, whatever the two are
           const uint32_t up = hi >= 32 ? kAll : hi <= 0 ? 0u : (1u << hi) - 1u;
           const uint32_t down = lo >= 32 ? kAll : lo <= 0 ? 0u : (1u << lo) - 1u;
@@ -533,7 +558,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         };
         auto mask = [&](uint32_t(&s)[32], int t, uint32_t here) {
           // (tokens past the sequence's end are not in `seen`)
-          const uint32_t see = here & bits(0, pos + 1 - t) & (bits(from - t, 32) | bits(0, p.sinks - t));
+          uint32_t see;
+          if constexpr (kTree) {
+            const int ctx = u.first_pos + 1;  // the context's end
+            see = here & bits(0, ctx - t);
+            if (p.window > 0) see &= bits(from - t, 32) | bits(0, p.sinks - t);
+            if (live && t + 32 > ctx) see |= here & tree_bits(p, u.row0 + static_cast<int>(r * inv_g >> 16), u.seq_row, ctx, t, pos);
+          } else {
+            see = here & bits(0, pos + 1 - t) & (bits(from - t, 32) | bits(0, p.sinks - t));
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[i] = see >> i & 1u ? s[i] : __float_as_uint(-INFINITY);
         };
@@ -867,7 +900,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       }
     } else if (warp == kSoftWarps + kCodeWarps + 1) {
       // ================================== planning =======================================
-      ChunkWalk<kTile> walk;
+      ChunkWalk<kTile, kTree> walk;
       walk.start(p, pre, worker, static_cast<int>(gridDim.x) / kCtas);  // (the tiles over the plan wait for the first piece)
       ChunkPiece q;
       Ring ro;
@@ -901,6 +934,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
           for (int i = lane; i < n * lines; i += 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + static_cast<long long>(i / lines) * p.hq * (kHeadDim * 2) + (i % lines) * 128));
         }
+        int last = 0;  // of a tree's rows, the furthest position
+        if (kTree && more && p.window > 0) {
+          for (int i = lane; i < n; i += 32) last = max(last, __ldg(p.positions + q.s.row0 + i0 + i));
+          last = max(__reduce_max_sync(kAll, last), q.s.base);
+        }
         if (!wait(piece_empty + ro.slot, ro.phase ^ 1u)) break;
         if (lane == 0) {
           WidePiece w = {};
@@ -910,8 +948,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
             w.kvh = q.kvh;
             w.row0 = q.s.row0 + i0;
             w.rows = n * p.group;
-            w.first_pos = q.s.base + i0;
-            w.last_pos = q.s.base + i0 + n - 1;
+            w.first_pos = kTree ? q.s.base - 1 : q.s.base + i0;
+            w.last_pos = kTree ? last : q.s.base + i0 + n - 1;
+            w.seq_row = q.s.row0;
             w.limit = q.s.limit;
             w.sink = q.k.sink;
             w.lo = q.k.lo;
@@ -938,10 +977,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   }
 }
 
-template <int DK, int BK, int DV, int BV, bool kPair>
+template <int DK, int BK, int DV, int BV, bool kPair, bool kTree>
 cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
   static SmemOptIn opt;
-  auto kern = vq_chunk_wide_kernel<DK, BK, DV, BV, kPair>;
+  auto kern = vq_chunk_wide_kernel<DK, BK, DV, BV, kPair, kTree>;
   constexpr size_t smem = WideSmem<DK, BK, DV, BV, kPair>::kTotal;
   cudaError_t e = ensure_smem(kern, smem, opt);
   if (e != cudaSuccess) return e;
@@ -961,24 +1000,35 @@ cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int DK, int BK, int DV, int BV>
+template <int DK, int BK, int DV, int BV, bool kTree>
 cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
-  return p.tile_rows == 2 * kTile ? launch_wide<DK, BK, DV, BV, true>(p, grid, stream)
-                                  : launch_wide<DK, BK, DV, BV, false>(p, grid, stream);
+  if constexpr (!kTree)
+    if (p.tile_rows != 2 * kTile) return launch_wide<DK, BK, DV, BV, false, false>(p, grid, stream);
+  return launch_wide<DK, BK, DV, BV, true, kTree>(p, grid, stream);
+}
+
+template <bool kTree>
+cudaError_t launch_format(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid, cudaStream_t stream) {
+  if (k_sub == 8 && k_bits == 12 && v_sub == 8 && v_bits == 12) return launch_wide<8, 12, 8, 12, kTree>(p, grid, stream);
+  if (k_bits == 8 && (k_sub == 2 || k_sub == 4)) {
+    const bool k4 = k_sub == 4;
+    if (v_sub == 4 && v_bits == 8) return k4 ? launch_wide<4, 8, 4, 8, kTree>(p, grid, stream) : launch_wide<2, 8, 4, 8, kTree>(p, grid, stream);
+    if (v_sub == 4 && v_bits == 9) return k4 ? launch_wide<4, 8, 4, 9, kTree>(p, grid, stream) : launch_wide<2, 8, 4, 9, kTree>(p, grid, stream);
+    if (v_sub == 2 && v_bits == 8) return k4 ? launch_wide<4, 8, 2, 8, kTree>(p, grid, stream) : launch_wide<2, 8, 2, 8, kTree>(p, grid, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
                               cudaStream_t stream) {
-  if (k_sub == 8 && k_bits == 12 && v_sub == 8 && v_bits == 12) return launch_wide<8, 12, 8, 12>(p, grid, stream);
-  if (k_bits == 8 && (k_sub == 2 || k_sub == 4)) {
-    const bool k4 = k_sub == 4;
-    if (v_sub == 4 && v_bits == 8) return k4 ? launch_wide<4, 8, 4, 8>(p, grid, stream) : launch_wide<2, 8, 4, 8>(p, grid, stream);
-    if (v_sub == 4 && v_bits == 9) return k4 ? launch_wide<4, 8, 4, 9>(p, grid, stream) : launch_wide<2, 8, 4, 9>(p, grid, stream);
-    if (v_sub == 2 && v_bits == 8) return k4 ? launch_wide<4, 8, 2, 8>(p, grid, stream) : launch_wide<2, 8, 2, 8>(p, grid, stream);
-  }
-  return cudaErrorInvalidValue;
+  return launch_format<false>(p, k_sub, k_bits, v_sub, v_bits, grid, stream);
+}
+
+cudaError_t launch_tree_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
+                             cudaStream_t stream) {
+  return launch_format<true>(p, k_sub, k_bits, v_sub, v_bits, grid, stream);
 }
 
 }  // namespace vqk

@@ -156,6 +156,45 @@ struct SlotsParams {
   int batch, max_pages, free_capacity, page_size, max_tokens;
 };
 
+// Keys and values from a projection's rows to codes in the pools (tensors: 0 keys, 1 values).
+struct AppendParams {
+  const int32_t* positions;    // [T]; negative: the token is left out
+  const int64_t* slots;        // [T]
+  const void* src[2];          // [T] rows of `stride` elements, hkv x 128 from the row's start
+  long long stride[2];
+  const float* lambda;         // fp32 [Hkv][128]
+  const void* cb[2];           // fp16 codebooks [2^bits][sub]
+  uint8_t* pool[2];            // [num_pages][Hkv][P][row bytes]
+  int32_t* status;
+  long long num_slots;         // num_pages * P
+  unsigned long long freq[64]; // turns per position of pair i, as a 64-bit fraction
+  double factor;               // multiplies sine and cosine
+  int rotary_dim, interleaved, bf16;
+  int num_tokens, hkv, page_size;
+  int sub[2], bits[2], row_bytes[2];
+  int kv_ctas;                 // CTAs of each tensor; those after them turn queries (set by the launcher)
+  RotaryParams q;              // the queries (heads[0] 0: none)
+};
+
+// The accepted ones of each sequence's drafted tokens, moved together in all layers' pools.
+constexpr int kKeepMaxLayers = 128, kKeepMaxTokens = 256;
+struct KeepParams {
+  const int32_t* seq_lens;     // [B] (may be seq_lens_out)
+  const int32_t* cu;           // [B + 1]
+  const int32_t* keep;         // [B][max_keep]
+  const int32_t* keep_lens;    // [B]
+  const int32_t* page_table;   // [B][max_pages]
+  int32_t* free_pages;         // [free_capacity]
+  const int32_t* num_free;     // [1] (may be num_free_out)
+  int32_t* seq_lens_out;       // [B]
+  int32_t* num_free_out;       // [1]
+  int32_t* status;
+  long long num_pages;
+  int batch, max_keep, max_pages, free_capacity, page_size, hkv, layers;
+  int row_bytes[2];
+  uint8_t* pool[2][kKeepMaxLayers];
+};
+
 // A tile of query rows whose keys more than one worker of the chunk kernel
 // took: worker c (the record's index) began it in slot 2c + 1, workers
 // c + 1 .. last went on in their slots 2c'.  tokens 0: none.
@@ -185,6 +224,10 @@ struct ChunkParams {
   int window, sinks;          // window 0: none
   int tile_tok, tile_rows;    // tokens and (padded) rows of a tile; of 256 rows, 128 have half the tokens
   int gap, min_range;         // a tile's fixed cost and a worker's least share, in tokens
+  // A tree of drafted tokens per sequence (the kernels with kTree):
+  const unsigned long long* masks;  // [T][mask_words] bit j of a row: it sees the sequence's j-th drafted token
+  const int32_t* positions;   // [T] (with a window)
+  int mask_words;
   float qscale;               // softmax scale * log2(e) / sqrt(128)
   unsigned long long timeout_ns;
 };
@@ -347,6 +390,8 @@ cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool ove
 cudaError_t launch_dequant(const DequantParams& p, int grid_x, cudaStream_t stream);
 int dequant_tokens_per_cta();
 cudaError_t launch_rotary(RotaryParams p, bool bf16, int sms, cudaStream_t stream);
+cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream);
+cudaError_t launch_keep(const KeepParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream);
 constexpr int kSlotsMaxBatch = 16384;
 // Chunk attention, tile_rows 8 or 16 (narrow), 128 or 256 (wide; 256: a pair of CTAs); the merge of either.
@@ -354,8 +399,11 @@ cudaError_t launch_chunk_narrow(const ChunkParams& p, int k_sub, int k_bits, int
                                 cudaStream_t stream);
 cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
                               cudaStream_t stream);
+cudaError_t launch_tree_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
+                             cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int workers, cudaStream_t stream);
 constexpr int kChunkMaxBatch = 1024;
+constexpr int kTreeMaxTokens = 256;  // drafted tokens per sequence
 constexpr int kFewGroups = 4;  // workers per CTA of the kernel for 8 rows and fewer
 
 }  // namespace vqk

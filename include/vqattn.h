@@ -466,6 +466,44 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
                                 int32_t max_seq_len, int32_t max_new_len, int32_t num_sms);
 
 /*
+ * Attention of a tree of drafted tokens per sequence over the quantized cache, for
+ * checking several continuations in one step.  The drafted tokens' own codes are
+ * in the cache already (vq_append_kv or vq_encode_kv, at the slots that
+ * vq_append_slots gives): token j of sequence b's n = cu_new_lens[b + 1] -
+ * cu_new_lens[b] sits at place seq_lens[b] - n + j, whatever its depth.
+ * The row of drafted token i sees every cached token before the drafted ones,
+ * and of those token j where bit j of its mask is set (its own too; a path to the
+ * root is mask[i] = mask[parent] | 1 << i).  With a window it sees of all these
+ * only tokens at a position x > t - window or x < num_sinks, t being its own
+ * position: that of a cached token is its place, that of a drafted one
+ * positions[row], or the first drafted token's place where that is further.
+ * A row that sees nothing (pages out of range, nothing cached and no bit) is zero.
+ *   tree_masks    uint64 [num_tokens][mask_words], 16-byte aligned, bit j of a
+ *                 row being bit j % 64 of word j / 64; bits from n on name nothing.
+ *   mask_words    at least max_new_len / 64, rounded up; at most 64.
+ *   positions     int32 [num_tokens] (as vq_append_kv takes them); needed with a
+ *                 window, else not read.
+ *   max_new_len   host bound of a sequence's drafted tokens, up to 256.
+ * Everything else as in vq_chunk_attention, with cu_new_lens needed; a sequence
+ * with more drafted tokens than tokens is left out too (VQ_DEV_BAD_LENGTH).
+ */
+vq_status vq_tree_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                            const void* q, const float* lambda, const void* codebook_k,
+                            const void* codebook_v, const void* k_pool, const void* v_pool,
+                            int64_t num_pages, const int32_t* page_table,
+                            int32_t max_pages_per_seq, const int32_t* seq_lens,
+                            int32_t max_seq_len, const int32_t* cu_new_lens, int32_t max_new_len,
+                            const uint64_t* tree_masks, int32_t mask_words,
+                            const int32_t* positions, int32_t window, int32_t num_sinks,
+                            float softmax_scale, void* out, void* workspace,
+                            size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Workspace bytes of vq_tree_attention (num_sms <= 0: the current device).
+ * Pure host arithmetic otherwise.  Returns 0 for invalid arguments. */
+size_t vq_tree_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t num_tokens,
+                               int32_t max_seq_len, int32_t max_new_len, int32_t num_sms);
+
+/*
  * Page tables, slot map, positions and row offsets of one serving step, from
  * request lengths that live on the device: what vq_encode_kv (slot_mapping),
  * vq_rotary (positions), vq_chunk_attention (cu_new_lens, seq_lens,
@@ -564,6 +602,75 @@ vq_status vq_rotary(const vq_rotary_config* config, int32_t num_tokens, const in
                     int32_t dtype, const void* q, int64_t q_stride, int32_t num_q_heads,
                     void* q_out, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                     int32_t num_kv_heads, void* k_out, void* v_out, void* stream);
+
+/*
+ * Append keys and values to the cache straight from a projection's rows: keys
+ * turned by their positions on the way (as vq_rotary turns them), smoothed,
+ * transformed and coded, values coded (as vq_encode_kv codes them); queries are
+ * turned for the attention calls.  One launch for what vq_rotary and vq_encode_kv
+ * do in two, without the rotated keys and copied values between them: keys go from
+ * their rows to codes without a rounding, so codes may differ from the two calls',
+ * which round the turned keys to fp16.
+ * A code is the nearest centroid's in exact arithmetic, the lowest index where
+ * several are equally near: scores too close to tell apart in fp32 are formed
+ * again in 64 bits (keys from the rows on).
+ *   config        as in vq_rotary (head_dim that of the layout).
+ *   positions     int32 [num_tokens]; a token with a negative position is left
+ *                 out altogether (its row of q_out is left as it was).
+ *   slot_mapping  int64 [num_tokens]: a negative slot stores nothing (the token's
+ *                 query is turned all the same); a slot >= num_pages * P stores
+ *                 nothing and reports VQ_DEV_BAD_SLOT.  No two tokens share a slot.
+ *   dtype, q, k, v and their strides: as in vq_rotary, with the layout's heads.  k
+ *                 and v are needed; q may be NULL, with q_out.
+ *   q_out         fp16 [num_tokens][Hq][D]; may be q (VQ_FP16, stride Hq x D), else
+ *                 overlaps no input.
+ *   lambda, codebooks, pools, num_pages, status: as in vq_encode_kv.
+ * Every layout that vq_decode_attention supports.  Codes of a vector with
+ * infinities or NaN are some codes.  num_tokens == 0 is a no-op returning VQ_OK.
+ */
+vq_status vq_append_kv(const vq_layout* layout, const vq_rotary_config* config,
+                       int32_t num_tokens, const int32_t* positions,
+                       const int64_t* slot_mapping, int32_t dtype, const void* q,
+                       int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, const float* lambda, const void* codebook_k,
+                       const void* codebook_v, void* q_out, void* k_pool, void* v_pool,
+                       int64_t num_pages, int32_t* status, void* stream);
+
+/*
+ * Keep the accepted ones of a step's drafted tokens: their codes move together
+ * behind the context, in the pools of all layers, the sequences get shorter, and
+ * the pages that are left empty go back on the free stack of vq_append_slots.
+ *   Of sequence b's n = cu_new_lens[b + 1] - cu_new_lens[b] drafted tokens, at
+ *   places base = seq_lens[b] - n and on, those with indices keep[b][0 ..
+ *   keep_lens[b] - 1] (ascending, no index twice) stay: keep[b][i] moves to place base + i.
+ *   seq_lens      int32 [batch], the drafted tokens among them.
+ *   keep          int32 [batch][max_keep]; entries from keep_lens[b] on are not read.
+ *   keep_lens     int32 [batch], 0 .. min(n, max_keep).
+ *   page_table    int32 [batch][max_pages_per_seq], only read.
+ *   num_layers    layers that share the page table, 1 .. 128; k_pools and v_pools
+ *                 are HOST arrays of as many pool pointers (num_pages pages each).
+ *   free_pages    int32 [free_capacity], num_free int32 [1]: pages ceil((base +
+ *                 keep_lens[b]) / P) to ceil(seq_lens[b] / P) - 1 are written at
+ *                 free_pages[*num_free ..], sequences in order, of each the last
+ *                 page first.  Table entries stay as they are.
+ *   seq_lens_out  int32 [batch] = base + keep_lens[b]; may be seq_lens.
+ *   num_free_out  int32 [1]; may be num_free.
+ * A sequence whose lengths or indices are out of range (VQ_DEV_BAD_LENGTH), or with a
+ * page outside [0, num_pages) among those of its drafted tokens (VQ_DEV_BAD_PAGE), is left as it
+ * is, with all its drafted tokens.  Where the pages do not fit behind *num_free,
+ * or that is outside [0, free_capacity], none is given back
+ * (VQ_DEV_BAD_LENGTH).  Of several faults one is reported.
+ *   batch 0 .. 16384, max_keep 0 .. 256.  Outputs other than the two pairs
+ *   named above must not overlap inputs; no pool is given twice.
+ * Two kernels on `stream`.  batch == 0 is a no-op returning VQ_OK (num_free_out is not written).
+ */
+vq_status vq_keep_tokens(const vq_layout* layout, int32_t batch, const int32_t* seq_lens,
+                         const int32_t* cu_new_lens, const int32_t* keep, int32_t max_keep,
+                         const int32_t* keep_lens, const int32_t* page_table,
+                         int32_t max_pages_per_seq, int64_t num_pages, int32_t num_layers,
+                         void* const* k_pools, void* const* v_pools, int32_t* free_pages,
+                         int32_t free_capacity, const int32_t* num_free, int32_t* seq_lens_out,
+                         int32_t* num_free_out, int32_t* status, void* stream);
 
 /*
  * Decode attention for callers that cannot allocate device memory.
