@@ -5,7 +5,20 @@
 //   k' = R(position) k,  k~ = k' diag(lambda)^-1 H_D,  code i = argmin_j ||k~_i - C_k[j]||^2,
 //   v's code i = argmin_j ||v_i - C_v[j]||^2,  the lowest j where several are equal.
 //
-// One warp per vector, everything in 64 bits.
+//
+// The search is a product: score ||c||^2 - 2 x . c orders centroids as the distance does, so 16 sub-vectors
+// against 8 centroids are one warp mma (tf32: -2 c is fp16 and exact in it, x goes in as high and low
+// part, side by side in the k dimension or one product after the other for sub-vectors of 8; ||c||^2 is
+// the accumulator's start).  Of 32 centroids a lane holds 8 scores of a row; it keeps their minimum
+// only, with the smallest and second smallest minimum so far and which group the smallest was: 4.5
+// instructions for 128 scores instead of 7 for 32 in a scan.
+//
+// Codes are exact.  In steps, each for the sub-vectors that the one before cannot tell:
+//   1. the group with the smallest score, if no other comes within the products' error;
+//   2. its 8 centroids by fp32 distances ||x - c||^2 (their error is relative to the distance, not to x):
+//      the nearest, if no other comes within the error of these and, for keys, of x itself;
+//   3. all centroids by fp32 distances (one warp), equal centroids counting as one;
+//   4. everything in 64 bits, for keys from the rows on (one warp).
 #include "vq_rotary.cuh"
 
 namespace vqk {
@@ -103,6 +116,11 @@ __device__ __forceinline__ void store_codes(const AppendParams& p, int which, co
   uint32_t* const row = reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * p.page_size + off) * p.row_bytes[which]);
   for (int w = lane; w < words; w += 32) {
     uint32_t x = 0;
+    if (bits == 8) {  // four codes a word
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + 4 * w);
+      row[w] = __byte_perm(c.x, c.y, 0x6420);
+      continue;
+    }
     for (int i = 32 * w / bits; i < count && i * bits < 32 * w + 32; ++i) {
       const int at = i * bits - 32 * w;
       x |= at >= 0 ? static_cast<uint32_t>(codes[i]) << at : static_cast<uint32_t>(codes[i]) >> -at;
@@ -119,49 +137,449 @@ __device__ __forceinline__ long long append_slot(const AppendParams& p, long lon
   return slot >= 0 && slot < p.num_slots ? slot : -1;
 }
 
-template <bool kBf16, bool kWhole>
-__global__ void __launch_bounds__(kAppThreads) vq_append_kernel(const __grid_constant__ AppendParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (static_cast<int>(blockIdx.x) >= 2 * p.kv_ctas) {  // queries
-    const long long b = static_cast<long long>(blockIdx.x) - 2 * p.kv_ctas, shares = (p.q.heads[0] + p.q.heads_per_y - 1) / p.q.heads_per_y;
-    rotary_share<kBf16, kWhole>(p.q, b / shares, static_cast<int>(b % shares));
-    return;
+// ---- the codebook in shared memory: -2 c, 8 centroids a block, and ||c||^2 -------------------------------------
+// Word of element e of centroid j: j d + e, but for d = 8 the lower and the upper halves of a block's 8 centroids
+// one after the other, so that the products' operands are one word a lane without bank conflicts.
+template <int D>
+__device__ __forceinline__ int centroid_word(int j, int e) {
+  return D == 8 ? (j >> 3) * 64 + (e >> 2) * 32 + (j & 7) * 4 + (e & 3) : j * D + e;
+}
+
+template <int D>
+__device__ __forceinline__ void fill_codebook(const __half* cb, int n, float* tab, float* norm, int* top) {
+  for (int j = threadIdx.x; j < n; j += kAppThreads) {
+    float c[D], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < D; ++e) {
+      c[e] = __half2float(__ldg(cb + j * D + e));
+      sum = fmaf(c[e], c[e], sum);
+    }
+#pragma unroll
+    for (int e = 0; e < D; ++e) tab[centroid_word<D>(j, e)] = -2.f * c[e];
+    norm[j] = sum;
+    const int high = __reduce_max_sync(kAll, __float_as_int(sum));  // (not negative: ordered like their bits; n is a multiple of the threads)
+    if ((threadIdx.x & 31) == 0) atomicMax(top, high);
   }
-  const int which = blockIdx.x & 1;
-  __shared__ uint16_t codes[kAppWarps][kHeadDim];
+}
+
+// Centroid j times -2.
+template <int D>
+__device__ __forceinline__ void load_centroid(const float* tab, int j, float (&c)[D]) {
+#pragma unroll
+  for (int e = 0; e < D; e += D < 4 ? 2 : 4) {
+    const float* at = tab + centroid_word<D>(j, e);
+    if constexpr (D == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(at);
+      c[0] = v.x, c[1] = v.y;
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(at);
+      c[e] = v.x, c[e + 1] = v.y, c[e + 2] = v.z, c[e + 3] = v.w;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ float distance(const float (&x)[D], const float (&c)[D]) {  // c: times -2
+  float d = 0.f;
+#pragma unroll
+  for (int e = 0; e < D; ++e) {
+    const float y = fmaf(0.5f, c[e], x[e]);
+    d = fmaf(y, y, d);
+  }
+  return d;
+}
+
+// ---- products -----------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                       float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma_k4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, float c0, float c1, float c2, float c3) {
+  asm volatile("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%8,%9,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(b0), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Smallest and second smallest of two such pairs, with what the smallest is (the lower of equals).
+__device__ __forceinline__ void join_best(float& best, float& second, int& at, int lanes) {
+  const float ob = __shfl_xor_sync(kAll, best, lanes), os = __shfl_xor_sync(kAll, second, lanes);
+  const int oa = __shfl_xor_sync(kAll, at, lanes);
+  second = min3(second, os, fmaxf(best, ob));
+  at = ob < best || (ob == best && oa < at) ? oa : at;
+  best = fminf(best, ob);
+}
+
+// Elements 4 lane .. 4 lane + 3 of a vector as they are coded (one warp).  Of keys the angles' sines and cosines
+// stay with the lane while the token stays the same.
+struct Angles {
+  long long t = -1;
+  float co[4], si[4];
+};
+__device__ __forceinline__ void load_raw(const AppendParams& p, const uint16_t* row, int e, float (&x)[4]) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + e));
+  const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t v = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+    x[i] = p.bf16 ? to_float<true>(v) : to_float<false>(v);
+  }
+}
+
+__device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* row, long long t, int h, int lane, Angles& a, float (&x)[4]) {
+  const int r = p.rotary_dim, half = r / 2;
+  if (a.t != t) {
+    a.t = t;
+    const unsigned long long pos = static_cast<unsigned long long>(__ldg(p.positions + t));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      if (p.interleaved && (i & 1)) {
+        a.co[i] = a.co[i - 1];
+        a.si[i] = a.si[i - 1];
+      } else if (e < r) {
+        const unsigned long long turn = p.freq[p.interleaved ? e >> 1 : e < half ? e : e - half] * pos;
+        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, a.si + i, a.co + i);  // 2^-31
+        a.co[i] *= static_cast<float>(p.factor);
+        a.si[i] *= static_cast<float>(p.factor);
+      }
+    }
+  }
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      if (4 * lane + i < r) {
+        const float y = x[i] * a.co[i] - x[i + 1] * a.si[i];
+        x[i + 1] = x[i + 1] * a.co[i] + x[i] * a.si[i];
+        x[i] = y;
+      }
+  } else if (4 * lane < r) {
+    float y[4];
+    if ((half & 3) == 0) {
+      load_raw(p, row, 4 * lane < half ? 4 * lane + half : 4 * lane - half, y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 4 * lane + i;
+        const uint16_t v = __ldg(row + (e < half ? e + half : e < r ? e - half : e));
+        y[i] = p.bf16 ? to_float<true>(v) : to_float<false>(v);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * lane + i;
+      if (e < r) x[i] = e < half ? x[i] * a.co[i] - y[i] * a.si[i] : x[i] * a.co[i] + y[i] * a.si[i];
+    }
+  }
+  const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + h * kHeadDim) + lane);
+  x[0] /= lam.x;
+  x[1] /= lam.y;
+  x[2] /= lam.z;
+  x[3] /= lam.w;
+  fwht128_warp(x, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
+}
+
+// Steps 3 and 4 of a sub-vector that the steps before could not tell (one warp; rare, so not inlined).
+template <int D>
+__device__ __noinline__ int settle(const AppendParams& p, int which, long long t, int h, int s, const float* xs, const float* tab, float of_x) {
+  const int lane = threadIdx.x & 31, n = 1 << p.bits[which];
+  float x[D], c[D], near[D];
+#pragma unroll
+  for (int e = 0; e < D; ++e) x[e] = xs[s * D + e];
+  float best = INFINITY, none = INFINITY;
+  int at = 0x7fffffff;
+  for (int j = lane; j < n; j += 32) {
+    load_centroid<D>(tab, j, c);
+    const float d = distance<D>(x, c);
+    if (d < best) {
+      best = d;
+      at = j;
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) join_best(best, none, at, m);
+  if (best < INFINITY) {  // (else too far off for fp32, or not a number)
+    float second = INFINITY;
+    load_centroid<D>(tab, at, near);
+    for (int j = lane; j < n; j += 32) {
+      load_centroid<D>(tab, j, c);
+      bool same = true;
+#pragma unroll
+      for (int e = 0; e < D; ++e) same &= c[e] == near[e];
+      if (!same) second = fminf(second, distance<D>(x, c));
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) second = fminf(second, __shfl_xor_sync(kAll, second, m));
+    if (second == INFINITY || second > best + second * 1.9073486e-6f + of_x * sqrtf(second)) return at;  // 2^-19
+  }
+  double y[4];
+  exact_vector(p, which, t, h, lane, y);
+  return exact_code(p, which, s, y, lane);
+}
+
+// Rows, codebook and scratch of the CTA.  Shared memory: the table, the norms, then for each warp its vectors in fp32
+// and their codes.
+template <int D, int R>
+struct AppendShape {
+  static constexpr int kVectors = R * 16 * D / kHeadDim;  // of a warp's pass: R tiles of 16 sub-vectors
+  static_assert(kVectors >= 1 && kVectors * kHeadDim == R * 16 * D, "whole vectors");
+  static constexpr int kWarpBytes = kVectors * kHeadDim * 4 + R * 16 * 2;
+};
+
+// One tensor's vectors: R tiles of 16 sub-vectors a pass and warp.
+template <int D, int R>
+__device__ __forceinline__ void append_tensor(const AppendParams& p, int which, int cta, int ctas, uint8_t* smem, int* top) {
+  using Shape = AppendShape<D, R>;
+  constexpr int NV = Shape::kVectors, kSubs = kHeadDim / D;  // sub-vectors of a vector
+  const int n = 1 << p.bits[which];
+  float* const tab = reinterpret_cast<float*>(smem);
+  float* const norm = tab + n * D;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* const mine = smem + n * (D + 1) * 4 + warp * Shape::kWarpBytes;
+  float* const xs = reinterpret_cast<float*>(mine);
+  uint16_t* const codes = reinterpret_cast<uint16_t*>(xs + NV * kHeadDim);
+  fill_codebook<D>(static_cast<const __half*>(p.cb[which]), n, tab, norm, top);
+  __syncthreads();
+  const float cmax2 = __int_as_float(*top), cmax = sqrtf(cmax2);
   const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv;
-  for (long long v = static_cast<long long>(blockIdx.x >> 1) * kAppWarps + warp; v < vectors; v += static_cast<long long>(p.kv_ctas) * kAppWarps) {
-    const long long t = v / p.hkv;
-    const int h = static_cast<int>(v % p.hkv);
-    const long long slot = append_slot(p, t, lane == 0);
-    if (slot < 0) continue;
-    double x[4];
-    exact_vector(p, which, t, h, lane, x);
-    for (int s = 0; s < kHeadDim / p.sub[which]; ++s) {
-      const int code = exact_code(p, which, s, x, lane);
-      if (lane == 0) codes[warp][s] = static_cast<uint16_t>(code);
+  Angles angles;
+
+  for (long long v0 = (static_cast<long long>(cta) * kAppWarps + warp) * NV; v0 < vectors; v0 += static_cast<long long>(ctas) * kAppWarps * NV) {
+    // ---- the vectors as they are coded ---------------------------------------------------------------------
+    long long slot[NV];
+    float raw[NV][4], of_x[NV];  // of_x: what x's own error can make of a difference of distances, times the distance's root
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const long long t = (v0 + v) / p.hkv;
+      slot[v] = v0 + v < vectors ? append_slot(p, t, lane == 0) : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[v][i] = 0.f;
+      if (slot[v] >= 0) load_raw(p, static_cast<const uint16_t*>(p.src[which]) + t * p.stride[which] + (v0 + v) % p.hkv * kHeadDim, 4 * lane, raw[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      of_x[v] = 0.f;
+      if (which == 0 && slot[v] >= 0) {
+        const long long t = (v0 + v) / p.hkv;
+        const int h = static_cast<int>((v0 + v) % p.hkv);
+        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + t * p.stride[0] + h * kHeadDim, t, h, lane, angles, raw[v]);
+        float sum = fmaf(raw[v][0], raw[v][0], fmaf(raw[v][1], raw[v][1], fmaf(raw[v][2], raw[v][2], raw[v][3] * raw[v][3])));
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
+        // Each element of k~ is off by about 2^-24 of its rms in rotation, division and butterflies (eight of these are
+        // 2^-24 |k~|); a difference of two distances by at most 2 |error| |c - c'| <= 4 sqrt(d) 2^-24 |k~| sqrt(distance).
+        of_x[v] = 4.f * sqrtf(D * sum) * 5.9604645e-8f;
+      }
+      *reinterpret_cast<float4*>(xs + v * kHeadDim + 4 * lane) = make_float4(raw[v][0], raw[v][1], raw[v][2], raw[v][3]);
     }
     __syncwarp();
-    store_codes(p, which, codes[warp], slot, h, lane);
+    // ---- operands: lane (g, c) has rows g and g + 8 of each tile -----------------------------------------------
+    constexpr int kA = D == 2 ? 2 : D == 4 ? 4 : 8;
+    uint32_t a[R][kA];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float* const x = xs + r * 16 * D;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // row g + 8 half
+        if constexpr (D == 2) {  // k: high parts of both elements, low parts
+          const float y = x[(g + 8 * half) * 2 + (c & 1)];
+          const uint32_t hi = to_tf32(y);
+          a[r][half] = c < 2 ? hi : to_tf32(y - __uint_as_float(hi));
+        } else {
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) {
+            const float y = x[(g + 8 * half) * D + 4 * e + c];
+            const uint32_t hi = to_tf32(y), lo = to_tf32(y - __uint_as_float(hi));
+            if constexpr (D == 4) {  // k: high parts of the four elements, low parts
+              a[r][half] = hi;
+              a[r][2 + half] = lo;
+            } else {  // high parts of the eight elements, then a product of the low parts
+              a[r][2 * e + half] = hi;
+              a[r][4 + 2 * e + half] = lo;
+            }
+          }
+        }
+      }
+    }
+    // ---- groups of 32 centroids, 8 of a row's scores a lane --------------------------------------------------
+    float best[R][2], second[R][2];
+    int at[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        best[r][half] = second[r][half] = INFINITY;
+        at[r][half] = 0;
+      }
+    for (int group = 0; group < n / 32; ++group) {
+      float low[R][2];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int nb = 4 * group + b;
+        const float2 start = *reinterpret_cast<const float2*>(norm + 8 * nb + 2 * c);
+        uint32_t b0, b1 = 0;
+        if constexpr (D == 2) {
+          b0 = __float_as_uint(tab[(8 * nb + g) * 2 + (c & 1)]);
+        } else if constexpr (D == 4) {
+          b0 = b1 = __float_as_uint(tab[32 * nb + lane]);
+        } else {
+          b0 = __float_as_uint(tab[64 * nb + lane]);
+          b1 = __float_as_uint(tab[64 * nb + 32 + lane]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float s[4];
+          if constexpr (D == 2) {
+            mma_k4(s, a[r][0], a[r][1], b0, start.x, start.y, start.x, start.y);
+          } else {
+            mma_k8(s, a[r][0], a[r][1], a[r][2], a[r][3], b0, b1, start.x, start.y, start.x, start.y);
+            if constexpr (D == 8) mma_k8(s, a[r][4], a[r][5], a[r][6], a[r][7], b0, b1, s[0], s[1], s[2], s[3]);
+          }
+          low[r][0] = b == 0 ? fminf(s[0], s[1]) : min3(low[r][0], s[0], s[1]);
+          low[r][1] = b == 0 ? fminf(s[2], s[3]) : min3(low[r][1], s[2], s[3]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          second[r][half] = fminf(second[r][half], fmaxf(best[r][half], low[r][half]));
+          at[r][half] = low[r][half] < best[r][half] ? group : at[r][half];
+          best[r][half] = fminf(best[r][half], low[r][half]);
+        }
+    }
+    // ---- steps 1 and 2: a quad has two rows, a lane two of a group's 8 centroids of each -----------------------
+    uint32_t open[R];  // bit 4 g + i: row g + 8 i is not told yet
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      bool unsure[2];
+      int code[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        int id = 4 * at[r][half] + c;
+        join_best(best[r][half], second[r][half], id, 1);
+        join_best(best[r][half], second[r][half], id, 2);
+        const int row = 16 * r + g + 8 * half;
+        float x[D], y[D];
+#pragma unroll
+        for (int e = 0; e < D; ++e) x[e] = xs[row * D + e];
+        float x2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < D; ++e) x2 = fmaf(x[e], x[e], x2);
+        // the products' error: at most 2^-18 of ||c||^2 + 2 |x| |c| each
+        const bool near = second[r][half] <= best[r][half] + 7.6293945e-6f * fmaf(2.f * cmax, sqrtf(x2), cmax2);
+        const int j = 32 * (id >> 2) + 8 * c + 2 * (id & 3);  // lane c: block c of the group
+        load_centroid<D>(tab, j, y);
+        float d0 = distance<D>(x, y);
+        load_centroid<D>(tab, j + 1, y);
+        const float d1 = distance<D>(x, y);
+        float far = fmaxf(d0, d1);
+        int k = d1 < d0 ? j + 1 : j;
+        d0 = fminf(d0, d1);
+        join_best(d0, far, k, 1);
+        join_best(d0, far, k, 2);
+        // (not a number or too far off for fp32: unsure)
+        unsure[half] = near || !(far > d0 + far * 1.9073486e-6f + of_x[16 * r / kSubs] * sqrtf(far));
+        code[half] = k;
+      }
+      if (c < 2) codes[16 * r + g + 8 * c] = static_cast<uint16_t>(c ? code[1] : code[0]);
+      open[r] = __ballot_sync(kAll, c < 2 && (c ? unsure[1] : unsure[0]));
+    }
     __syncwarp();
+    // ---- steps 3 and 4 ------------------------------------------------------------------------------------------
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      uint32_t todo = open[r];
+      while (todo) {
+        constexpr int kTiles = kSubs / 16;  // of a vector
+        const int v = r / kTiles, bit = __ffs(todo) - 1, row = 16 * r + (bit >> 2) + 8 * (bit & 1);
+        todo &= todo - 1u;
+        if (slot[v] < 0) continue;
+        const int code = settle<D>(p, which, (v0 + v) / p.hkv, static_cast<int>((v0 + v) % p.hkv), row % kSubs, xs + v * kHeadDim, tab, of_x[v]);
+        if (lane == 0) codes[row] = static_cast<uint16_t>(code);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (slot[v] >= 0) store_codes(p, which, codes + v * kSubs, slot[v], static_cast<int>((v0 + v) % p.hkv), lane);
+    __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(kAppThreads, 2) vq_append_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ __align__(16) uint8_t app_smem[];
+  __shared__ int top;  // the largest ||c||^2
+  const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
+  if (static_cast<int>(blockIdx.x) >= ctas) {  // queries
+    const long long b = static_cast<long long>(blockIdx.x) - ctas, shares = (p.q.heads[0] + p.q.heads_per_y - 1) / p.q.heads_per_y;
+    const bool whole = p.interleaved || p.rotary_dim % 16 == 0;
+    const int y = static_cast<int>(b % shares);
+    if (p.bf16) whole ? rotary_share<true, true>(p.q, b / shares, y) : rotary_share<true, false>(p.q, b / shares, y);
+    else whole ? rotary_share<false, true>(p.q, b / shares, y) : rotary_share<false, false>(p.q, b / shares, y);
+    return;
+  }
+  const int which = static_cast<int>(blockIdx.x) >= ctas0, cta = static_cast<int>(blockIdx.x) - which * ctas0;
+  if (threadIdx.x == 0) top = 0;
+  __syncthreads();
+  switch (p.sub[which] + (p.few ? 16 : 0)) {
+    case 2:
+    case 18: append_tensor<2, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
+    case 4: append_tensor<4, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
+    case 20: append_tensor<4, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
+    case 8: append_tensor<8, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
+    default: append_tensor<8, 1>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream) {
+  static SmemOptIn opt;
   const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv;
-  const long long most = (vectors + kAppWarps - 1) / kAppWarps;
-  p.kv_ctas = static_cast<int>(most < 4LL * sms ? most : 4LL * sms);
-  long long grid = 2LL * p.kv_ctas;
+  // one vector per warp and pass while that leaves no warp without work
+  p.few = 2 * vectors <= 2LL * sms * kAppWarps;
+  size_t smem = 0;
+  long long most[2];
+  double cost[2];
+  for (int i = 0; i < 2; ++i) {
+    const int d = p.sub[i], n = 1 << p.bits[i], per_pass = d == 2 || p.few ? 1 : d / 2;
+    const size_t bytes = static_cast<size_t>(n) * (d + 1) * 4 + kAppWarps * per_pass * (kHeadDim * 4 + kHeadDim / d * 2);
+    smem = bytes > smem ? bytes : smem;
+    const long long per_cta = static_cast<long long>(kAppWarps) * per_pass;
+    most[i] = (vectors + per_cta - 1) / per_cta;
+    cost[i] = static_cast<double>(kHeadDim / d) * n * (d == 8 ? 2 : 1) + (i == 0 ? 3000 : 1000);  // scores, and what comes before them
+  }
+  cudaError_t e = ensure_smem(vq_append_kernel, smem, opt);
+  if (e != cudaSuccess) return e;
+  // both tensors' CTAs fit the GPU at once, shared by what they cost
+  const int slots = (smem > 100 * 1024 ? 1 : 2) * sms;
+  for (int i = 0; i < 2; ++i) {
+    const long long share = static_cast<long long>(slots * cost[i] / (cost[0] + cost[1]));
+    p.kv_ctas[i] = static_cast<int>(most[i] < share ? most[i] : share < 1 ? 1 : share);
+  }
+  if (most[0] + most[1] <= slots)
+    for (int i = 0; i < 2; ++i) p.kv_ctas[i] = static_cast<int>(most[i]);
+  long long grid = p.kv_ctas[0] + p.kv_ctas[1];
   if (p.q.heads[0] > 0) {
     const dim3 g = rotary_grid(p.q, sms);
     grid += static_cast<long long>(g.x) * g.y;
   }
-  const bool whole = p.interleaved || p.rotary_dim % 16 == 0;
-  auto kern = p.bf16 ? (whole ? vq_append_kernel<true, true> : vq_append_kernel<true, false>)
-                     : (whole ? vq_append_kernel<false, true> : vq_append_kernel<false, false>);
-  kern<<<static_cast<unsigned>(grid), kAppThreads, 0, stream>>>(p);
+  vq_append_kernel<<<static_cast<unsigned>(grid), kAppThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -172,7 +172,7 @@ struct AppendParams {
   int rotary_dim, interleaved, bf16;
   int num_tokens, hkv, page_size;
   int sub[2], bits[2], row_bytes[2];
-  int kv_ctas;                 // CTAs of each tensor; those after them turn queries (set by the launcher)
+  int kv_ctas[2], few;         // CTAs of each tensor, those after them turn queries; one vector per pass (set by the launcher)
   RotaryParams q;              // the queries (heads[0] 0: none)
 };
 
