@@ -25,7 +25,7 @@ namespace vqk {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kAppThreads = kRotThreads, kAppWarps = kAppThreads / 32;
+constexpr int kAppThreads = kRotThreads, kAppThreadsMost = 512;  // (with a large codebook one CTA of more threads fits an SM)
 
 __device__ __forceinline__ double row_value(const AppendParams& p, const uint16_t* row, int e) {
   const uint16_t x = __ldg(row + e);
@@ -112,8 +112,9 @@ __device__ __forceinline__ int exact_code(const AppendParams& p, int which, int 
 // A vector's codes into its row of the pool (one warp): lane w makes words w, w + 32, .. of the row.
 __device__ __forceinline__ void store_codes(const AppendParams& p, int which, const uint16_t* codes, long long slot, int h, int lane) {
   const int bits = p.bits[which], count = kHeadDim / p.sub[which], words = p.row_bytes[which] / 4;
-  const long long page = slot / p.page_size, off = slot % p.page_size;
-  uint32_t* const row = reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * p.page_size + off) * p.row_bytes[which]);
+  const unsigned P = p.page_size;
+  const long long page = slot >> 32 ? slot / P : static_cast<unsigned>(slot) / P, off = slot - page * P;
+  uint32_t* const row = reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * P + off) * p.row_bytes[which]);
   for (int w = lane; w < words; w += 32) {
     uint32_t x = 0;
     if (bits == 8) {  // four codes a word
@@ -146,8 +147,8 @@ __device__ __forceinline__ int centroid_word(int j, int e) {
 }
 
 template <int D>
-__device__ __forceinline__ void fill_codebook(const __half* cb, int n, float* tab, float* norm, int* top) {
-  for (int j = threadIdx.x; j < n; j += kAppThreads) {
+__device__ __forceinline__ void fill_codebook(const __half* cb, int n, float* tab, float2* norm, int* top) {
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
     float c[D], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < D; ++e) {
@@ -156,7 +157,8 @@ __device__ __forceinline__ void fill_codebook(const __half* cb, int n, float* ta
     }
 #pragma unroll
     for (int e = 0; e < D; ++e) tab[centroid_word<D>(j, e)] = -2.f * c[e];
-    norm[j] = sum;
+    float* const at = reinterpret_cast<float*>(norm + (j & ~1)) + (j & 1);  // a pair of norms twice, as a product's start
+    at[0] = at[2] = sum;
     const int high = __reduce_max_sync(kAll, __float_as_int(sum));  // (not negative: ordered like their bits; n is a multiple of the threads)
     if ((threadIdx.x & 31) == 0) atomicMax(top, high);
   }
@@ -211,6 +213,13 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   float d;
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// (fp32's own square root takes as long as a centroid's distance, and what it is for here has room)
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Smallest and second smallest of two such pairs, with what the smallest is (the lower of equals).
@@ -324,7 +333,7 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
     }
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) second = fminf(second, __shfl_xor_sync(kAll, second, m));
-    if (second == INFINITY || second > best + second * 1.9073486e-6f + of_x * sqrtf(second)) return at;  // 2^-19
+    if (second == INFINITY || second > best + second * 1.9073486e-6f + of_x * root(second)) return at;  // 2^-19
   }
   double y[4];
   exact_vector(p, which, t, h, lane, y);
@@ -347,36 +356,45 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
   constexpr int NV = Shape::kVectors, kSubs = kHeadDim / D;  // sub-vectors of a vector
   const int n = 1 << p.bits[which];
   float* const tab = reinterpret_cast<float*>(smem);
-  float* const norm = tab + n * D;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* const mine = smem + n * (D + 1) * 4 + warp * Shape::kWarpBytes;
+  float2* const norm = reinterpret_cast<float2*>(tab + n * D);  // (|c_j|^2, |c_j+1|^2) of the pair, for either of it
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* const mine = smem + n * (D + 2) * 4 + warp * Shape::kWarpBytes;
   float* const xs = reinterpret_cast<float*>(mine);
   uint16_t* const codes = reinterpret_cast<uint16_t*>(xs + NV * kHeadDim);
   fill_codebook<D>(static_cast<const __half*>(p.cb[which]), n, tab, norm, top);
   __syncthreads();
-  const float cmax2 = __int_as_float(*top), cmax = sqrtf(cmax2);
-  const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv;
+  const float cmax2 = __int_as_float(*top);
+  // A warp's passes are next to each other, so that a token's angles serve its heads.
+  const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv, passes = (vectors + NV - 1) / NV;
+  const long long per = (passes + static_cast<long long>(ctas) * warps - 1) / (static_cast<long long>(ctas) * warps);
+  long long v0 = (static_cast<long long>(cta) * warps + warp) * per * NV;
+  const long long v1 = min(v0 + per * NV, vectors);
+  int t0 = static_cast<int>(v0 / p.hkv), h0 = static_cast<int>(v0 - static_cast<long long>(t0) * p.hkv);
   Angles angles;
 
-  for (long long v0 = (static_cast<long long>(cta) * kAppWarps + warp) * NV; v0 < vectors; v0 += static_cast<long long>(ctas) * kAppWarps * NV) {
+  for (; v0 < v1; v0 += NV) {
+    int tok[NV], head[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      tok[v] = t0;
+      head[v] = h0;
+      if (++h0 == p.hkv) h0 = 0, ++t0;
+    }
     // ---- the vectors as they are coded ---------------------------------------------------------------------
     long long slot[NV];
     float raw[NV][4], of_x[NV];  // of_x: what x's own error can make of a difference of distances, times the distance's root
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const long long t = (v0 + v) / p.hkv;
-      slot[v] = v0 + v < vectors ? append_slot(p, t, lane == 0) : -1;
+      slot[v] = v0 + v < v1 ? append_slot(p, tok[v], lane == 0) : -1;
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw[v][i] = 0.f;
-      if (slot[v] >= 0) load_raw(p, static_cast<const uint16_t*>(p.src[which]) + t * p.stride[which] + (v0 + v) % p.hkv * kHeadDim, 4 * lane, raw[v]);
+      if (slot[v] >= 0) load_raw(p, static_cast<const uint16_t*>(p.src[which]) + tok[v] * p.stride[which] + head[v] * kHeadDim, 4 * lane, raw[v]);
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       of_x[v] = 0.f;
       if (which == 0 && slot[v] >= 0) {
-        const long long t = (v0 + v) / p.hkv;
-        const int h = static_cast<int>((v0 + v) % p.hkv);
-        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + t * p.stride[0] + h * kHeadDim, t, h, lane, angles, raw[v]);
+        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok[v] * p.stride[0] + head[v] * kHeadDim, tok[v], head[v], lane, angles, raw[v]);
         float sum = fmaf(raw[v][0], raw[v][0], fmaf(raw[v][1], raw[v][1], fmaf(raw[v][2], raw[v][2], raw[v][3] * raw[v][3])));
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
@@ -430,7 +448,7 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int nb = 4 * group + b;
-        const float2 start = *reinterpret_cast<const float2*>(norm + 8 * nb + 2 * c);
+        const float4 start = *reinterpret_cast<const float4*>(norm + 8 * nb + 2 * c);
         uint32_t b0, b1 = 0;
         if constexpr (D == 2) {
           b0 = __float_as_uint(tab[(8 * nb + g) * 2 + (c & 1)]);
@@ -444,9 +462,9 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
         for (int r = 0; r < R; ++r) {
           float s[4];
           if constexpr (D == 2) {
-            mma_k4(s, a[r][0], a[r][1], b0, start.x, start.y, start.x, start.y);
+            mma_k4(s, a[r][0], a[r][1], b0, start.x, start.y, start.z, start.w);
           } else {
-            mma_k8(s, a[r][0], a[r][1], a[r][2], a[r][3], b0, b1, start.x, start.y, start.x, start.y);
+            mma_k8(s, a[r][0], a[r][1], a[r][2], a[r][3], b0, b1, start.x, start.y, start.z, start.w);
             if constexpr (D == 8) mma_k8(s, a[r][4], a[r][5], a[r][6], a[r][7], b0, b1, s[0], s[1], s[2], s[3]);
           }
           low[r][0] = b == 0 ? fminf(s[0], s[1]) : min3(low[r][0], s[0], s[1]);
@@ -462,42 +480,50 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
           best[r][half] = fminf(best[r][half], low[r][half]);
         }
     }
-    // ---- steps 1 and 2: a quad has two rows, a lane two of a group's 8 centroids of each -----------------------
-    uint32_t open[R];  // bit 4 g + i: row g + 8 i is not told yet
+    // ---- steps 1 and 2: a quad has two rows; lanes c < 2 go on with row g, the others with row g + 8 ------------
+    uint32_t open[R];  // bit 4 g + 2 i: row g + 8 i is not told yet
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      bool unsure[2];
-      int code[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        int id = 4 * at[r][half] + c;
-        join_best(best[r][half], second[r][half], id, 1);
-        join_best(best[r][half], second[r][half], id, 2);
-        const int row = 16 * r + g + 8 * half;
-        float x[D], y[D];
-#pragma unroll
-        for (int e = 0; e < D; ++e) x[e] = xs[row * D + e];
-        float x2 = 0.f;
-#pragma unroll
-        for (int e = 0; e < D; ++e) x2 = fmaf(x[e], x[e], x2);
-        // the products' error: at most 2^-18 of ||c||^2 + 2 |x| |c| each
-        const bool near = second[r][half] <= best[r][half] + 7.6293945e-6f * fmaf(2.f * cmax, sqrtf(x2), cmax2);
-        const int j = 32 * (id >> 2) + 8 * c + 2 * (id & 3);  // lane c: block c of the group
-        load_centroid<D>(tab, j, y);
-        float d0 = distance<D>(x, y);
-        load_centroid<D>(tab, j + 1, y);
-        const float d1 = distance<D>(x, y);
-        float far = fmaxf(d0, d1);
-        int k = d1 < d0 ? j + 1 : j;
-        d0 = fminf(d0, d1);
-        join_best(d0, far, k, 1);
-        join_best(d0, far, k, 2);
-        // (not a number or too far off for fp32: unsure)
-        unsure[half] = near || !(far > d0 + far * 1.9073486e-6f + of_x[16 * r / kSubs] * sqrtf(far));
-        code[half] = k;
+      const int half = c >> 1, row = 16 * r + g + 8 * half;
+      float b = half ? best[r][1] : best[r][0], sec = half ? second[r][1] : second[r][0];
+      int id = 4 * (half ? at[r][1] : at[r][0]) + c;
+      {  // the other pair's share of this row, for this pair's share of its row
+        const float ob = __shfl_xor_sync(kAll, half ? best[r][0] : best[r][1], 2), os = __shfl_xor_sync(kAll, half ? second[r][0] : second[r][1], 2);
+        const int oi = __shfl_xor_sync(kAll, 4 * (half ? at[r][0] : at[r][1]) + c, 2);
+        sec = min3(sec, os, fmaxf(b, ob));
+        id = ob < b ? oi : id;
+        b = fminf(b, ob);
       }
-      if (c < 2) codes[16 * r + g + 8 * c] = static_cast<uint16_t>(c ? code[1] : code[0]);
-      open[r] = __ballot_sync(kAll, c < 2 && (c ? unsure[1] : unsure[0]));
+      join_best(b, sec, id, 1);
+      float x[D], y[D], x2 = 0.f;
+#pragma unroll
+      for (int e = 0; e < D; ++e) {
+        x[e] = xs[row * D + e];
+        x2 = fmaf(x[e], x[e], x2);
+      }
+      // The products' error: at most 2^-18 of ||c||^2 + 2 |x| |c| each, of centroids that are as near as the nearest, so
+      // with |c| up to |x| + distance (and no longer than the longest).
+      const float x1 = root(x2), reach = fmaf(1.01f, x1, root(fmaxf(b + x2, 0.f)));
+      const float c2 = fminf(reach * reach, cmax2);
+      const bool near = sec <= b + 7.6293945e-6f * fmaf(2.f * x1, root(c2), c2);
+      // of the group's four blocks this lane's two, two centroids each
+      const int j = 32 * (id >> 2) + 16 * (c & 1) + 2 * (id & 3);
+      float d0 = INFINITY, far = INFINITY;
+      int code = j;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = j + 8 * (i >> 1) + (i & 1);
+        load_centroid<D>(tab, k, y);
+        const float d = distance<D>(x, y);
+        far = fminf(far, fmaxf(d0, d));
+        code = d < d0 ? k : code;
+        d0 = fminf(d0, d);
+      }
+      join_best(d0, far, code, 1);
+      // (not a number or too far off for fp32: not told)
+      const bool unsure = near || !(far > d0 + far * 1.9073486e-6f + of_x[16 * r / kSubs] * root(far));  // 2^-19
+      if (!(c & 1)) codes[row] = static_cast<uint16_t>(code);
+      open[r] = __ballot_sync(kAll, unsure && !(c & 1));
     }
     __syncwarp();
     // ---- steps 3 and 4 ------------------------------------------------------------------------------------------
@@ -506,27 +532,28 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
       uint32_t todo = open[r];
       while (todo) {
         constexpr int kTiles = kSubs / 16;  // of a vector
-        const int v = r / kTiles, bit = __ffs(todo) - 1, row = 16 * r + (bit >> 2) + 8 * (bit & 1);
+        const int v = r / kTiles, bit = __ffs(todo) - 1, row = 16 * r + (bit >> 2) + 4 * (bit & 2);
         todo &= todo - 1u;
         if (slot[v] < 0) continue;
-        const int code = settle<D>(p, which, (v0 + v) / p.hkv, static_cast<int>((v0 + v) % p.hkv), row % kSubs, xs + v * kHeadDim, tab, of_x[v]);
+        const int code = settle<D>(p, which, tok[v], head[v], row % kSubs, xs + v * kHeadDim, tab, of_x[v]);
         if (lane == 0) codes[row] = static_cast<uint16_t>(code);
       }
     }
     __syncwarp();
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (slot[v] >= 0) store_codes(p, which, codes + v * kSubs, slot[v], static_cast<int>((v0 + v) % p.hkv), lane);
+      if (slot[v] >= 0) store_codes(p, which, codes + v * kSubs, slot[v], head[v], lane);
     __syncwarp();
   }
 }
 
-__global__ void __launch_bounds__(kAppThreads, 2) vq_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppThreadsMost, 1) vq_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(16) uint8_t app_smem[];
   __shared__ int top;  // the largest ||c||^2
   const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
   if (static_cast<int>(blockIdx.x) >= ctas) {  // queries
     const long long b = static_cast<long long>(blockIdx.x) - ctas, shares = (p.q.heads[0] + p.q.heads_per_y - 1) / p.q.heads_per_y;
+    if (threadIdx.x >= kAppThreads) return;
     const bool whole = p.interleaved || p.rotary_dim % 16 == 0;
     const int y = static_cast<int>(b % shares);
     if (p.bf16) whole ? rotary_share<true, true>(p.q, b / shares, y) : rotary_share<true, false>(p.q, b / shares, y);
@@ -541,7 +568,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) vq_append_kernel(const __grid_
     case 18: append_tensor<2, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
     case 4: append_tensor<4, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
     case 20: append_tensor<4, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
-    case 8: append_tensor<8, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
+    case 8: append_tensor<8, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
     default: append_tensor<8, 1>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
   }
 }
@@ -551,23 +578,25 @@ __global__ void __launch_bounds__(kAppThreads, 2) vq_append_kernel(const __grid_
 cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream) {
   static SmemOptIn opt;
   const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv;
+  const bool large = p.bits[0] >= 10 || p.bits[1] >= 10;
+  const int threads = large ? kAppThreadsMost : kAppThreads, warps = threads / 32;
   // one vector per warp and pass while that leaves no warp without work
-  p.few = 2 * vectors <= 2LL * sms * kAppWarps;
+  p.few = 2 * vectors <= 2LL * sms * (kAppThreads / 32);
   size_t smem = 0;
   long long most[2];
   double cost[2];
   for (int i = 0; i < 2; ++i) {
-    const int d = p.sub[i], n = 1 << p.bits[i], per_pass = d == 2 || p.few ? 1 : d / 2;
-    const size_t bytes = static_cast<size_t>(n) * (d + 1) * 4 + kAppWarps * per_pass * (kHeadDim * 4 + kHeadDim / d * 2);
+    const int d = p.sub[i], n = 1 << p.bits[i], per_pass = d == 2 || p.few ? 1 : 2;
+    const size_t bytes = static_cast<size_t>(n) * (d + 2) * 4 + warps * per_pass * (kHeadDim * 4 + kHeadDim / d * 2);
     smem = bytes > smem ? bytes : smem;
-    const long long per_cta = static_cast<long long>(kAppWarps) * per_pass;
+    const long long per_cta = static_cast<long long>(warps) * per_pass;
     most[i] = (vectors + per_cta - 1) / per_cta;
     cost[i] = static_cast<double>(kHeadDim / d) * n * (d == 8 ? 2 : 1) + (i == 0 ? 3000 : 1000);  // scores, and what comes before them
   }
   cudaError_t e = ensure_smem(vq_append_kernel, smem, opt);
   if (e != cudaSuccess) return e;
   // both tensors' CTAs fit the GPU at once, shared by what they cost
-  const int slots = (smem > 100 * 1024 ? 1 : 2) * sms;
+  const int slots = (large ? 1 : 2) * sms;
   for (int i = 0; i < 2; ++i) {
     const long long share = static_cast<long long>(slots * cost[i] / (cost[0] + cost[1]));
     p.kv_ctas[i] = static_cast<int>(most[i] < share ? most[i] : share < 1 ? 1 : share);
@@ -579,7 +608,7 @@ cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream) {
     const dim3 g = rotary_grid(p.q, sms);
     grid += static_cast<long long>(g.x) * g.y;
   }
-  vq_append_kernel<<<static_cast<unsigned>(grid), kAppThreads, smem, stream>>>(p);
+  vq_append_kernel<<<static_cast<unsigned>(grid), threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
