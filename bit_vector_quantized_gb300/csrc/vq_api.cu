@@ -1154,8 +1154,15 @@ ChunkWs chunk_ws(int tile_rows, int grid) {
   return w;
 }
 
-// Tile height of a call over trees of drafted tokens.
-int tree_tile_rows(const vq_layout&, int) { return 256; }
+// Tile height of a call over trees of drafted tokens.  VQ_TREE_ROWS=16|32|64|256 selects one explicitly (a tuning
+// switch for profiling).
+int tree_tile_rows(const vq_layout& L, int max_new_len) {
+  if (const char* env = std::getenv("VQ_TREE_ROWS"))
+    for (int rows : {16, 32, 64, 256})
+      if (std::atoi(env) == rows) return rows;
+  const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 64 : 256;
+}
 
 struct TreeArgs {
   const uint64_t* masks;
@@ -1270,7 +1277,7 @@ vq_status attention_of_rows(const vq_layout* layout, int32_t batch, int32_t num_
     p.mask_words = tree->mask_words;
     p.positions = tree->positions;
   }
-  auto launch = tree ? vqk::launch_tree_wide : wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;
+  auto launch = tree && wide ? vqk::launch_tree_wide : tree ? vqk::launch_tree : wide ? vqk::launch_chunk_wide : vqk::launch_chunk_narrow;
   cudaError_t e = launch(p, L.k_sub, L.k_bits, L.v_sub, L.v_bits, grid, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, tree ? "vq_tree_attention launch" : "vq_chunk_attention launch");
   e = vqk::launch_chunk_merge(p, chunk_workers(tile_rows, grid), static_cast<cudaStream_t>(stream));
@@ -1316,7 +1323,11 @@ size_t vq_tree_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t n
     return 0;
   const int sms = num_sms > 0 ? num_sms : device_sms();
   if (sms <= 0) return 0;
-  return chunk_ws(tree_tile_rows(*layout, max_new_len), std::max(sms, 2)).total;
+  size_t most = 0;  // a call with smaller bounds may take a smaller tile
+  const int need = tree_tile_rows(*layout, max_new_len);
+  for (int rows : {16, 32, 64, 256})
+    if (rows <= need) most = std::max(most, chunk_ws(rows, std::max(sms, 2)).total);
+  return most;
 }
 
 vq_status vq_tree_attention(const vq_layout* layout, int32_t batch, int32_t num_tokens,

@@ -61,10 +61,8 @@
 // 512 to 8192 tokens take 3 to 12 % longer than at 8 bits.
 #include <type_traits>
 
-#include "vq_chunk_common.cuh"
 #include "vq_chunk_soft.cuh"
-#include "vq_gather.cuh"
-#include "vq_tcgen05.cuh"
+#include "vq_chunk_wide.cuh"
 
 namespace vqk {
 namespace {
@@ -97,7 +95,7 @@ struct WideSmem {
   using Shape = WideShape<kPair>;
   static constexpr bool kWideCodes = DK == 8;      // 1.5-bit format: plain 64 KB tables
   static constexpr bool kSplitTable = BV == 9;     // 128-byte rows, K then V; else 256-byte rows (K, V)
-  static constexpr int kTable = kWideCodes ? 131072 : kSplitTable ? (256 + 512) * 128 : 65536;
+  static constexpr int kTable = WideTable<DK, BV>::kBytes;
   static constexpr int kVStages = kPair ? 3 : kWideCodes ? 1 : 2;
   static constexpr int kTiles = kTable;                             // K stages, then V stages
   static constexpr int kMisc = kTiles + (Shape::kKStages + kVStages) * Shape::kTileBytes;
@@ -112,94 +110,6 @@ struct WideSmem {
   static_assert((kChunkMaxBatch + 1 + 32) * 8 <= Shape::kTileBytes, "the plan shares a tile");
 };
 
-// Codes of kDims dims of a token (32 or 64; part 0 .. 128 / kDims - 1), loaded ahead of their use: the
-// loads are volatile, so that they stay where they are issued, and nothing is computed from the words
-// before align().
-template <int D, int B, int kDims>
-struct PartCodes {
-  static constexpr int kBits = B, kSub = D, kPieces = kDims / 8;  // 16-byte pieces of centroids
-  static constexpr int kCodes = kDims / D;
-  static constexpr int kWords = (kCodes * B + 31) / 32;  // (9- and 12-bit codes may start inside their first word)
-  uint32_t w[kWords];
-  static __device__ __forceinline__ int first_byte(int part) { return part * kCodes * B / 32 * 4; }
-  __device__ __forceinline__ void load(const uint8_t* at) {
-    if constexpr (B == 8 && kWords % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < kWords; i += 4)
-        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                     : "l"(at + 4 * i));
-    } else if constexpr (B == 8) {
-      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(at));
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[i]) : "l"(at + 4 * i));
-    }
-  }
-  // Code 0 to bit 0.
-  __device__ __forceinline__ void align(int part) {
-    if constexpr (kCodes * B % 32) {
-      const int s = part * kCodes * B & 31;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = i + 1 < kWords ? __funnelshift_r(w[i], w[i + 1], s) : w[i] >> s;
-    }
-  }
-  __device__ __forceinline__ uint32_t code(int i) const {
-    if constexpr (B == 8) {
-      return __byte_perm(w[i >> 2], 0u, 0x4440 | (i & 3));
-    } else {
-      const int bit = i * B, k = bit >> 5, s = bit & 31;
-      const uint32_t x = s + B > 32 ? __funnelshift_r(w[k], w[k + 1 < kWords ? k + 1 : k], s) : w[k] >> s;
-      return x & ((1u << B) - 1u);
-    }
-  }
-};
-static_assert(PartCodes<4, 9, 32>::kWords == 3 && PartCodes<4, 9, 64>::kWords == 5 && PartCodes<8, 12, 32>::kWords == 2 &&
-                  PartCodes<8, 12, 64>::kWords == 3,
-              "72 + 24, 144 + 16, 48 + 16 and 96 bits");
-
-// 16-byte piece c (dims 8c .. 8c + 7) of the part: its centroids.
-// kRowShift: log2 of the table's row bytes; lane: the lane's byte in a row.
-template <typename Codes, int kRowShift>
-__device__ __forceinline__ uint4 gather_piece(const Codes& x, int c, uint32_t lane) {
-  constexpr int D = Codes::kSub;
-  auto off = [&](int i) {
-    if constexpr (Codes::kBits == 8 && kRowShift == 8) return row_addr(x.w[i >> 2], lane, i & 3);
-    else return (x.code(i) << kRowShift) + lane;
-  };
-  if constexpr (D == 8) {
-    return tab128(off(c));
-  } else if constexpr (D == 4) {
-    const uint2 a = tab64(off(2 * c)), b = tab64(off(2 * c + 1));
-    return make_uint4(a.x, a.y, b.x, b.y);
-  } else {
-    return make_uint4(tab32(off(4 * c)), tab32(off(4 * c + 1)), tab32(off(4 * c + 2)), tab32(off(4 * c + 3)));
-  }
-}
-
-template <int DK, int BK, int DV, int BV>
-__device__ __forceinline__ void fill_wide_table(const ChunkParams& p) {
-  using W = WideSmem<DK, BK, DV, BV, false>;  // (the table is the same in a pair)
-  uint4* tab = reinterpret_cast<uint4*>(g_smem);
-  auto replicas = [](const void* cb, int row, bool four) {
-    if (four) {
-      const uint2 c = __ldg(static_cast<const uint2*>(cb) + row);
-      return make_uint4(c.x, c.y, c.x, c.y);
-    }
-    const uint32_t c = __ldg(static_cast<const uint32_t*>(cb) + row);
-    return make_uint4(c, c, c, c);
-  };
-  for (int i = threadIdx.x; i < W::kTable / 16; i += blockDim.x) {
-    if constexpr (W::kWideCodes) {
-      tab[i] = i < 4096 ? __ldg(static_cast<const uint4*>(p.cb_k) + i) : __ldg(static_cast<const uint4*>(p.cb_v) + i - 4096);
-    } else if constexpr (W::kSplitTable) {
-      tab[i] = i < 2048 ? replicas(p.cb_k, i >> 3, DK == 4) : replicas(p.cb_v, (i - 2048) >> 3, DV == 4);
-    } else {
-      tab[i] = i & 8 ? replicas(p.cb_v, i >> 4, DV == 4) : replicas(p.cb_k, i >> 4, DK == 4);
-    }
-  }
-}
-
 // Unnormalised Walsh-Hadamard transform of 64 registers.
 __device__ __forceinline__ void fwht64(float (&x)[64]) {
 #pragma unroll
@@ -211,66 +121,6 @@ __device__ __forceinline__ void fwht64(float (&x)[64]) {
         x[i] = a + b;
         x[i + s] = a - b;
       }
-}
-
-// The warpgroup's registers per thread from here on (all four warps call it).
-template <int N>
-__device__ __forceinline__ void reg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void reg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Maximum of three (fp32 bits), and a packed pair of fp32 additions.
-__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
-  return d;
-}
-__device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x0), "+f"(x1)
-      : "f"(y0), "f"(y1));
-}
-
-// A ring slot's position: phase flips each time the ring wraps.
-struct Ring {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ void next(uint32_t n) {
-    if (++slot == n) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
-
-// One piece of a tile as the planning warp hands it to the others.
-struct __align__(16) WidePiece {
-  int b, kvh;
-  int row0, rows;            // the tile's first row in q and out, and its rows (tokens x G)
-  int first_pos, last_pos;   // positions of its first and last token
-  int limit;                 // keys end here
-  int sink, lo, blk0, blk1;  // blocks [blk0, blk1) of its keys (ChunkKeys)
-  int slot;                  // partial slot or -1
-  int more;                  // 0: there is no piece, the range is done
-  int seq_row;               // (a tree:) row of the sequence's first drafted token; first_pos is the context's last token
-  int pad[2];
-  __device__ __forceinline__ int block(int i) const { return i < sink ? i : lo + (i - sink); }
-};
-static_assert(sizeof(WidePiece) == 64, "the pieces' place in shared memory");
-// Pieces under way.  The code warps look two blocks ahead of the one they store,
-// while the issuer may still wait for that one: of pieces of one block each,
-// the issuer has read the stored block's, and two more are needed ahead of
-// it (pieces without a block are not handed out).
-constexpr uint32_t kPieces = 4;
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
 }
 
 // Which of tokens t .. t + 31 a row of a tree sees among the drafted ones, which begin at token `ctx` (its
