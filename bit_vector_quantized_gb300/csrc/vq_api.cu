@@ -1154,14 +1154,14 @@ ChunkWs chunk_ws(int tile_rows, int grid) {
   return w;
 }
 
-// Tile height of a call over trees of drafted tokens.  VQ_TREE_ROWS=16|32|64|256 selects one explicitly (a tuning
+// Tile height of a call over trees of drafted tokens.  VQ_TREE_ROWS=16|32|128|256 selects one explicitly (a tuning
 // switch for profiling).
 int tree_tile_rows(const vq_layout& L, int max_new_len) {
   if (const char* env = std::getenv("VQ_TREE_ROWS"))
-    for (int rows : {16, 32, 64, 256})
+    for (int rows : {16, 32, 128, 256})
       if (std::atoi(env) == rows) return rows;
   const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 64 : 256;
+  return rows <= 16 ? 16 : rows <= 64 ? 32 : rows <= 128 ? 128 : 256;
 }
 
 struct TreeArgs {
@@ -1325,7 +1325,7 @@ size_t vq_tree_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t n
   if (sms <= 0) return 0;
   size_t most = 0;  // a call with smaller bounds may take a smaller tile
   const int need = tree_tile_rows(*layout, max_new_len);
-  for (int rows : {16, 32, 64, 256})
+  for (int rows : {16, 32, 128, 256})
     if (rows <= need) most = std::max(most, chunk_ws(rows, std::max(sms, 2)).total);
   return most;
 }

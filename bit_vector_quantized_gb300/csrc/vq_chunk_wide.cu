@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
   uint32_t* const masks = reinterpret_cast<uint32_t*>(bars + 28);  // [kMasks][4] tokens that have a page
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+  volatile uint32_t* const done = tmem_at + 2;  // (a tree:) blocks whose values are under way
   float* const tops = reinterpret_cast<float*>(g_smem + W::kMisc + 704);  // [2][2][128] maxima of a row's two halves
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     if (tid == 0 && rank == 0) write_record(p, worker, nullptr);
     return;
   }
-  fill_wide_table<DK, BK, DV, BV>(p);
+  if constexpr (!kTree) fill_wide_table<DK, BK, DV, BV>(p, tid, kWideThreads);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(ready + i, soft + kCodeWarps + passed);
@@ -202,15 +203,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     mbar_init(drain, 1);
     for (int i = 0; i < static_cast<int>(kPieces); ++i) {
       mbar_init(piece_full + i, 1);
-      mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 1);
+      mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 1 + (kTree ? 1 : 0));
     }
     mbar_init_fence();
     *abort_flag = 0;
+    if constexpr (kTree) *done = 0;
   }
   if (warp == kSoftWarps + kCodeWarps) tmem_alloc<kPair>(tmem_at, kCols);
   long long* const pre = reinterpret_cast<long long*>(tiles);  // the plan, before the first tile is written
   tc_fence_before();
-  chunk_plan<kTree>(p, pre, pre + kChunkMaxBatch + 1);
+  if constexpr (kTree) __syncthreads();
+  else chunk_plan(p, pre, pre + kChunkMaxBatch + 1);
   tc_fence_after();
   // All 512 columns are this CTA's, so they start at column 0; the constant keeps the
   // products' operands in uniform registers.
@@ -223,6 +226,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     return;
   }
   if constexpr (kPair) cluster_sync();  // the barriers of both are there before either arrives on the other's
+
+  if constexpr (kTree) {  // the planning warp plans while the others fill the table
+    if (warp != kSoftWarps + kCodeWarps + 1) {
+      fill_wide_table<DK, BK, DV, BV>(p, warp > kSoftWarps + kCodeWarps + 1 ? tid - 32 : tid, kWideThreads - 32);
+      asm volatile("bar.sync 6, %0;" ::"n"(kWideThreads - 32) : "memory");
+    }
+  }
 
   // Bounded wait; on a timeout the CTA is given up.  The warps' form is uniform over the warp.
   auto wait_one = [&](uint64_t* bar, uint32_t phase, auto cluster) {
@@ -690,7 +700,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       bool ok = true;
       while (ok && next_piece(u)) {
         if (blocks == 0) ok = pass(start, 0);
-        for (int j = u.blk0; ok && j < u.blk1; ++j, ++blocks) ok = pass(ready + (blocks & 3u), (blocks >> 2) & 1u);
+        for (int j = u.blk0; ok && j < u.blk1; ++j, ++blocks) {
+          ok = pass(ready + (blocks & 3u), (blocks >> 2) & 1u);
+          if constexpr (kTree)
+            if (lane == 0) *done = blocks;
+        }
       }
     } else if (warp == kSoftWarps + kCodeWarps) {
       constexpr uint32_t kScores = tc_idesc(kCtas * kTile, kTile, false), kValues = tc_idesc(kCtas * kTile, kHeadDim, true);
@@ -738,6 +752,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
           }
           __syncwarp();
           rv.next(NV);
+          if constexpr (kTree)
+            if (lane == 0) *done = blk;
           if (j + 2 < nblk) scores(blk + 2);
         }
         blocks += nblk;
@@ -751,6 +767,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     } else if (warp == kSoftWarps + kCodeWarps + 1) {
       // ================================== planning =======================================
       ChunkWalk<kTile, kTree> walk;
+      if constexpr (kTree) tree_plan(p, pre);
       walk.start(p, pre, worker, static_cast<int>(gridDim.x) / kCtas);  // (the tiles over the plan wait for the first piece)
       ChunkPiece q;
       Ring ro;
@@ -815,6 +832,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         ro.next(kPieces);
       }
       if (!recorded && lane == 0 && rank == 0) write_record(p, worker, nullptr);
+    } else if (kTree && warp == kSoftWarps + kCodeWarps + 2) {
+      CodePrefetch prefetch;  // (of a pair one CTA K, one V)
+      while (next_piece(u)) prefetch.piece(p, u, KROW, VROW, rank ? 8 : 0, kPair && !rank ? 8 : 16, done, abort_flag);
     }
   }
   tc_fence_before();
@@ -852,9 +872,8 @@ cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
 
 template <int DK, int BK, int DV, int BV, bool kTree>
 cudaError_t launch_wide(const ChunkParams& p, int grid, cudaStream_t stream) {
-  if constexpr (!kTree)
-    if (p.tile_rows != 2 * kTile) return launch_wide<DK, BK, DV, BV, false, false>(p, grid, stream);
-  return launch_wide<DK, BK, DV, BV, true, kTree>(p, grid, stream);
+  return p.tile_rows == 2 * kTile ? launch_wide<DK, BK, DV, BV, true, kTree>(p, grid, stream)
+                                  : launch_wide<DK, BK, DV, BV, false, kTree>(p, grid, stream);
 }
 
 template <bool kTree>

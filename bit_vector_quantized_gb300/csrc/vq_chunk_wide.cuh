@@ -83,7 +83,7 @@ struct WideTable {
 };
 
 template <int DK, int BK, int DV, int BV>
-__device__ __forceinline__ void fill_wide_table(const ChunkParams& p) {
+__device__ __forceinline__ void fill_wide_table(const ChunkParams& p, int thread, int threads) {
   using W = WideTable<DK, BV>;
   uint4* tab = reinterpret_cast<uint4*>(g_smem);
   auto replicas = [](const void* cb, int row, bool four) {
@@ -94,7 +94,7 @@ __device__ __forceinline__ void fill_wide_table(const ChunkParams& p) {
     const uint32_t c = __ldg(static_cast<const uint32_t*>(cb) + row);
     return make_uint4(c, c, c, c);
   };
-  for (int i = threadIdx.x; i < W::kBytes / 16; i += blockDim.x) {
+  for (int i = thread; i < W::kBytes / 16; i += threads) {
     if constexpr (W::kWideCodes) {
       tab[i] = i < 4096 ? __ldg(static_cast<const uint4*>(p.cb_k) + i) : __ldg(static_cast<const uint4*>(p.cb_v) + i - 4096);
     } else if constexpr (W::kSplitTable) {
@@ -158,6 +158,62 @@ static_assert(sizeof(WidePiece) == 64, "the pieces' place in shared memory");
 // the issuer has read the stored block's, and two more are needed ahead of
 // it (pieces without a block are not handed out).
 constexpr uint32_t kPieces = 4;
+
+// pre[b]: the estimated length of the sequences before b, all KV heads (one warp).
+__device__ __forceinline__ void tree_plan(const ChunkParams& p, long long* pre) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    long long w = 0;
+    if (b < p.batch) {
+      bool bad = false;
+      const ChunkSeq s = chunk_seq<true>(p, b, bad);
+      if (bad && blockIdx.x == 0) report(p.status, kDevBadLength);
+      w = p.hkv * chunk_sum<true>(p, s, (s.n + p.tile_tok - 1) / p.tile_tok);
+    }
+    long long in = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += v;
+    }
+    if (b < p.batch) pre[b] = before + in - w;
+    before += __shfl_sync(0xffffffffu, in, 31);
+  }
+  if (lane == 0) pre[p.batch] = before;
+  __syncwarp();
+}
+
+// Codes on their way to L2 ahead of the warps that expand them (one warp, a piece at a time).  Those ask for a block's
+// codes one block ahead, which covers L2's latency and not the memory's; where few tiles share a sequence nearly
+// every code comes from there.  A lane takes 16 tokens of K or V; at most kAhead blocks ahead of `done`, which the
+// issuing warp moves on.  first: lanes' granules of a block, 0 .. 7 K and 8 .. 15 V, taken from `from` to `to` - 1.
+constexpr int kAhead = 16;
+struct CodePrefetch {
+  uint32_t blocks = 0;  // over all pieces
+  __device__ __forceinline__ void piece(const ChunkParams& p, const WidePiece& u, int k_row, int v_row, int from, int to, volatile uint32_t* done,
+                                        volatile int* abort) {
+    const int lane = threadIdx.x & 31, per = to - from, at_once = 32 / per;
+    const int32_t* const pages = p.page_table + static_cast<long long>(u.b) * p.max_pages;
+    const int granule = from + lane % per;
+    for (int i0 = u.blk0; i0 < u.blk1; i0 += at_once) {
+      // (only a pace: whoever does not move for long is not waited for)
+      for (int spin = 0; spin < 200 && static_cast<int>(blocks + (i0 - u.blk0) - *done) > kAhead && !*abort; ++spin) __nanosleep(100);
+      const int i = i0 + lane / per, t = i < u.blk1 ? u.block(i) * 128 + (granule & 7) * 16 : u.limit;
+      if (t < u.limit) {
+        const int page = __ldg(pages + t / p.page_size);
+        if (page >= 0 && page < p.num_pages) {
+          const int row = granule < 8 ? k_row : v_row;
+          const long long at = (static_cast<long long>(page) * p.hkv + u.kvh) * p.page_size + t % p.page_size;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((granule < 8 ? p.k_pool : p.v_pool) + at * row), "r"(16 * row) : "memory");
+        }
+      }
+      __syncwarp();
+    }
+    blocks += u.blk1 - u.blk0;
+  }
+};
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;

@@ -401,7 +401,7 @@ cudaError_t launch_chunk_wide(const ChunkParams& p, int k_sub, int k_bits, int v
                               cudaStream_t stream);
 cudaError_t launch_tree_wide(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid,
                              cudaStream_t stream);
-// The same with 16, 32 or 64 rows.
+// The same with 16 or 32 rows.
 cudaError_t launch_tree(const ChunkParams& p, int k_sub, int k_bits, int v_sub, int v_bits, int grid, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int workers, cudaStream_t stream);
 constexpr int kChunkMaxBatch = 1024;

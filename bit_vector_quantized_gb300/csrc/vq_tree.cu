@@ -4,7 +4,7 @@
 // those that its bits name.  Tens of rows, and every code of the context to expand for them: what costs is not the
 // products but the way of the centroids through shared memory.  So the products stand the other way round than in
 // vq_chunk_wide.cu, the tokens as rows of the scores and the dims as rows of the output, N query rows as columns:
-//   S^T [128 tokens x N] = K~ Q~^T,  P^T = 2^(S^T - m),  O^T [128 dims x N] += V^T P^T  (N = 16, 32 or 64).
+//   S^T [128 tokens x N] = K~ Q~^T,  P^T = 2^(S^T - m),  O^T [128 dims x N] += V^T P^T  (N = 16 or 32).
 //
 //   * K~ goes from the gathers straight into tensor memory (a thread's token is a lane), V as 16-byte pieces into
 //     swizzled shared memory (rows of dims, the token as k), so of a block of 128 tokens 96 KB are gathered and stored
@@ -26,45 +26,39 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
 constexpr float kUnset = 1e30f;      // minus the maximum of a row that has seen nothing
 constexpr int kBlockTok = 128;       // tokens of a block
-constexpr int kSoftWarps = 8, kCodeWarps = 16;
-constexpr int kTreeThreads = (kSoftWarps + kCodeWarps + 4) * 32;
-// Registers per thread: 72 at the launch (896 threads), then 256 soft + 512 code + 128 issue = 896 x 72.
-constexpr int kSoftRegs = 104, kCodeRegs = 64, kIssueRegs = 40;
-static_assert(8 * kSoftRegs + 16 * kCodeRegs + 4 * kIssueRegs <= 28 * 72, "the block's registers at the launch");
-constexpr uint32_t kColS = 0, kColO = 128, kColK = 192, kCols = 512;  // S twice, O, K~ three times
-constexpr uint32_t kKStages = 3;
+constexpr int kCodeWarps = 16;
+constexpr uint32_t kKStages = 4;
+
+// A softmax thread takes one token and 16 rows.
+constexpr int kColumns = 16;
+template <int N>
+struct TreeShape {
+  static constexpr int kSoftWarps = 4 * (N / kColumns), kThreads = (kSoftWarps + kCodeWarps + 4) * 32;
+  // Registers per thread: 80 at the launch of 768 threads, 72 of 896, then their shares
+  static constexpr int kLaunch = N == 16 ? 80 : 72, kSoft = N == 16 ? 128 : 80, kCode = 72, kIssue = N == 16 ? 56 : 40;
+  static_assert(kSoftWarps * kSoft + kCodeWarps * kCode + 4 * kIssue <= (kThreads / 32) * kLaunch, "the block's registers at the launch");
+  // Tensor memory: S of high and low parts, twice; O; K~ of blocks under way.
+  static constexpr uint32_t kColS = 0, kColO = 4 * N, kCols = 512, kColK = kCols - 64 * kKStages;
+  static_assert(kColO + N <= kColK, "columns");
+};
 constexpr int kMasks = 4;            // token masks in flight (vq_chunk_wide.cu has why four are enough)
 
 template <int DK, int BK, int DV, int BV, int N>
 struct TreeSmem {
   using Table = WideTable<DK, BV>;
-  static constexpr int kVTile = kBlockTok * kHeadDim * 2, kPTile = kBlockTok * 128;  // (P: 64 rows' places whatever N)
-  static constexpr int kQTile = N * kHeadDim * 2;                                    // high parts; as much for the low
-  static constexpr int kVStages = Table::kWideCodes ? 1 : 2;
+  static constexpr int kVTile = kBlockTok * kHeadDim * 2, kVStages = 2;
+  static constexpr int kPTile = kBlockTok * 128;       // P of two blocks: rows of tokens of 128 bytes, a block's in either half
+  static constexpr int kQTile = 2 * N * kHeadDim * 2;  // rows of high parts, then of low parts
   static constexpr int kV = Table::kBytes;
   static constexpr int kP = kV + kVStages * kVTile;
-  static constexpr int kQ = kP + 2 * kPTile;
-  static constexpr int kMisc = kQ + 2 * kQTile;
+  static constexpr int kQ = kP + kPTile;
+  static constexpr int kMisc = kQ + kQTile;
   static constexpr int kBars = 32 * 8 + kPieces * 64 + kMasks * 16 + 16;
   static constexpr int kTops = kMisc + kBars;  // [N] minus the maxima, [N] scales, [4][N] maxima or sums of the warps
   static constexpr int kTotal = kTops + 6 * N * 4;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
-  static_assert((kChunkMaxBatch + 1 + 33) * 8 <= kVTile, "the plan shares a tile");
+  static_assert((kChunkMaxBatch + 1) * 8 <= kVTile, "the plan shares a tile");
 };
-
-// Columns of the warp's 32 lanes, one lane per thread.
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[C]) {
-  if constexpr (C == 8) tmem_ld8(addr, r);
-  else if constexpr (C == 16) tmem_ld16(addr, r);
-  else tmem_ld32(addr, r);
-}
-template <int C>
-__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[C]) {
-  if constexpr (C == 8) tmem_st8(addr, r);
-  else if constexpr (C == 16) tmem_st16(addr, r);
-  else tmem_st32(addr, r);
-}
 
 __device__ __forceinline__ float warp_max(float x) {  // (numbers before NaN)
   float y;
@@ -73,9 +67,11 @@ __device__ __forceinline__ float warp_max(float x) {  // (numbers before NaN)
 }
 
 template <int DK, int BK, int DV, int BV, int N>
-__global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(const ChunkParams p) {
   using W = TreeSmem<DK, BK, DV, BV, N>;
-  constexpr int NV = W::kVStages, NC = N / 2;  // columns of a softmax thread
+  using Shape = TreeShape<N>;
+  constexpr int NV = W::kVStages, NC = kColumns, kSoftWarps = Shape::kSoftWarps;
+  constexpr uint32_t kColS = Shape::kColS, kColO = Shape::kColO, kColK = Shape::kColK, kCols = Shape::kCols;
   constexpr int KROW = ((kHeadDim / DK) * BK + 31) / 32 * 4, VROW = ((kHeadDim / DV) * BV + 31) / 32 * 4;
   constexpr bool kWideCodes = W::Table::kWideCodes, kSplitTable = W::Table::kSplitTable;
   uint8_t* const tiles = g_smem + W::kV;
@@ -83,7 +79,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
   uint64_t* const ready = bars;            // [4] by block b: P of b, the V tile of b, the K tile of b + 2
   uint64_t* const start = ready + 4;       // K tiles of blocks 0 and 1
   uint64_t* const k_empty = start + 1;     // [kKStages] scores done, the tile is free
-  uint64_t* const v_empty = k_empty + 3;   // [2]
+  uint64_t* const v_empty = k_empty + 4;   // [2]
   uint64_t* const s_full = v_empty + 2;    // [4] by block: the scores are done, the tokens' masks are there
   uint64_t* const o_full = s_full + 4;     // [2] values of a piece's last block but one, and of its last
   uint64_t* const q_full = o_full + 2;     // Q~ stored, O read
@@ -94,6 +90,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
   uint32_t* const masks = reinterpret_cast<uint32_t*>(pieces + kPieces);              // [kMasks][4] tokens that have a page
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
+  volatile uint32_t* const done = tmem_at + 2;  // blocks whose values are under way
   float* const neg_max = reinterpret_cast<float*>(g_smem + W::kTops);  // [N]
   float* const scales = neg_max + N;                                   // [N]
   float* const tops = scales + N;                                      // [4][N]
@@ -105,13 +102,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
     if (tid == 0) write_record(p, worker, nullptr);
     return;
   }
-  fill_wide_table<DK, BK, DV, BV>(p);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(ready + i, kSoftWarps + kCodeWarps);
+      mbar_init(ready + i, kSoftWarps + 4 + 4);
       mbar_init(s_full + i, 1 + 4);
     }
-    mbar_init(start, kCodeWarps);  // (the K warps, for two blocks each)
+    mbar_init(start, 8);
     for (uint32_t i = 0; i < kKStages; ++i) mbar_init(k_empty + i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(v_empty + i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(o_full + i, 1);
@@ -119,15 +115,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
     mbar_init(drain, 1);
     for (int i = 0; i < static_cast<int>(kPieces); ++i) {
       mbar_init(piece_full + i, 1);
-      mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 1);
+      mbar_init(piece_empty + i, kSoftWarps + kCodeWarps + 2);
     }
     mbar_init_fence();
     *abort_flag = 0;
+    *done = 0;
   }
   if (warp == kSoftWarps + kCodeWarps) tmem_alloc<false>(tmem_at, kCols);
-  long long* const pre = reinterpret_cast<long long*>(tiles);  // the plan, before the first tile is written
   tc_fence_before();
-  chunk_plan<true>(p, pre, pre + kChunkMaxBatch + 1);
+  __syncthreads();
   tc_fence_after();
   // All 512 columns are this CTA's, so they start at column 0; the constant keeps the products' operands uniform.
   constexpr uint32_t tmem = 0;
@@ -137,6 +133,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
     __syncthreads();
     if (warp == kSoftWarps + kCodeWarps) tmem_free<false>(*tmem_at, kCols);
     return;
+  }
+
+  // The planning warp plans while the others fill the table.
+  if (warp != kSoftWarps + kCodeWarps + 1) {
+    fill_wide_table<DK, BK, DV, BV>(p, warp > kSoftWarps + kCodeWarps + 1 ? tid - 32 : tid, Shape::kThreads - 32);
+    asm volatile("bar.sync 6, %0;" ::"n"(Shape::kThreads - 32) : "memory");
   }
 
   // Bounded wait, uniform over the warp; on a timeout the CTA is given up.
@@ -161,8 +163,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
   WidePiece u = {};
 
   if (warp < kSoftWarps) {
-    // ====== a thread per token and half of the rows: columns NC g .. NC g + NC - 1 ======================
-    reg_inc<kSoftRegs>();
+    // ====== a thread per token, and all rows or half of them: columns NC g .. NC g + NC - 1 ==============
+    reg_inc<Shape::kSoft>();
     const int quarter = warp & 3, g = warp >> 2, G = p.group, tok = 32 * quarter + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t inv_g = 65536u / G + 1u;  // r / G = r * inv_g >> 16 for r < 128
@@ -206,9 +208,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
         uint2 vh, vl;
         split_pair(x[0] * p.qscale, x[1] * p.qscale, vh.x, vl.x);
         split_pair(x[2] * p.qscale, x[3] * p.qscale, vh.y, vl.y);
-        uint8_t* const at = qs + (lane >> 4) * (N * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+        uint8_t* const at = qs + (lane >> 4) * (2 * N * 128) + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
         *reinterpret_cast<uint2*>(at) = vh;
-        *reinterpret_cast<uint2*>(at + W::kQTile) = vl;
+        *reinterpret_cast<uint2*>(at + N * 128) = vl;  // (N is a multiple of eight)
       }
       if (tid < N) neg_max[tid] = kUnset;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -223,16 +225,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
       const int nblk = u.blk1 - u.blk0, ctx = u.first_pos + 1;
       for (int j = 0; j < nblk; ++j) {
         ok = ok && wait(s_full + (blocks & 3u), (blocks >> 2) & 1u);
-        const uint32_t col_s = tmem + lanes + kColS + N * (blocks & 1u) + NC * g;
+        const uint32_t col_s = tmem + lanes + kColS + 2 * N * (blocks & 1u) + NC * g;
         uint32_t s[NC];
         // a token's scores, minus infinity where a row does not see it
         auto scores = [&]() {
-          tmem_ld<NC>(col_s, s);
+          uint32_t low[NC];
+          tmem_ld16(col_s, s);
+          tmem_ld16(col_s + N, low);
           const int t0 = u.block(u.blk0 + j) * kBlockTok, t = t0 + tok;
           const uint4 seen = *reinterpret_cast<const uint4*>(masks + (blocks % kMasks) * 4);
           const bool whole = t0 + kBlockTok <= ctx && (p.window == 0 || t0 > u.last_pos - p.window || t0 + kBlockTok <= p.sinks) &&
                              (seen.x & seen.y & seen.z & seen.w) == kAll;
           tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            float x0 = __uint_as_float(s[c]), x1 = __uint_as_float(s[c + 1]);
+            add2(x0, x1, __uint_as_float(low[c]), __uint_as_float(low[c + 1]));
+            s[c] = __float_as_uint(x0), s[c + 1] = __float_as_uint(x1);
+          }
           if (whole) return;
           const uint32_t here = quarter == 0 ? seen.x : quarter == 1 ? seen.y : quarter == 2 ? seen.z : seen.w;
           const bool there = here >> lane & 1u;
@@ -300,16 +310,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
               ok = j + 1 < nblk ? wait(s_full + ((blocks + 1) & 3u), ((blocks + 1) >> 2) & 1u) : wait(o_full, ends0 & 1u);
               if (ok) {
                 tc_fence_after();
-                constexpr int kHalf = NC < 16 ? NC : 16;
+                uint32_t o[NC];
+                tmem_ld16(tmem + lanes + kColO + NC * g, o);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c0 = 0; c0 < NC; c0 += kHalf) {
-                  uint32_t o[kHalf];
-                  tmem_ld<kHalf>(tmem + lanes + kColO + NC * g + c0, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int c = 0; c < kHalf; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * scales[NC * g + c0 + c]);
-                  tmem_st<kHalf>(tmem + lanes + kColO + NC * g + c0, o);
-                }
+                for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * scales[NC * g + c]);
+                tmem_st16(tmem + lanes + kColO + NC * g, o);
                 tmem_wait_st();
               }
             }
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
         if (ok) {
           // p and its sums; P^T as rows of tokens.  (The scores of this block came after the values of the one before
           // the last, so its place in shared memory is free.)
-          const uint32_t row = smem_addr(ps) + (blocks & 1u) * W::kPTile + tok * 128;
+          const uint32_t row = smem_addr(ps) + tok * 128;
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 8) {
             uint32_t w[4];
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
               const __half2 h = __floats2half2_rn(x0, x1);
               w[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            const uint32_t piece = (NC * g + c0) / 8;
+            const uint32_t piece = (NC * g + c0) / 8 + 4 * (blocks & 1u);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((piece ^ (tok & 7)) << 4)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                          : "memory");
           }
@@ -355,178 +361,167 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
       for (int m = NC; m < 32; m <<= 1) l[0] += __shfl_xor_sync(kAll, l[0], m);
       if (lane < NC) tops[quarter * N + NC * g + lane] = l[0];
       half_sync();
+      if (quarter == 0 && lane < NC) {
+        const int r = NC * g + lane;
+        const float sum = (tops[r] + tops[N + r]) + (tops[2 * N + r] + tops[3 * N + r]);
+        scales[r] = sum == 0.f ? 0.f : 1.f / sum;
+        if (u.slot >= 0 && r < u.rows)
+          p.ws_ml[static_cast<long long>(u.slot) * N + r] = make_float2(neg_max[r] == kUnset ? -INFINITY : -neg_max[r], sum);
+      }
+      half_sync();
       if (ok) {
         tc_fence_after();
         const int dim = tok;  // lanes are dims now
-        constexpr int kHalf = NC < 16 ? NC : 16;
+        uint32_t o[NC];
+        tmem_ld16(tmem + lanes + kColO + NC * g, o);
+        tmem_wait_ld();
 #pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += kHalf) {
-          uint32_t o[kHalf];
-          tmem_ld<kHalf>(tmem + lanes + kColO + NC * g + c0, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < kHalf; ++c) {
-            const int r = NC * g + c0 + c;
-            if (r >= u.rows) continue;
-            const float sum = (tops[r] + tops[N + r]) + (tops[2 * N + r] + tops[3 * N + r]);
-            if (u.slot >= 0) {
-              const long long at = static_cast<long long>(u.slot) * N + r;
-              p.ws_o[at * kHeadDim + dim] = __uint_as_float(o[c]);
-              if (dim == 0) p.ws_ml[at] = make_float2(neg_max[r] == kUnset ? -INFINITY : -neg_max[r], sum);
-            } else {
-              const int token = static_cast<int>(r * inv_g >> 16);
-              const long long row = static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (r - token * G);
-              static_cast<__half*>(p.out)[row * kHeadDim + dim] = __float2half_rn(__uint_as_float(o[c]) * (sum == 0.f ? 0.f : 1.f / sum));
-            }
+        for (int c = 0; c < NC; ++c) {
+          const int r = NC * g + c;
+          if (r >= u.rows) continue;
+          if (u.slot >= 0) {
+            p.ws_o[(static_cast<long long>(u.slot) * N + r) * kHeadDim + dim] = __uint_as_float(o[c]);
+          } else {
+            const int token = static_cast<int>(r * inv_g >> 16);
+            const long long row = static_cast<long long>(u.row0 + token) * p.hq + u.kvh * G + (r - token * G);
+            static_cast<__half*>(p.out)[row * kHeadDim + dim] = __float2half_rn(__uint_as_float(o[c]) * scales[r]);
           }
         }
       }
     }
   } else if (warp < kSoftWarps + kCodeWarps) {
     // ================================= code warps ======================================
-    reg_dec<kCodeRegs>();
-    // The first eight expand K, the others V, each at its own pace; a thread takes 64 dims of a token.  K: a warp's
-    // tokens are the lanes of tensor memory that it may write.
-    auto expand = [&](auto codes, auto row_bytes, const uint8_t* pool, int tok, int part, uint32_t table, uint32_t stages, uint64_t* empty,
-                      auto is_k, bool masking) {
+    reg_dec<Shape::kCode>();
+    // Eight expand K, eight V, four of them every other block; a thread takes one token's 128 dims.  K: a warp's tokens
+    // are the lanes of tensor memory that it may write.  (A token that cannot be read gets what stands in the
+    // registers for codes: some centroids, whose scores are masked and whose p is 0.)
+    const int set = (warp >> 2) & 1, tok = 32 * (warp & 3) + lane;
+    auto expand = [&](auto codes, auto row_bytes, const uint8_t* pool, uint32_t table, auto is_k) {
       using Codes = decltype(codes);
       constexpr int kRow = decltype(row_bytes)::value;
       constexpr bool kIsK = decltype(is_k)::value;
       constexpr int kShift = kWideCodes ? 4 : kSplitTable ? 7 : 8;
-      // Block iterator, two blocks ahead of the tiles: the token's page; then its codes one ahead.  The page and the
-      // offset in it follow from the block before, by 128 tokens, where blocks adjoin; rows are counted by 16.
-      pool += (tok % 16) * kRow + Codes::first_byte(part);
-      const int per_page = p.page_size / 16, step_page = kBlockTok / p.page_size, step_off = kBlockTok / 16 - step_page * per_page;
+      constexpr uint32_t kStages = kIsK ? kKStages : NV;
+      uint64_t* const empty = kIsK ? k_empty : v_empty;
+      // The set's blocks: a block's page is looked up two ahead of it, its codes are asked for one ahead.
+      pool += (tok % 16) * kRow;
+      const int per_page = p.page_size / 16;
       bool more = true;
-      int i = 0, t = 0, lp = 0, off = 0;
+      int i = set;
       const int32_t* pages = nullptr;
       u.blk1 = 0;
-      u.sink = -1;
       struct Where {
         int page, off, kvh;
         bool in, any;  // the token exists; the block exists
       };
       auto advance = [&]() {
         Where x = {0, 0, 0, false, false};
-        bool jump = i == u.sink;
         while (more && i >= u.blk1) {
+          const int over = i - u.blk1;
           more = next_piece(u);
-          i = more ? u.blk0 : 0;
-          jump = true;
+          i = more ? u.blk0 + over : 0;
           pages = p.page_table + static_cast<long long>(u.b) * p.max_pages;
         }
         if (!more) return x;
-        if (jump) {
-          t = u.block(i) * kBlockTok + tok;
-          lp = t / p.page_size;
-          off = (t - lp * p.page_size) / 16;
-        } else {
-          t += kBlockTok;
-          lp += step_page;
-          off += step_off;
-          if (off >= per_page) {
-            off -= per_page;
-            ++lp;
-          }
-        }
-        ++i;
+        const int t = u.block(i) * kBlockTok + tok, lp = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+        i += 2;
         x.any = true;
         x.in = t < u.limit;
         x.kvh = u.kvh;
-        x.off = off;
-        // (volatile like the codes' loads: it is to be under way an iteration before its use)
+        x.off = (t - lp * p.page_size) / 16;
+        // (volatile like the codes' loads: it is to be under way before its use)
         if (x.in) asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(x.page) : "l"(pages + lp));
         return x;
       };
-      bool has = false, has_next = false;  // the token can be read
-      Codes now, next;
-      auto fetch = [&](const Where& x, Codes& y) {
+      Codes now;
+      auto fetch = [&](const Where& x) {  // whether the token can be read
         const bool good = x.in && static_cast<unsigned long long>(x.page) < static_cast<unsigned long long>(p.num_pages);
         if (good) {
           const uint32_t row16 = static_cast<uint32_t>(x.page * p.hkv + x.kvh) * per_page + x.off;
-          y.load(pool + static_cast<unsigned long long>(row16) * (16 * kRow));
+          now.load(pool + static_cast<unsigned long long>(row16) * (16 * kRow));
         } else if (x.in) {
           report(p.status, kDevBadPage);
         }
         return good;
       };
-      const uint32_t v_at = smem_addr(tiles) + part * (kBlockTok * 128) + tok * 128 + ((tok & 7) << 4);
-      const uint32_t k_at = tmem + (static_cast<uint32_t>(tok & 96) << 16) + kColK + 32 * part;
+      const uint32_t v_at = smem_addr(tiles) + tok * 128 + ((tok & 7) << 4);
+      const uint32_t k_at = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColK;
       const Where first = advance();
       Where ahead = advance();
-      bool any = first.any;
-      if (any) has = fetch(first, now);
-      Ring ring;
-      uint32_t blocks = 0;
+      bool any = first.any, has = any && fetch(first);
+      uint32_t blk = set, stage = set, phase = 1;
+      auto next_stage = [&]() {
+        blk += 2;
+        stage += 2;
+        if (stage >= kStages) {
+          stage -= kStages;
+          phase ^= 1u;
+        }
+      };
+      auto arrive = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(!kIsK ? ready + (blk & 3u) : blk < 2 ? start : ready + ((blk - 2) & 3u));
+      };
       while (any) {
-        const Where then = ahead;
-        ahead = advance();
-        has_next = then.any && fetch(then, next);
-        if (masking) {  // the tokens of the block that can be read
+        if constexpr (!kIsK) {  // the tokens of the block that can be read
           const uint32_t seen = __ballot_sync(kAll, has);
           if (lane == 0) {
-            masks[(blocks % kMasks) * 4 + tok / 32] = seen;
-            mbar_arrive(s_full + (blocks & 3u));
+            masks[(blk % kMasks) * 4 + (warp & 3)] = seen;
+            mbar_arrive(s_full + (blk & 3u));
           }
         }
-        if (!wait(empty + ring.slot, ring.phase ^ 1u)) break;
-        now.align(part);
+        if (!wait(empty + stage, phase)) break;
+        now.align(0);
         if constexpr (kIsK) {
           tc_fence_after();
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int c0 = 0; c0 < 16; c0 += 4) {
             uint32_t w[16];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 v = has ? gather_piece<Codes, kShift>(now, 4 * half + c, table) : make_uint4(0, 0, 0, 0);
+              const uint4 v = gather_piece<Codes, kShift>(now, c0 + c, table);
               w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
             }
-            __syncwarp();
-            tmem_st16(k_at + 64 * ring.slot + 16 * half, w);
+            tmem_st16(k_at + 64 * stage + 4 * c0, w);
           }
+        } else {
+          const uint32_t at = v_at + stage * W::kVTile;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint4 v = gather_piece<Codes, kShift>(now, c, table);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"((at ^ ((c & 7) << 4)) + (c >> 3) * (kBlockTok * 128)), "r"(v.x), "r"(v.y), "r"(v.z),
+                         "r"(v.w)
+                         : "memory");
+          }
+        }
+        const Where then = ahead;
+        any = then.any;
+        has = any && fetch(then);
+        ahead = advance();
+        if constexpr (kIsK) {
           tmem_wait_st();
           tc_fence_before();
         } else {
-          const uint32_t at = v_at + ring.slot * W::kVTile;
-#pragma unroll
-          for (int c = 0; c < Codes::kPieces; ++c) {
-            const uint4 v = has ? gather_piece<Codes, kShift>(now, c, table) : make_uint4(0, 0, 0, 0);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(!kIsK ? ready + (blocks & 3u) : blocks < 2 ? start : ready + ((blocks - 2) & 3u));
-        ring.next(stages);
-        ++blocks;
-        now = next;
-        has = has_next;
-        any = then.any;
+        arrive();
+        next_stage();
       }
-      // The last two blocks have no K tile to wait for; its arrivals come in their turn all the same (unless the CTA
-      // was given up).
-      if (kIsK && !any) {
-        for (uint32_t end = blocks + 2; blocks < end; ++blocks) {
-          if (!wait(empty + ring.slot, ring.phase ^ 1u)) break;
-          if (lane == 0) mbar_arrive(blocks < 2 ? start : ready + ((blocks - 2) & 3u));
-          ring.next(stages);
-        }
-      }
+      // The last two blocks have no K tile to wait for; its arrivals come in their turn all the same, one of either set
+      // (unless the CTA was given up).
+      if (kIsK && !any && wait(empty + stage, phase)) arrive();
     };
-    const int tok = 32 * (warp & 3) + lane, part = (warp >> 2) & 1;
     const uint32_t rep_k = DK == 4 ? (lane & 15) * 8 : lane * 4, rep_v = DV == 4 ? (lane & 15) * 8 : lane * 4;
     if (warp < kSoftWarps + kCodeWarps / 2)
-      expand(PartCodes<DK, BK, 64>{}, std::integral_constant<int, KROW>{}, p.k_pool, tok, part, kWideCodes ? 0u : rep_k, kKStages, k_empty,
-             std::true_type{}, false);
+      expand(PartCodes<DK, BK, kHeadDim>{}, std::integral_constant<int, KROW>{}, p.k_pool, kWideCodes ? 0u : rep_k, std::true_type{});
     else
-      expand(PartCodes<DV, BV, 64>{}, std::integral_constant<int, VROW>{}, p.v_pool, tok, part,
-             kWideCodes ? 65536u : (kSplitTable ? 32768u : 128u) + rep_v, NV, v_empty, std::false_type{}, part == 0);
+      expand(PartCodes<DV, BV, kHeadDim>{}, std::integral_constant<int, VROW>{}, p.v_pool,
+             kWideCodes ? 65536u : (kSplitTable ? 32768u : 128u) + rep_v, std::false_type{});
   } else {
     // ================================= the products ====================================
-    reg_dec<kIssueRegs>();
+    reg_dec<Shape::kIssue>();
     if (warp == kSoftWarps + kCodeWarps) {
-      constexpr uint32_t kScores = tc_idesc(kBlockTok, N, false), kValues = tc_idesc_rows_k(kHeadDim, N);
+      constexpr uint32_t kScores = tc_idesc(kBlockTok, 2 * N, false), kValues = tc_idesc_rows_k(kHeadDim, N);
       const uint32_t v0 = smem_addr(tiles), q0 = smem_addr(g_smem + W::kQ), p0 = smem_addr(g_smem + W::kP);
       Ring rk, rv;
       uint32_t blocks = 0, tiles_done = 0;
@@ -537,11 +532,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
         auto scores = [&](uint32_t blk) {  // of block blk, whose K tile is there
           if (elect_one()) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)  // high and low part of q~
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc_mma_ts<false>(tmem + kColS + N * (blk & 1u), tmem + kColK + 64 * rk.slot + 8 * ks,
-                                 tc_desc(q0 + part * W::kQTile + (ks >> 2) * (N * 128) + (ks & 3) * 32, 16), kScores, part > 0 || ks > 0);
+            for (int ks = 0; ks < 8; ++ks)  // columns: the rows' high parts, then their low parts
+              tc_mma_ts<false>(tmem + kColS + 2 * N * (blk & 1u), tmem + kColK + 64 * rk.slot + 8 * ks,
+                               tc_desc(q0 + (ks >> 2) * (2 * N * 128) + (ks & 3) * 32, 16), kScores, ks > 0);
             tc_commit<false>(s_full + (blk & 3u));
             tc_commit<false>(k_empty + rk.slot);
           }
@@ -559,7 +552,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vt = v0 + rv.slot * W::kVTile, pt = p0 + (blk & 1u) * W::kPTile;
+            const uint32_t vt = v0 + rv.slot * W::kVTile, pt = p0 + (blk & 1u) * 64;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               tc_mma_ss(tmem + kColO, tc_desc(vt + ks * 2048, kBlockTok * 128), tc_desc(pt + ks * 2048, kBlockTok * 128), kValues,
@@ -569,6 +562,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
           }
           __syncwarp();
           rv.next(NV);
+          if (lane == 0) *done = blk;
           if (j + 2 < nblk) scores(blk + 2);
         }
         blocks += nblk;
@@ -581,8 +575,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
       }
     } else if (warp == kSoftWarps + kCodeWarps + 1) {
       // ================================== planning =======================================
+      long long* const pre = reinterpret_cast<long long*>(tiles);  // the plan: the tiles over it wait for the first piece
+      tree_plan(p, pre);
       ChunkWalk<kBlockTok, true> walk;
-      walk.start(p, pre, worker, gridDim.x);  // (the tiles over the plan wait for the first piece)
+      walk.start(p, pre, worker, gridDim.x);
       ChunkPiece q;
       Ring ro;
       bool recorded = false;
@@ -605,6 +601,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
             }
           }
           continue;
+        }
+        if (more) {  // the query rows, for the softmax warps a piece later
+          const char* rows = reinterpret_cast<const char*>(static_cast<const __half*>(p.q) +
+                                                           (static_cast<long long>(q.s.row0 + i0) * p.hq + q.kvh * p.group) * kHeadDim);
+          const int lines = 2 * p.group;  // a token's rows, 128 bytes each line
+          for (int i = lane; i < n * lines; i += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + static_cast<long long>(i / lines) * p.hq * (kHeadDim * 2) + (i % lines) * 128));
         }
         int last = 0;  // of the rows, the furthest position
         if (more && p.window > 0) {
@@ -637,6 +640,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) vq_tree_kernel(const ChunkPar
         ro.next(kPieces);
       }
       if (!recorded && lane == 0) write_record(p, worker, nullptr);
+    } else if (warp == kSoftWarps + kCodeWarps + 2) {
+      CodePrefetch prefetch;
+      while (next_piece(u)) prefetch.piece(p, u, KROW, VROW, 0, 16, done, abort_flag);
     }
   }
   tc_fence_before();
@@ -655,14 +661,12 @@ cudaError_t launch_rows(const ChunkParams& p, int grid, cudaStream_t stream) {
   constexpr size_t smem = TreeSmem<DK, BK, DV, BV, N>::kTotal;
   cudaError_t e = ensure_smem(kern, smem, opt);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kTreeThreads), smem, stream, p, false);
+  return launch_pdl(kern, dim3(grid), dim3(TreeShape<N>::kThreads), smem, stream, p, false);
 }
 
 template <int DK, int BK, int DV, int BV>
 cudaError_t launch_format(const ChunkParams& p, int grid, cudaStream_t stream) {
-  return p.tile_rows == 16   ? launch_rows<DK, BK, DV, BV, 16>(p, grid, stream)
-         : p.tile_rows == 32 ? launch_rows<DK, BK, DV, BV, 32>(p, grid, stream)
-                             : launch_rows<DK, BK, DV, BV, 64>(p, grid, stream);
+  return p.tile_rows == 16 ? launch_rows<DK, BK, DV, BV, 16>(p, grid, stream) : launch_rows<DK, BK, DV, BV, 32>(p, grid, stream);
 }
 
 }  // namespace
