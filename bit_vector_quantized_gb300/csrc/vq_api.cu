@@ -1161,7 +1161,9 @@ int tree_tile_rows(const vq_layout& L, int max_new_len) {
     for (int rows : {16, 32, 128, 256})
       if (std::atoi(env) == rows) return rows;
   const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
-  return rows <= 16 ? 16 : rows <= 64 ? 32 : rows <= 128 ? 128 : 256;
+  const int per_tile = 128 / (L.num_q_heads / L.num_kv_heads);  // tokens of 128 rows
+  const bool three = max_new_len > 2 * per_tile && max_new_len <= 3 * per_tile && L.k_bits != 12;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || three ? 128 : 256;
 }
 
 struct TreeArgs {
@@ -1323,10 +1325,10 @@ size_t vq_tree_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t n
     return 0;
   const int sms = num_sms > 0 ? num_sms : device_sms();
   if (sms <= 0) return 0;
-  size_t most = 0;  // a call with smaller bounds may take a smaller tile
+  size_t most = 0;  // a call with smaller bounds may take another tile (of 128 rows also 256)
   const int need = tree_tile_rows(*layout, max_new_len);
   for (int rows : {16, 32, 128, 256})
-    if (rows <= need) most = std::max(most, chunk_ws(rows, std::max(sms, 2)).total);
+    if (rows <= need || need == 128) most = std::max(most, chunk_ws(rows, std::max(sms, 2)).total);
   return most;
 }
 
