@@ -20,6 +20,10 @@
 //   3. all centroids by fp32 distances (one warp), equal centroids counting as one;
 //   4. everything in 64 bits, for keys from the rows on (one warp).
 #include "vq_rotary.cuh"
+#include "vq_tcgen05.cuh"
+
+#include <algorithm>
+#include <cstdlib>
 
 namespace vqk {
 namespace {
@@ -109,22 +113,25 @@ __device__ __forceinline__ int exact_code(const AppendParams& p, int which, int 
   return at;
 }
 
-// A vector's codes into its row of the pool (one warp): lane w makes words w, w + 32, .. of the row.
-__device__ __forceinline__ void store_codes(const AppendParams& p, int which, const uint16_t* codes, long long slot, int h, int lane) {
-  const int bits = p.bits[which], count = kHeadDim / p.sub[which], words = p.row_bytes[which] / 4;
+// Codes first .. first + count - 1 of a vector into its row of the pool (one warp), a word a lane; the words that they
+// fill are theirs alone.
+__device__ __forceinline__ void store_codes(const AppendParams& p, int which, const uint16_t* codes, int first, int count, long long slot, int h,
+                                            int lane) {
+  const int bits = p.bits[which], words = count * bits / 32;  // (whole words in every format)
   const unsigned P = p.page_size;
   const long long page = slot >> 32 ? slot / P : static_cast<unsigned>(slot) / P, off = slot - page * P;
-  uint32_t* const row = reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * P + off) * p.row_bytes[which]);
+  uint32_t* const row =
+      reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * P + off) * p.row_bytes[which]) + first * bits / 32;
   for (int w = lane; w < words; w += 32) {
     uint32_t x = 0;
     if (bits == 8) {  // four codes a word
       const uint2 c = *reinterpret_cast<const uint2*>(codes + 4 * w);
-      row[w] = __byte_perm(c.x, c.y, 0x6420);
-      continue;
-    }
-    for (int i = 32 * w / bits; i < count && i * bits < 32 * w + 32; ++i) {
-      const int at = i * bits - 32 * w;
-      x |= at >= 0 ? static_cast<uint32_t>(codes[i]) << at : static_cast<uint32_t>(codes[i]) >> -at;
+      x = __byte_perm(c.x, c.y, 0x6420);
+    } else {
+      for (int i = 32 * w / bits; i < count && i * bits < 32 * w + 32; ++i) {
+        const int at = i * bits - 32 * w;
+        x |= at >= 0 ? static_cast<uint32_t>(codes[i]) << at : static_cast<uint32_t>(codes[i]) >> -at;
+      }
     }
     row[w] = x;
   }
@@ -542,9 +549,19 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
     __syncwarp();
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (slot[v] >= 0) store_codes(p, which, codes + v * kSubs, slot[v], head[v], lane);
+      if (slot[v] >= 0) store_codes(p, which, codes + v * kSubs, 0, kSubs, slot[v], head[v], lane);
     __syncwarp();
   }
+}
+
+// The CTAs from `first` on turn queries.
+__device__ __forceinline__ void append_queries(const AppendParams& p, int first) {
+  const long long b = static_cast<long long>(blockIdx.x) - first, shares = (p.q.heads[0] + p.q.heads_per_y - 1) / p.q.heads_per_y;
+  if (threadIdx.x >= kAppThreads) return;
+  const bool whole = p.interleaved || p.rotary_dim % 16 == 0;
+  const int y = static_cast<int>(b % shares);
+  if (p.bf16) whole ? rotary_share<true, true>(p.q, b / shares, y) : rotary_share<true, false>(p.q, b / shares, y);
+  else whole ? rotary_share<false, true>(p.q, b / shares, y) : rotary_share<false, false>(p.q, b / shares, y);
 }
 
 __global__ void __launch_bounds__(kAppThreadsMost, 1) vq_append_kernel(const __grid_constant__ AppendParams p) {
@@ -552,12 +569,7 @@ __global__ void __launch_bounds__(kAppThreadsMost, 1) vq_append_kernel(const __g
   __shared__ int top;  // the largest ||c||^2
   const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
   if (static_cast<int>(blockIdx.x) >= ctas) {  // queries
-    const long long b = static_cast<long long>(blockIdx.x) - ctas, shares = (p.q.heads[0] + p.q.heads_per_y - 1) / p.q.heads_per_y;
-    if (threadIdx.x >= kAppThreads) return;
-    const bool whole = p.interleaved || p.rotary_dim % 16 == 0;
-    const int y = static_cast<int>(b % shares);
-    if (p.bf16) whole ? rotary_share<true, true>(p.q, b / shares, y) : rotary_share<true, false>(p.q, b / shares, y);
-    else whole ? rotary_share<false, true>(p.q, b / shares, y) : rotary_share<false, false>(p.q, b / shares, y);
+    append_queries(p, ctas);
     return;
   }
   const int which = static_cast<int>(blockIdx.x) >= ctas0, cta = static_cast<int>(blockIdx.x) - which * ctas0;
@@ -573,11 +585,276 @@ __global__ void __launch_bounds__(kAppThreadsMost, 1) vq_append_kernel(const __g
   }
 }
 
+// ---- 8- and 9-bit codes: the products on the tensor cores ----------------------------------------------------------
+// A team of four warps takes 128 sub-vectors at a time, a lane one of them (sub-vectors of 2: a vector is two warps',
+// who both prepare it); two teams a CTA, two CTAs an SM, 128 columns of tensor memory a team.  Operands are rows of
+// 128 bytes, of which a product's k takes 32: (x high, x low | 1, 1, 1, 0 ..) against (-2 c, -2 c | ||c||^2 in three
+// parts), for sub-vectors of 2 all in one.
+constexpr int kTcThreads = 256, kTcChunk = 128, kTcGroup = 16;
+
+template <int D>
+__device__ __forceinline__ void fill_products(const __half* cb, int n, uint8_t* rows, float* tab, int* top) {
+  for (int j = threadIdx.x; j < n; j += kTcThreads) {
+    float c[D], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < D; ++e) {
+      c[e] = __half2float(__ldg(cb + j * D + e));
+      sum = fmaf(c[e], c[e], sum);
+      c[e] *= -2.f;
+    }
+#pragma unroll
+    for (int e = 0; e < D; ++e) tab[j * D + e] = c[e];
+    const uint32_t n1 = to_tf32(sum), n2 = to_tf32(sum - __uint_as_float(n1));
+    const uint32_t n3 = to_tf32(sum - __uint_as_float(n1) - __uint_as_float(n2));
+    auto piece = [&](int i) { return reinterpret_cast<uint4*>(rows + j * 128 + ((i ^ (j & 7)) << 4)); };
+    if constexpr (D == 2) {
+      const uint32_t c0 = __float_as_uint(c[0]), c1 = __float_as_uint(c[1]);
+      *piece(0) = make_uint4(c0, c1, c0, c1);
+      *piece(1) = make_uint4(n1, n2, n3, 0u);
+    } else {
+      const uint4 v = make_uint4(__float_as_uint(c[0]), __float_as_uint(c[1]), __float_as_uint(c[2]), __float_as_uint(c[3]));
+      *piece(0) = v;
+      *piece(1) = v;
+      *piece(2) = make_uint4(n1, n2, n3, 0u);
+      *piece(3) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    const int high = __reduce_max_sync(kAll, __float_as_int(sum));  // (not negative: ordered like their bits; n is a multiple of the threads)
+    if ((threadIdx.x & 31) == 0) atomicMax(top, high);
+  }
+}
+
+struct TcSmem {  // offsets from the 1024-aligned start
+  int rows[2], cb, tab, xs, codes, total;
+};
+__host__ __device__ inline TcSmem tc_smem(int d, int n) {
+  TcSmem s;
+  s.rows[0] = 0;
+  s.rows[1] = 128 * 128;
+  s.cb = 2 * 128 * 128;
+  s.tab = s.cb + n * 128;
+  s.xs = s.tab + n * d * 4;
+  s.codes = s.xs + (kTcThreads / 32) * kHeadDim * 4;
+  s.total = s.codes + (kTcThreads / 32) * 32 * 2;
+  return s;
+}
+
+template <int D>
+__device__ __forceinline__ void append_products(const AppendParams& p, int which, int cta, int ctas, uint8_t* smem, int* top, uint32_t tmem,
+                                                uint64_t* bars, volatile int* abort_flag) {
+  constexpr int kVectors = 128 * D / kHeadDim;  // of a team's tile
+  const int n = 1 << p.bits[which];
+  const TcSmem at = tc_smem(D, n);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp >> 2, w = warp & 3;
+  uint8_t* const rows = smem + at.rows[team];
+  float* const tab = reinterpret_cast<float*>(smem + at.tab);
+  float* const xs = reinterpret_cast<float*>(smem + at.xs) + warp * kHeadDim;
+  uint16_t* const codes = reinterpret_cast<uint16_t*>(smem + at.codes) + warp * 32;
+  uint64_t* const bar = bars + team;
+  const uint32_t cols = tmem + kTcChunk * team, mine = cols + (static_cast<uint32_t>(32 * w) << 16);
+  auto row_piece = [&](int row, int i) { return reinterpret_cast<uint4*>(rows + row * 128 + ((i ^ (row & 7)) << 4)); };
+  auto team_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + team) : "memory"); };
+  fill_products<D>(static_cast<const __half*>(p.cb[which]), n, smem + at.cb, tab, top);
+  {  // the ones that take the norms
+    const int row = 32 * w + lane;
+    const uint32_t one = __float_as_uint(1.f);
+    *row_piece(row, D == 2 ? 1 : 2) = make_uint4(one, one, one, 0u);
+    if constexpr (D == 4) *row_piece(row, 3) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  const float cmax2 = __int_as_float(*top);
+  const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv, tiles = (vectors + kVectors - 1) / kVectors;
+  const long long per = (tiles + 2LL * ctas - 1) / (2LL * ctas);
+  const long long tile0 = (2LL * cta + team) * per, tile1 = min(tile0 + per, tiles);
+  const int vec = D == 4 ? w : w >> 1, half = D == 4 ? 0 : w & 1;  // this warp's vector of the tile, and which half of its sub-vectors
+  long long v = tile0 * kVectors + vec;
+  int tok = static_cast<int>(v / p.hkv), head = static_cast<int>(v - static_cast<long long>(tok) * p.hkv);
+  uint32_t phase = 0;
+  Angles angles;
+
+  for (long long tile = tile0; tile < tile1; ++tile) {
+    // ---- the vector as it is coded; its rows of the operand --------------------------------------------------------
+    const long long slot = v < vectors ? append_slot(p, tok, lane == 0) : -1;
+    float raw[4] = {0.f, 0.f, 0.f, 0.f}, of_x = 0.f;
+    if (slot >= 0) {
+      const uint16_t* const src = static_cast<const uint16_t*>(p.src[which]) + tok * p.stride[which] + head * kHeadDim;
+      load_raw(p, src, 4 * lane, raw);
+      if (which == 0) {
+        turn_key(p, src, tok, head, lane, angles, raw);
+        float sum = fmaf(raw[0], raw[0], fmaf(raw[1], raw[1], fmaf(raw[2], raw[2], raw[3] * raw[3])));
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
+        of_x = 4.f * root(D * sum) * 5.9604645e-8f;  // (append_tensor has the reason)
+      }
+    }
+    *reinterpret_cast<float4*>(xs + 4 * lane) = make_float4(raw[0], raw[1], raw[2], raw[3]);
+    __syncwarp();
+    float x[D], x2 = 0.f;
+    uint32_t hi[D], lo[D];
+#pragma unroll
+    for (int e = 0; e < D; ++e) {
+      x[e] = D == 4 ? raw[e & 3] : xs[(32 * half + lane) * D + e];
+      x2 = fmaf(x[e], x[e], x2);
+      hi[e] = to_tf32(x[e]);
+      lo[e] = to_tf32(x[e] - __uint_as_float(hi[e]));
+    }
+    if constexpr (D == 2) {
+      *row_piece(32 * w + lane, 0) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+    } else {
+      *row_piece(32 * w + lane, 0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *row_piece(32 * w + lane, 1) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    // ---- scores of 128 centroids at a time; of 16 their minimum ------------------------------------------------------
+    float best = INFINITY, second = INFINITY;
+    int id = 0;
+    bool ok = true;
+    for (int c0 = 0; c0 < n; c0 += kTcChunk) {
+      tc_fence_before();
+      team_sync();  // the operand is there, the columns are read
+      tc_fence_after();
+      if (w == 0) {
+        if (lane == 0) {
+          const uint32_t a = smem_addr(rows), b = smem_addr(smem + at.cb) + c0 * 128;
+          tc_mma_tf32(cols, tc_desc(a, 16), tc_desc(b, 16), tc_idesc_tf32(128, kTcChunk), false);
+          if constexpr (D == 4) tc_mma_tf32(cols, tc_desc(a + 32, 16), tc_desc(b + 32, 16), tc_idesc_tf32(128, kTcChunk), true);
+          tc_commit<false>(bar);
+        }
+        __syncwarp();
+      }
+      ok = __all_sync(kAll, mbar_wait_bounded(bar, phase, abort_flag, p.timeout_ns)) && ok;
+      phase ^= 1u;
+      tc_fence_after();
+#pragma unroll 1
+      for (int g0 = 0; g0 < kTcChunk / kTcGroup; g0 += 2) {
+        const float m0 = tmem_min16(mine + kTcGroup * g0), m1 = tmem_min16(mine + kTcGroup * (g0 + 1));
+        tmem_wait_ld();
+        const float low[2] = {m0, m1};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          second = fminf(second, fmaxf(best, low[i]));
+          id = low[i] < best ? c0 + kTcGroup * (g0 + i) : id;
+          best = fminf(best, low[i]);
+        }
+      }
+    }
+    // ---- steps 1 and 2: a lane's group, each lane beginning elsewhere in it (banks) ----------------------------------
+    const float x1 = root(x2), reach = fmaf(1.01f, x1, root(fmaxf(best + x2, 0.f)));
+    const float c2 = fminf(reach * reach, cmax2);
+    const bool near = second <= best + 7.6293945e-6f * fmaf(2.f * x1, root(c2), c2);
+    float d0 = INFINITY, far = INFINITY;
+    int code = id;
+#pragma unroll 4
+    for (int i = 0; i < kTcGroup; ++i) {
+      const int j = id + ((i + lane) & (kTcGroup - 1));
+      float y[D];
+      load_centroid<D>(tab, j, y);
+      const float d = distance<D>(x, y);
+      far = fminf(far, fmaxf(d0, d));
+      code = d < d0 ? j : code;
+      d0 = fminf(d0, d);
+    }
+    const bool unsure = near || !(far > d0 + far * 1.9073486e-6f + of_x * root(far));
+    // ---- steps 3 and 4 ------------------------------------------------------------------------------------------------
+    uint32_t todo = slot >= 0 ? __ballot_sync(kAll, unsure) : 0u;
+    while (todo) {
+      const int i = __ffs(todo) - 1;
+      todo &= todo - 1u;
+      const int told = settle<D>(p, which, tok, head, 32 * half + i, xs, tab, of_x);
+      if (lane == i) code = told;
+    }
+    codes[lane] = static_cast<uint16_t>(code);
+    __syncwarp();
+    if (slot >= 0) store_codes(p, which, codes, 32 * half, 32, slot, head, lane);
+    __syncwarp();
+    v += kVectors;
+    head += kVectors;
+    while (head >= p.hkv) head -= p.hkv, ++tok;
+    // (a wait that gave up: the team leaves together, here)
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbar.red.and.pred b, %2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+                 : "=r"(all) : "r"(static_cast<uint32_t>(ok)), "r"(1 + team) : "memory");
+    if (!all) {
+      if (w == 0 && lane == 0) report(p.status, kDevTimeout);
+      break;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kTcThreads, 2) vq_append_tc_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ __align__(16) uint8_t app_smem[];
+  __shared__ int top, abort_flag;  // the largest ||c||^2
+  __shared__ uint32_t tmem_at;
+  __shared__ uint64_t bars[2];
+  const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
+  if (static_cast<int>(blockIdx.x) >= ctas) {  // queries
+    append_queries(p, ctas);
+    return;
+  }
+  const int which = static_cast<int>(blockIdx.x) >= ctas0, cta = static_cast<int>(blockIdx.x) - which * ctas0;
+  uint8_t* const smem = app_smem + (-smem_addr(app_smem) & 1023u);
+  if (threadIdx.x == 0) {
+    top = abort_flag = 0;
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    mbar_init_fence();
+  }
+  if (threadIdx.x < 32) tmem_alloc<false>(&tmem_at, 2 * kTcChunk);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  if (p.sub[which] == 2) append_products<2>(p, which, cta, p.kv_ctas[which], smem, &top, tmem, bars, &abort_flag);
+  else append_products<4>(p, which, cta, p.kv_ctas[which], smem, &top, tmem, bars, &abort_flag);
+  tc_fence_before();
+  __syncthreads();  // (a product that a team gave up on has had the wait's limit to end)
+  tc_fence_after();
+  if (threadIdx.x < 32) tmem_free<false>(tmem, 2 * kTcChunk);
+}
+
+}  // namespace
+
+namespace {
+
+// CTAs of the two tensors: `most` of each where they fit the GPU at once, else shared by what they cost.
+void share_ctas(AppendParams& p, const long long (&most)[2], const double (&cost)[2], int slots) {
+  for (int i = 0; i < 2; ++i) {
+    const long long share = static_cast<long long>(slots * cost[i] / (cost[0] + cost[1]));
+    p.kv_ctas[i] = static_cast<int>(most[0] + most[1] <= slots || most[i] < share ? most[i] : share < 1 ? 1 : share);
+  }
+}
+
+cudaError_t launch_products(AppendParams p, int sms, long long queries, cudaStream_t stream) {
+  static SmemOptIn opt;
+  const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv;
+  size_t smem = 80 * 1024;  // (no third CTA on an SM: it would wait for tensor memory)
+  long long most[2];
+  double cost[2];
+  for (int i = 0; i < 2; ++i) {
+    const int d = p.sub[i], n = 1 << p.bits[i], per_cta = 2 * 128 * d / kHeadDim;
+    smem = std::max(smem, static_cast<size_t>(tc_smem(d, n).total + 1024));
+    most[i] = (vectors + per_cta - 1) / per_cta;
+    cost[i] = (4.0 / d) * (n + (i == 0 ? 500 : 250));  // scores, and what else a vector takes
+  }
+  cudaError_t e = ensure_smem(vq_append_tc_kernel, smem, opt);
+  if (e != cudaSuccess) return e;
+  share_ctas(p, most, cost, 2 * sms);
+  p.timeout_ns = 2000000000ULL;
+  vq_append_tc_kernel<<<static_cast<unsigned>(p.kv_ctas[0] + p.kv_ctas[1] + queries), kTcThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream) {
   static SmemOptIn opt;
   const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv;
+  long long queries = 0;  // CTAs
+  if (p.q.heads[0] > 0) {
+    const dim3 g = rotary_grid(p.q, sms);
+    queries = static_cast<long long>(g.x) * g.y;
+  }
+  if (p.bits[0] < 10 && p.bits[1] < 10 && !std::getenv("VQ_APPEND_WARP")) return launch_products(p, sms, queries, stream);
   const bool large = p.bits[0] >= 10 || p.bits[1] >= 10;
   const int threads = large ? kAppThreadsMost : kAppThreads, warps = threads / 32;
   // one vector per warp and pass while that leaves no warp without work
@@ -595,20 +872,8 @@ cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream) {
   }
   cudaError_t e = ensure_smem(vq_append_kernel, smem, opt);
   if (e != cudaSuccess) return e;
-  // both tensors' CTAs fit the GPU at once, shared by what they cost
-  const int slots = (large ? 1 : 2) * sms;
-  for (int i = 0; i < 2; ++i) {
-    const long long share = static_cast<long long>(slots * cost[i] / (cost[0] + cost[1]));
-    p.kv_ctas[i] = static_cast<int>(most[i] < share ? most[i] : share < 1 ? 1 : share);
-  }
-  if (most[0] + most[1] <= slots)
-    for (int i = 0; i < 2; ++i) p.kv_ctas[i] = static_cast<int>(most[i]);
-  long long grid = p.kv_ctas[0] + p.kv_ctas[1];
-  if (p.q.heads[0] > 0) {
-    const dim3 g = rotary_grid(p.q, sms);
-    grid += static_cast<long long>(g.x) * g.y;
-  }
-  vq_append_kernel<<<static_cast<unsigned>(grid), threads, smem, stream>>>(p);
+  share_ctas(p, most, cost, (large ? 1 : 2) * sms);
+  vq_append_kernel<<<static_cast<unsigned>(p.kv_ctas[0] + p.kv_ctas[1] + queries), threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 

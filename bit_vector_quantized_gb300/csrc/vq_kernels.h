@@ -173,6 +173,7 @@ struct AppendParams {
   int num_tokens, hkv, page_size;
   int sub[2], bits[2], row_bytes[2];
   int kv_ctas[2], few;         // CTAs of each tensor, those after them turn queries; one vector per pass (set by the launcher)
+  unsigned long long timeout_ns;
   RotaryParams q;              // the queries (heads[0] 0: none)
 };
 

@@ -71,7 +71,16 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         : "memory");
 }
 
-// The same with A in shared memory too.
+// kind::tf32: fp32 words read as tf32, eight of k an instruction, both operands in shared memory (rows of 32 words).
+__device__ __forceinline__ void tc_mma_tf32(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+// kind::f16 with A in shared memory too.
 __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
@@ -113,7 +122,12 @@ constexpr uint32_t tc_idesc(int m, int n, bool b_rows_k) {
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// The same with A in shared memory, its rows there being k too.
+// tf32 operands with k along the rows of both.
+constexpr uint32_t tc_idesc_tf32(int m, int n) {
+  return (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// fp16 operands with A in shared memory, its rows there being k too.
 constexpr uint32_t tc_idesc_rows_k(int m, int n) { return tc_idesc(m, n, true) | 1u << 15; }
 
 // B (or A) in shared memory: rows of 128 bytes (64 fp16) in groups of eight, 1024-byte
@@ -135,6 +149,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
+}
+// The smallest of a lane's 16 columns.
+__device__ __forceinline__ float tmem_min16(uint32_t addr) {
+  uint32_t r[16], m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.min.f32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %16, [%17];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(m)
+      : "r"(addr));
+  (void)r;
+  return __uint_as_float(m);
 }
 // 16 columns.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
