@@ -244,8 +244,7 @@ struct Angles {
   long long t = -1;
   float co[4], si[4];
 };
-__device__ __forceinline__ void load_raw(const AppendParams& p, const uint16_t* row, int e, float (&x)[4]) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + e));
+__device__ __forceinline__ void raw_values(const AppendParams& p, uint2 w, float (&x)[4]) {
   const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -254,7 +253,18 @@ __device__ __forceinline__ void load_raw(const AppendParams& p, const uint16_t* 
   }
 }
 
-__device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* row, long long t, int h, int lane, Angles& a, float (&x)[4]) {
+__device__ __forceinline__ void load_raw(const AppendParams& p, const uint16_t* row, int e, float (&x)[4]) {
+  raw_values(p, __ldg(reinterpret_cast<const uint2*>(row + e)), x);
+}
+
+// The other members of the lane's pairs, where they are one aligned piece of the row (else found by turn_key).
+__device__ __forceinline__ bool pair_piece(const AppendParams& p, int lane, int& e) {
+  const int half = p.rotary_dim / 2;
+  e = 4 * lane < half ? 4 * lane + half : 4 * lane - half;
+  return !p.interleaved && (half & 3) == 0 && 4 * lane < p.rotary_dim;
+}
+
+__device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* row, uint2 pair, long long t, int h, int lane, Angles& a, float (&x)[4]) {
   const int r = p.rotary_dim, half = r / 2;
   if (a.t != t) {
     a.t = t;
@@ -284,7 +294,7 @@ __device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* 
   } else if (4 * lane < r) {
     float y[4];
     if ((half & 3) == 0) {
-      load_raw(p, row, 4 * lane < half ? 4 * lane + half : 4 * lane - half, y);
+      raw_values(p, pair, y);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -389,19 +399,26 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
     }
     // ---- the vectors as they are coded ---------------------------------------------------------------------
     long long slot[NV];
+    uint2 pair[NV];
     float raw[NV][4], of_x[NV];  // of_x: what x's own error can make of a difference of distances, times the distance's root
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       slot[v] = v0 + v < v1 ? append_slot(p, tok[v], lane == 0) : -1;
 #pragma unroll
       for (int i = 0; i < 4; ++i) raw[v][i] = 0.f;
-      if (slot[v] >= 0) load_raw(p, static_cast<const uint16_t*>(p.src[which]) + tok[v] * p.stride[which] + head[v] * kHeadDim, 4 * lane, raw[v]);
+      pair[v] = make_uint2(0u, 0u);
+      if (slot[v] >= 0) {
+        const uint16_t* const src = static_cast<const uint16_t*>(p.src[which]) + tok[v] * p.stride[which] + head[v] * kHeadDim;
+        load_raw(p, src, 4 * lane, raw[v]);
+        int e;
+        if (which == 0 && pair_piece(p, lane, e)) pair[v] = __ldg(reinterpret_cast<const uint2*>(src + e));
+      }
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       of_x[v] = 0.f;
       if (which == 0 && slot[v] >= 0) {
-        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok[v] * p.stride[0] + head[v] * kHeadDim, tok[v], head[v], lane, angles, raw[v]);
+        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok[v] * p.stride[0] + head[v] * kHeadDim, pair[v], tok[v], head[v], lane, angles, raw[v]);
         float sum = fmaf(raw[v][0], raw[v][0], fmaf(raw[v][1], raw[v][1], fmaf(raw[v][2], raw[v][2], raw[v][3] * raw[v][3])));
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
@@ -666,21 +683,40 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
   const long long vectors = static_cast<long long>(p.num_tokens) * p.hkv, tiles = (vectors + kVectors - 1) / kVectors;
   const long long per = (tiles + 2LL * ctas - 1) / (2LL * ctas);
   const long long tile0 = (2LL * cta + team) * per, tile1 = min(tile0 + per, tiles);
-  const int vec = D == 4 ? w : w >> 1, half = D == 4 ? 0 : w & 1;  // this warp's vector of the tile, and which half of its sub-vectors
-  long long v = tile0 * kVectors + vec;
+  // This warp's vector of a tile, and which half of its sub-vectors.  One tile's are as far apart as there are tiles, so that
+  // a warp's follow each other and a token's angles serve its heads.
+  const int vec = D == 4 ? w : w >> 1, half = D == 4 ? 0 : w & 1;
+  const long long v0 = tile0 * kVectors, v1 = min(tile1 * kVectors, vectors), run = tile1 - tile0;
+  long long v = v0 + vec * run;
+  const long long v_end = min(v + run, v1);
   int tok = static_cast<int>(v / p.hkv), head = static_cast<int>(v - static_cast<long long>(tok) * p.hkv);
   uint32_t phase = 0;
   Angles angles;
+  // A tile's rows are asked for one tile ahead.
+  struct Ahead {
+    long long slot;
+    uint2 raw, pair;
+  } next;
+  auto ask = [&](long long at, int t, int h) {
+    Ahead a = {-1, make_uint2(0u, 0u), make_uint2(0u, 0u)};
+    if (at >= v_end) return a;
+    a.slot = append_slot(p, t, lane == 0);
+    const uint16_t* const src = static_cast<const uint16_t*>(p.src[which]) + t * p.stride[which] + h * kHeadDim;
+    a.raw = __ldg(reinterpret_cast<const uint2*>(src + 4 * lane));
+    int e;
+    if (which == 0 && pair_piece(p, lane, e)) a.pair = __ldg(reinterpret_cast<const uint2*>(src + e));
+    return a;
+  };
+  next = ask(v, tok, head);
 
   for (long long tile = tile0; tile < tile1; ++tile) {
     // ---- the vector as it is coded; its rows of the operand --------------------------------------------------------
-    const long long slot = v < vectors ? append_slot(p, tok, lane == 0) : -1;
+    const long long slot = next.slot;
     float raw[4] = {0.f, 0.f, 0.f, 0.f}, of_x = 0.f;
     if (slot >= 0) {
-      const uint16_t* const src = static_cast<const uint16_t*>(p.src[which]) + tok * p.stride[which] + head * kHeadDim;
-      load_raw(p, src, 4 * lane, raw);
+      raw_values(p, next.raw, raw);
       if (which == 0) {
-        turn_key(p, src, tok, head, lane, angles, raw);
+        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok * p.stride[0] + head * kHeadDim, next.pair, tok, head, lane, angles, raw);
         float sum = fmaf(raw[0], raw[0], fmaf(raw[1], raw[1], fmaf(raw[2], raw[2], raw[3] * raw[3])));
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
@@ -705,6 +741,9 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
       *row_piece(32 * w + lane, 1) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    ++v;
+    const int tok1 = head + 1 == p.hkv ? tok + 1 : tok, head1 = head + 1 == p.hkv ? 0 : head + 1;
+    next = ask(v, tok1, head1);
     // ---- scores of 128 centroids at a time; of 16 their minimum ------------------------------------------------------
     float best = INFINITY, second = INFINITY;
     int id = 0;
@@ -767,9 +806,8 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
     __syncwarp();
     if (slot >= 0) store_codes(p, which, codes, 32 * half, 32, slot, head, lane);
     __syncwarp();
-    v += kVectors;
-    head += kVectors;
-    while (head >= p.hkv) head -= p.hkv, ++tok;
+    tok = tok1;
+    head = head1;
     // (a wait that gave up: the team leaves together, here)
     uint32_t all;
     asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbar.red.and.pred b, %2, 128, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
