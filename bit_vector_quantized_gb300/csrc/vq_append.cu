@@ -74,43 +74,16 @@ __device__ __forceinline__ void exact_vector(const AppendParams& p, int which, l
   for (int i = 0; i < 4; ++i) x[i] *= 0.08838834764831845;  // 1 / sqrt(128)
 }
 
-// Nearest centroid of sub-vector s in 64 bits (one warp; the same in all lanes).
-__device__ __forceinline__ int exact_code(const AppendParams& p, int which, int s, const double (&x)[4], int lane) {
-  const int d = p.sub[which], n = 1 << p.bits[which];
-  double y[8];
+// Sub-vector s of such a vector, in all lanes.
+template <int D>
+__device__ __forceinline__ void exact_part(int s, const double (&x)[4], double (&y)[D]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = (s * d + i) % kHeadDim;  // (past the sub-vector: not used)
+  for (int i = 0; i < D; ++i) {
+    const int e = s * D + i;
     const double v0 = __shfl_sync(kAll, x[0], e >> 2), v1 = __shfl_sync(kAll, x[1], e >> 2);
     const double v2 = __shfl_sync(kAll, x[2], e >> 2), v3 = __shfl_sync(kAll, x[3], e >> 2);
     y[i] = (e & 3) == 0 ? v0 : (e & 3) == 1 ? v1 : (e & 3) == 2 ? v2 : v3;
   }
-  const __half* const cb = static_cast<const __half*>(p.cb[which]);
-  double best = INFINITY;
-  int at = 0;
-  for (int j = lane; j < n; j += 32) {
-    double score = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < d) {
-        const double c = __half2float(__ldg(cb + j * d + i));
-        score += c * (c - 2.0 * y[i]);
-      }
-    if (score < best) {
-      best = score;
-      at = j;
-    }
-  }
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const double other = __shfl_xor_sync(kAll, best, m);
-    const int its = __shfl_xor_sync(kAll, at, m);
-    if (other < best || (other == best && its < at)) {
-      best = other;
-      at = its;
-    }
-  }
-  return at;
 }
 
 // Codes first .. first + count - 1 of a vector into its row of the pool (one warp), a word a lane; the words that they
@@ -326,21 +299,23 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
   float x[D], c[D], near[D];
 #pragma unroll
   for (int e = 0; e < D; ++e) x[e] = xs[s * D + e];
-  float best = INFINITY, none = INFINITY;
+  float best = INFINITY, second = INFINITY;
   int at = 0x7fffffff;
   for (int j = lane; j < n; j += 32) {
     load_centroid<D>(tab, j, c);
     const float d = distance<D>(x, c);
-    if (d < best) {
-      best = d;
-      at = j;
-    }
+    second = fminf(second, fmaxf(best, d));
+    at = d < best ? j : at;
+    best = fminf(best, d);
   }
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) join_best(best, none, at, m);
+  for (int m = 1; m < 32; m <<= 1) join_best(best, second, at, m);
   if (best < INFINITY) {  // (else too far off for fp32, or not a number)
-    float second = INFINITY;
+    auto clear = [&]() { return second == INFINITY || second > best + second * 1.9073486e-6f + of_x * root(second); };  // 2^-19
+    if (clear()) return at;
+    // equal centroids count as one
     load_centroid<D>(tab, at, near);
+    second = INFINITY;
     for (int j = lane; j < n; j += 32) {
       load_centroid<D>(tab, j, c);
       bool same = true;
@@ -350,12 +325,39 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
     }
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) second = fminf(second, __shfl_xor_sync(kAll, second, m));
-    if (second == INFINITY || second > best + second * 1.9073486e-6f + of_x * root(second)) return at;  // 2^-19
+    if (clear()) return at;
   }
-  double y[4];
-  exact_vector(p, which, t, h, lane, y);
-  return exact_code(p, which, s, y, lane);
+  // In 64 bits, those that fp32 does not rule out (all, where it told nothing).
+  const float limit = best + 2.f * (best * 1.9073486e-6f + of_x * root(best));
+  double full[4], y[D], nearest = INFINITY;
+  exact_vector(p, which, t, h, lane, full);
+  exact_part<D>(s, full, y);
+  at = 0;
+  for (int j = lane; j < n; j += 32) {
+    load_centroid<D>(tab, j, c);
+    if (distance<D>(x, c) > limit) continue;
+    double score = 0.0;
+#pragma unroll
+    for (int e = 0; e < D; ++e) score += 0.25 * c[e] * (c[e] + 4.0 * y[e]);  // (c: times -2)
+    if (score < nearest) {
+      nearest = score;
+      at = j;
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const double other = __shfl_xor_sync(kAll, nearest, m);
+    const int its = __shfl_xor_sync(kAll, at, m);
+    if (other < nearest || (other == nearest && its < at)) {
+      nearest = other;
+      at = its;
+    }
+  }
+  return at;
 }
+
+template <int D>
+constexpr float kBand = D == 8 ? 7.6293945e-6f : 3.8146973e-6f;  // 2^-17, 2^-18: two scores' errors
 
 // Rows, codebook and scratch of the CTA.  Shared memory: the table, the norms, then for each warp its vectors in fp32
 // and their codes.
@@ -422,9 +424,10 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
         float sum = fmaf(raw[v][0], raw[v][0], fmaf(raw[v][1], raw[v][1], fmaf(raw[v][2], raw[v][2], raw[v][3] * raw[v][3])));
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
-        // Each element of k~ is off by about 2^-24 of its rms in rotation, division and butterflies (eight of these are
-        // 2^-24 |k~|); a difference of two distances by at most 2 |error| |c - c'| <= 4 sqrt(d) 2^-24 |k~| sqrt(distance).
-        of_x[v] = 4.f * sqrtf(D * sum) * 5.9604645e-8f;
+        // Each element of k~ is off by 1.3 2^-24 of its rms (rotation, division, butterflies: independent roundings), a
+        // difference of two distances by 2 error . (c - c'), |c - c'| up to twice the distance's root: this is nine
+        // times its deviation, and more than an error that all elements share can make of it.
+        of_x[v] = 4.f * root(sum) * 5.9604645e-8f;
       }
       *reinterpret_cast<float4*>(xs + v * kHeadDim + 4 * lane) = make_float4(raw[v][0], raw[v][1], raw[v][2], raw[v][3]);
     }
@@ -525,11 +528,12 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
         x[e] = xs[row * D + e];
         x2 = fmaf(x[e], x[e], x2);
       }
-      // The products' error: at most 2^-18 of ||c||^2 + 2 |x| |c| each, of centroids that are as near as the nearest, so
+      // The products' error: at most 2^-18 (sub-vectors of 8; of fewer 2^-19) of ||c||^2 + 2 |x| |c| each: products of 11 bits by
+      // 11 are exact, each of up to 19 sums is off by 2^-23 of it at most, x without its high and low parts by 2^-22, of centroids that are as near as the nearest, so
       // with |c| up to |x| + distance (and no longer than the longest).
       const float x1 = root(x2), reach = fmaf(1.01f, x1, root(fmaxf(b + x2, 0.f)));
       const float c2 = fminf(reach * reach, cmax2);
-      const bool near = sec <= b + 7.6293945e-6f * fmaf(2.f * x1, root(c2), c2);
+      const bool near = sec <= b + kBand<D> * fmaf(2.f * x1, root(c2), c2);
       // of the group's four blocks this lane's two, two centroids each
       const int j = 32 * (id >> 2) + 16 * (c & 1) + 2 * (id & 3);
       float d0 = INFINITY, far = INFINITY;
@@ -720,7 +724,7 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
         float sum = fmaf(raw[0], raw[0], fmaf(raw[1], raw[1], fmaf(raw[2], raw[2], raw[3] * raw[3])));
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
-        of_x = 4.f * root(D * sum) * 5.9604645e-8f;  // (append_tensor has the reason)
+        of_x = 4.f * root(sum) * 5.9604645e-8f;  // (append_tensor has the reason)
       }
     }
     *reinterpret_cast<float4*>(xs + 4 * lane) = make_float4(raw[0], raw[1], raw[2], raw[3]);
@@ -780,7 +784,7 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
     // ---- steps 1 and 2: a lane's group, each lane beginning elsewhere in it (banks) ----------------------------------
     const float x1 = root(x2), reach = fmaf(1.01f, x1, root(fmaxf(best + x2, 0.f)));
     const float c2 = fminf(reach * reach, cmax2);
-    const bool near = second <= best + 7.6293945e-6f * fmaf(2.f * x1, root(c2), c2);
+    const bool near = second <= best + kBand<D> * fmaf(2.f * x1, root(c2), c2);
     float d0 = INFINITY, far = INFINITY;
     int code = id;
 #pragma unroll 4
