@@ -915,8 +915,8 @@ def _layers_arg(pools, name, device, shape):
     torch = _torch()
     if isinstance(pools, torch.Tensor):
         first = _arg(pools, torch.uint8, name, device, (pools.shape[0],) + shape)
-        step = pools.stride(0)
-        return [first + i * step for i in range(pools.shape[0])]
+        step, n = pools.stride(0), pools.shape[0]
+        return range(first, first + n * step, step) if n * step else [first] * n
     return [_arg(x, torch.uint8, f"{name}[{i}]", device, shape) for i, x in enumerate(pools)]
 
 

@@ -5,31 +5,39 @@
 //   k' = R(position) k,  k~ = k' diag(lambda)^-1 H_D,  code i = argmin_j ||k~_i - C_k[j]||^2,
 //   v's code i = argmin_j ||v_i - C_v[j]||^2,  the lowest j where several are equal.
 //
-//
-// The search is a product: score ||c||^2 - 2 x . c orders centroids as the distance does, so 16 sub-vectors
-// against 8 centroids are one warp mma (tf32: -2 c is fp16 and exact in it, x goes in as high and low
-// part, side by side in the k dimension or one product after the other for sub-vectors of 8; ||c||^2 is
-// the accumulator's start).  Of 32 centroids a lane holds 8 scores of a row; it keeps their minimum
-// only, with the smallest and second smallest minimum so far and which group the smallest was: 4.5
-// instructions for 128 scores instead of 7 for 32 in a scan.
+// The search is a product: ||c||^2 - 2 x . c orders centroids as the distance does, so sub-vectors against centroids
+// are a matrix product with a very short k, in tf32: -2 c is fp16 and exact in it, x goes in as high and low part side
+// by side in k, ||c||^2 in three parts against ones (or as the sums' start).  Of a group of centroids a lane keeps the
+// smallest score only, with the smallest and second smallest so far and which group the smallest was.
 //
 // Codes are exact.  In steps, each for the sub-vectors that the one before cannot tell:
 //   1. the group with the smallest score, if no other comes within the products' error;
-//   2. its 8 centroids by fp32 distances ||x - c||^2 (their error is relative to the distance, not to x):
+//   2. its centroids by fp32 distances ||x - c||^2 (their error is relative to the distance, not to x):
 //      the nearest, if no other comes within the error of these and, for keys, of x itself;
 //   3. all centroids by fp32 distances (one warp), equal centroids counting as one;
-//   4. everything in 64 bits, for keys from the rows on (one warp).
+//   4. in 64 bits, for keys from the rows on, the centroids that fp32 does not rule out (one warp).
+// Of drawn sub-vectors of 4 step 1 leaves 4 in 10 000, step 2 one in 100 000 of keys; tests put all of them there.
+//
+// Two kernels.  8- and 9-bit codes: tcgen05, 128 sub-vectors by 128 centroids a product; tensor memory gives the
+// minima of 16 columns as it is read (tcgen05.ld.red).  12-bit codes, whose 4096 centroids do not fit shared memory as
+// operands of 128 bytes: m16n8k8 warp mma, groups of 32 of which a lane holds 8 scores.  Warp mma for the others
+// too took 209 us where tcgen05 takes 183 (4099 bf16 tokens of 8 KV heads at (2,8) and (4,9)), 271 and 225 (8192
+// tokens at (4,8)), 16 and 15.5 (64 tokens).
+//
+// What bounds them: latency and instructions, at 16 warps an SM (128 registers; 80 for 24 warps spill).  The first
+// kernel issues in 45 % of the cycles, about 1000 warp instructions for a vector of 32 sub-vectors: a third the scores
+// and their minima, a quarter step 2, the rotation and transform of a key 270, its share of the queries 120.  Floors
+// are far: 25 us for the bytes of 8192 tokens.  Two chunks of 64 centroids under way instead of one of 128: 280 us.
 #include "vq_rotary.cuh"
 #include "vq_tcgen05.cuh"
 
 #include <algorithm>
-#include <cstdlib>
 
 namespace vqk {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kAppThreads = kRotThreads, kAppThreadsMost = 512;  // (with a large codebook one CTA of more threads fits an SM)
+constexpr int kAppThreads = 512;  // of the warp-mma kernel, whose codebook leaves room for one CTA an SM
 
 __device__ __forceinline__ double row_value(const AppendParams& p, const uint16_t* row, int e) {
   const uint16_t x = __ldg(row + e);
@@ -120,7 +128,7 @@ __device__ __forceinline__ long long append_slot(const AppendParams& p, long lon
 
 // ---- the codebook in shared memory: -2 c, 8 centroids a block, and ||c||^2 -------------------------------------
 // Word of element e of centroid j: j d + e, but for d = 8 the lower and the upper halves of a block's 8 centroids
-// one after the other, so that the products' operands are one word a lane without bank conflicts.
+// one after the other, so that warp mma's operands are one word a lane without bank conflicts.
 template <int D>
 __device__ __forceinline__ int centroid_word(int j, int e) {
   return D == 8 ? (j >> 3) * 64 + (e >> 2) * 32 + (j & 7) * 4 + (e & 3) : j * D + e;
@@ -183,11 +191,6 @@ __device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, 
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-__device__ __forceinline__ void mma_k4(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, float c0, float c1, float c2, float c3) {
-  asm volatile("mma.sync.aligned.m16n8k4.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%8,%9,%10};"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a0), "r"(a1), "r"(b0), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 __device__ __forceinline__ float min3(float a, float b, float c) {
   float d;
@@ -368,7 +371,7 @@ struct AppendShape {
   static constexpr int kWarpBytes = kVectors * kHeadDim * 4 + R * 16 * 2;
 };
 
-// One tensor's vectors: R tiles of 16 sub-vectors a pass and warp.
+// One tensor's vectors by warp mma: R tiles of 16 sub-vectors a pass and warp.
 template <int D, int R>
 __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, int cta, int ctas, uint8_t* smem, int* top) {
   using Shape = AppendShape<D, R>;
@@ -433,33 +436,18 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
     }
     __syncwarp();
     // ---- operands: lane (g, c) has rows g and g + 8 of each tile -----------------------------------------------
-    constexpr int kA = D == 2 ? 2 : D == 4 ? 4 : 8;
-    uint32_t a[R][kA];
+    uint32_t a[R][8];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float* const x = xs + r * 16 * D;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // row g + 8 half
-        if constexpr (D == 2) {  // k: high parts of both elements, low parts
-          const float y = x[(g + 8 * half) * 2 + (c & 1)];
+      for (int half = 0; half < 2; ++half)  // row g + 8 half
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // high parts of the eight elements, then a product of the low parts
+          const float y = xs[r * 16 * D + (g + 8 * half) * D + 4 * e + c];
           const uint32_t hi = to_tf32(y);
-          a[r][half] = c < 2 ? hi : to_tf32(y - __uint_as_float(hi));
-        } else {
-#pragma unroll
-          for (int e = 0; e < D / 4; ++e) {
-            const float y = x[(g + 8 * half) * D + 4 * e + c];
-            const uint32_t hi = to_tf32(y), lo = to_tf32(y - __uint_as_float(hi));
-            if constexpr (D == 4) {  // k: high parts of the four elements, low parts
-              a[r][half] = hi;
-              a[r][2 + half] = lo;
-            } else {  // high parts of the eight elements, then a product of the low parts
-              a[r][2 * e + half] = hi;
-              a[r][4 + 2 * e + half] = lo;
-            }
-          }
+          a[r][2 * e + half] = hi;
+          a[r][4 + 2 * e + half] = to_tf32(y - __uint_as_float(hi));
         }
-      }
-    }
     // ---- groups of 32 centroids, 8 of a row's scores a lane --------------------------------------------------
     float best[R][2], second[R][2];
     int at[R][2];
@@ -476,24 +464,12 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
       for (int b = 0; b < 4; ++b) {
         const int nb = 4 * group + b;
         const float4 start = *reinterpret_cast<const float4*>(norm + 8 * nb + 2 * c);
-        uint32_t b0, b1 = 0;
-        if constexpr (D == 2) {
-          b0 = __float_as_uint(tab[(8 * nb + g) * 2 + (c & 1)]);
-        } else if constexpr (D == 4) {
-          b0 = b1 = __float_as_uint(tab[32 * nb + lane]);
-        } else {
-          b0 = __float_as_uint(tab[64 * nb + lane]);
-          b1 = __float_as_uint(tab[64 * nb + 32 + lane]);
-        }
+        const uint32_t b0 = __float_as_uint(tab[64 * nb + lane]), b1 = __float_as_uint(tab[64 * nb + 32 + lane]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float s[4];
-          if constexpr (D == 2) {
-            mma_k4(s, a[r][0], a[r][1], b0, start.x, start.y, start.z, start.w);
-          } else {
-            mma_k8(s, a[r][0], a[r][1], a[r][2], a[r][3], b0, b1, start.x, start.y, start.z, start.w);
-            if constexpr (D == 8) mma_k8(s, a[r][4], a[r][5], a[r][6], a[r][7], b0, b1, s[0], s[1], s[2], s[3]);
-          }
+          mma_k8(s, a[r][0], a[r][1], a[r][2], a[r][3], b0, b1, start.x, start.y, start.z, start.w);
+          mma_k8(s, a[r][4], a[r][5], a[r][6], a[r][7], b0, b1, s[0], s[1], s[2], s[3]);
           low[r][0] = b == 0 ? fminf(s[0], s[1]) : min3(low[r][0], s[0], s[1]);
           low[r][1] = b == 0 ? fminf(s[2], s[3]) : min3(low[r][1], s[2], s[3]);
         }
@@ -578,14 +554,14 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
 // The CTAs from `first` on turn queries.
 __device__ __forceinline__ void append_queries(const AppendParams& p, int first) {
   const long long b = static_cast<long long>(blockIdx.x) - first, shares = (p.q.heads[0] + p.q.heads_per_y - 1) / p.q.heads_per_y;
-  if (threadIdx.x >= kAppThreads) return;
+  if (threadIdx.x >= kRotThreads) return;
   const bool whole = p.interleaved || p.rotary_dim % 16 == 0;
   const int y = static_cast<int>(b % shares);
   if (p.bf16) whole ? rotary_share<true, true>(p.q, b / shares, y) : rotary_share<true, false>(p.q, b / shares, y);
   else whole ? rotary_share<false, true>(p.q, b / shares, y) : rotary_share<false, false>(p.q, b / shares, y);
 }
 
-__global__ void __launch_bounds__(kAppThreadsMost, 1) vq_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 1) vq_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(16) uint8_t app_smem[];
   __shared__ int top;  // the largest ||c||^2
   const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
@@ -596,14 +572,8 @@ __global__ void __launch_bounds__(kAppThreadsMost, 1) vq_append_kernel(const __g
   const int which = static_cast<int>(blockIdx.x) >= ctas0, cta = static_cast<int>(blockIdx.x) - which * ctas0;
   if (threadIdx.x == 0) top = 0;
   __syncthreads();
-  switch (p.sub[which] + (p.few ? 16 : 0)) {
-    case 2:
-    case 18: append_tensor<2, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
-    case 4: append_tensor<4, 4>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
-    case 20: append_tensor<4, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
-    case 8: append_tensor<8, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
-    default: append_tensor<8, 1>(p, which, cta, p.kv_ctas[which], app_smem, &top); break;
-  }
+  if (p.few) append_tensor<8, 1>(p, which, cta, p.kv_ctas[which], app_smem, &top);
+  else append_tensor<8, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top);
 }
 
 // ---- 8- and 9-bit codes: the products on the tensor cores ----------------------------------------------------------
@@ -896,26 +866,24 @@ cudaError_t launch_append(AppendParams p, int sms, cudaStream_t stream) {
     const dim3 g = rotary_grid(p.q, sms);
     queries = static_cast<long long>(g.x) * g.y;
   }
-  if (p.bits[0] < 10 && p.bits[1] < 10 && !std::getenv("VQ_APPEND_WARP")) return launch_products(p, sms, queries, stream);
-  const bool large = p.bits[0] >= 10 || p.bits[1] >= 10;
-  const int threads = large ? kAppThreadsMost : kAppThreads, warps = threads / 32;
+  if (p.bits[0] < 10 && p.bits[1] < 10) return launch_products(p, sms, queries, stream);
   // one vector per warp and pass while that leaves no warp without work
-  p.few = 2 * vectors <= 2LL * sms * (kAppThreads / 32);
+  const int warps = kAppThreads / 32;
+  p.few = vectors <= static_cast<long long>(sms) * warps / 2;
   size_t smem = 0;
   long long most[2];
   double cost[2];
   for (int i = 0; i < 2; ++i) {
-    const int d = p.sub[i], n = 1 << p.bits[i], per_pass = d == 2 || p.few ? 1 : 2;
-    const size_t bytes = static_cast<size_t>(n) * (d + 2) * 4 + warps * per_pass * (kHeadDim * 4 + kHeadDim / d * 2);
-    smem = bytes > smem ? bytes : smem;
-    const long long per_cta = static_cast<long long>(warps) * per_pass;
-    most[i] = (vectors + per_cta - 1) / per_cta;
-    cost[i] = static_cast<double>(kHeadDim / d) * n * (d == 8 ? 2 : 1) + (i == 0 ? 3000 : 1000);  // scores, and what comes before them
+    const int d = p.sub[i], n = 1 << p.bits[i], per_pass = p.few ? 1 : 2;
+    if (d != 8) return cudaErrorInvalidValue;
+    smem = std::max(smem, static_cast<size_t>(n) * (d + 2) * 4 + warps * per_pass * (kHeadDim * 4 + kHeadDim / d * 2));
+    most[i] = (vectors + warps * per_pass - 1) / (warps * per_pass);
+    cost[i] = 2.0 * (kHeadDim / d) * n + (i == 0 ? 3000 : 1000);  // scores, and what comes before them
   }
   cudaError_t e = ensure_smem(vq_append_kernel, smem, opt);
   if (e != cudaSuccess) return e;
-  share_ctas(p, most, cost, (large ? 1 : 2) * sms);
-  vq_append_kernel<<<static_cast<unsigned>(p.kv_ctas[0] + p.kv_ctas[1] + queries), threads, smem, stream>>>(p);
+  share_ctas(p, most, cost, sms);
+  vq_append_kernel<<<static_cast<unsigned>(p.kv_ctas[0] + p.kv_ctas[1] + queries), kAppThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -150,16 +150,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-// The smallest of a lane's 16 columns.
+// The smallest of a lane's 16 columns (which come with it, unused).
 __device__ __forceinline__ float tmem_min16(uint32_t addr) {
-  uint32_t r[16], m;
+  [[maybe_unused]] uint32_t r[16];
+  uint32_t m;
   asm volatile(
       "tcgen05.ld.red.sync.aligned.32x32b.x16.min.f32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %16, [%17];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(m)
       : "r"(addr));
-  (void)r;
   return __uint_as_float(m);
 }
 // 16 columns.
