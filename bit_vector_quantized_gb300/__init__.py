@@ -932,14 +932,15 @@ def keep_tokens(layout: vq_layout, seq_lens, cu_new_lens, keep, keep_lens, page_
     D, H, P, B = L.head_dim, L.num_kv_heads, L.page_size, seq_lens.shape[0]
     if page_table.dim() != 2 or keep.dim() != 2:
         raise ValueError("page_table and keep must be [B][max_pages] and [B][max_keep]")
-    if len(k_pools) != len(v_pools):
+    layers = len(k_pools)
+    if layers != len(v_pools):
         raise ValueError("k_pools and v_pools have different numbers of layers")
-    if len(k_pools) == 0:
+    if layers == 0:
         raise ValueError("there are no pools")
-    width, most, free, pages = page_table.shape[1], keep.shape[1], free_pages.numel(), k_pools[0].shape[0]
+    pages = k_pools.shape[1] if isinstance(k_pools, torch.Tensor) else k_pools[0].shape[0]
+    width, most, free = page_table.shape[1], keep.shape[1], free_pages.numel()
     kp = _layers_arg(k_pools, "k_pools", dev, (pages, H, P, (D // L.k_sub * L.k_bits + 31) // 32 * 4))
     vp = _layers_arg(v_pools, "v_pools", dev, (pages, H, P, (D // L.v_sub * L.v_bits + 31) // 32 * 4))
-    layers = len(kp)
     args = (_arg(seq_lens, i32, "seq_lens", dev, (B,)), _arg(cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)),
             _arg(keep, i32, "keep", dev, (B, most)), most, _arg(keep_lens, i32, "keep_lens", dev, (B,)),
             _arg(page_table, i32, "page_table", dev, (B, width)), width, pages, layers,

@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(kBookThreads) vq_keep_book_kernel(const __grid
   const int per = (p.batch + kBookThreads - 1) / kBookThreads;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
   long long sum = 0;
+  KeepSeq s = {};  // (of one sequence a thread, what it found serves twice)
   for (int b = b0; b < b1; ++b) {
-    const KeepSeq s = check(b);
+    s = check(b);
     if (s.bad != kDevOk) report(p.status, s.bad);
     sum += gone(s);
   }
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kBookThreads) vq_keep_book_kernel(const __grid
   const bool fits = num_free >= 0 && num_free <= p.free_capacity && all <= p.free_capacity - num_free;
   pdl_wait();  // the moves have read the lengths
   for (int b = b0; b < b1; ++b) {
-    const KeepSeq s = check(b);
+    if (per > 1) s = check(b);
     const int n = gone(s), last = pages(s.len) - 1;
     if (fits)
       for (int i = 0; i < n; ++i) p.free_pages[num_free + at + i] = __ldg(p.page_table + static_cast<long long>(b) * p.max_pages + last - i);
@@ -153,9 +154,9 @@ __global__ void __launch_bounds__(kBookThreads) vq_keep_book_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_keep(const KeepParams& p, int sms, cudaStream_t stream) {
-  // CTAs per sequence: enough for two per SM, at most one per eight tasks
+  // CTAs per sequence: enough for eight per SM (its loads and stores are one round trip each), at most one per eight tasks
   const int tasks = (2 * p.layers * p.hkv + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
-  const int want = (2 * sms + p.batch - 1) / p.batch;
+  const int want = (8 * sms + p.batch - 1) / p.batch;
   const int y = want < tasks ? want : tasks;
   cudaError_t e = launch_pdl(vq_keep_move_kernel, dim3(p.batch, y), dim3(kMoveThreads), 0, stream, p, false);
   if (e != cudaSuccess) return e;
