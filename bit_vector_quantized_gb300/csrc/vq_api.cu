@@ -1154,7 +1154,16 @@ ChunkWs chunk_ws(int tile_rows, int grid) {
   return w;
 }
 
-// Tile height of a call over trees of drafted tokens.  VQ_TREE_ROWS=16|32|128|256 selects one explicitly (a tuning
+// Tile height of a call over trees of drafted tokens, by the rows of its longest (sequence, KV head): 16 or 32 of
+// vq_tree.cu where they hold them, else 128 (or what three of these hold, but for the 1.5-bit format) or 256 of
+// vq_chunk_wide.cu.  Measured as above (device time, merge included, cold L2; 4 heads per KV head):
+//   16 rows, batch 8: 45 us at 16, 49 at 32, 55 at 128; 20 to 32 rows: 61 at 16, 49 to 51 at 32, 55 at 128;
+//     batch 16 at (2,8): 76 at 32, 86 at 128; 1.5 bit, batch 48: 16 rows 154, 162 and 166, 28 rows 281, 171 and 168
+//   64 rows, batch 8: 72 us at 32, 55 at 128, 78 at 256; 96 and 128 rows: 59 at 128, 80 at 256
+//   192 rows, batch 8: 84 us at 128 and at 256; batch 16 at (2,8): 150 and 133; 250 rows at (2,8), (4,9): 274 and 233;
+//     256 rows, 1.5 bit: 86 and 78; ragged trees of 1 to 61 tokens (bound 244 rows): 136 and 145 (left to 256)
+//   320 rows, batch 8: 117 us at 128, 131 at 256; 384 rows, batch 16 at (2,8): 215 and 238
+// VQ_TREE_ROWS=16|32|128|256 selects one explicitly (a tuning
 // switch for profiling).
 int tree_tile_rows(const vq_layout& L, int max_new_len) {
   if (const char* env = std::getenv("VQ_TREE_ROWS"))

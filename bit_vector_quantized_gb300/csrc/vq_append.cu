@@ -21,13 +21,15 @@
 // Two kernels.  8- and 9-bit codes: tcgen05, 128 sub-vectors by 128 centroids a product; tensor memory gives the
 // minima of 16 columns as it is read (tcgen05.ld.red).  12-bit codes, whose 4096 centroids do not fit shared memory as
 // operands of 128 bytes: m16n8k8 warp mma, groups of 32 of which a lane holds 8 scores.  Warp mma for the others
-// too took 209 us where tcgen05 takes 183 (4099 bf16 tokens of 8 KV heads at (2,8) and (4,9)), 271 and 225 (8192
+// too took 209 us where tcgen05 takes 177 (4099 bf16 tokens of 8 KV heads at (2,8) and (4,9)), 271 and 215 (8192
 // tokens at (4,8)), 16 and 15.5 (64 tokens).
 //
-// What bounds them: latency and instructions, at 16 warps an SM (128 registers; 80 for 24 warps spill).  The first
-// kernel issues in 45 % of the cycles, about 1000 warp instructions for a vector of 32 sub-vectors: a third the scores
-// and their minima, a quarter step 2, the rotation and transform of a key 270, its share of the queries 120.  Floors
-// are far: 25 us for the bytes of 8192 tokens.  Two chunks of 64 centroids under way instead of one of 128: 280 us.
+// What bounds them.  tcgen05: instructions and latency at 16 warps an SM (128 registers; with 80 for 24 warps they
+// spill: 265 us), issuing in 53 % of the cycles, about 1000 warp instructions for a vector of 32 sub-vectors: a quarter the
+// scores and their minima, a quarter step 2, rotation and transform of a key 270, its queries 120.  The queries' CTAs
+// come last and take 20 to 27 us of 215.  The floor is 25 us, the bytes of 8192 tokens.  Two chunks of 64 centroids
+// under way instead of one of 128 took 280 us, minima of 8 columns instead of 16 the same time.  Warp mma: the
+// tensor pipe is 53 % busy with products of k = 8 (333 tokens of 8 KV heads: 135 us, floor 3).
 #include "vq_rotary.cuh"
 #include "vq_tcgen05.cuh"
 
@@ -757,7 +759,7 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
     const bool near = second <= best + kBand<D> * fmaf(2.f * x1, root(c2), c2);
     float d0 = INFINITY, far = INFINITY;
     int code = id;
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < kTcGroup; ++i) {
       const int j = id + ((i + lane) & (kTcGroup - 1));
       float y[D];

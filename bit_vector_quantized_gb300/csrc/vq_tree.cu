@@ -11,10 +11,21 @@
 //     and 32 KB read by the tensor core, where tiles of query rows take 128 KB and 96 KB.
 //   * Q~ stays in shared memory, high and low fp16 parts, for the tile (scores keep about fp32 accuracy); P is
 //     rounded to fp16 once (p <= 2^8, relative 2^-11), as everywhere in chunk attention.
-//   * Eight warps do the softmax: a thread has one token and N / 2 rows.  The rows' maxima are in shared memory and
+//     So high and low parts are columns of one product of 2 N.
+//   * Four or eight warps do the softmax: a thread has one token and 16 rows.  The rows' maxima are in shared memory and
 //     may lag by 2^8, so the usual block needs no maximum over the tokens, only a vote whether one moved.
-//   * Eight warps expand K, eight V, one thread issues, one warp plans, as in vq_chunk_wide.cu, whose rings, barriers and
-//     bounded waits these are.
+//   * Eight warps expand K, eight V, four of them every other block, a thread a whole token; one thread issues, one warp
+//     plans, as in vq_chunk_wide.cu, whose rings, barriers and bounded waits these are.  (All of them at every block, a
+//     thread half a token: 249 us instead of 190 for 16 tiles of 16 rows over 32K tokens, by instructions.)
+//   * The planning warp plans while the others fill the table, and one warp sends the codes to L2 ahead of the others.
+//
+// What bounds it.  N = 16: the shared-memory pipe, 1150 cycles of it for a block of 128 tokens by counters, of 1370
+// that a block takes ((4,8) codes); (2,8) keys and 9-bit values 2000.  N = 32 a little more (2600 at (2,8), (4,9));
+// at 1.5 bit 2650, the gathers of the plain tables meeting in the same banks.  Around the blocks a piece costs 5.5 us
+// (q~, the first block's maxima, sums and output), the start 6 us.  Measured, merge included: 16 rows of each of 8
+// sequences of 4000 to 8000 tokens, 8 KV heads: 45 us, 32 rows 51; 32 rows over 32K 41 (tiles of 128 rows: 55, 55 and
+// 45); 28 rows of each of 48 sequences of 3000 to 6000 at 1.5 bit 167 us (168).  A variant for 64 rows did not
+// beat tiles of 128: its softmax threads, 32 rows each, spilled.
 #include <type_traits>
 
 #include "vq_chunk_wide.cuh"
