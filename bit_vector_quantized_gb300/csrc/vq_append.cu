@@ -28,7 +28,8 @@
 // spill: 265 us), issuing in 53 % of the cycles, about 1000 warp instructions for a vector of 32 sub-vectors: a quarter the
 // scores and their minima, a quarter step 2, rotation and transform of a key 270, its queries 120.  The queries' CTAs
 // come last and take 20 to 27 us of 215.  The floor is 25 us, the bytes of 8192 tokens.  Two chunks of 64 centroids
-// under way instead of one of 128 took 280 us, minima of 8 columns instead of 16 the same time.  Warp mma: the
+// under way instead of one of 128 took 280 us, minima of 8 columns instead of 16
+// nothing for it and 199 us instead of 183 at (2,8), (4,9).  Warp mma: the
 // tensor pipe is 53 % busy with products of k = 8 (333 tokens of 8 KV heads: 135 us, floor 3).
 #include "vq_rotary.cuh"
 #include "vq_tcgen05.cuh"
