@@ -15,6 +15,7 @@ Build it with ``python -m bit_vector_quantized_gb300.build``.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import NamedTuple, Optional, Tuple
@@ -911,13 +912,16 @@ class KeptTokens(NamedTuple):
 
 
 def _layers_arg(pools, name, device, shape):
-    """Device pointers of the layers' pools: one tensor [layers][..], or one tensor per layer."""
+    """Device pointers of the layers' pools: one tensor [layers][..], or one tensor per layer.
+    (Filled as an array of the standard library's: 1 us for 32 layers, as one of ctypes 3.)"""
     torch = _torch()
     if isinstance(pools, torch.Tensor):
         first = _arg(pools, torch.uint8, name, device, (pools.shape[0],) + shape)
         step, n = pools.stride(0), pools.shape[0]
-        return range(first, first + n * step, step) if n * step else [first] * n
-    return [_arg(x, torch.uint8, f"{name}[{i}]", device, shape) for i, x in enumerate(pools)]
+        at = range(first, first + n * step, step) if n * step else [first] * n
+    else:
+        at = [_arg(x, torch.uint8, f"{name}[{i}]", device, shape) or 0 for i, x in enumerate(pools)]
+    return (ctypes.c_uint64 * len(at)).from_buffer(array.array("Q", at))
 
 
 def keep_tokens(layout: vq_layout, seq_lens, cu_new_lens, keep, keep_lens, page_table, k_pools, v_pools, free_pages,
@@ -944,8 +948,7 @@ def keep_tokens(layout: vq_layout, seq_lens, cu_new_lens, keep, keep_lens, page_
     args = (_arg(seq_lens, i32, "seq_lens", dev, (B,)), _arg(cu_new_lens, i32, "cu_new_lens", dev, (B + 1,)),
             _arg(keep, i32, "keep", dev, (B, most)), most, _arg(keep_lens, i32, "keep_lens", dev, (B,)),
             _arg(page_table, i32, "page_table", dev, (B, width)), width, pages, layers,
-            (ctypes.c_void_p * layers)(*kp), (ctypes.c_void_p * layers)(*vp),
-            _arg(free_pages, i32, "free_pages", dev, (free,)), free, _arg(num_free, i32, "num_free", dev, (1,)))
+            kp, vp, _arg(free_pages, i32, "free_pages", dev, (free,)), free, _arg(num_free, i32, "num_free", dev, (1,)))
 
     def call(st):
         r = KeptTokens(torch.empty(B, dtype=i32, device=dev) if seq_lens_out is None else seq_lens_out,

@@ -1161,18 +1161,26 @@ ChunkWs chunk_ws(int tile_rows, int grid) {
 //     batch 16 at (2,8): 76 at 32, 86 at 128; 1.5 bit, batch 48: 16 rows 154, 162 and 166, 28 rows 281, 171 and 168
 //   64 rows, batch 8: 72 us at 32, 55 at 128, 78 at 256; 96 and 128 rows: 59 at 128, 80 at 256
 //   192 rows, batch 8: 84 us at 128 and at 256; batch 16 at (2,8): 150 and 133; 250 rows at (2,8), (4,9): 274 and 233;
-//     256 rows, 1.5 bit: 86 and 78; ragged trees of 1 to 61 tokens (bound 244 rows): 136 and 145 (left to 256)
+//     256 rows, 1.5 bit: 86 and 78
 //   320 rows, batch 8: 117 us at 128, 131 at 256; 384 rows, batch 16 at (2,8): 215 and 238
+// Trees of different sizes under a bound of two tiles of 128 rows: one such tile takes about 0.7 of the time of a tile of
+// 256, two of them 1.1, so 128 wins where a third of the sequences need one only.  For sizes spread evenly that is a mean
+// of at most 96 rows and a quarter of the bound.  (Sequences without drafted tokens lower the mean too.)  At 128 | 256:
+//   1 to 61 tokens, batch 24, (2,8): 139 | 150 and, all contexts 4000 to 8000, 166 | 184; 1 to 64, batch 8, 72 | 82; 16 to 64,
+//     182 | 184; 5 heads, (2,8), (4,9), 1 to 50, 211 | 225; 1.5 bit, 1 to 64 145 | 154, 16 to 64 154 | 154
+//   above that mean: 20 to 50 of 5 heads 250 | 229, 30 to 40 186 | 186 (24 to 64 at (4,8) 127 | 131)
 // VQ_TREE_ROWS=16|32|128|256 selects one explicitly (a tuning
 // switch for profiling).
-int tree_tile_rows(const vq_layout& L, int max_new_len) {
+int tree_tile_rows(const vq_layout& L, int batch, int num_tokens, int max_new_len) {
   if (const char* env = std::getenv("VQ_TREE_ROWS"))
     for (int rows : {16, 32, 128, 256})
       if (std::atoi(env) == rows) return rows;
-  const long long rows = static_cast<long long>(max_new_len) * (L.num_q_heads / L.num_kv_heads);
-  const int per_tile = 128 / (L.num_q_heads / L.num_kv_heads);  // tokens of 128 rows
+  const int group = L.num_q_heads / L.num_kv_heads;
+  const long long rows = static_cast<long long>(max_new_len) * group;
+  const int per_tile = 128 / group;  // tokens of 128 rows
   const bool three = max_new_len > 2 * per_tile && max_new_len <= 3 * per_tile && L.k_bits != 12;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || three ? 128 : 256;
+  const bool ragged = max_new_len <= 2 * per_tile && static_cast<long long>(num_tokens) * group <= (96 + rows / 4) * batch;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || three || ragged ? 128 : 256;
 }
 
 struct TreeArgs {
@@ -1232,7 +1240,7 @@ vq_status attention_of_rows(const vq_layout* layout, int32_t batch, int32_t num_
   }
   const int sms = device_sms();
   if (sms <= 0) return fail(VQ_ERR_CUDA, "no CUDA device");
-  const int tile_rows = tree ? tree_tile_rows(L, max_new_len) : chunk_tile_rows(L, max_new_len);
+  const int tile_rows = tree ? tree_tile_rows(L, batch, num_tokens, max_new_len) : chunk_tile_rows(L, max_new_len);
   const int grid = tile_rows == 256 ? std::max(sms & ~1, 2) : sms;
   const ChunkWs ws = chunk_ws(tile_rows, grid);
   if (workspace_bytes < ws.total)
@@ -1335,7 +1343,7 @@ size_t vq_tree_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t n
   const int sms = num_sms > 0 ? num_sms : device_sms();
   if (sms <= 0) return 0;
   size_t most = 0;  // a call with smaller bounds may take another tile (of 128 rows also 256)
-  const int need = tree_tile_rows(*layout, max_new_len);
+  const int need = tree_tile_rows(*layout, batch, num_tokens, max_new_len);
   for (int rows : {16, 32, 128, 256})
     if (rows <= need || need == 128) most = std::max(most, chunk_ws(rows, std::max(sms, 2)).total);
   return most;

@@ -76,3 +76,14 @@ def test_keep_tokens_refusals():
     vq.vq_keep_tokens(**dict(args, batch=0, seq_lens=None, keep=None))
     with pytest.raises(ValueError, match="layers"):
         vq.vq_keep_tokens(**dict(args, k_pools=[FAKE]))
+
+
+def test_a_tree_workspace_serves_every_call_within_its_bounds():
+    """The tile height depends on all of batch, tokens and the longest sequence's; a workspace does not run short for smaller ones."""
+    for L in (vq.make_layout(), vq.make_layout(num_q_heads=40, num_kv_heads=8), vq.make_layout(k_sub=8, k_bits=12, v_sub=8, v_bits=12)):
+        for B, T, n in [(8, 300, 64), (8, 512, 64), (24, 1464, 61), (4, 1000, 250), (16, 100, 8), (1, 96, 96)]:
+            most = vq.vq_tree_workspace_bytes(L, B, T, 5000, n, 152)
+            for b in range(1, B + 1):
+                for t in (1, T // 7, T // 3, T // 2, T):
+                    for m in {min(m, n) for m in (1, 4, 8, 9, n // 3, n // 2, n - 1, n)}:
+                        assert vq.vq_tree_workspace_bytes(L, b, t, 5000, m, 152) <= most, (B, T, n, b, t, m)

@@ -69,6 +69,13 @@ def test_ragged_batch_with_idle_sequences(n):
     c.check(200, 20)
 
 
+@pytest.mark.parametrize("rows", [16, 32, 128, 256])
+def test_every_tile_height_takes_every_batch(rows, monkeypatch):
+    """The height is a matter of time only: a ragged batch with idle sequences, at each of them."""
+    monkeypatch.setenv("VQ_TREE_ROWS", str(rows))
+    TreeCase(FORMATS[1], 8, 2, 64, [70, 300, 0, 1500, 64, 129], [64, 3, 0, 40, 0, 9], seed=rows).check()
+
+
 @pytest.mark.parametrize("fmt", [FORMATS[0], FORMATS[2], FORMATS[6]])
 @pytest.mark.parametrize("n", [2, 16, 33, 90])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (4096, 4)])
