@@ -189,7 +189,8 @@ __device__ __forceinline__ void tree_plan(const ChunkParams& p, long long* pre) 
 // codes one block ahead, which covers L2's latency and not the memory's; where few tiles share a sequence nearly
 // every code comes from there.  A lane takes 16 tokens of K or V; at most kAhead blocks ahead of `done`, which the
 // issuing warp moves on.  (26 drafted tokens of each of 16 sequences of 8000 to 16 000: 230 -> 225 us; 12 tokens with
-// tiles of 16 rows 610 -> 526; nothing where the codes were in L2 already.)  first: lanes' granules of a block, 0 .. 7 K and 8 .. 15 V, taken from `from` to `to` - 1.
+// tiles of 16 rows 610 -> 526; nothing where the codes were in L2 already.)  Granules of a block: 0 .. 7 K, 8 .. 15 V,
+// taken from `from` to `to` - 1.
 constexpr int kAhead = 16;
 struct CodePrefetch {
   uint32_t blocks = 0;  // over all pieces
