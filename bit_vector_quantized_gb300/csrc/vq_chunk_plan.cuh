@@ -45,6 +45,15 @@
 namespace vqk {
 namespace {
 
+// Slots of the ring by which a planning warp hands pieces to a CTA's other warps (vq_chunk_wide.cu, vq_tree.cu; a piece
+// has a block at least).  A slot is used again once every warp has taken its piece, and the warps that expand codes take
+// pieces ahead of the blocks that they store, so with too few slots the warps wait in a circle.  The products of block b
+// need the K tile of block b + 2, and the warps that store that one have looked kAhead blocks further: where every
+// piece is one block, at piece b + 2 + kAhead, whose slot must be that of a piece which the issuing warp has taken, b at the
+// latest.  (Fewer blocks than that at the end or the start wait for fewer pieces.)  A slot less is too few.
+constexpr int kWideAhead = 2, kWidePieces = 2 + kWideAhead;  // every block, and its page two ahead
+constexpr int kTreeAhead = 4, kTreePieces = 2 + kTreeAhead;  // every other block, and its page two of its own ahead
+
 struct ChunkSeq {
   int row0;   // first row (new token) in q and out
   int n;      // new tokens (0: nothing to do)

@@ -73,6 +73,7 @@ constexpr int kTile = 128;           // query rows of a CTA's tile, and tokens o
 constexpr int kSoftWarps = 8, kCodeWarps = 16;
 constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kCols = 512;
+constexpr uint32_t kPieces = kWidePieces;
 
 // One CTA alone, or the two CTAs of a pair that share a block's tiles.
 template <bool kPair>

@@ -153,12 +153,6 @@ struct __align__(16) WidePiece {
   __device__ __forceinline__ int block(int i) const { return i < sink ? i : lo + (i - sink); }
 };
 static_assert(sizeof(WidePiece) == 64, "the pieces' place in shared memory");
-// Pieces under way.  The code warps look two blocks ahead of the one they store,
-// while the issuer may still wait for that one: of pieces of one block each,
-// the issuer has read the stored block's, and two more are needed ahead of
-// it (pieces without a block are not handed out).
-constexpr uint32_t kPieces = 4;
-
 // pre[b]: the estimated length of the sequences before b, all KV heads (one warp).
 __device__ __forceinline__ void tree_plan(const ChunkParams& p, long long* pre) {
   const int lane = threadIdx.x & 31;

@@ -39,6 +39,10 @@ constexpr float kUnset = 1e30f;      // minus the maximum of a row that has seen
 constexpr int kBlockTok = 128;       // tokens of a block
 constexpr int kCodeWarps = 16;
 constexpr uint32_t kKStages = 4;
+constexpr int kCodeSets = 2;         // the code warps of a side take every other block
+constexpr uint32_t kPieces = kTreePieces;
+constexpr int kBarriers = 20 + 2 * kTreePieces;  // (one to spare: what follows is 16-byte aligned)
+static_assert(kTreeAhead == 2 * kCodeSets, "a code warp arrives for a block once it has looked two of its own further");
 
 // A softmax thread takes one token and 16 rows.
 constexpr int kColumns = 16;
@@ -64,7 +68,7 @@ struct TreeSmem {
   static constexpr int kP = kV + kVStages * kVTile;
   static constexpr int kQ = kP + kPTile;
   static constexpr int kMisc = kQ + kQTile;
-  static constexpr int kBars = 32 * 8 + kPieces * 64 + kMasks * 16 + 16;
+  static constexpr int kBars = kBarriers * 8 + kTreePieces * 64 + kMasks * 16 + 16;
   static constexpr int kTops = kMisc + kBars;  // [N] minus the maxima, [N] scales, [4][N] maxima or sums of the warps
   static constexpr int kTotal = kTops + 6 * N * 4;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
   uint64_t* const drain = q_full + 1;
   uint64_t* const piece_full = drain + 1;              // [kPieces] planning warp -> everybody
   uint64_t* const piece_empty = piece_full + kPieces;  // [kPieces]
-  WidePiece* const pieces = reinterpret_cast<WidePiece*>(bars + 32);                  // [kPieces]
+  WidePiece* const pieces = reinterpret_cast<WidePiece*>(bars + kBarriers);           // [kPieces]
   uint32_t* const masks = reinterpret_cast<uint32_t*>(pieces + kPieces);              // [kMasks][4] tokens that have a page
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
         }
         if (!more) return x;
         const int t = u.block(i) * kBlockTok + tok, lp = p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
-        i += 2;
+        i += kCodeSets;
         x.any = true;
         x.in = t < u.limit;
         x.kvh = u.kvh;
@@ -462,8 +466,8 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
       bool any = first.any, has = any && fetch(first);
       uint32_t blk = set, stage = set, phase = 1;
       auto next_stage = [&]() {
-        blk += 2;
-        stage += 2;
+        blk += kCodeSets;
+        stage += kCodeSets;
         if (stage >= kStages) {
           stage -= kStages;
           phase ^= 1u;
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
         const Where then = ahead;
         any = then.any;
         has = any && fetch(then);
-        ahead = advance();
+        ahead = advance();  // (may wait for pieces up to kTreeAhead blocks on, before this block's arrival: the ring holds them)
         if constexpr (kIsK) {
           tmem_wait_st();
           tc_fence_before();
