@@ -208,6 +208,10 @@ __device__ __forceinline__ float root(float x) {
   return y;
 }
 
+// Whether a centroid at fp32 distance d is farther off than one at `best` in truth too: the two distances are off by 2^-19 of
+// the farther together, and by what the vector's own error makes of them (of_x).
+__device__ __forceinline__ bool apart(float d, float best, float of_x) { return d > best + d * 1.9073486e-6f + of_x * root(d); }
+
 // Smallest and second smallest of two such pairs, with what the smallest is (the lower of equals).
 __device__ __forceinline__ void join_best(float& best, float& second, int& at, int lanes) {
   const float ob = __shfl_xor_sync(kAll, best, lanes), os = __shfl_xor_sync(kAll, second, lanes);
@@ -317,7 +321,7 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) join_best(best, second, at, m);
   if (best < INFINITY) {  // (else too far off for fp32, or not a number)
-    auto clear = [&]() { return second == INFINITY || second > best + second * 1.9073486e-6f + of_x * root(second); };  // 2^-19
+    auto clear = [&]() { return second == INFINITY || apart(second, best, of_x); };
     if (clear()) return at;
     // equal centroids count as one
     load_centroid<D>(tab, at, near);
@@ -334,14 +338,13 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
     if (clear()) return at;
   }
   // In 64 bits, those that fp32 does not rule out (all, where it told nothing).
-  const float limit = best + 2.f * (best * 1.9073486e-6f + of_x * root(best));
   double full[4], y[D], nearest = INFINITY;
   exact_vector(p, which, t, h, lane, full);
   exact_part<D>(s, full, y);
   at = 0;
   for (int j = lane; j < n; j += 32) {
     load_centroid<D>(tab, j, c);
-    if (distance<D>(x, c) > limit) continue;
+    if (apart(distance<D>(x, c), best, of_x)) continue;
     double score = 0.0;
 #pragma unroll
     for (int e = 0; e < D; ++e) score += 0.25 * c[e] * (c[e] + 4.0 * y[e]);  // (c: times -2)
@@ -528,7 +531,7 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
       }
       join_best(d0, far, code, 1);
       // (not a number or too far off for fp32: not told)
-      const bool unsure = near || !(far > d0 + far * 1.9073486e-6f + of_x[16 * r / kSubs] * root(far));  // 2^-19
+      const bool unsure = near || !apart(far, d0, of_x[16 * r / kSubs]);
       if (!(c & 1)) codes[row] = static_cast<uint16_t>(code);
       open[r] = __ballot_sync(kAll, unsure && !(c & 1));
     }
@@ -770,7 +773,7 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
       code = d < d0 ? j : code;
       d0 = fminf(d0, d);
     }
-    const bool unsure = near || !(far > d0 + far * 1.9073486e-6f + of_x * root(far));
+    const bool unsure = near || !apart(far, d0, of_x);
     // ---- steps 3 and 4 ------------------------------------------------------------------------------------------------
     uint32_t todo = slot >= 0 ? __ballot_sync(kAll, unsure) : 0u;
     while (todo) {
