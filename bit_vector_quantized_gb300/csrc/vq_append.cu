@@ -11,7 +11,7 @@
 // smallest score only, with the smallest and second smallest so far and which group the smallest was.
 //
 // Codes are exact.  In steps, each for the sub-vectors that the one before cannot tell:
-//   1. the group with the smallest score, if no other comes within the products' error;
+//   1. the group with the smallest score, if no other comes within the products' error and, for keys, that of x itself;
 //   2. its centroids by fp32 distances ||x - c||^2 (their error is relative to the distance, not to x):
 //      the nearest, if no other comes within the error of these and, for keys, of x itself;
 //   3. all centroids by fp32 distances (one warp), equal centroids counting as one;
@@ -368,6 +368,18 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
 template <int D>
 constexpr float kBand = D == 8 ? 7.6293945e-6f : 3.8146973e-6f;  // 2^-17, 2^-18: two scores' errors
 
+// Step 1: whether the second best group of a sub-vector may hold the nearest centroid, from the two groups' scores and |x|^2.
+// The products' error: at most 2^-18 (sub-vectors of 8; of fewer 2^-19) of ||c||^2 + 2 |x| |c| each: products of 11 bits by
+// 11 are exact, each of up to 19 sums is off by 2^-23 of it at most, x without its high and low parts by 2^-22, of centroids
+// that are as near as the nearest, so with |c| up to |x| + distance (and no longer than the longest).
+// And the vector's own: apart() holds for what is farther than root(nearest) + of_x.
+template <int D>
+__device__ __forceinline__ bool groups_near(float best, float second, float x2, float cmax2, float of_x) {
+  const float x1 = root(x2), nearest = fmaxf(best + x2, 0.f), reach = fmaf(1.01f, x1, root(nearest));
+  const float c2 = fminf(reach * reach, cmax2), band = kBand<D> * fmaf(2.f * x1, root(c2), c2);
+  return !(second > best + band + of_x * fmaf(2.f, root(nearest + band), of_x));
+}
+
 // Rows, codebook and scratch of the CTA.  Shared memory: the table, the norms, then for each warp its vectors in fp32
 // and their codes.
 template <int D, int R>
@@ -510,12 +522,7 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
         x[e] = xs[row * D + e];
         x2 = fmaf(x[e], x[e], x2);
       }
-      // The products' error: at most 2^-18 (sub-vectors of 8; of fewer 2^-19) of ||c||^2 + 2 |x| |c| each: products of 11 bits by
-      // 11 are exact, each of up to 19 sums is off by 2^-23 of it at most, x without its high and low parts by 2^-22, of centroids that are as near as the nearest, so
-      // with |c| up to |x| + distance (and no longer than the longest).
-      const float x1 = root(x2), reach = fmaf(1.01f, x1, root(fmaxf(b + x2, 0.f)));
-      const float c2 = fminf(reach * reach, cmax2);
-      const bool near = sec <= b + kBand<D> * fmaf(2.f * x1, root(c2), c2);
+      const bool near = groups_near<D>(b, sec, x2, cmax2, of_x[16 * r / kSubs]);
       // of the group's four blocks this lane's two, two centroids each
       const int j = 32 * (id >> 2) + 16 * (c & 1) + 2 * (id & 3);
       float d0 = INFINITY, far = INFINITY;
@@ -758,9 +765,7 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
       }
     }
     // ---- steps 1 and 2: a lane's group, each lane beginning elsewhere in it (banks) ----------------------------------
-    const float x1 = root(x2), reach = fmaf(1.01f, x1, root(fmaxf(best + x2, 0.f)));
-    const float c2 = fminf(reach * reach, cmax2);
-    const bool near = second <= best + kBand<D> * fmaf(2.f * x1, root(c2), c2);
+    const bool near = groups_near<D>(best, second, x2, cmax2, of_x);
     float d0 = INFINITY, far = INFINITY;
     int code = id;
 #pragma unroll

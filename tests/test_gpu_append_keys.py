@@ -31,9 +31,9 @@ def case(fmt, tokens, seed, dtype=torch.float16, **kw):
 
 
 @pytest.mark.parametrize("fmt", [FORMATS[0], FORMATS[1], FORMATS[6]])
-@pytest.mark.parametrize("other", [1])
+@pytest.mark.parametrize("other", [1, 200])
 def test_small_parts_of_a_long_key(fmt, other):
-    """All but one sub-vector are about halfway between two small centroids, in one group of the search; what the
+    """All but one sub-vector are about halfway between two small centroids, in one group of the search or in two; what the
     key's roundings move them by grows with the whole key."""
     c = case(fmt, 1, 5)
     rng = np.random.default_rng(6)
