@@ -13,10 +13,14 @@
 // Codes are exact.  In steps, each for the sub-vectors that the one before cannot tell:
 //   1. the group with the smallest score, if no other comes within the products' error and, for keys, that of x itself;
 //   2. its centroids by fp32 distances ||x - c||^2 (their error is relative to the distance, not to x):
-//      the nearest, if no other comes within the error of these and, for keys, of x itself;
-//   3. all centroids by fp32 distances (one warp), equal centroids counting as one;
-//   4. in 64 bits, for keys from the rows on, the centroids that fp32 does not rule out (one warp).
-// Of drawn sub-vectors of 4 step 1 leaves 4 in 10 000, step 2 one in 100 000 of keys; tests put all of them there.
+//      the nearest, if no other comes within the error of these and, for keys, of x itself (turn_key counts it);
+//   3. the group's centroids (all, where step 1 could not tell) by fp32 distances once more (one warp): those as near as that,
+//      equal ones counting as one;
+//   4. these in 64 bits, for keys from the rows on (one warp).
+// The errors are bounds, not deviations: what fp32 tells is so for every key.  They leave one to three of 10 000
+// sub-vectors of drawn keys to steps 3 and 4, where the errors themselves are some fifteen times smaller.  Those
+// wait for the end of a CTA's vectors, when its warps share them (at once they held up their teams: 202 us instead of 195 for 4099
+// bf16 tokens at (2,8) and (4,9), 244 instead of 234 for 8192 at (4,8), 149 instead of 135 for 333 at 1.5 bit).
 //
 // Two kernels.  8- and 9-bit codes: tcgen05, 128 sub-vectors by 128 centroids a product; tensor memory gives the
 // minima of 16 columns as it is read (tcgen05.ld.red).  12-bit codes, whose 4096 centroids do not fit shared memory as
@@ -33,6 +37,7 @@
 // tensor pipe is 53 % busy with products of k = 8 (333 tokens of 8 KV heads: 135 us, floor 3).
 #include "vq_rotary.cuh"
 #include "vq_tcgen05.cuh"
+#include "vq_turn.cuh"
 
 #include <algorithm>
 
@@ -47,25 +52,43 @@ __device__ __forceinline__ double row_value(const AppendParams& p, const uint16_
   return p.bf16 ? to_float<true>(x) : to_float<false>(x);
 }
 
-// Elements 4 lane .. 4 lane + 3 of a vector as they are coded, in 64 bits (one warp).
+// Elements 4 lane .. 4 lane + 3 of a vector as they are coded, in 64 bits (one warp).  64-bit instructions issue at a
+// fifteenth of the 32-bit ones' rate, so an angle's sine and cosine are formed once and by turn_sincos.
 __device__ __forceinline__ void exact_vector(const AppendParams& p, int which, long long t, int h, int lane, double (&x)[4]) {
   const uint16_t* const row = static_cast<const uint16_t*>(p.src[which]) + t * p.stride[which] + h * kHeadDim;
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = row_value(p, row, 4 * lane + i);
   if (which != 0) return;
-  const int half = p.rotary_dim / 2;
+  const int r = p.rotary_dim, half = r / 2;
   const unsigned long long pos = static_cast<unsigned long long>(__ldg(p.positions + t));
+  auto first = [&](int e) { return p.interleaved ? !(e & 1) : e < half; };
+  auto pair = [&](int e) { return p.interleaved ? e >> 1 : e < half ? e : e - half; };
+  double si[4], co[4];
+  const bool shared = p.interleaved || (half & 3) == 0;  // two of the lane's elements have one angle, or two lanes have the same four
+  const int step = p.interleaved ? 2 : 1, count = shared ? 2 : 4, from = shared && !p.interleaved && 4 * lane >= half ? 2 : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    si[i] = 0.0;
+    co[i] = 1.0;
+    if (i < count && 4 * lane + from + step * i < r) turn_sincos(p.freq[pair(4 * lane + from + step * i)] * pos, si[i], co[i]);
+  }
+  if (p.interleaved) {
+    si[2] = si[3] = si[1], co[2] = co[3] = co[1];
+    si[1] = si[0], co[1] = co[0];
+  } else if (shared) {
+    const int other = 4 * lane >= r ? lane : 4 * lane < half ? lane + half / 4 : lane - half / 4;
+    const double s0 = __shfl_sync(kAll, si[0], other), s1 = __shfl_sync(kAll, si[1], other);
+    const double c0 = __shfl_sync(kAll, co[0], other), c1 = __shfl_sync(kAll, co[1], other);
+    const bool low = from == 0;
+    si[2] = low ? s0 : si[0], si[3] = low ? s1 : si[1], co[2] = low ? c0 : co[0], co[3] = low ? c1 : co[1];
+    si[0] = low ? si[0] : s0, si[1] = low ? si[1] : s1, co[0] = low ? co[0] : c0, co[1] = low ? co[1] : c1;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = 4 * lane + i;
-    if (e < p.rotary_dim) {
-      const bool first = p.interleaved ? !(e & 1) : e < half;
-      const int pair = p.interleaved ? e >> 1 : first ? e : e - half;
-      const int other = p.interleaved ? e ^ 1 : first ? e + half : e - half;
-      double si, co;  // (the fraction of a turn, in half turns)
-      sincospi(static_cast<double>(static_cast<long long>(p.freq[pair] * pos)) * 1.0842021724855044e-19, &si, &co);
-      const double y = row_value(p, row, other);
-      x[i] = p.factor * (first ? x[i] * co - y * si : x[i] * co + y * si);
+    if (e < r) {
+      const double y = row_value(p, row, p.interleaved ? e ^ 1 : e < half ? e + half : e - half);
+      x[i] = p.factor * (first(e) ? x[i] * co[i] - y * si[i] : x[i] * co[i] + y * si[i]);
     }
     x[i] /= __ldg(p.lambda + h * kHeadDim + e);
   }
@@ -97,15 +120,18 @@ __device__ __forceinline__ void exact_part(int s, const double (&x)[4], double (
   }
 }
 
+__device__ __forceinline__ uint32_t* code_row(const AppendParams& p, int which, long long slot, int h) {
+  const unsigned P = p.page_size;
+  const long long page = slot >> 32 ? slot / P : static_cast<unsigned>(slot) / P, off = slot - page * P;
+  return reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * P + off) * p.row_bytes[which]);
+}
+
 // Codes first .. first + count - 1 of a vector into its row of the pool (one warp), a word a lane; the words that they
 // fill are theirs alone.
 __device__ __forceinline__ void store_codes(const AppendParams& p, int which, const uint16_t* codes, int first, int count, long long slot, int h,
                                             int lane) {
   const int bits = p.bits[which], words = count * bits / 32;  // (whole words in every format)
-  const unsigned P = p.page_size;
-  const long long page = slot >> 32 ? slot / P : static_cast<unsigned>(slot) / P, off = slot - page * P;
-  uint32_t* const row =
-      reinterpret_cast<uint32_t*>(p.pool[which] + ((page * p.hkv + h) * P + off) * p.row_bytes[which]) + first * bits / 32;
+  uint32_t* const row = code_row(p, which, slot, h) + first * bits / 32;
   for (int w = lane; w < words; w += 32) {
     uint32_t x = 0;
     if (bits == 8) {  // four codes a word
@@ -247,8 +273,28 @@ __device__ __forceinline__ bool pair_piece(const AppendParams& p, int lane, int&
   return !p.interleaved && (half & 3) == 0 && 4 * lane < p.rotary_dim;
 }
 
-__device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* row, uint2 pair, long long t, int h, int lane, Angles& a, float (&x)[4]) {
+// Squared norm of a rotated pair (x, y) under one of its channels' factor / lambda.
+__device__ __forceinline__ float smoothed_pair(float x, float y, float inv) {
+  const float a = x * inv, b = y * inv;
+  return fmaf(a, a, b * b);
+}
+
+// Turns, smooths and transforms a key's elements 4 lane .. 4 lane + 3.  Returns four times the most that the key as it is
+// here can be off by in a sub-vector, which is what apart() wants: a difference of two distances moves by 2 error . (c - c'),
+// and |c - c'| is up to twice the root of the farther one.  With u = 2^-24 (half a step of 1, relative), the pairs' norms w
+// (unturned, times the factor, by a channel's own lambda, so that a strong channel counts beside a partner of small lambda), |k~|:
+//   * rotation, of a pair's norm: the angle's rounding pi / 4 u, sine and cosine an ulp each (1.42 u), the two products
+//     and their sum 2 u, together under 4.3 u; the factor's own rounding and the products with it, where it is not 1, 2 u;
+//   * of |k~|: the division u, seven butterflies 7 u, the last product and its constant 1.3 u: under 9.4 u.
+// The transform keeps norms, so that is the most in all of the key, and also the most that one sub-vector can get of it: it does
+// where the key follows a row of the transform and its elements round alike.  (a |w| + b |k~|)^2 <= (1 + t) a^2 |w|^2 +
+// (1 + 1 / t) b^2 |k~|^2 for any t; t = 1.04 gives at most 13.2 u root(|k~|^2 + 0.22 |w|^2), 0.47 with a factor.
+__device__ __forceinline__ float turn_key(const AppendParams& p, const uint16_t* row, uint2 pair, long long t, int h, int lane, Angles& a, float (&x)[4]) {
   const int r = p.rotary_dim, half = r / 2;
+  const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + h * kHeadDim) + lane);
+  const float factor = static_cast<float>(p.factor), inv[4] = {__fdividef(factor, lam.x), __fdividef(factor, lam.y), __fdividef(factor, lam.z),
+                                                               __fdividef(factor, lam.w)};
+  float pairs = 0.f;
   if (a.t != t) {
     a.t = t;
     const unsigned long long pos = static_cast<unsigned long long>(__ldg(p.positions + t));
@@ -260,7 +306,11 @@ __device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* 
         a.si[i] = a.si[i - 1];
       } else if (e < r) {
         const unsigned long long turn = p.freq[p.interleaved ? e >> 1 : e < half ? e : e - half] * pos;
-        sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, a.si + i, a.co + i);  // 2^-31
+        // (folded to half a turn around none, where its rounding to fp32 is half as far off)
+        const uint32_t at = static_cast<uint32_t>(turn >> 32);
+        const bool fold = (at + 0x40000000u) >> 31;
+        sincospif(static_cast<float>(static_cast<int>(fold ? 0x80000000u - at : at)) * 4.656612873077393e-10f, a.si + i, a.co + i);  // 2^-31
+        if (fold) a.co[i] = -a.co[i];
         a.co[i] *= static_cast<float>(p.factor);
         a.si[i] *= static_cast<float>(p.factor);
       }
@@ -270,6 +320,7 @@ __device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* 
 #pragma unroll
     for (int i = 0; i < 4; i += 2)
       if (4 * lane + i < r) {
+        pairs += smoothed_pair(x[i], x[i + 1], inv[i]) + smoothed_pair(x[i], x[i + 1], inv[i + 1]);
         const float y = x[i] * a.co[i] - x[i + 1] * a.si[i];
         x[i + 1] = x[i + 1] * a.co[i] + x[i] * a.si[i];
         x[i] = y;
@@ -289,10 +340,12 @@ __device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = 4 * lane + i;
-      if (e < r) x[i] = e < half ? x[i] * a.co[i] - y[i] * a.si[i] : x[i] * a.co[i] + y[i] * a.si[i];
+      if (e < r) {
+        pairs += smoothed_pair(x[i], y[i], inv[i]);
+        x[i] = e < half ? x[i] * a.co[i] - y[i] * a.si[i] : x[i] * a.co[i] + y[i] * a.si[i];
+      }
     }
   }
-  const float4 lam = __ldg(reinterpret_cast<const float4*>(p.lambda + h * kHeadDim) + lane);
   x[0] /= lam.x;
   x[1] /= lam.y;
   x[2] /= lam.z;
@@ -300,51 +353,45 @@ __device__ __forceinline__ void turn_key(const AppendParams& p, const uint16_t* 
   fwht128_warp(x, lane);
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] *= 0.08838834764831845f;  // 1 / sqrt(128)
+  float sum = fmaf(__double_as_longlong(p.factor) == 0x3ff0000000000000LL ? 0.22f : 0.47f, pairs, fmaf(x[0], x[0], fmaf(x[1], x[1], fmaf(x[2], x[2], x[3] * x[3]))));
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
+  return 53.f * 5.9604645e-8f * root(sum);
 }
 
-// Steps 3 and 4 of a sub-vector that the steps before could not tell (one warp; rare, so not inlined).
+// Steps 3 and 4 of sub-vector s, of which the steps before found `code` (not told apart from others): among its group's
+// centroids, or with `all` all of them (one warp; rare, so not inlined).
 template <int D>
-__device__ __noinline__ int settle(const AppendParams& p, int which, long long t, int h, int s, const float* xs, const float* tab, float of_x) {
-  const int lane = threadIdx.x & 31, n = 1 << p.bits[which];
+__device__ __noinline__ int settle(const AppendParams& p, int which, long long t, int h, int s, const float* xs, const float* tab, float of_x, int code,
+                                   bool all) {
+  constexpr int kGroup = D == 8 ? 32 : 16;  // of step 1
+  const int lane = threadIdx.x & 31, j0 = all ? 0 : code & -kGroup, end = all ? 1 << p.bits[which] : j0 + kGroup;
   float x[D], c[D], near[D];
 #pragma unroll
   for (int e = 0; e < D; ++e) x[e] = xs[s * D + e];
-  float best = INFINITY, second = INFINITY;
-  int at = 0x7fffffff;
-  for (int j = lane; j < n; j += 32) {
+  load_centroid<D>(tab, code, near);
+  const float best = distance<D>(x, near);
+  // Whatever is past this is apart() from `best`: its root is past root(best) + of_x.
+  const float limit = (best + of_x * fmaf(2.f, root(best), of_x)) * 1.0000038f;  // 1 + 2^-18
+  int open[2] = {}, count = 0;  // of this lane
+  bool other = false;           // one that is not `code`'s centroid by another index
+  for (int j = j0 + lane; j < end; j += 32) {
     load_centroid<D>(tab, j, c);
-    const float d = distance<D>(x, c);
-    second = fminf(second, fmaxf(best, d));
-    at = d < best ? j : at;
-    best = fminf(best, d);
+    if (distance<D>(x, c) > limit) continue;  // (all are open where fp32 tells nothing: too far off, or not a number)
+    if (count < 2) open[count] = j;
+    ++count;
+#pragma unroll
+    for (int e = 0; e < D; ++e) other |= !(c[e] == near[e]);
   }
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) join_best(best, second, at, m);
-  if (best < INFINITY) {  // (else too far off for fp32, or not a number)
-    auto clear = [&]() { return second == INFINITY || apart(second, best, of_x); };
-    if (clear()) return at;
-    // equal centroids count as one
-    load_centroid<D>(tab, at, near);
-    second = INFINITY;
-    for (int j = lane; j < n; j += 32) {
-      load_centroid<D>(tab, j, c);
-      bool same = true;
-#pragma unroll
-      for (int e = 0; e < D; ++e) same &= c[e] == near[e];
-      if (!same) second = fminf(second, distance<D>(x, c));
-    }
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) second = fminf(second, __shfl_xor_sync(kAll, second, m));
-    if (clear()) return at;
-  }
-  // In 64 bits, those that fp32 does not rule out (all, where it told nothing).
+  const bool few = __all_sync(kAll, count <= 2);
+  if (!__any_sync(kAll, other)) return __reduce_min_sync(kAll, count ? open[0] : code);
+  // ---- in 64 bits ----------------------------------------------------------------------------------------------
   double full[4], y[D], nearest = INFINITY;
   exact_vector(p, which, t, h, lane, full);
   exact_part<D>(s, full, y);
-  at = 0;
-  for (int j = lane; j < n; j += 32) {
+  int at = code;
+  auto look = [&](int j) {
     load_centroid<D>(tab, j, c);
-    if (apart(distance<D>(x, c), best, of_x)) continue;
     double score = 0.0;
 #pragma unroll
     for (int e = 0; e < D; ++e) score += 0.25 * c[e] * (c[e] + 4.0 * y[e]);  // (c: times -2)
@@ -352,17 +399,72 @@ __device__ __noinline__ int settle(const AppendParams& p, int which, long long t
       nearest = score;
       at = j;
     }
+  };
+  if (few) {
+    if (count > 0) look(open[0]);
+    if (count > 1) look(open[1]);
+  } else {
+    for (int j = j0 + lane; j < end; j += 32) look(j);
   }
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const double other = __shfl_xor_sync(kAll, nearest, m);
-    const int its = __shfl_xor_sync(kAll, at, m);
-    if (other < nearest || (other == nearest && its < at)) {
-      nearest = other;
-      at = its;
+    const double its = __shfl_xor_sync(kAll, nearest, m);
+    const int j = __shfl_xor_sync(kAll, at, m);
+    if (its < nearest || (its == nearest && j < at)) {
+      nearest = its;
+      at = j;
     }
   }
   return at;
+}
+
+// What steps 1 and 2 leave open waits for the end of the CTA's vectors: its warps share it then, where each would hold up its
+// team at once.
+struct OpenCode {
+  int t, h, s, code;  // s: the sub-vector, and kAllGroups where step 1 told none
+};
+constexpr int kOpenCodes = 64, kAllGroups = 0x10000;
+struct OpenList {
+  int count;  // (may pass kOpenCodes: those were settled at once)
+  OpenCode at[kOpenCodes];
+};
+
+// Puts the lanes' open codes (`todo`: one bit a lane) on the list; returns those that found no place.
+__device__ __forceinline__ uint32_t put_open(OpenList& list, uint32_t todo, int t, int h, int s, int code, bool all) {
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(&list.count, __popc(todo));
+  at = __shfl_sync(kAll, at, 0) + __popc(todo & ((1u << lane) - 1u));
+  const bool mine = todo >> lane & 1u, room = at < kOpenCodes;
+  if (mine && room) list.at[at] = {t, h, all ? s | kAllGroups : s, code};
+  return __ballot_sync(kAll, mine && !room);
+}
+
+// One of them (one warp; xs: 128 floats of the warp's): the vector once more, steps 3 and 4, the code in its row put right.
+template <int D>
+__device__ __noinline__ void settle_open(const AppendParams& p, int which, const OpenCode& open, const float* tab, float* xs) {
+  const int lane = threadIdx.x & 31, t = open.t, h = open.h, s = open.s & (kAllGroups - 1);
+  const uint16_t* const src = static_cast<const uint16_t*>(p.src[which]) + t * p.stride[which] + h * kHeadDim;
+  float raw[4], of_x = 0.f;
+  load_raw(p, src, 4 * lane, raw);
+  if (which == 0) {
+    uint2 pair = make_uint2(0u, 0u);
+    int e;
+    if (pair_piece(p, lane, e)) pair = __ldg(reinterpret_cast<const uint2*>(src + e));
+    Angles angles;
+    of_x = turn_key(p, src, pair, t, h, lane, angles, raw);
+  }
+  __syncwarp();
+  *reinterpret_cast<float4*>(xs + 4 * lane) = make_float4(raw[0], raw[1], raw[2], raw[3]);
+  __syncwarp();
+  const int code = settle<D>(p, which, t, h, s, xs, tab, of_x, open.code, open.s & kAllGroups);
+  if (code == open.code || lane != 0) return;
+  // Bits of the row's words; another warp may be at others of them.
+  const int bit = s * p.bits[which];
+  const unsigned long long change = static_cast<unsigned long long>(code ^ open.code) << (bit & 31);
+  uint32_t* const word = code_row(p, which, append_slot(p, t, false), h) + (bit >> 5);
+  atomicXor(word, static_cast<uint32_t>(change));
+  if (change >> 32) atomicXor(word + 1, static_cast<uint32_t>(change >> 32));
 }
 
 template <int D>
@@ -391,7 +493,7 @@ struct AppendShape {
 
 // One tensor's vectors by warp mma: R tiles of 16 sub-vectors a pass and warp.
 template <int D, int R>
-__device__ __forceinline__ void append_tensor(const AppendParams& p, int which, int cta, int ctas, uint8_t* smem, int* top) {
+__device__ __forceinline__ void append_tensor(const AppendParams& p, int which, int cta, int ctas, uint8_t* smem, int* top, OpenList& list) {
   using Shape = AppendShape<D, R>;
   constexpr int NV = Shape::kVectors, kSubs = kHeadDim / D;  // sub-vectors of a vector
   const int n = 1 << p.bits[which];
@@ -423,7 +525,7 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
     // ---- the vectors as they are coded ---------------------------------------------------------------------
     long long slot[NV];
     uint2 pair[NV];
-    float raw[NV][4], of_x[NV];  // of_x: what x's own error can make of a difference of distances, times the distance's root
+    float raw[NV][4], of_x[NV];  // of_x: turn_key's, of values (which are exact) 0
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       slot[v] = v0 + v < v1 ? append_slot(p, tok[v], lane == 0) : -1;
@@ -440,16 +542,9 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       of_x[v] = 0.f;
-      if (which == 0 && slot[v] >= 0) {
-        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok[v] * p.stride[0] + head[v] * kHeadDim, pair[v], tok[v], head[v], lane, angles, raw[v]);
-        float sum = fmaf(raw[v][0], raw[v][0], fmaf(raw[v][1], raw[v][1], fmaf(raw[v][2], raw[v][2], raw[v][3] * raw[v][3])));
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
-        // Each element of k~ is off by 1.3 2^-24 of its rms (rotation, division, butterflies: independent roundings), a
-        // difference of two distances by 2 error . (c - c'), |c - c'| up to twice the distance's root: this is nine
-        // times its deviation, and more than an error that all elements share can make of it.
-        of_x[v] = 4.f * root(sum) * 5.9604645e-8f;
-      }
+      if (which == 0 && slot[v] >= 0)
+        of_x[v] = turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok[v] * p.stride[0] + head[v] * kHeadDim, pair[v], tok[v], head[v], lane, angles,
+                           raw[v]);
       *reinterpret_cast<float4*>(xs + v * kHeadDim + 4 * lane) = make_float4(raw[v][0], raw[v][1], raw[v][2], raw[v][3]);
     }
     __syncwarp();
@@ -502,7 +597,8 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
         }
     }
     // ---- steps 1 and 2: a quad has two rows; lanes c < 2 go on with row g, the others with row g + 8 ------------
-    uint32_t open[R];  // bit 4 g + 2 i: row g + 8 i is not told yet
+    uint32_t open[R];  // of lanes 4 g + 2 i: row g + 8 i is not told yet, and found no place on the list
+    int found[R];      // (of the lane's row, and kAllGroups)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int half = c >> 1, row = 16 * r + g + 8 * half;
@@ -540,7 +636,9 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
       // (not a number or too far off for fp32: not told)
       const bool unsure = near || !apart(far, d0, of_x[16 * r / kSubs]);
       if (!(c & 1)) codes[row] = static_cast<uint16_t>(code);
-      open[r] = __ballot_sync(kAll, unsure && !(c & 1));
+      found[r] = near ? code | kAllGroups : code;
+      open[r] = __ballot_sync(kAll, unsure && !(c & 1) && slot[16 * r / kSubs] >= 0);
+      if (open[r]) open[r] = put_open(list, open[r], tok[16 * r / kSubs], head[16 * r / kSubs], row % kSubs, code, near);
     }
     __syncwarp();
     // ---- steps 3 and 4 ------------------------------------------------------------------------------------------
@@ -549,10 +647,9 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
       uint32_t todo = open[r];
       while (todo) {
         constexpr int kTiles = kSubs / 16;  // of a vector
-        const int v = r / kTiles, bit = __ffs(todo) - 1, row = 16 * r + (bit >> 2) + 4 * (bit & 2);
+        const int v = r / kTiles, bit = __ffs(todo) - 1, row = 16 * r + (bit >> 2) + 4 * (bit & 2), was = __shfl_sync(kAll, found[r], bit);
         todo &= todo - 1u;
-        if (slot[v] < 0) continue;
-        const int code = settle<D>(p, which, tok[v], head[v], row % kSubs, xs + v * kHeadDim, tab, of_x[v]);
+        const int code = settle<D>(p, which, tok[v], head[v], row % kSubs, xs + v * kHeadDim, tab, of_x[v], was & (kAllGroups - 1), was & kAllGroups);
         if (lane == 0) codes[row] = static_cast<uint16_t>(code);
       }
     }
@@ -562,6 +659,8 @@ __device__ __forceinline__ void append_tensor(const AppendParams& p, int which, 
       if (slot[v] >= 0) store_codes(p, which, codes + v * kSubs, 0, kSubs, slot[v], head[v], lane);
     __syncwarp();
   }
+  __syncthreads();
+  for (int i = warp; i < min(list.count, kOpenCodes); i += warps) settle_open<D>(p, which, list.at[i], tab, xs);
 }
 
 // The CTAs from `first` on turn queries.
@@ -577,16 +676,17 @@ __device__ __forceinline__ void append_queries(const AppendParams& p, int first)
 __global__ void __launch_bounds__(kAppThreads, 1) vq_append_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(16) uint8_t app_smem[];
   __shared__ int top;  // the largest ||c||^2
+  __shared__ OpenList list;
   const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
   if (static_cast<int>(blockIdx.x) >= ctas) {  // queries
     append_queries(p, ctas);
     return;
   }
   const int which = static_cast<int>(blockIdx.x) >= ctas0, cta = static_cast<int>(blockIdx.x) - which * ctas0;
-  if (threadIdx.x == 0) top = 0;
+  if (threadIdx.x == 0) top = list.count = 0;
   __syncthreads();
-  if (p.few) append_tensor<8, 1>(p, which, cta, p.kv_ctas[which], app_smem, &top);
-  else append_tensor<8, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top);
+  if (p.few) append_tensor<8, 1>(p, which, cta, p.kv_ctas[which], app_smem, &top, list);
+  else append_tensor<8, 2>(p, which, cta, p.kv_ctas[which], app_smem, &top, list);
 }
 
 // ---- 8- and 9-bit codes: the products on the tensor cores ----------------------------------------------------------
@@ -644,7 +744,7 @@ __host__ __device__ inline TcSmem tc_smem(int d, int n) {
 
 template <int D>
 __device__ __forceinline__ void append_products(const AppendParams& p, int which, int cta, int ctas, uint8_t* smem, int* top, uint32_t tmem,
-                                                uint64_t* bars, volatile int* abort_flag) {
+                                                uint64_t* bars, volatile int* abort_flag, OpenList& list) {
   constexpr int kVectors = 128 * D / kHeadDim;  // of a team's tile
   const int n = 1 << p.bits[which];
   const TcSmem at = tc_smem(D, n);
@@ -702,13 +802,8 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
     float raw[4] = {0.f, 0.f, 0.f, 0.f}, of_x = 0.f;
     if (slot >= 0) {
       raw_values(p, next.raw, raw);
-      if (which == 0) {
-        turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok * p.stride[0] + head * kHeadDim, next.pair, tok, head, lane, angles, raw);
-        float sum = fmaf(raw[0], raw[0], fmaf(raw[1], raw[1], fmaf(raw[2], raw[2], raw[3] * raw[3])));
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) sum += __shfl_xor_sync(kAll, sum, m);
-        of_x = 4.f * root(sum) * 5.9604645e-8f;  // (append_tensor has the reason)
-      }
+      if (which == 0)
+        of_x = turn_key(p, static_cast<const uint16_t*>(p.src[0]) + tok * p.stride[0] + head * kHeadDim, next.pair, tok, head, lane, angles, raw);
     }
     *reinterpret_cast<float4*>(xs + 4 * lane) = make_float4(raw[0], raw[1], raw[2], raw[3]);
     __syncwarp();
@@ -781,10 +876,11 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
     const bool unsure = near || !apart(far, d0, of_x);
     // ---- steps 3 and 4 ------------------------------------------------------------------------------------------------
     uint32_t todo = slot >= 0 ? __ballot_sync(kAll, unsure) : 0u;
+    if (todo) todo = put_open(list, todo, tok, head, 32 * half + lane, code, near);
     while (todo) {
-      const int i = __ffs(todo) - 1;
+      const int i = __ffs(todo) - 1, was = __shfl_sync(kAll, near ? code | kAllGroups : code, i);
       todo &= todo - 1u;
-      const int told = settle<D>(p, which, tok, head, 32 * half + i, xs, tab, of_x);
+      const int told = settle<D>(p, which, tok, head, 32 * half + i, xs, tab, of_x, was & (kAllGroups - 1), was & kAllGroups);
       if (lane == i) code = told;
     }
     codes[lane] = static_cast<uint16_t>(code);
@@ -802,11 +898,14 @@ __device__ __forceinline__ void append_products(const AppendParams& p, int which
       break;
     }
   }
+  __syncthreads();
+  for (int i = warp; i < min(list.count, kOpenCodes); i += kTcThreads / 32) settle_open<D>(p, which, list.at[i], tab, xs);
 }
 
 __global__ void __launch_bounds__(kTcThreads, 2) vq_append_tc_kernel(const __grid_constant__ AppendParams p) {
   extern __shared__ __align__(16) uint8_t app_smem[];
   __shared__ int top, abort_flag;  // the largest ||c||^2
+  __shared__ OpenList list;
   __shared__ uint32_t tmem_at;
   __shared__ uint64_t bars[2];
   const int ctas0 = p.kv_ctas[0], ctas = ctas0 + p.kv_ctas[1];
@@ -817,7 +916,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) vq_append_tc_kernel(const __gri
   const int which = static_cast<int>(blockIdx.x) >= ctas0, cta = static_cast<int>(blockIdx.x) - which * ctas0;
   uint8_t* const smem = app_smem + (-smem_addr(app_smem) & 1023u);
   if (threadIdx.x == 0) {
-    top = abort_flag = 0;
+    top = abort_flag = list.count = 0;
     mbar_init(bars, 1);
     mbar_init(bars + 1, 1);
     mbar_init_fence();
@@ -827,8 +926,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) vq_append_tc_kernel(const __gri
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
-  if (p.sub[which] == 2) append_products<2>(p, which, cta, p.kv_ctas[which], smem, &top, tmem, bars, &abort_flag);
-  else append_products<4>(p, which, cta, p.kv_ctas[which], smem, &top, tmem, bars, &abort_flag);
+  if (p.sub[which] == 2) append_products<2>(p, which, cta, p.kv_ctas[which], smem, &top, tmem, bars, &abort_flag, list);
+  else append_products<4>(p, which, cta, p.kv_ctas[which], smem, &top, tmem, bars, &abort_flag, list);
   tc_fence_before();
   __syncthreads();  // (a product that a team gave up on has had the wait's limit to end)
   tc_fence_after();
@@ -857,7 +956,9 @@ cudaError_t launch_products(AppendParams p, int sms, long long queries, cudaStre
     const int d = p.sub[i], n = 1 << p.bits[i], per_cta = 2 * 128 * d / kHeadDim;
     smem = std::max(smem, static_cast<size_t>(tc_smem(d, n).total + 1024));
     most[i] = (vectors + per_cta - 1) / per_cta;
-    cost[i] = (4.0 / d) * (n + (i == 0 ? 500 : 250));  // scores, and what else a vector takes
+    // scores and what else the sub-vectors take, a key's rotation and open codes (240: 8192 tokens at (4,8) 228 us, without 233;
+    // as part of the sub-vectors' it would be twice as much at (2,8): 4099 tokens 201 us instead of 195)
+    cost[i] = (4.0 / d) * (n + (i == 0 ? 380 : 250)) + (i == 0 ? 240 : 0);
   }
   cudaError_t e = ensure_smem(vq_append_tc_kernel, smem, opt);
   if (e != cudaSuccess) return e;
