@@ -1154,33 +1154,36 @@ ChunkWs chunk_ws(int tile_rows, int grid) {
   return w;
 }
 
-// Tile height of a call over trees of drafted tokens, by the rows of its longest (sequence, KV head): 16 or 32 of
-// vq_tree.cu where they hold them, else 128 (or what three of these hold, but for the 1.5-bit format) or 256 of
-// vq_chunk_wide.cu.  Measured as above (device time, merge included, cold L2; 4 heads per KV head):
-//   16 rows, batch 8: 45 us at 16, 49 at 32, 55 at 128; 20 to 32 rows: 61 at 16, 49 to 51 at 32, 55 at 128;
-//     batch 16 at (2,8): 76 at 32, 86 at 128; 1.5 bit, batch 48: 16 rows 154, 162 and 166, 28 rows 281, 171 and 168
-//   64 rows, batch 8: 72 us at 32, 55 at 128, 78 at 256; 96 and 128 rows: 59 at 128, 80 at 256
-//   192 rows, batch 8: 84 us at 128 and at 256; batch 16 at (2,8): 150 and 133; 250 rows at (2,8), (4,9): 274 and 233;
-//     256 rows, 1.5 bit: 86 and 78
-//   320 rows, batch 8: 117 us at 128, 131 at 256; 384 rows, batch 16 at (2,8): 215 and 238
+// Tile height of a call over trees of drafted tokens, by the rows of its longest (sequence, KV head): 16 or (but for the 1.5-bit
+// format) 32 of vq_tree.cu where they hold them, else 128 (or what three of these hold, but for the 1.5-bit format) or 256
+// of vq_chunk_wide.cu.  Measured (us a call of many, merge included, inputs that change; contexts of 4000 to 8000, 4 heads
+// per KV head, (4,8) where nothing else is said):
+//   16 rows, batch 8: 41 at 16, 49 at 32, 55 at 128; 20 to 32 rows: 59 at 16, 49 at 32, 56 at 128
+//   1.5 bit, contexts of 3000 to 6000, batch 48: 16 rows 153 at 16, 185 at 128; 28 rows 288 at 16, 186 at 128
+//   64 rows, batch 8: 74 at 32, 57 at 128, 84 at 256
+//   192 rows, batch 8: 92 at 128, 89 at 256; batch 16 at (2,8): 161 and 154; 250 rows at (2,8), (4,9): 175 and 161;
+//     256 rows, 1.5 bit: 110 and 96
+//   320 rows, batch 8: 124 at 128, 146 at 256; 384 rows, batch 16 at (2,8): 239 and 284
 // Trees of different sizes under a bound of two tiles of 128 rows: one such tile takes about 0.7 of the time of a tile of
 // 256, two of them 1.1, so 128 wins where a third of the sequences need one only.  For sizes spread evenly that is a mean
-// of at most 96 rows and a quarter of the bound.  (Sequences without drafted tokens lower the mean too.)  At 128 | 256:
-//   1 to 61 tokens, batch 24, (2,8): 139 | 150 and, all contexts 4000 to 8000, 166 | 184; 1 to 64, batch 8, 72 | 82; 16 to 64,
-//     182 | 184; 5 heads, (2,8), (4,9), 1 to 50, 211 | 225; 1.5 bit, 1 to 64 145 | 154, 16 to 64 154 | 154
-//   above that mean: 20 to 50 of 5 heads 250 | 229, 30 to 40 186 | 186 (24 to 64 at (4,8) 127 | 131)
-// VQ_TREE_ROWS=16|32|128|256 selects one explicitly (a tuning
-// switch for profiling).
+// of at most 96 rows and a quarter of the bound.  (Sequences without drafted tokens lower the mean too.)  At 128 | 256, batch
+// 24, contexts of 0 to 9001:
+//   1 to 61 tokens at (2,8) 144 | 168, 1 to 50 of 5 heads at (2,8), (4,9) 153 | 172, 1 to 64 at 1.5 bit 162 | 169
+//   above that mean: 20 to 50 of 5 heads 178 | 175
+// The mean is that of num_tokens, the rows of the tensors: where a captured graph has rows for the bound of every sequence, the
+// mean is the bound and the height 256.
+// VQ_TREE_ROWS=16|32|128|256 selects one explicitly (a tuning switch for profiling).
 int tree_tile_rows(const vq_layout& L, int batch, int num_tokens, int max_new_len) {
+  const int group = L.num_q_heads / L.num_kv_heads;
+  const int narrow = L.k_bits == 12 ? 16 : 32;  // the most of vq_tree.cu
   if (const char* env = std::getenv("VQ_TREE_ROWS"))
     for (int rows : {16, 32, 128, 256})
-      if (std::atoi(env) == rows) return rows;
-  const int group = L.num_q_heads / L.num_kv_heads;
+      if (std::atoi(env) == rows && (rows <= narrow || rows >= 128)) return rows;
   const long long rows = static_cast<long long>(max_new_len) * group;
   const int per_tile = 128 / group;  // tokens of 128 rows
   const bool three = max_new_len > 2 * per_tile && max_new_len <= 3 * per_tile && L.k_bits != 12;
   const bool ragged = max_new_len <= 2 * per_tile && static_cast<long long>(num_tokens) * group <= (96 + rows / 4) * batch;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || three || ragged ? 128 : 256;
+  return rows <= 16 ? 16 : rows <= narrow ? 32 : rows <= 128 || three || ragged ? 128 : 256;
 }
 
 struct TreeArgs {

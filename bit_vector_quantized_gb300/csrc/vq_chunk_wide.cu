@@ -29,7 +29,8 @@
 //     (tensor memory has its columns) 2.1e-4 is all that is left, but a block has
 //     32 products instead of 24: a chunk of 2048 in 32K took 1215 us instead of
 //     943, chunks of 1000 with a window of 1024 161 instead of 132, 5 drafted
-//     tokens 203 instead of 158.
+//     tokens 203 instead of 158.  (Trees of drafted tokens have P's low part: 66 us instead of 60 for a
+//     tree of 64 in 32K, 270 instead of 225 for trees of 26, batch 16 at (2,8), (4,9).)
 //   * One warp walks the CTA's pieces and hands them to the others, so that
 //     none of them carries the walk in registers.
 //   * Tensor memory, all 512 columns: S twice (P overwrites its S, so the
@@ -68,7 +69,7 @@ namespace vqk {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
+constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8 (a tree's 2^15)
 constexpr int kTile = 128;           // query rows of a CTA's tile, and tokens of a block
 constexpr int kSoftWarps = 8, kCodeWarps = 16;
 constexpr int kWideThreads = (kSoftWarps + kCodeWarps + 4) * 32;  // the issuer's warpgroup has two busy warps
@@ -382,23 +383,43 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       return u.blk1 - u.blk0;
     };
     // ---- a block: its scores, their masks and maximum, P with the maximum so far -----------------
-    auto passes = [&](float v) { return v > m + kSlack || (m == -INFINITY && v > -INFINITY); };
+    constexpr float kLead = kTree ? kLift : 0.f;  // (m: the maximum so far less this)
+    auto passes = [&](float v) { return v > m + (kSlack + kLead) || (m == -INFINITY && v > -INFINITY); };
     auto col_s = [&]() { return tmem + lanes + kColS + 128 * (blocks & 1u) + 64 * g; };
     auto meet = [&]() { return tops + (blocks & 1u) * 2 * kTile; };
-    // p, its sum, and P in fp16 over its own scores
+    // p, its sum, and P in fp16 over its own scores (of a tree two parts, the low one 16 columns behind the high one)
     auto store_p = [&](const uint32_t(&s)[32], uint32_t at, float mu) {
-      uint32_t w[16];
+      if constexpr (kTree) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
-        add2(x0, x1, mu, mu);
-        x0 = fast_exp2(x0);
-        x1 = fast_exp2(x1);
-        add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x0, x1);
-        const __half2 h = __floats2half2_rn(x0, x1);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int c = 0; c < 16; c += 4) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = c + j;
+            float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+            add2(x0, x1, mu, mu);
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x0, x1);
+            cut_pair(x0, x1, hi[j], lo[j]);
+          }
+          tmem_st4(at + c, hi);
+          tmem_st4(at + 16 + c, lo);
+        }
+      } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+          add2(x0, x1, mu, mu);
+          x0 = fast_exp2(x0);
+          x1 = fast_exp2(x1);
+          add2(sum[2 * (i & 1)], sum[2 * (i & 1) + 1], x0, x1);
+          const __half2 h = __floats2half2_rn(x0, x1);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        tmem_st16(at, w);
       }
-      tmem_st16(at, w);
     };
     auto scores_wait = [&]() { return wait(s_full + (blocks & 3u), (blocks >> 2) & 1u); };
     auto block_half = [&](int j) {
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
       again = again || __any_sync(kAll, passes(other));
       if (again) {  // (both warps of the rows come here)
         mx = fmaxf(mx, other);
-        const float m_new = passes(mx) ? mx : m;
+        const float m_new = passes(mx) ? mx - kLead : m;
         const float scale = m_new == m ? 1.f : fast_exp2(m - m_new);  // 0 while nothing is accumulated
         m = m_new;
         l *= scale;
@@ -750,6 +771,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
             for (int ks = 0; ks < 8; ++ks)  // P of tokens 32 c .. 32 c + 31 sits at column 32 c
               tc_mma_ts<kPair>(tmem + kColO, tmem + kColS + 128 * sb + 32 * (ks >> 1) + 8 * (ks & 1),
                                tc_desc(vt + ks * 2048, kTile * 128), kValues, j > 0 || ks > 0);
+            if constexpr (kTree) {  // P's low parts
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_ts<kPair>(tmem + kColO, tmem + kColS + 128 * sb + 16 + 32 * (ks >> 1) + 8 * (ks & 1),
+                                 tc_desc(vt + ks * 2048, kTile * 128), kValues, true);
+            }
             tc_commit<kPair>(v_empty + rv.slot);
             if (j + 2 >= nblk) tc_commit<kPair>(o_full + (j + 1 == nblk));
           }

@@ -128,6 +128,20 @@ __device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
       : "f"(y0), "f"(y1));
 }
 
+// A tree's weights p = 2^(s - m) are products' operands as two fp16 parts, 22 bits: with the first alone outputs were off by
+// 2.0e-4 to 2.8e-4 (relative, against 64 bits), of which their own rounding is 1.9e-4 to 2.1e-4, and that is all that is left.
+// m is the maximum less kLift.  The maximum may lag by 2^8, so p stays under 2^15, and fp16, which ends at 2^16 above and is
+// subnormal under 2^-14, has all bits down to 2^-21 of the largest weight; below it p is off by up to 2^-31 of that.  (The
+// tensor core's fp32 sums drop what is under 2^-24 of what they hold already.)
+constexpr float kLift = 7.f;
+
+// p0 and p1 (not negative) -> fp16 pairs of their first 11 bits and of the next 11.
+__device__ __forceinline__ void cut_pair(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(p1), "f"(p0));
+  add2(p0, p1, __uint_as_float((__float_as_uint(p0) & 0xffffe000u) | 0x80000000u), __uint_as_float((__float_as_uint(p1) & 0xffffe000u) | 0x80000000u));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(p1), "f"(p0));
+}
+
 // A ring slot's position: phase flips each time the ring wraps.
 struct Ring {
   uint32_t slot = 0, phase = 0;

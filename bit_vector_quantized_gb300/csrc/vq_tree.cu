@@ -9,9 +9,8 @@
 //   * K~ goes from the gathers straight into tensor memory (a thread's token is a lane), V as 16-byte pieces into
 //     swizzled shared memory (rows of dims, the token as k), so of a block of 128 tokens 96 KB are gathered and stored
 //     and 32 KB read by the tensor core, where tiles of query rows take 128 KB and 96 KB.
-//   * Q~ stays in shared memory, high and low fp16 parts, for the tile (scores keep about fp32 accuracy); P is
-//     rounded to fp16 once (p <= 2^8, relative 2^-11), as everywhere in chunk attention.
-//     So high and low parts are columns of one product of 2 N.
+//   * Q~ stays in shared memory, high and low fp16 parts, for the tile (scores keep about fp32 accuracy), and so does P of a
+//     block (vq_chunk_wide.cuh has why).  High and low parts are columns of one product of 2 N, in either product.
 //   * Four or eight warps do the softmax: a thread has one token and 16 rows.  The rows' maxima are in shared memory and
 //     may lag by 2^8, so the usual block needs no maximum over the tokens, only a vote whether one moved.
 //   * Eight warps expand K, eight V, four of them every other block, a thread a whole token; one thread issues, one warp
@@ -34,8 +33,8 @@ namespace vqk {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^8
-constexpr float kUnset = 1e30f;      // minus the maximum of a row that has seen nothing
+constexpr float kSlack = 8.f;        // the running maximum may lag by this much (log2 units): p <= 2^(8 + kLift)
+constexpr float kUnset = 1e30f;      // in place of kLift minus the maximum, of a row that has seen nothing
 constexpr int kBlockTok = 128;       // tokens of a block
 constexpr int kCodeWarps = 16;
 constexpr uint32_t kKStages = 4;
@@ -54,7 +53,7 @@ struct TreeShape {
   static_assert(kSoftWarps * kSoft + kCodeWarps * kCode + 4 * kIssue <= (kThreads / 32) * kLaunch, "the block's registers at the launch");
   // Tensor memory: S of high and low parts, twice; O; K~ of blocks under way.
   static constexpr uint32_t kColS = 0, kColO = 4 * N, kCols = 512, kColK = kCols - 64 * kKStages;
-  static_assert(kColO + N <= kColK, "columns");
+  static_assert(kColO + 2 * N <= kColK, "columns");
 };
 constexpr int kMasks = 4;            // token masks in flight (vq_chunk_wide.cu has why four are enough)
 
@@ -62,7 +61,9 @@ template <int DK, int BK, int DV, int BV, int N>
 struct TreeSmem {
   using Table = WideTable<DK, BV>;
   static constexpr int kVTile = kBlockTok * kHeadDim * 2, kVStages = 2;
-  static constexpr int kPTile = kBlockTok * 128;       // P of two blocks: rows of tokens of 128 bytes, a block's in either half
+  // P of two blocks: rows of tokens of 128 bytes, the rows' high parts and then their low ones; N = 16: two blocks' in a row.
+  static constexpr uint32_t kPNext = N == 16 ? 64 : kBlockTok * 128;  // from an even block's to an odd one's
+  static constexpr int kPTile = (N == 16 ? 1 : 2) * kBlockTok * 128;
   static constexpr int kQTile = 2 * N * kHeadDim * 2;  // rows of high parts, then of low parts
   static constexpr int kV = Table::kBytes;
   static constexpr int kP = kV + kVStages * kVTile;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
   uint32_t* const tmem_at = masks + kMasks * 4;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_at + 1);
   volatile uint32_t* const done = tmem_at + 2;  // blocks whose values are under way
-  float* const neg_max = reinterpret_cast<float*>(g_smem + W::kTops);  // [N]
+  float* const neg_max = reinterpret_cast<float*>(g_smem + W::kTops);  // [N] kLift minus the maxima
   float* const scales = neg_max + N;                                   // [N]
   float* const tops = scales + N;                                      // [4][N]
 
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
             if (!see) s[c] = __float_as_uint(-INFINITY);
           }
         };
-        // minus the maxima so far; whether one is passed
+        // minus the maxima so far, plus kLift; whether one is passed
         auto shift = [&]() {
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
           float top = max3(s[0], s[1], s[2]);
 #pragma unroll
           for (int c = 3; c + 1 < NC; c += 2) top = max3(__float_as_uint(top), s[c], s[c + 1]);
-          return fmaxf(top, __uint_as_float(s[NC - 1])) > kSlack;
+          return fmaxf(top, __uint_as_float(s[NC - 1])) > kSlack + kLift;
         };
         bool passed = false;
         if (ok) {
@@ -312,9 +313,10 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
           if (quarter == 0 && lane < NC) {
             const float top = fmaxf(fmaxf(tops[col], tops[N + col]), fmaxf(tops[2 * N + col], tops[3 * N + col]));
             const bool unset = old == -kUnset;
-            const bool moves = top > -INFINITY && (unset || top > old + kSlack);
-            scales[col] = moves && !unset ? fast_exp2(old - top) : 1.f;  // (unset: nothing is accumulated)
-            if (moves) neg_max[col] = -top;
+            const bool moves = top > -INFINITY && (unset || top > old + (kSlack + kLift));
+            const float next = kLift - top;
+            scales[col] = moves && !unset ? fast_exp2(old + next) : 1.f;  // (unset: nothing is accumulated)
+            if (moves) neg_max[col] = next;
           }
           half_sync();
           if (ok) {
@@ -331,6 +333,11 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
 #pragma unroll
                 for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * scales[NC * g + c]);
                 tmem_st16(tmem + lanes + kColO + NC * g, o);
+                tmem_ld16(tmem + lanes + kColO + N + NC * g, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * scales[NC * g + c]);
+                tmem_st16(tmem + lanes + kColO + N + NC * g, o);
                 tmem_wait_st();
               }
             }
@@ -342,16 +349,19 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
           const uint32_t row = smem_addr(ps) + tok * 128;
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 8) {
-            uint32_t w[4];
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float x0 = fast_exp2(__uint_as_float(s[c0 + 2 * i])), x1 = fast_exp2(__uint_as_float(s[c0 + 2 * i + 1]));
               add2(l[c0 + 2 * i], l[c0 + 2 * i + 1], x0, x1);
-              const __half2 h = __floats2half2_rn(x0, x1);
-              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              cut_pair(x0, x1, hi[i], lo[i]);
             }
-            const uint32_t piece = (NC * g + c0) / 8 + 4 * (blocks & 1u);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((piece ^ (tok & 7)) << 4)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+            const uint32_t piece = (NC * g + c0) / 8 + (N == 16 ? 4 * (blocks & 1u) : 0u);
+            const uint32_t tile = row + (N == 16 ? 0u : (blocks & 1u) * W::kPNext);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + ((piece ^ (tok & 7)) << 4)), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (((piece + N / 8) ^ (tok & 7)) << 4)), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]),
+                         "r"(lo[3])
                          : "memory");
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -390,6 +400,13 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
         uint32_t o[NC];
         tmem_ld16(tmem + lanes + kColO + NC * g, o);
         tmem_wait_ld();
+        {  // of the low parts
+          uint32_t low[NC];
+          tmem_ld16(tmem + lanes + kColO + N + NC * g, low);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(low[c]));
+        }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int r = NC * g + c;
@@ -536,7 +553,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
     // ================================= the products ====================================
     reg_dec<Shape::kIssue>();
     if (warp == kSoftWarps + kCodeWarps) {
-      constexpr uint32_t kScores = tc_idesc(kBlockTok, 2 * N, false), kValues = tc_idesc_rows_k(kHeadDim, N);
+      constexpr uint32_t kScores = tc_idesc(kBlockTok, 2 * N, false), kValues = tc_idesc_rows_k(kHeadDim, 2 * N);
       const uint32_t v0 = smem_addr(tiles), q0 = smem_addr(g_smem + W::kQ), p0 = smem_addr(g_smem + W::kP);
       Ring rk, rv;
       uint32_t blocks = 0, tiles_done = 0;
@@ -567,7 +584,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vt = v0 + rv.slot * W::kVTile, pt = p0 + (blk & 1u) * 64;
+            const uint32_t vt = v0 + rv.slot * W::kVTile, pt = p0 + (blk & 1u) * W::kPNext;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
               tc_mma_ss(tmem + kColO, tc_desc(vt + ks * 2048, kBlockTok * 128), tc_desc(pt + ks * 2048, kBlockTok * 128), kValues,
@@ -681,7 +698,10 @@ cudaError_t launch_rows(const ChunkParams& p, int grid, cudaStream_t stream) {
 
 template <int DK, int BK, int DV, int BV>
 cudaError_t launch_format(const ChunkParams& p, int grid, cudaStream_t stream) {
-  return p.tile_rows == 16 ? launch_rows<DK, BK, DV, BV, 16>(p, grid, stream) : launch_rows<DK, BK, DV, BV, 32>(p, grid, stream);
+  if (p.tile_rows == 16) return launch_rows<DK, BK, DV, BV, 16>(p, grid, stream);
+  // (32 rows not beside the 1.5-bit format's tables, which leave no room for P's second tile)
+  if constexpr (BK != 12) return launch_rows<DK, BK, DV, BV, 32>(p, grid, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

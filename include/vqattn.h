@@ -478,6 +478,9 @@ size_t vq_chunk_workspace_bytes(const vq_layout* layout, int32_t batch, int32_t 
  * position: that of a cached token is its place, that of a drafted one
  * positions[row], or the first drafted token's place where that is further.
  * A row that sees nothing (pages out of range, nothing cached and no bit) is zero.
+ * Weights have 22 bits and are summed in fp32: outputs are off by their own rounding to
+ * fp16 (and where one token's weight is past 2^24 times that of many others, by what these
+ * would add to it: a sum of N values loses at most N 2^-23 of the largest).
  *   tree_masks    uint64 [num_tokens][mask_words], 16-byte aligned, bit j of a
  *                 row being bit j % 64 of word j / 64; bits from n on name nothing.
  *   mask_words    at least max_new_len / 64, rounded up; at most 64.
