@@ -191,8 +191,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
     if (tid == 0 && rank == 0) write_record(p, worker, nullptr);
     return;
   }
-  // (blockDim.x, not the constant: with it the loop is unrolled otherwise, prompts at 1.5 bit take 96.4 us instead of 94.4)
-  if constexpr (!kTree) fill_wide_table<DK, BK, DV, BV>(p, tid, blockDim.x);
+  if constexpr (!kTree) fill_wide_table<DK, BK, DV, BV>(p);
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(ready + i, soft + kCodeWarps + passed);

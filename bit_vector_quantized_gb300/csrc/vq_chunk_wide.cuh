@@ -82,8 +82,10 @@ struct WideTable {
   static constexpr int kBytes = kWideCodes ? 131072 : kSplitTable ? (256 + 512) * 128 : 65536;
 };
 
+// (By thread `thread` of `threads`, or, with 0, by all of the CTA's.  Those step by the built-in variables themselves: with the
+// kernel's own copies of them 5 drafted tokens, batch 16, take 158.4 us instead of 156.5.)
 template <int DK, int BK, int DV, int BV>
-__device__ __forceinline__ void fill_wide_table(const ChunkParams& p, int thread, int threads) {
+__device__ __forceinline__ void fill_wide_table(const ChunkParams& p, int thread = 0, int threads = 0) {
   using W = WideTable<DK, BV>;
   uint4* tab = reinterpret_cast<uint4*>(g_smem);
   auto replicas = [](const void* cb, int row, bool four) {
@@ -94,7 +96,7 @@ __device__ __forceinline__ void fill_wide_table(const ChunkParams& p, int thread
     const uint32_t c = __ldg(static_cast<const uint32_t*>(cb) + row);
     return make_uint4(c, c, c, c);
   };
-  for (int i = thread; i < W::kBytes / 16; i += threads) {
+  auto put = [&](int i) {
     if constexpr (W::kWideCodes) {
       tab[i] = i < 4096 ? __ldg(static_cast<const uint4*>(p.cb_k) + i) : __ldg(static_cast<const uint4*>(p.cb_v) + i - 4096);
     } else if constexpr (W::kSplitTable) {
@@ -102,6 +104,11 @@ __device__ __forceinline__ void fill_wide_table(const ChunkParams& p, int thread
     } else {
       tab[i] = i & 8 ? replicas(p.cb_v, i >> 4, DV == 4) : replicas(p.cb_k, i >> 4, DK == 4);
     }
+  };
+  if (threads) {
+    for (int i = thread; i < W::kBytes / 16; i += threads) put(i);
+  } else {
+    for (int i = threadIdx.x; i < W::kBytes / 16; i += blockDim.x) put(i);
   }
 }
 
