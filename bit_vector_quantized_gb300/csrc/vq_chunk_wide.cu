@@ -668,8 +668,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) vq_chunk_wide_kernel(const Ch
         now.align(part);
 #pragma unroll
         for (int c = 0; c < Codes::kPieces; ++c) {
-          // (a tree's token that cannot be read: some centroids, whose scores are masked and whose p is 0)
-          const uint4 v = kTree || has ? gather_piece<Codes, kShift>(now, c, table) : make_uint4(0, 0, 0, 0);
+          // (a tree's token that cannot be read: some centroid of K, whose score is masked, but zeros of V: p is 0, and a
+          // centroid that no code names may be no number)
+          const uint4 v = (kTree && is_k) || has ? gather_piece<Codes, kShift>(now, c, table) : make_uint4(0, 0, 0, 0);
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (c << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                        : "memory");
         }

@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
     reg_dec<Shape::kCode>();
     // Eight expand K, eight V, four of them every other block; a thread takes one token's 128 dims.  K: a warp's tokens
     // are the lanes of tensor memory that it may write.  (A token that cannot be read gets what stands in the
-    // registers for codes: some centroids, whose scores are masked and whose p is 0.)
+    // registers for codes: some centroid of K, whose score is masked, and zeros of V: p is 0, but a centroid that no code
+    // names may be no number.)
     const int set = (warp >> 2) & 1, tok = 32 * (warp & 3) + lane;
     auto expand = [&](auto codes, auto row_bytes, const uint8_t* pool, uint32_t table, auto is_k) {
       using Codes = decltype(codes);
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(TreeShape<N>::kThreads, 1) vq_tree_kernel(cons
           const uint32_t at = v_at + stage * W::kVTile;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const uint4 v = gather_piece<Codes, kShift>(now, c, table);
+            const uint4 v = has ? gather_piece<Codes, kShift>(now, c, table) : make_uint4(0, 0, 0, 0);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"((at ^ ((c & 7) << 4)) + (c >> 3) * (kBlockTok * 128)), "r"(v.x), "r"(v.y), "r"(v.z),
                          "r"(v.w)
                          : "memory");
