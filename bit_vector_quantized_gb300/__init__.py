@@ -956,6 +956,8 @@ def keep_tokens(layout: vq_layout, seq_lens, cu_new_lens, keep, keep_lens, page_
         _check(lib().vq_keep_tokens(ctypes.byref(layout), B, *args, _arg(r[0], i32, "seq_lens_out", dev, (B,)),
                                     _arg(r[1], i32, "num_free_out", dev, (1,)),
                                     _arg(status, i32, "status", dev, (1,)), st))
+        if B == 0 and r.num_free is not num_free:  # (the call writes nothing then)
+            r.num_free.copy_(num_free)
         return r
 
     return _launch(dev, stream, call)

@@ -665,7 +665,8 @@ vq_status vq_append_kv(const vq_layout* layout, const vq_rotary_config* config,
  * (VQ_DEV_BAD_LENGTH).  Of several faults one is reported.
  *   batch 0 .. 16384, max_keep 0 .. 256.  Outputs other than the two pairs
  *   named above must not overlap inputs; no pool is given twice.
- * Two kernels on `stream`.  batch == 0 is a no-op returning VQ_OK (num_free_out is not written).
+ * Two kernels on `stream`.  batch == 0 is a no-op returning VQ_OK (num_free_out is not written;
+ * the Python call copies num_free there).
  */
 vq_status vq_keep_tokens(const vq_layout* layout, int32_t batch, const int32_t* seq_lens,
                          const int32_t* cu_new_lens, const int32_t* keep, int32_t max_keep,
