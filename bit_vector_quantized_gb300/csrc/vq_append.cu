@@ -25,16 +25,16 @@
 // Two kernels.  8- and 9-bit codes: tcgen05, 128 sub-vectors by 128 centroids a product; tensor memory gives the
 // minima of 16 columns as it is read (tcgen05.ld.red).  12-bit codes, whose 4096 centroids do not fit shared memory as
 // operands of 128 bytes: m16n8k8 warp mma, groups of 32 of which a lane holds 8 scores.  Warp mma for the others
-// too took 209 us where tcgen05 takes 177 (4099 bf16 tokens of 8 KV heads at (2,8) and (4,9)), 271 and 215 (8192
-// tokens at (4,8)), 16 and 15.5 (64 tokens).
+// too took 209 us where tcgen05 took 177 (4099 bf16 tokens of 8 KV heads at (2,8) and (4,9)), 271 and 215 (8192
+// tokens at (4,8)), 16 and 15.5 (64 tokens), all with narrower bounds on a key's error than now.
 //
 // What bounds them.  tcgen05: instructions and latency at 16 warps an SM (128 registers; with 80 for 24 warps they
-// spill: 265 us), issuing in 53 % of the cycles, about 1000 warp instructions for a vector of 32 sub-vectors: a quarter the
-// scores and their minima, a quarter step 2, rotation and transform of a key 270, its queries 120.  The queries' CTAs
-// come last and take 20 to 27 us of 215.  The floor is 25 us, the bytes of 8192 tokens.  Two chunks of 64 centroids
-// under way instead of one of 128 took 280 us, minima of 8 columns instead of 16
+// spill: 265 us), issuing in 55 % of the cycles, about 1100 warp instructions for a vector of 32 sub-vectors: a quarter the
+// scores and their minima, a quarter step 2, rotation, transform and bound of a key 330, its queries 120.  The queries' CTAs
+// come last and take 20 to 27 us of 229, steps 3 and 4 about 8.  The floor is 25 us, the bytes of 8192 tokens.  In an earlier
+// state (215 us) two chunks of 64 centroids under way instead of one of 128 took 280 us, minima of 8 columns instead of 16
 // nothing for it and 199 us instead of 183 at (2,8), (4,9).  Warp mma: the
-// tensor pipe is 53 % busy with products of k = 8 (333 tokens of 8 KV heads: 135 us, floor 3).
+// tensor pipe is 49 % busy with products of k = 8 (333 tokens of 8 KV heads: 135 us, floor 3).
 #include "vq_rotary.cuh"
 #include "vq_tcgen05.cuh"
 #include "vq_turn.cuh"

@@ -18,13 +18,13 @@
 //     thread half a token: 249 us instead of 190 for 16 tiles of 16 rows over 32K tokens, by instructions.)
 //   * The planning warp plans while the others fill the table, and one warp sends the codes to L2 ahead of the others.
 //
-// What bounds it.  N = 16: the shared-memory pipe, 1150 cycles of it for a block of 128 tokens by counters, of 1370
-// that a block takes ((4,8) codes); (2,8) keys and 9-bit values 2000.  N = 32 a little more (2600 at (2,8), (4,9));
-// at 1.5 bit 2650, the gathers of the plain tables meeting in the same banks.  Around the blocks a piece costs 5.5 us
-// (q~, the first block's maxima, sums and output), the start 6 us.  Measured, merge included: 16 rows of each of 8
-// sequences of 4000 to 8000 tokens, 8 KV heads: 45 us, 32 rows 51; 32 rows over 32K 41 (tiles of 128 rows: 55, 55 and
-// 45); 28 rows of each of 48 sequences of 3000 to 6000 at 1.5 bit 167 us (168).  A variant for 64 rows did not
-// beat tiles of 128: its softmax threads, 32 rows each, spilled.
+// What bounds it.  No pipe is full by counters (16 rows of each of 8 sequences of 4000 to 8000, (4,8)): shared memory 29 %,
+// issue 27 %, tensor 7 %; the warps wait for codes and, around the blocks, for one another (a piece's q~, first
+// maxima, sums and output cost about 5 us, the start 6).  A block of 128 tokens takes 1110 wavefronts of shared memory there,
+// 1940 at 1.5 bit, where half of them are the plain tables' bank conflicts (pipe 60 % busy).  Measured, merge included, 8 KV
+// heads: 16 rows of each of those 8 sequences 42 us, 32 rows 49 (tiles of 128 rows 55 and 56); of each of
+// 16 sequences of 32K 202 and 275 at (4,8), 226 and 305 at (2,8), (4,9), 296 for 16 rows at 1.5 bit; 32 rows over one
+// sequence of 32K 39.  A variant for 64 rows did not beat tiles of 128: its softmax threads, 32 rows each, spilled.
 #include <type_traits>
 
 #include "vq_chunk_wide.cuh"
